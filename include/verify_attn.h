@@ -208,6 +208,60 @@ va_status verify_attn_sparse(const va_shape *shape, const void *q, const void *k
                              size_t ws_bytes, va_stream stream);
 
 /*
+ * Score shaping: what some target models do to their attention scores, beyond
+ * the scale.  For query head h at position pos_q and a key at position pos_k,
+ *   s = scale q.k
+ *   s = softcap tanh(s / softcap)                    (softcap > 0)
+ *   s = s - slopes[h] |pos_q - pos_k|                (slopes given)
+ * and the key is visible when
+ *   pos_q - pos_k < window                           (window > 0)
+ *   and, for a prefix slot j, j >= key_start[b]      (key_start given)
+ * on top of the draft mask.  Distances are counted in cache slots: a prefix
+ * key's position is its slot, draft token t's is token_pos[b][t].  token_pos
+ * NULL means L_b + t (a chain); a tree or a mask with a window or slopes must
+ * give it (L_b + depth for a tree).
+ *   softcap     0 (none) or 1e-6 .. 1e6
+ *   window      0 (none) or 1 .. 2^23; 1 leaves each token its own position
+ *   slopes      [Hq] fp32, finite (any sign)
+ *   key_start   [B] int32, the first visible prefix slot: the start of the
+ *               current document in a cache that packs several, or of the live
+ *               rows of a left-padded one.  <= 0 hides nothing, >= L_b the
+ *               whole prefix
+ *   token_pos   [B][T] int32, |token_pos - L_b| < 2^23 (device-checked: recorded
+ *               as VA_ERR_DEVICE_BOUNDS and clamped)
+ * All pointers are device pointers; each may be NULL.  Prefix tiles that no
+ * row sees are not read, and what a hidden key holds does not matter: a K or V
+ * row that no row of its (sequence, kv-head) sees may be NaN or infinite (one
+ * that some row sees has to be finite), and page entries of pages that lie
+ * wholly below the lowest visible slot may be out of range (a window cache that
+ * has given them back).
+ */
+typedef struct {
+  float softcap;
+  int window;
+  const float *slopes;
+  const int32_t *key_start;
+  const int32_t *token_pos;
+} va_score_mod;
+
+/*
+ * verify_attn_dense and verify_attn_paged with score shaping: the same layouts,
+ * draft masks, workspace, outputs and errors.  q and the draft keys are taken
+ * as stored (rotated by verify_rope_draft_* where the model rotates).  A row
+ * that sees no key gets out = 0 and lse = -inf.  mod must not be NULL.
+ */
+va_status verify_attn_dense_mod(const va_shape *shape, const va_score_mod *mod, const void *q, const void *k_cache,
+                                const void *v_cache, int max_cache_len, const int32_t *seqlens,
+                                const int32_t *tree_parent, const uint32_t *tree_mask, void *out, float *lse,
+                                void *workspace, size_t ws_bytes, va_stream stream);
+
+va_status verify_attn_paged_mod(const va_shape *shape, const va_score_mod *mod, const void *q, const void *k_pages,
+                                const void *v_pages, int num_pages, int page_size, const int32_t *page_table,
+                                int max_pages_per_seq, const int32_t *seqlens, const int32_t *tree_parent,
+                                const uint32_t *tree_mask, void *out, float *lse, void *workspace, size_t ws_bytes,
+                                va_stream stream);
+
+/*
  * Exact log-sum-exp merge of partial attentions of the same rows (LongSpec
  * 2.C, the log-sum-exp fusion): lse = ln sum_s exp(lse_s), out = sum_s
  * exp(lse_s - lse) * o_s.  o_parts [n_parts][n_rows][D] fp32 (each part
@@ -367,6 +421,85 @@ va_status verify_commit_kv_paged(const va_shape *shape, void *k_pages, void *v_p
                                  int page_size, const int32_t *page_table, int max_pages_per_seq,
                                  const int32_t *seqlens, const int32_t *path, const int32_t *n_accept,
                                  int32_t *seqlens_out, void *workspace, va_stream stream);
+
+/*
+ * Accumulated attention weight: the attention that the accepted tokens of a
+ * step gave to every cached key, added to running totals per kv-head.  A cache
+ * is evicted by these totals (verify_build_index takes them as its score).
+ * Call it after verify_commit_kv_*, with the prefix lengths L_b from before the
+ * commit and the verification call's q and lse: accepted row i < a (a =
+ * n_accept[b]) is draft token path[b][i], now at slot L_b + i, and
+ *   p(h, i, j) = exp(s(q[b][path[i]][h], key j) - lse[b][h][path[i]]), j <= L_b + i
+ *   weight[b][g][j] = (j < L_b ? decay * weight[b][g][j] : 0)
+ *                     + sum over the heads h of kv-head g and i < a of p(h, i, j)
+ * for j < L_b + a; totals past that are not touched.  Committed slots
+ * L_b .. L_b+a-1 start their total here, so it needs no clearing.  The sums are
+ * fp32, in a fixed order.
+ *   shape: B, T (<= 64), Hq, Hkv, scale; sizes and types as for the
+ *     attention calls (see va_shape).
+ *   mod: the score shaping of the verification call, or NULL; its token_pos is
+ *     not read (accepted row i is at L_b + i).
+ *   q [B][T][Hq][D] and the keys as they were scored (rotated where the model
+ *     rotates), 16-byte aligned; lse [B][Hq][T]; path [B][T] int32 as
+ *     verify_accept_greedy returns it (NULL: path[i] = i), n_accept [B] int32
+ *     (NULL: T).  Rows with lse = -inf add nothing.
+ *   decay in [0, 1]; weight fp32 [B][Hkv][weight_stride].
+ *   Dense: k_cache [B][max_cache_len][Hkv][D].  Paged: as verify_attn_paged.
+ * L_b + a must fit the cache and weight_stride, and path entries [0, T)
+ * (device-checked: a bad sequence is left alone, a bad path entry adds
+ * nothing; VA_ERR_DEVICE_BOUNDS in `workspace`, which may be NULL).
+ */
+va_status verify_accumulate_weight_dense(const va_shape *shape, const va_score_mod *mod, const void *q,
+                                         const void *k_cache, int max_cache_len, const int32_t *seqlens,
+                                         const int32_t *path, const int32_t *n_accept, const float *lse, float decay,
+                                         float *weight, int weight_stride, void *workspace, va_stream stream);
+
+va_status verify_accumulate_weight_paged(const va_shape *shape, const va_score_mod *mod, const void *q,
+                                         const void *k_pages, int num_pages, int page_size, const int32_t *page_table,
+                                         int max_pages_per_seq, const int32_t *seqlens, const int32_t *path,
+                                         const int32_t *n_accept, const float *lse, float decay, float *weight,
+                                         int weight_stride, void *workspace, va_stream stream);
+
+/*
+ * Eviction: the rows of a keep set move to the front of the cache, in place.
+ * For every (sequence, kv-head), row indices[b][h][j] of K, V and weight moves
+ * to slot j, j < n_indices[b][h]; later slots keep what they hold.  The new
+ * length is seqlens_out[b] = n_indices[b][0].  Every kv-head keeps its own
+ * rows, so slot j may hold another token in each; distances (va_score_mod) then
+ * count kept rows.
+ *   indices [B][Hkv][max_indices] and n_indices [B][Hkv] int32 as
+ *     verify_build_index writes them (with the accumulated weight as its
+ *     scores): strictly increasing entries in [0, L_b), the same n in every
+ *     kv-head of a sequence.
+ *   shape: B, Hkv, D and dtype (T, Hq and scale are not used); rows of D
+ *     elements must be a multiple of 16 bytes, at most 1 KB; caches 16-byte
+ *     aligned.  B * Hkv <= 2048.
+ *   weight fp32 [B][Hkv][weight_stride], or NULL.
+ *   seqlens_out [B], must not alias seqlens.
+ *   scratch: caller-owned device memory of at least
+ *     verify_evict_kv_scratch_size() bytes, 256-byte aligned, initialised once
+ *     with verify_attn_workspace_init() and left as it was by every completed
+ *     call; calls that run concurrently need separate ones.
+ *   Paged: pages as for verify_attn_paged.  A page that two sequences share is
+ *     written by both: copy it first.  Whole pages past the new length are free
+ *     afterwards.
+ * A sequence with a bad length or count is left alone (seqlens_out = L_b) and
+ * a bad index or page leaves its row in place; both are recorded as
+ * VA_ERR_DEVICE_BOUNDS in `workspace` (may be NULL), and the kept rows of that
+ * sequence are then undefined.
+ */
+size_t verify_evict_kv_scratch_size(int B, int Hkv, int max_indices);
+
+va_status verify_evict_kv_dense(const va_shape *shape, void *k_cache, void *v_cache, int max_cache_len,
+                                const int32_t *seqlens, const int32_t *indices, const int32_t *n_indices,
+                                int max_indices, float *weight, int weight_stride, int32_t *seqlens_out, void *scratch,
+                                size_t scratch_bytes, void *workspace, va_stream stream);
+
+va_status verify_evict_kv_paged(const va_shape *shape, void *k_pages, void *v_pages, int num_pages, int page_size,
+                                const int32_t *page_table, int max_pages_per_seq, const int32_t *seqlens,
+                                const int32_t *indices, const int32_t *n_indices, int max_indices, float *weight,
+                                int weight_stride, int32_t *seqlens_out, void *scratch, size_t scratch_bytes,
+                                void *workspace, va_stream stream);
 
 /* Wait for `stream`, read and clear the device status word of `workspace`.
  * Returns VA_OK or the first device-side error recorded since the last check.

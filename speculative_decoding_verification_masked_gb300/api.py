@@ -30,6 +30,11 @@ class VerifyAttnError(RuntimeError):
         self.status = status
 
 
+class VaScoreMod(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int), ("slopes", ctypes.c_void_p),
+                ("key_start", ctypes.c_void_p), ("token_pos", ctypes.c_void_p)]
+
+
 class VaShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int),
                 ("D", ctypes.c_int), ("dtype", ctypes.c_int), ("scale", ctypes.c_float),
@@ -61,6 +66,18 @@ _SIGS = {
                                      _P]),
     "verify_head_importance_scratch_size": (_SZ, [_I, _I, _I, _I]),
     "verify_head_importance": (_I, [ctypes.POINTER(VaShape), _P, _P, _I, _P, _P, _I, _P, _I, _P, _SZ, _P, _P]),
+    "verify_attn_dense_mod": (_I, [ctypes.POINTER(VaShape), ctypes.POINTER(VaScoreMod), _P, _P, _P, _I, _P, _P, _P, _P,
+                                   _P, _P, _SZ, _P]),
+    "verify_attn_paged_mod": (_I, [ctypes.POINTER(VaShape), ctypes.POINTER(VaScoreMod), _P, _P, _P, _I, _I, _P, _I, _P,
+                                   _P, _P, _P, _P, _P, _SZ, _P]),
+    "verify_accumulate_weight_dense": (_I, [ctypes.POINTER(VaShape), ctypes.POINTER(VaScoreMod), _P, _P, _I, _P, _P, _P,
+                                            _P, ctypes.c_float, _P, _I, _P, _P]),
+    "verify_accumulate_weight_paged": (_I, [ctypes.POINTER(VaShape), ctypes.POINTER(VaScoreMod), _P, _P, _I, _I, _P, _I,
+                                            _P, _P, _P, _P, ctypes.c_float, _P, _I, _P, _P]),
+    "verify_evict_kv_scratch_size": (_SZ, [_I, _I, _I]),
+    "verify_evict_kv_dense": (_I, [ctypes.POINTER(VaShape), _P, _P, _I, _P, _P, _P, _I, _P, _I, _P, _P, _SZ, _P, _P]),
+    "verify_evict_kv_paged": (_I, [ctypes.POINTER(VaShape), _P, _P, _I, _I, _P, _I, _P, _P, _P, _I, _P, _I, _P, _P,
+                                   _SZ, _P, _P]),
     "verify_attn_check_status": (_I, [_P, _P]),
     "verify_attn_last_error": (ctypes.c_char_p, []),
     "verify_attn_version": (ctypes.c_char_p, []),
@@ -373,6 +390,219 @@ def verify_head_importance(q, k_cache, seqlens, heads, score=None, score_stride=
                                         scratch.ptr, scratch.nbytes,
                                         workspace.ptr if workspace is not None else None, _stream(stream)))
     return score
+
+
+# ----------------------------------------------------------------------------
+# score shaping, accumulated attention weight, eviction
+# ----------------------------------------------------------------------------
+
+def _arg(t, name, shape, dtype, device):
+    """Device pointer of a contiguous tensor of this shape (None = any size), type and device; None stays None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor or None")
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must live on the GPU")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, q or the cache on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError("tensor arguments must be contiguous")
+    return t.data_ptr()
+
+
+def _need(t, name, dim):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must live on the GPU")
+    if t.dim() != dim:
+        raise ValueError(f"{name}: expected {dim} dimensions, got {list(t.shape)}")
+
+
+def _run_on(device, stream, name, *args):
+    """Call library function `name` with `device` current, on `stream` (that
+    device's current stream by default); args end before the stream."""
+    f = getattr(lib(), name)
+    with torch.cuda.device(device):
+        s = torch.cuda.current_stream(device) if stream is None else stream
+        _check(f(*args, ctypes.c_void_p(s.cuda_stream)))
+
+
+def _own(make, device, stream):
+    """A workspace made for one call: its memory is not reused before the work on `stream` is done."""
+    with torch.cuda.device(device):
+        ws = make()
+    if stream is not None:
+        ws.buffer.record_stream(stream)
+    return ws
+
+
+class ScoreMod:
+    """Score shaping of a target model (see va_score_mod in include/verify_attn.h):
+    tanh cap, sliding window, distance slopes fp32 [Hq], first visible prefix
+    slots int32 [B], positions of the draft tokens int32 [B][T].  Keeps
+    references to the tensors; they are read when a call runs."""
+
+    def __init__(self, softcap=0.0, window=0, slopes=None, key_start=None, token_pos=None):
+        self.softcap, self.window = float(softcap), int(window)
+        self.slopes, self.key_start, self.token_pos = slopes, key_start, token_pos
+
+    def struct(self, B, T, Hq, device) -> VaScoreMod:
+        return VaScoreMod(self.softcap, self.window, _arg(self.slopes, "slopes", (Hq,), torch.float32, device),
+                          _arg(self.key_start, "key_start", (B,), torch.int32, device),
+                          _arg(self.token_pos, "token_pos", (B, T), torch.int32, device))
+
+
+def _mod_call(layout, q, k, v, table, seqlens, mod, tree_parent, tree_mask, out, lse, workspace, scale, stream):
+    _need(q, "q", 4)
+    _need(k, "the key cache", 4)
+    B, T, Hq, D = q.shape
+    n0, n1, Hkv = k.shape[:3]
+    dev = q.device
+    if not isinstance(mod, ScoreMod):
+        raise TypeError("mod: expected a ScoreMod")
+    shape = _shape_of(q, Hkv, scale)
+    out, lse = _outputs(q, out, lse)
+    cache = (B, None, Hkv, D) if layout == "dense" else (None, None, Hkv, D)
+    kv = [_arg(q, "q", (B, T, Hq, D), q.dtype, dev), _arg(k, "the key cache", cache, q.dtype, dev),
+          _arg(v, "the value cache", tuple(k.shape), q.dtype, dev)]
+    if seqlens is None or (layout == "paged" and table is None):
+        raise TypeError("seqlens and page_table must be tensors")
+    geo = [n1] if layout == "dense" else [n0, n1, _arg(table, "page_table", (B, None), torch.int32, dev), table.shape[1]]
+    m = mod.struct(B, T, Hq, dev)
+    rest = [_arg(seqlens, "seqlens", (B,), torch.int32, dev), _arg(tree_parent, "tree_parent", (B, T), torch.int32, dev),
+            _arg(tree_mask, "tree_mask", (B, T, (T + 31) // 32), torch.int32, dev),
+            _arg(out, "out", (B, T, Hq, D), q.dtype, dev), _arg(lse, "lse", (B, Hq, T), torch.float32, dev)]
+    ws = workspace
+    if ws is None:
+        ws = _own(lambda: Workspace.for_shape(shape, dev, stream), dev, stream)
+    elif ws.buffer.device != dev:
+        raise ValueError(f"workspace is on {ws.buffer.device}, q on {dev}")
+    _run_on(dev, stream, f"verify_attn_{layout}_mod", ctypes.byref(shape), ctypes.byref(m), *kv, *geo, *rest, ws.ptr,
+            ws.nbytes)
+    return out, lse
+
+
+def verify_attn_dense_mod(q, k_cache, v_cache, seqlens, mod: ScoreMod, tree_parent=None, tree_mask=None, out=None,
+                          lse=None, workspace: Workspace = None, scale=None, stream=None):
+    """verify_attn_dense with score shaping; returns (out [B][T][Hq][D], lse [B][Hq][T])."""
+    return _mod_call("dense", q, k_cache, v_cache, None, seqlens, mod, tree_parent, tree_mask, out, lse, workspace,
+                     scale, stream)
+
+
+def verify_attn_paged_mod(q, k_pages, v_pages, page_table, seqlens, mod: ScoreMod, tree_parent=None, tree_mask=None,
+                          out=None, lse=None, workspace: Workspace = None, scale=None, stream=None):
+    """verify_attn_paged with score shaping; pages [P][page][Hkv][D], page_table int32 [B][max_pages]."""
+    return _mod_call("paged", q, k_pages, v_pages, page_table, seqlens, mod, tree_parent, tree_mask, out, lse,
+                     workspace, scale, stream)
+
+
+def _status_ptr(workspace, device):
+    if workspace is None:
+        return None
+    if workspace.buffer.device != device:
+        raise ValueError(f"workspace is on {workspace.buffer.device}, the cache on {device}")
+    return workspace.ptr
+
+
+def _weight_call(layout, q, k, table, seqlens, lse, weight, mod, path, n_accept, decay, scale, workspace, stream):
+    _need(q, "q", 4)
+    _need(k, "the key cache", 4)
+    _need(weight, "weight", 3)
+    B, T, Hq, D = q.shape
+    n0, n1, Hkv = k.shape[:3]
+    dev = q.device
+    shape = _shape_of(q, Hkv, scale)
+    cache = (B, None, Hkv, D) if layout == "dense" else (None, None, Hkv, D)
+    if seqlens is None or lse is None or (layout == "paged" and table is None):
+        raise TypeError("seqlens, lse and page_table must be tensors")
+    if mod is not None and not isinstance(mod, ScoreMod):
+        raise TypeError("mod: expected a ScoreMod or None")
+    m = mod.struct(B, T, Hq, dev) if mod is not None else None
+    geo = [n1] if layout == "dense" else [n0, n1, _arg(table, "page_table", (B, None), torch.int32, dev), table.shape[1]]
+    _run_on(dev, stream, f"verify_accumulate_weight_{layout}", ctypes.byref(shape),
+            ctypes.byref(m) if m is not None else None, _arg(q, "q", (B, T, Hq, D), q.dtype, dev),
+            _arg(k, "the key cache", cache, q.dtype, dev), *geo, _arg(seqlens, "seqlens", (B,), torch.int32, dev),
+            _arg(path, "path", (B, T), torch.int32, dev), _arg(n_accept, "n_accept", (B,), torch.int32, dev),
+            _arg(lse, "lse", (B, Hq, T), torch.float32, dev), float(decay),
+            _arg(weight, "weight", (B, Hkv, None), torch.float32, dev), weight.shape[2], _status_ptr(workspace, dev))
+    return weight
+
+
+def verify_accumulate_weight_dense(q, k_cache, seqlens, lse, weight, mod: ScoreMod = None, path=None, n_accept=None,
+                                   decay=1.0, scale=None, workspace: Workspace = None, stream=None):
+    """Add the attention the accepted tokens gave to every cached key to weight
+    fp32 [B][Hkv][stride], in place (after the commit, with the seqlens from
+    before it and the verification call's q and lse); returns weight."""
+    return _weight_call("dense", q, k_cache, None, seqlens, lse, weight, mod, path, n_accept, decay, scale, workspace,
+                        stream)
+
+
+def verify_accumulate_weight_paged(q, k_pages, page_table, seqlens, lse, weight, mod: ScoreMod = None, path=None,
+                                   n_accept=None, decay=1.0, scale=None, workspace: Workspace = None, stream=None):
+    """The same totals over a paged cache."""
+    return _weight_call("paged", q, k_pages, page_table, seqlens, lse, weight, mod, path, n_accept, decay, scale,
+                        workspace, stream)
+
+
+class EvictScratch(Workspace):
+    """Caller-owned device scratch of the eviction, initialised once."""
+
+    def __init__(self, B, Hkv, max_indices, device=None, stream=None):
+        n = int(lib().verify_evict_kv_scratch_size(int(B), int(Hkv), int(max_indices)))
+        if n == 0:
+            _check(VA_ERR_INVALID_ARG)
+        super().__init__(n, device=device, stream=stream)
+
+
+def _evict_call(layout, k, v, table, seqlens, indices, n_indices, weight, seqlens_out, scratch, workspace, stream):
+    _need(k, "the key cache", 4)
+    _need(indices, "indices", 3)
+    n0, n1, Hkv, D = k.shape
+    B = indices.shape[0]
+    dev = k.device
+    if seqlens is None or n_indices is None or v is None or (layout == "paged" and table is None):
+        raise TypeError("the caches, seqlens, n_indices and page_table must be tensors")
+    if seqlens_out is None:
+        seqlens_out = torch.empty(B, dtype=torch.int32, device=dev)
+    shape = make_shape(B, 1, Hkv, Hkv, D, _dtype_code(k), 1.0)
+    cache = (B, None, Hkv, D) if layout == "dense" else (None, None, Hkv, D)
+    geo = [n1] if layout == "dense" else [n0, n1, _arg(table, "page_table", (B, None), torch.int32, dev), table.shape[1]]
+    args = [_arg(k, "the key cache", cache, k.dtype, dev), _arg(v, "the value cache", tuple(k.shape), k.dtype, dev),
+            *geo, _arg(seqlens, "seqlens", (B,), torch.int32, dev),
+            _arg(indices, "indices", (B, Hkv, None), torch.int32, dev),
+            _arg(n_indices, "n_indices", (B, Hkv), torch.int32, dev), indices.shape[2],
+            _arg(weight, "weight", (B, Hkv, None), torch.float32, dev), weight.shape[2] if weight is not None else 0,
+            _arg(seqlens_out, "seqlens_out", (B,), torch.int32, dev)]
+    sc = scratch
+    if sc is None:
+        sc = _own(lambda: EvictScratch(B, Hkv, max(indices.shape[2], 1), dev, stream), dev, stream)
+    elif sc.buffer.device != dev:
+        raise ValueError(f"scratch is on {sc.buffer.device}, the cache on {dev}")
+    _run_on(dev, stream, f"verify_evict_kv_{layout}", ctypes.byref(shape), *args, sc.ptr, sc.nbytes,
+            _status_ptr(workspace, dev))
+    return seqlens_out
+
+
+def verify_evict_kv_dense(k_cache, v_cache, seqlens, indices, n_indices, weight=None, seqlens_out=None,
+                          scratch: EvictScratch = None, workspace: Workspace = None, stream=None):
+    """Move the kept rows indices [B][Hkv][n] of k_cache / v_cache [B][len][Hkv][D]
+    (and of weight fp32 [B][Hkv][stride]) to the front, in place; returns the
+    new lengths."""
+    return _evict_call("dense", k_cache, v_cache, None, seqlens, indices, n_indices, weight, seqlens_out, scratch,
+                       workspace, stream)
+
+
+def verify_evict_kv_paged(k_pages, v_pages, page_table, seqlens, indices, n_indices, weight=None, seqlens_out=None,
+                          scratch: EvictScratch = None, workspace: Workspace = None, stream=None):
+    """The same eviction through a page table; pages [P][page][Hkv][D]."""
+    return _evict_call("paged", k_pages, v_pages, page_table, seqlens, indices, n_indices, weight, seqlens_out,
+                       scratch, workspace, stream)
 
 
 def verify_attn_check_status(workspace: Workspace, stream=None):

@@ -16,8 +16,10 @@
 #include "va_common.cuh"
 #include "va_kernels.h"
 #include "va_commit.h"
+#include "va_evict.h"
 #include "va_score.h"
 #include "va_rope.h"
+#include "va_weight.h"
 #include "verify_attn_testing.h"
 
 namespace {
@@ -136,7 +138,8 @@ bool tck_enabled() {
   return !(e != nullptr && strcmp(e, "mma") == 0);
 }
 
-RowPlan row_plan(const va_shape &s) {
+// (Calls with score shaping always take the tcgen05 kernels at d128.)
+RowPlan row_plan(const va_shape &s, bool shaped = false) {
   RowPlan r;
   r.R = (s.Hq / s.Hkv) * s.T;
   r.use_tc = 0;
@@ -147,7 +150,7 @@ RowPlan row_plan(const va_shape &s) {
     r.use_tc = 1;
     r.RG = 4;
     r.rows_pad = r.R > 128 ? 256 : 128;
-  } else if (s.D == 128 && tck_enabled()) {
+  } else if (s.D == 128 && (shaped || tck_enabled())) {
     r.use_tc = 2;
     r.RG = 4;
     r.rows_pad = r.R <= 16 ? 16 : (r.R <= 32 ? 32 : 64);
@@ -182,8 +185,8 @@ va_status check_shape(const va_shape *s) {
   return VA_OK;
 }
 
-size_t workspace_bytes(const va_shape &s, int sm_count) {
-  const RowPlan rp = row_plan(s);
+size_t workspace_bytes(const va_shape &s, int sm_count, bool shaped = false) {
+  const RowPlan rp = row_plan(s, shaped);
   const int slots = rp.S + rp.cps * sm_count;  // one partial slot per (segment, CTA) boundary
   return va::ws_layout(rp.S, slots, rp.rows_pad, s.D).total;
 }
@@ -218,20 +221,54 @@ va_status check_common(const Common &c) {
   return VA_OK;
 }
 
+// Checks a call's score shaping and turns it into kernel parameters.  The
+// scores come out in units of `unit` (log2 e: base 2).  `draft_mask`: the call
+// has a tree or a mask, whose tokens' positions are not those of a chain.
+va_status check_mod(const va_score_mod &m, float scale, float unit, bool draft_mask, va::ModParams &mp) {
+  if (m.softcap != 0.f && !(m.softcap >= 1e-6f && m.softcap <= 1e6f))
+    return fail(VA_ERR_INVALID_ARG, "softcap=%g must be 0 or in [1e-6, 1e6]", (double)m.softcap);
+  if (m.softcap != 0.f && !isfinite(scale / m.softcap))
+    return fail(VA_ERR_INVALID_ARG, "scale / softcap overflows");
+  if (m.window < 0 || m.window > va::kModMaxWindow)
+    return fail(VA_ERR_INVALID_ARG, "window=%d must be in [0, 2^23]", m.window);
+  if (!aligned(m.slopes, 4) || !aligned(m.key_start, 4) || !aligned(m.token_pos, 4))
+    return fail(VA_ERR_INVALID_ARG, "slopes, key_start and token_pos must be 4-byte aligned");
+  if (draft_mask && (m.window > 0 || m.slopes != nullptr) && m.token_pos == nullptr)
+    return fail(VA_ERR_INVALID_ARG, "a window or slopes with a tree or a mask need token_pos");
+  memset(&mp, 0, sizeof mp);
+  mp.on = 1;
+  mp.softcap = m.softcap;
+  mp.in_mul = m.softcap > 0.f ? scale / m.softcap : 0.f;
+  mp.out_mul = (m.softcap > 0.f ? m.softcap : scale) * unit;
+  mp.window = m.window;
+  mp.slopes = m.slopes;
+  mp.key_start = m.key_start;
+  mp.token_pos = m.token_pos;
+  return VA_OK;
+}
+
 va_status run_attention(const Common &c, int layout, const void *k, const void *v, int len_cap, int num_pages,
                         int page_size, const int32_t *page_table, int max_pages, const int32_t *indices,
-                        const int32_t *n_indices, int max_indices, cudaStream_t stream) {
+                        const int32_t *n_indices, int max_indices, cudaStream_t stream,
+                        const va_score_mod *mod = nullptr) {
   const va_shape &s = *c.shape;
   int dev = 0;
+  va::ModParams mp;
+  memset(&mp, 0, sizeof mp);
+  if (mod != nullptr) {
+    const va_status st = check_mod(*mod, s.scale, va::kModLog2e, c.parent != nullptr || c.mask != nullptr, mp);
+    if (st != VA_OK) return st;
+  }
   const int sms = device_sm_count(&dev);
   if (sms <= 0) return fail(VA_ERR_CUDA, "no usable CUDA device");
-  const size_t need = workspace_bytes(s, sms);
+  const size_t need = workspace_bytes(s, sms, mod != nullptr);
   if (c.ws_bytes < need)
     return fail(VA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", c.ws_bytes, need);
-  const RowPlan rp = row_plan(s);
+  const RowPlan rp = row_plan(s, mod != nullptr);
 
   va::AttnParams p;
   memset(&p, 0, sizeof p);
+  p.mod = mp;
   p.B = s.B;
   p.T = s.T;
   p.Hq = s.Hq;
@@ -311,7 +348,7 @@ va_status run_attention(const Common &c, int layout, const void *k, const void *
   // more than 128 packed rows with K/V tiles by TMA: VA_MANY_ROWS_KERNEL=tcp
   // selects the two-M-tile kernel of 128-key tiles instead of the 64-key
   // rows-on-lanes kernel
-  if (p.use_tc == 1 && p.rows_pad == 256 && p.tma_box > 0) {
+  if (p.use_tc == 1 && p.rows_pad == 256 && p.tma_box > 0 && mod == nullptr) {
     const char *e = getenv("VA_MANY_ROWS_KERNEL");
     if (e != nullptr && strcmp(e, "tcp") == 0) p.use_tc = 3;
   }
@@ -328,9 +365,152 @@ va_status run_attention(const Common &c, int layout, const void *k, const void *
   return ok();
 }
 
+va_status attn_dense(const Common &c, const void *k_cache, const void *v_cache, int max_cache_len,
+                     const va_score_mod *mod, cudaStream_t stream) {
+  va_status st = check_common(c);
+  if (st != VA_OK) return st;
+  if (k_cache == nullptr || v_cache == nullptr) return fail(VA_ERR_INVALID_ARG, "k_cache and v_cache must not be NULL");
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return fail(VA_ERR_INVALID_ARG, "caches must be 16-byte aligned");
+  if (max_cache_len < c.shape->T)
+    return fail(VA_ERR_INVALID_ARG, "max_cache_len=%d is smaller than T=%d", max_cache_len, c.shape->T);
+  return run_attention(c, VA_LAYOUT_DENSE, k_cache, v_cache, max_cache_len, 0, 1, nullptr, 0, nullptr, nullptr, 0,
+                       stream, mod);
+}
+
+va_status attn_paged(const Common &c, const void *k_pages, const void *v_pages, int num_pages, int page_size,
+                     const int32_t *page_table, int max_pages_per_seq, const va_score_mod *mod, cudaStream_t stream) {
+  va_status st = check_common(c);
+  if (st != VA_OK) return st;
+  if (k_pages == nullptr || v_pages == nullptr || page_table == nullptr)
+    return fail(VA_ERR_INVALID_ARG, "k_pages, v_pages and page_table must not be NULL");
+  if (!aligned(k_pages, 16) || !aligned(v_pages, 16)) return fail(VA_ERR_INVALID_ARG, "pages must be 16-byte aligned");
+  if (page_size < 1 || page_size > 1024 || (page_size & (page_size - 1)) != 0)
+    return fail(VA_ERR_INVALID_ARG, "page_size=%d must be a power of two in [1, 1024]", page_size);
+  if (num_pages < 1 || max_pages_per_seq < 1) return fail(VA_ERR_INVALID_ARG, "num_pages and max_pages_per_seq must be >= 1");
+  const long long cap = (long long)max_pages_per_seq * page_size;
+  if (cap < c.shape->T) return fail(VA_ERR_INVALID_ARG, "max_pages_per_seq*page_size is smaller than T");
+  if (cap >= (1ll << 30)) return fail(VA_ERR_UNSUPPORTED, "max_pages_per_seq*page_size too large");
+  return run_attention(c, VA_LAYOUT_PAGED, k_pages, v_pages, (int)cap, num_pages, page_size, page_table,
+                       max_pages_per_seq, nullptr, nullptr, 0, stream, mod);
+}
+
 }  // namespace
 
 namespace {
+// The page arguments of the calls outside attention: fills the geometry of a
+// paged cache of at least `least` slots a sequence.
+template <typename P>
+va_status check_pages(P &p, const int32_t *page_table, int num_pages, int page_size, int max_pages_per_seq, int least) {
+  if (page_table == nullptr) return fail(VA_ERR_INVALID_ARG, "page_table must not be NULL");
+  if (page_size < 1 || page_size > 1024 || (page_size & (page_size - 1)) != 0)
+    return fail(VA_ERR_INVALID_ARG, "page_size=%d must be a power of two in [1, 1024]", page_size);
+  if (num_pages < 1 || max_pages_per_seq < 1) return fail(VA_ERR_INVALID_ARG, "num_pages and max_pages_per_seq must be >= 1");
+  const long long cap = (long long)max_pages_per_seq * page_size;
+  if (cap < least || cap >= (1ll << 30))
+    return fail(VA_ERR_INVALID_ARG, "max_pages_per_seq * page_size = %lld must be in [%d, 2^30)", cap, least);
+  p.len_cap = (int)cap;
+  p.page_table = page_table;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages_per_seq;
+  while ((1 << p.page_shift) < page_size) ++p.page_shift;
+  return VA_OK;
+}
+
+va_status weight_common(const va_shape *shape, const va_score_mod *mod, const void *q, const void *k,
+                        const int32_t *seqlens, const int32_t *path, const int32_t *n_accept, const float *lse,
+                        float decay, float *weight, int weight_stride, void *workspace, va::WeightParams &p) {
+  va_status st = check_shape(shape);
+  if (st != VA_OK) return st;
+  if (q == nullptr || k == nullptr || seqlens == nullptr || lse == nullptr || weight == nullptr)
+    return fail(VA_ERR_INVALID_ARG, "q, the key cache, seqlens, lse and weight must not be NULL");
+  if (!aligned(q, 16) || !aligned(k, 16)) return fail(VA_ERR_INVALID_ARG, "q and the key cache must be 16-byte aligned");
+  if (!aligned(lse, 4) || !aligned(weight, 4) || !aligned(path, 4) || !aligned(n_accept, 4))
+    return fail(VA_ERR_INVALID_ARG, "lse, weight, path and n_accept must be 4-byte aligned");
+  if (!(decay >= 0.f && decay <= 1.f)) return fail(VA_ERR_INVALID_ARG, "decay must be in [0, 1]");
+  if (weight_stride < 1 || weight_stride > (1 << 30))
+    return fail(VA_ERR_INVALID_ARG, "weight_stride=%d must be in [1, 2^30]", weight_stride);
+  if (workspace != nullptr && !aligned(workspace, 256)) return fail(VA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  memset(&p, 0, sizeof p);
+  p.B = shape->B;
+  p.T = shape->T;
+  p.Hq = shape->Hq;
+  p.Hkv = shape->Hkv;
+  p.D = shape->D;
+  p.dtype = shape->dtype;
+  p.q = q;
+  p.k = k;
+  p.seqlens = seqlens;
+  p.path = path;
+  p.n_accept = n_accept;
+  p.lse = lse;
+  p.decay = decay;
+  p.weight = weight;
+  p.stride = weight_stride;
+  p.status = static_cast<int *>(workspace);
+  const va_score_mod none = {0.f, 0, nullptr, nullptr, nullptr};
+  // natural units; accepted row i sits at L_b + i, so no token_pos
+  st = check_mod(mod != nullptr ? *mod : none, shape->scale, 1.f, false, p.mod);
+  if (st != VA_OK) return st;
+  p.mod.token_pos = nullptr;
+  return VA_OK;
+}
+
+va_status run_weight(const va::WeightParams &p, cudaStream_t stream) {
+  cudaError_t e = va::launch_accumulate_weight(p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "accumulated weight launch");
+  return ok();
+}
+
+va_status run_evict(const va::EvictParams &p, cudaStream_t stream) {
+  cudaError_t e = va::launch_evict_kv(p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "eviction launch");
+  return ok();
+}
+
+va_status evict_common(const va_shape *shape, void *k, void *v, const int32_t *seqlens, const int32_t *indices,
+                       const int32_t *n_indices, int max_indices, float *weight, int weight_stride,
+                       int32_t *seqlens_out, void *scratch, size_t scratch_bytes, void *workspace, va::EvictParams &p) {
+  if (shape == nullptr) return fail(VA_ERR_INVALID_ARG, "shape is NULL");
+  if (shape->B < 1 || shape->Hkv < 1) return fail(VA_ERR_INVALID_ARG, "B and Hkv must be >= 1");
+  if ((long long)shape->B * shape->Hkv > kMaxSegments)
+    return fail(VA_ERR_UNSUPPORTED, "B*Hkv = %lld exceeds %d", (long long)shape->B * shape->Hkv, kMaxSegments);
+  if (shape->dtype != VA_DTYPE_BF16 && shape->dtype != VA_DTYPE_FP32)
+    return fail(VA_ERR_INVALID_ARG, "unknown dtype %d", (int)shape->dtype);
+  const int es = shape->dtype == VA_DTYPE_BF16 ? 2 : 4;
+  if (shape->D < 1 || shape->D > 1024 || (shape->D * es) % 16 != 0 || shape->D * es > 1024)
+    return fail(VA_ERR_UNSUPPORTED, "rows of D=%d elements must be a multiple of 16 bytes, at most 1 KB", shape->D);
+  if (k == nullptr || v == nullptr || seqlens == nullptr || indices == nullptr || n_indices == nullptr ||
+      seqlens_out == nullptr)
+    return fail(VA_ERR_INVALID_ARG, "caches, seqlens, indices, n_indices and seqlens_out must not be NULL");
+  if (!aligned(k, 16) || !aligned(v, 16)) return fail(VA_ERR_INVALID_ARG, "caches must be 16-byte aligned");
+  if (seqlens_out == seqlens) return fail(VA_ERR_INVALID_ARG, "seqlens_out must not alias seqlens");
+  if (max_indices < 1 || max_indices > (1 << 30))
+    return fail(VA_ERR_INVALID_ARG, "max_indices=%d must be in [1, 2^30]", max_indices);
+  if (weight != nullptr && (weight_stride < 1 || !aligned(weight, 4)))
+    return fail(VA_ERR_INVALID_ARG, "weight must be 4-byte aligned and weight_stride >= 1");
+  if (scratch == nullptr || !aligned(scratch, 256)) return fail(VA_ERR_WORKSPACE, "scratch must be 256-byte aligned");
+  const size_t need = va::evict_scratch_bytes(shape->B, shape->Hkv, max_indices);
+  if (scratch_bytes < need) return fail(VA_ERR_WORKSPACE, "scratch has %zu bytes, %zu needed", scratch_bytes, need);
+  if (workspace != nullptr && !aligned(workspace, 256)) return fail(VA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  memset(&p, 0, sizeof p);
+  p.B = shape->B;
+  p.Hkv = shape->Hkv;
+  p.row_bytes = shape->D * es;
+  p.k = k;
+  p.v = v;
+  p.seqlens = seqlens;
+  p.indices = indices;
+  p.n_indices = n_indices;
+  p.max_indices = max_indices;
+  p.weight = weight;
+  p.stride = weight_stride;
+  p.seqlens_out = seqlens_out;
+  p.scratch = scratch;
+  p.status = static_cast<int *>(workspace);
+  p.wait_ns = wait_limit_ns();
+  return VA_OK;
+}
+
 va_status commit_common(const va_shape *shape, void *k, void *v, const int32_t *seqlens, const int32_t *path,
                         const int32_t *n_accept, int32_t *seqlens_out, void *workspace, va::CommitParams &cp) {
   if (shape == nullptr) return fail(VA_ERR_INVALID_ARG, "shape is NULL");
@@ -419,15 +599,27 @@ va_status verify_attn_dense(const va_shape *shape, const void *q, const void *k_
                             int max_cache_len, const int32_t *seqlens, const int32_t *tree_parent,
                             const uint32_t *tree_mask, const int32_t *positions, void *out, float *lse,
                             void *workspace, size_t ws_bytes, va_stream stream) {
-  Common c{shape, q, seqlens, tree_parent, tree_mask, positions, out, lse, workspace, ws_bytes};
-  va_status st = check_common(c);
-  if (st != VA_OK) return st;
-  if (k_cache == nullptr || v_cache == nullptr) return fail(VA_ERR_INVALID_ARG, "k_cache and v_cache must not be NULL");
-  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return fail(VA_ERR_INVALID_ARG, "caches must be 16-byte aligned");
-  if (max_cache_len < shape->T)
-    return fail(VA_ERR_INVALID_ARG, "max_cache_len=%d is smaller than T=%d", max_cache_len, shape->T);
-  return run_attention(c, VA_LAYOUT_DENSE, k_cache, v_cache, max_cache_len, 0, 1, nullptr, 0, nullptr, nullptr, 0,
-                       (cudaStream_t)stream);
+  return attn_dense(Common{shape, q, seqlens, tree_parent, tree_mask, positions, out, lse, workspace, ws_bytes},
+                    k_cache, v_cache, max_cache_len, nullptr, (cudaStream_t)stream);
+}
+
+va_status verify_attn_dense_mod(const va_shape *shape, const va_score_mod *mod, const void *q, const void *k_cache,
+                                const void *v_cache, int max_cache_len, const int32_t *seqlens,
+                                const int32_t *tree_parent, const uint32_t *tree_mask, void *out, float *lse,
+                                void *workspace, size_t ws_bytes, va_stream stream) {
+  if (mod == nullptr) return fail(VA_ERR_INVALID_ARG, "mod must not be NULL");
+  return attn_dense(Common{shape, q, seqlens, tree_parent, tree_mask, nullptr, out, lse, workspace, ws_bytes}, k_cache,
+                    v_cache, max_cache_len, mod, (cudaStream_t)stream);
+}
+
+va_status verify_attn_paged_mod(const va_shape *shape, const va_score_mod *mod, const void *q, const void *k_pages,
+                                const void *v_pages, int num_pages, int page_size, const int32_t *page_table,
+                                int max_pages_per_seq, const int32_t *seqlens, const int32_t *tree_parent,
+                                const uint32_t *tree_mask, void *out, float *lse, void *workspace, size_t ws_bytes,
+                                va_stream stream) {
+  if (mod == nullptr) return fail(VA_ERR_INVALID_ARG, "mod must not be NULL");
+  return attn_paged(Common{shape, q, seqlens, tree_parent, tree_mask, nullptr, out, lse, workspace, ws_bytes}, k_pages,
+                    v_pages, num_pages, page_size, page_table, max_pages_per_seq, mod, (cudaStream_t)stream);
 }
 
 va_status verify_attn_paged(const va_shape *shape, const void *q, const void *k_pages, const void *v_pages,
@@ -435,20 +627,9 @@ va_status verify_attn_paged(const va_shape *shape, const void *q, const void *k_
                             const int32_t *seqlens, const int32_t *tree_parent, const uint32_t *tree_mask,
                             const int32_t *positions, void *out, float *lse, void *workspace, size_t ws_bytes,
                             va_stream stream) {
-  Common c{shape, q, seqlens, tree_parent, tree_mask, positions, out, lse, workspace, ws_bytes};
-  va_status st = check_common(c);
-  if (st != VA_OK) return st;
-  if (k_pages == nullptr || v_pages == nullptr || page_table == nullptr)
-    return fail(VA_ERR_INVALID_ARG, "k_pages, v_pages and page_table must not be NULL");
-  if (!aligned(k_pages, 16) || !aligned(v_pages, 16)) return fail(VA_ERR_INVALID_ARG, "pages must be 16-byte aligned");
-  if (page_size < 1 || page_size > 1024 || (page_size & (page_size - 1)) != 0)
-    return fail(VA_ERR_INVALID_ARG, "page_size=%d must be a power of two in [1, 1024]", page_size);
-  if (num_pages < 1 || max_pages_per_seq < 1) return fail(VA_ERR_INVALID_ARG, "num_pages and max_pages_per_seq must be >= 1");
-  const long long cap = (long long)max_pages_per_seq * page_size;
-  if (cap < shape->T) return fail(VA_ERR_INVALID_ARG, "max_pages_per_seq*page_size is smaller than T");
-  if (cap >= (1ll << 30)) return fail(VA_ERR_UNSUPPORTED, "max_pages_per_seq*page_size too large");
-  return run_attention(c, VA_LAYOUT_PAGED, k_pages, v_pages, (int)cap, num_pages, page_size, page_table,
-                       max_pages_per_seq, nullptr, nullptr, 0, (cudaStream_t)stream);
+  return attn_paged(Common{shape, q, seqlens, tree_parent, tree_mask, positions, out, lse, workspace, ws_bytes},
+                    k_pages, v_pages, num_pages, page_size, page_table, max_pages_per_seq, nullptr,
+                    (cudaStream_t)stream);
 }
 
 va_status verify_attn_sparse(const va_shape *shape, const void *q, const void *k_cache, const void *v_cache,
@@ -706,6 +887,71 @@ va_status verify_commit_kv_paged(const va_shape *shape, void *k_pages, void *v_p
   cudaError_t e = va::launch_commit_kv(cp, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "commit launch");
   return ok();
+}
+
+va_status verify_accumulate_weight_dense(const va_shape *shape, const va_score_mod *mod, const void *q,
+                                         const void *k_cache, int max_cache_len, const int32_t *seqlens,
+                                         const int32_t *path, const int32_t *n_accept, const float *lse, float decay,
+                                         float *weight, int weight_stride, void *workspace, va_stream stream) {
+  va::WeightParams p;
+  va_status st = weight_common(shape, mod, q, k_cache, seqlens, path, n_accept, lse, decay, weight, weight_stride,
+                               workspace, p);
+  if (st != VA_OK) return st;
+  if (max_cache_len < 1 || max_cache_len >= (1 << 30))
+    return fail(VA_ERR_INVALID_ARG, "max_cache_len=%d must be in [1, 2^30)", max_cache_len);
+  p.len_cap = max_cache_len;
+  return run_weight(p, (cudaStream_t)stream);
+}
+
+va_status verify_accumulate_weight_paged(const va_shape *shape, const va_score_mod *mod, const void *q,
+                                         const void *k_pages, int num_pages, int page_size, const int32_t *page_table,
+                                         int max_pages_per_seq, const int32_t *seqlens, const int32_t *path,
+                                         const int32_t *n_accept, const float *lse, float decay, float *weight,
+                                         int weight_stride, void *workspace, va_stream stream) {
+  va::WeightParams p;
+  va_status st = weight_common(shape, mod, q, k_pages, seqlens, path, n_accept, lse, decay, weight, weight_stride,
+                               workspace, p);
+  if (st != VA_OK) return st;
+  st = check_pages(p, page_table, num_pages, page_size, max_pages_per_seq, 1);
+  if (st != VA_OK) return st;
+  return run_weight(p, (cudaStream_t)stream);
+}
+
+size_t verify_evict_kv_scratch_size(int B, int Hkv, int max_indices) {
+  if (B < 1 || Hkv < 1 || max_indices < 1 || (long long)B * Hkv > kMaxSegments || max_indices > (1 << 30)) {
+    fail(VA_ERR_INVALID_ARG, "B=%d Hkv=%d max_indices=%d: sizes must be >= 1, B*Hkv at most %d, max_indices at most 2^30",
+         B, Hkv, max_indices, kMaxSegments);
+    return 0;
+  }
+  return va::evict_scratch_bytes(B, Hkv, max_indices);
+}
+
+va_status verify_evict_kv_dense(const va_shape *shape, void *k_cache, void *v_cache, int max_cache_len,
+                                const int32_t *seqlens, const int32_t *indices, const int32_t *n_indices,
+                                int max_indices, float *weight, int weight_stride, int32_t *seqlens_out, void *scratch,
+                                size_t scratch_bytes, void *workspace, va_stream stream) {
+  va::EvictParams p;
+  va_status st = evict_common(shape, k_cache, v_cache, seqlens, indices, n_indices, max_indices, weight, weight_stride,
+                              seqlens_out, scratch, scratch_bytes, workspace, p);
+  if (st != VA_OK) return st;
+  if (max_cache_len < 1 || max_cache_len >= (1 << 30))
+    return fail(VA_ERR_INVALID_ARG, "max_cache_len=%d must be in [1, 2^30)", max_cache_len);
+  p.len_cap = max_cache_len;
+  return run_evict(p, (cudaStream_t)stream);
+}
+
+va_status verify_evict_kv_paged(const va_shape *shape, void *k_pages, void *v_pages, int num_pages, int page_size,
+                                const int32_t *page_table, int max_pages_per_seq, const int32_t *seqlens,
+                                const int32_t *indices, const int32_t *n_indices, int max_indices, float *weight,
+                                int weight_stride, int32_t *seqlens_out, void *scratch, size_t scratch_bytes,
+                                void *workspace, va_stream stream) {
+  va::EvictParams p;
+  va_status st = evict_common(shape, k_pages, v_pages, seqlens, indices, n_indices, max_indices, weight, weight_stride,
+                              seqlens_out, scratch, scratch_bytes, workspace, p);
+  if (st != VA_OK) return st;
+  st = check_pages(p, page_table, num_pages, page_size, max_pages_per_seq, 1);
+  if (st != VA_OK) return st;
+  return run_evict(p, (cudaStream_t)stream);
 }
 
 va_status verify_attn_check_status(void *workspace, va_stream stream) {

@@ -58,7 +58,7 @@ struct Cfg : StageGeom<Tin, D> {
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
-template <typename Tin, int D, int RG, int CPS, bool kRope>
+template <typename Tin, int D, int RG, int CPS, bool kRope, bool kMod>
 __global__ void __launch_bounds__(kThreads, CPS)
     verify_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv) {
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
     fence_mbar_init();
   }
   // ---- plan: tiles per segment, exclusive scan, this CTA's tile range ----
-  const CtaRange cr = plan_cta(p, tstart);
+  const CtaRange cr = plan_cta<kTK, kMod>(p, tstart);
   if (c >= cr.G) return;
   const long long total = cr.total;
   const int G = cr.G;
@@ -107,19 +107,20 @@ __global__ void __launch_bounds__(kThreads, CPS)
 
   if (warp == kNWC) {
     bool pok = true;
-    produce_tiles<Tin, D, NS>(p, &tmk, &tmv, tstart, cr, stages, full, empty, abort_flag, use_tma, pok);
+    produce_tiles<Tin, D, NS, kTK, NS, 1, -1, kMod>(p, &tmk, &tmv, tstart, cr, stages, full, empty, abort_flag, use_tma, pok);
     return;
   }
 
   // ============================ consumer warps ============================
-  const float cl2 = p.scale * kLog2e;  // scores are kept raw; exp2 takes scale*log2(e)
+  // scores are kept raw and exp2 takes scale*log2(e); shaped scores are in base-2 units already
+  const float cl2 = kMod ? 1.f : p.scale * kLog2e;
   const int group = p.Hq / p.Hkv;
   int it = 0;
   bool ok = true;
   int rope_b = -1;  // sequence whose rotary table is in shared memory
 
   for (int s = s0; s < S && tstart[s] < t1; ++s) {
-    const Seg g = seg_info(p, s, false);
+    const Seg g = seg_info<kMod, kTK>(p, s, false);
     const int lt0 = max(tstart[s], t0) - tstart[s];
     const int lt1 = min(tstart[s + 1], t1) - tstart[s];
     const int first_cta = owner_cta(tstart[s], total, G);
@@ -132,6 +133,30 @@ __global__ void __launch_bounds__(kThreads, CPS)
     const bool has_draft = lt1 * kTK > g.n_prefix;
     uint64_t tl = 0, th = 0;
     if (has_draft && p.parent != nullptr) warp_tree_rows(p, g.b, tl, th);
+    uint64_t seen = ~0ull;  // score shaping: the draft keys that some token sees
+    if (kMod && has_draft) {
+      uint64_t lo, hi;
+      draft_rows(p, draft_prefetch(p, g.b), lo, hi);
+      seen = lane < p.T ? mod_window_row(p.mod, p.T, g.b, lane, g.L, lo) : 0ull;
+      if (lane + 32 < p.T) seen |= mod_window_row(p.mod, p.T, g.b, lane + 32, g.L, hi);
+      seen = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)seen) |
+             (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(seen >> 32)) << 32;
+    }
+    // V rows of tile lt that the consumers zero (0 * V must stay 0): TMA brought
+    // whole boxes past the segment end; with score shaping, every key no row sees
+    auto zero_tile = [&](int lt) {
+      if (kMod) return lt * kTK < g.lo || lt * kTK + kTK > g.n_prefix;
+      return use_tma && lt * kTK + kTK > g.nkeys;
+    };
+    auto zero_row = [&](int k) {
+      if (kMod && (k < g.lo || (k >= g.n_prefix && k < g.nkeys && !((seen >> (k - g.n_prefix)) & 1ull)))) return true;
+      return k >= g.nkeys;
+    };
+    // position of segment key k relative to L (score shaping)
+    auto key_off = [&](int k) {
+      return k >= g.n_prefix && k < g.nkeys ? (float)mod_off(p.mod, p.T, g.b, k - g.n_prefix, g.L)
+                                            : (float)(k - g.n_prefix);
+    };
     if (kRope && g.b != rope_b) {
       // rotary table of this sequence's draft tokens, kept while the CTA stays
       // on the sequence (the previous segment's readers are past the barrier first)
@@ -172,7 +197,18 @@ __global__ void __launch_bounds__(kThreads, CPS)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint64_t m = has_draft ? draft_row(p, g.b, trow[h], tl, th) : 0ull;
-        rmask[h] = m;
+        rmask[h] = kMod && has_draft ? mod_window_row(p.mod, p.T, g.b, trow[h], g.L, m) : m;
+      }
+      float ns[2] = {0.f, 0.f}, qoff[2] = {0.f, 0.f};  // score shaping, per row: slope, offset from L,
+      int first[2] = {0, 0};                           // first visible key
+      if constexpr (kMod) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int o = mod_off(p.mod, p.T, g.b, trow[h], g.L);
+          ns[h] = rvalid[h] ? mod_slope(p.mod, g.hkv * group + rr[h] % group) : 0.f;
+          qoff[h] = (float)o;
+          first[h] = mod_first_slot(p.mod, g.b, o, g.L) - g.base;
+        }
       }
       {
         const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(p.q);
@@ -221,13 +257,12 @@ __global__ void __launch_bounds__(kThreads, CPS)
           const uint32_t ks_addr = smem_u32(stages + st * C::kStageBytes);
           const uint32_t vs_addr = ks_addr + C::kTileBytes;
           const int kb = kw * NK;
-          if (use_tma && lt * kTK + kTK > g.nkeys) {
-            // TMA brought whole 64-token boxes: V rows past the segment end may hold
-            // any bytes of the cache, so zero them (P is exactly 0 there, but 0*NaN is not)
+          if (zero_tile(lt)) {
+            // (P is exactly 0 there, but 0*NaN is not)
             uint8_t *vt = stages + st * C::kStageBytes + C::kTileBytes;
             for (int e = lane; e < NK * C::kChunks; e += 32) {
               const int r = kb + e / C::kChunks;
-              if (lt * kTK + r >= g.nkeys) *reinterpret_cast<uint4 *>(vt + swz(r, e % C::kChunks)) = make_uint4(0, 0, 0, 0);
+              if (zero_row(lt * kTK + r)) *reinterpret_cast<uint4 *>(vt + swz(r, e % C::kChunks)) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -250,6 +285,19 @@ __global__ void __launch_bounds__(kThreads, CPS)
           }
           // mask: keys past the segment end, and draft keys the row may not see
           const int tile_k = lt * kTK + kb;
+          if constexpr (kMod) {
+            const bool draft_tile = lt * kTK + kTK > g.n_prefix;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = tile_k + nt * 8 + 2 * tq + (e & 1);
+                const float d = qoff[e >> 1] - (draft_tile ? key_off(key) : (float)(key - g.n_prefix));
+                sacc[nt][e] = mod_score(p.mod, sacc[nt][e], ns[e >> 1], d);
+                if (key < first[e >> 1]) sacc[nt][e] = -INFINITY;
+              }
+            }
+          }
           if (lt * kTK + kTK > g.n_prefix) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -424,7 +472,15 @@ __global__ void __launch_bounds__(kThreads, CPS)
       {
         // every lane of the warp computes its own row's visibility (shuffles need the full warp)
         const uint64_t m = has_draft ? draft_row(p, g.b, t, tl, th) : 0ull;
-        rmask = m;
+        rmask = kMod && has_draft ? mod_window_row(p.mod, p.T, g.b, t, g.L, m) : m;
+      }
+      float ns = 0.f, qoff = 0.f;
+      int first = 0;
+      if constexpr (kMod) {
+        const int o = mod_off(p.mod, p.T, g.b, t, g.L);
+        ns = rv ? mod_slope(p.mod, hq) : 0.f;
+        qoff = (float)o;
+        first = mod_first_slot(p.mod, g.b, o, g.L) - g.base;
       }
       float qv[64];
       {
@@ -460,11 +516,11 @@ __global__ void __launch_bounds__(kThreads, CPS)
         if (ok) {
           const uint8_t *kt = stages + st * C::kStageBytes;
           uint8_t *vt = stages + st * C::kStageBytes + C::kTileBytes;
-          if (use_tma && lt * kTK + kTK > g.nkeys) {
+          if (zero_tile(lt)) {
             // zero V rows past the segment end (see the bf16 path); this warp's key half only
             for (int e = lane; e < 32 * C::kChunks; e += 32) {
               const int r = half * 32 + e / C::kChunks;
-              if (lt * kTK + r >= g.nkeys) *reinterpret_cast<uint4 *>(vt + swz(r, e % C::kChunks)) = make_uint4(0, 0, 0, 0);
+              if (zero_row(lt * kTK + r)) *reinterpret_cast<uint4 *>(vt + swz(r, e % C::kChunks)) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -485,6 +541,10 @@ __global__ void __launch_bounds__(kThreads, CPS)
             const int key = lt * kTK + half * 32 + kk;
             bool vis = key < g.nkeys;
             if (vis && key >= g.n_prefix) vis = (rmask >> (key - g.n_prefix)) & 1ull;
+            if constexpr (kMod) {
+              a = mod_score(p.mod, a, ns, qoff - key_off(key));
+              vis = vis && key >= first;
+            }
             sc[kk] = vis ? a : -INFINITY;
           }
           float mx = m;
@@ -767,9 +827,14 @@ template <typename Tin, int D, int RG, int CPS = 1>
 static cudaError_t launch_attn_t(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
                                  cudaStream_t stream) {
   const size_t smem = attn_smem_bytes<Tin, D, RG, CPS>(p);
-  // instances with and without the rotary embedding (code that never runs
-  // still costs the hot loop)
-  auto kern = p.positions != nullptr ? verify_attn_kernel<Tin, D, RG, CPS, true> : verify_attn_kernel<Tin, D, RG, CPS, false>;
+  // instances with the rotary embedding, with score shaping and with neither
+  // (code that never runs still costs the hot loop); d128 score shaping is left
+  // to the tcgen05 kernels
+  auto kern = p.positions != nullptr ? verify_attn_kernel<Tin, D, RG, CPS, true, false>
+                                     : verify_attn_kernel<Tin, D, RG, CPS, false, false>;
+  if constexpr (D == 64) {
+    if (p.mod.on) kern = verify_attn_kernel<Tin, D, RG, CPS, false, true>;
+  }
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, smem, stream>>>(p, tmk, tmv);

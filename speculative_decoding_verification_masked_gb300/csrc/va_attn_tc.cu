@@ -82,7 +82,7 @@ __device__ __forceinline__ uint32_t swz128(int r, int c) {
   return (uint32_t)((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-template <int NMT, bool kTma, bool kRope, int NS>
+template <int NMT, bool kTma, bool kRope, bool kMod, int NS>
 __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
     verify_attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv) {
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  const CtaRange cr = plan_cta(p, tstart);  // contains __syncthreads
+  const CtaRange cr = plan_cta<kTK, kMod>(p, tstart);  // contains __syncthreads
   if (c >= cr.G) return;
   const int t0 = cr.t0, t1 = cr.t1, s0 = cr.s0;
 
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
     bool pok = true;
     // at most NS-1 tiles in flight, and the second waits for the first: the
     // first tile of every CTA lands sooner when the kernel starts (-1 us)
-    produce_tiles<__nv_bfloat16, D, NS, kTK, NS - 1, 1, kTma ? 1 : 0>(p, &tmk, &tmv, tstart, cr, stages, full, empty,
+    produce_tiles<__nv_bfloat16, D, NS, kTK, NS - 1, 1, kTma ? 1 : 0, kMod>(p, &tmk, &tmv, tstart, cr, stages, full, empty,
                                                                   abort_flag, use_tma, pok);
     return;
   }
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
   named_bar_sync(kBarEnd, kSoftThreads + kMmaThreads);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const float cl2 = p.scale * kLog2e;
+  const float cl2 = kMod ? 1.f : p.scale * kLog2e;  // shaped scores are in base-2 units already
   const int group = p.Hq / p.Hkv;
 
   if (warp >= kMmaWarp0) {
@@ -170,9 +170,21 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
     auto wait_ok = [&](uint64_t *bar, uint32_t parity) { role_wait(bar, parity, ok, abort_flag, p.wait_ns, p.status); };
     // make stage `st` of tile lt ready for the MMAs: wait for it; on the dense
     // path zero the V rows past the segment end (TMA brought whole boxes)
-    auto acquire_stage = [&](int st, uint32_t ph, int lt, const Seg &g) {
+    // (with score shaping: every V row that no query row sees; `seen` = the
+    // draft keys some token sees)
+    auto acquire_stage = [&](int st, uint32_t ph, int lt, const Seg &g, uint64_t seen) {
       wait_ok(full + st, ph);
-      if (ok && use_tma && lt * kTK + kTK > g.nkeys) {
+      if (kMod) {
+        if (ok && (lt * kTK < g.lo || lt * kTK + kTK > g.n_prefix)) {
+          uint8_t *vt = stages + st * Geo::kStageBytes + Geo::kTileBytes;
+          for (int e = lane; e < kTK * Geo::kChunks; e += 32) {
+            const int r = e / Geo::kChunks, k = lt * kTK + r;
+            const bool hidden = k < g.lo || k >= g.nkeys || (k >= g.n_prefix && !((seen >> (k - g.n_prefix)) & 1ull));
+            if (hidden) *reinterpret_cast<uint4 *>(vt + swz(r, e % Geo::kChunks)) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+      } else if (ok && use_tma && lt * kTK + kTK > g.nkeys) {
         uint8_t *vt = stages + st * Geo::kStageBytes + Geo::kTileBytes;
         for (int e = lane; e < kTK * Geo::kChunks; e += 32) {
           const int r = e / Geo::kChunks;
@@ -219,9 +231,18 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
     };
 
     for (int s = s0; s < p.S && tstart[s] < t1; ++s) {
-      const Seg g = seg_info(p, s, false);
+      const Seg g = seg_info<kMod, kTK>(p, s, false);
       const int lt0 = max(tstart[s], t0) - tstart[s];
       const int lt1 = min(tstart[s + 1], t1) - tstart[s];
+      uint64_t seen = ~0ull;
+      if (kMod && !s_issuer && lt1 * kTK > g.n_prefix) {
+        uint64_t lo, hi;
+        draft_rows(p, draft_prefetch(p, g.b), lo, hi);
+        seen = lane < p.T ? mod_window_row(p.mod, p.T, g.b, lane, g.L, lo) : 0ull;
+        if (lane + 32 < p.T) seen |= mod_window_row(p.mod, p.T, g.b, lane + 32, g.L, hi);
+        seen = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)seen) |
+               (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(seen >> 32)) << 32;
+      }
       named_bar_sync(kBarQ, kSoftThreads + kMmaThreads);  // Q of this segment is in shared memory
       for (int lt = lt0; lt < lt1; ++lt, ++it, ++jt) {
         const int st = it % NS;
@@ -250,7 +271,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
           // the softmax wrote the P residual of this tile too (set before its
           // arrive on p_full; rewritten only after this PV has completed)
           const bool exact = lo_flag[2 * mi + b] != 0;
-          acquire_stage(st, (uint32_t)(it / NS) & 1u, lt, g);
+          acquire_stage(st, (uint32_t)(it / NS) & 1u, lt, g, seen);
           issue_pv(mi, b, st, lt == lt0, exact);
         }
         __syncwarp();
@@ -278,7 +299,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
   // split segments this CTA holds a part of (at most its first and its last)
   int n_split = 0, ms[2] = {0, 0}, mslot[2] = {0, 0}, mnp[2] = {0, 0}, mpart[2] = {0, 0};
   for (int s = s0; s < p.S && tstart[s] < t1; ++s) {
-    const Seg g = seg_info(p, s, false);
+    const Seg g = seg_info<kMod, kTK>(p, s, false);
     const int lt0 = max(tstart[s], t0) - tstart[s];
     const int lt1 = min(tstart[s + 1], t1) - tstart[s];
     const int first_cta = owner_cta(tstart[s], cr.total, cr.G);
@@ -367,6 +388,15 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
       draft_rows(p, dpre, tl, th);
       const uint64_t a = __shfl_sync(0xffffffffu, tl, t & 31), c2 = __shfl_sync(0xffffffffu, th, t & 31);
       rmask = t < 32 ? a : c2;
+      if (kMod) rmask = mod_window_row(p.mod, p.T, g.b, t, g.L, rmask);
+    }
+    float ns = 0.f, qoff = 0.f;  // score shaping: the row's (negated) slope and offset from L
+    int first = 0;               // and the first key it sees
+    if constexpr (kMod) {
+      const int o = mod_off(p.mod, p.T, g.b, t, g.L);
+      ns = rvalid ? mod_slope(p.mod, hq) : 0.f;
+      qoff = (float)o;
+      first = mod_first_slot(p.mod, g.b, o, g.L) - g.base;
     }
     float m_used = -INFINITY;  // reference max of the exponentials (raw score units)
     float l = 0.f;
@@ -388,9 +418,33 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
         for (int j = 0; j < 32; ++j) sv[32 + j] = __uint_as_float(w[j]);
       }
       const int k0 = lt * kTK;
-      const bool masked = k0 + kTK > g.n_prefix;
+      const bool masked = k0 + kTK > g.n_prefix || (kMod && k0 < g.hi);
+      if constexpr (kMod) {
+        if (p.mod.softcap > 0.f) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) sv[j] = capped_tanh(sv[j] * p.mod.in_mul, p.mod.out_mul);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) sv[j] *= p.mod.out_mul;
+        }
+        if (p.mod.slopes != nullptr) {
+          const float d0 = qoff - (float)(k0 - g.n_prefix);
+          if (k0 + kTK <= g.n_prefix) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j) sv[j] = fmaf(ns, fabsf(d0 - (float)j), sv[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 64; ++j) {
+              const int dk = k0 + j - g.n_prefix;  // draft key, or a prefix key below 0
+              const float d = dk >= 0 && dk < p.T ? qoff - (float)mod_off(p.mod, p.T, g.b, dk, g.L) : d0 - (float)j;
+              sv[j] = fmaf(ns, fabsf(d), sv[j]);
+            }
+          }
+        }
+      }
       if (masked) {
-        const uint64_t vis = tile_vis64(k0, g.n_prefix, g.nkeys, rmask);
+        uint64_t vis = tile_vis64(k0, g.n_prefix, g.nkeys, rmask);
+        if (kMod && first > k0) vis &= first - k0 >= 64 ? 0ull : ~0ull << (first - k0);
 #pragma unroll
         for (int j = 0; j < 64; ++j)
           if (!((vis >> j) & 1ull)) sv[j] = -INFINITY;
@@ -585,11 +639,11 @@ size_t attn_tc_smem_required(const AttnParams &p) {
   return p.rows_pad > 128 ? tc_smem_bytes<2, kTcStagesMin>(p) : tc_smem_bytes<1, kTcStagesMin>(p);
 }
 
-template <int NMT, bool kTma, bool kRope, int NS>
+template <int NMT, bool kTma, bool kRope, bool kMod, int NS>
 static cudaError_t launch_tc_ns(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
                                 cudaStream_t stream) {
   const size_t smem = tc_smem_bytes<NMT, NS>(p);
-  auto kern = verify_attn_tc_kernel<NMT, kTma, kRope, NS>;
+  auto kern = verify_attn_tc_kernel<NMT, kTma, kRope, kMod, NS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   // cooperative: every CTA is resident, so the wait for a segment's parts ends
@@ -606,18 +660,23 @@ static cudaError_t launch_tc_ns(const AttnParams &p, const CUtensorMap &tmk, con
   return cudaLaunchKernelEx(&cfg, kern, p, tmk, tmv);
 }
 
-// instances with and without the rotary embedding (code that never runs still
-// costs the hot loop), each with the deep ring or the minimum one
+// instances with the rotary embedding, with score shaping and with neither
+// (code that never runs still costs the hot loop), each with the deep ring or
+// the minimum one
 template <int NMT, bool kTma>
 static cudaError_t launch_tc_t(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
                                cudaStream_t stream) {
+  if (p.mod.on)
+    return tc_deep_ring<NMT>(p)
+               ? launch_tc_ns<NMT, kTma, false, true, kTcStagesMax>(p, tmk, tmv, grid, stream)
+               : launch_tc_ns<NMT, kTma, false, true, kTcStagesMin>(p, tmk, tmv, grid, stream);
   if (p.positions != nullptr)
     return tc_deep_ring<NMT>(p)
-               ? launch_tc_ns<NMT, kTma, true, kTcStagesMax>(p, tmk, tmv, grid, stream)
-               : launch_tc_ns<NMT, kTma, true, kTcStagesMin>(p, tmk, tmv, grid, stream);
+               ? launch_tc_ns<NMT, kTma, true, false, kTcStagesMax>(p, tmk, tmv, grid, stream)
+               : launch_tc_ns<NMT, kTma, true, false, kTcStagesMin>(p, tmk, tmv, grid, stream);
   return tc_deep_ring<NMT>(p)
-             ? launch_tc_ns<NMT, kTma, false, kTcStagesMax>(p, tmk, tmv, grid, stream)
-             : launch_tc_ns<NMT, kTma, false, kTcStagesMin>(p, tmk, tmv, grid, stream);
+             ? launch_tc_ns<NMT, kTma, false, false, kTcStagesMax>(p, tmk, tmv, grid, stream)
+             : launch_tc_ns<NMT, kTma, false, false, kTcStagesMin>(p, tmk, tmv, grid, stream);
 }
 
 cudaError_t launch_attention_tc(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,

@@ -80,8 +80,11 @@ struct TkSmem {
   static constexpr int kRedOff = kKeyMaskOff + 512;        // float4 [NR]: per-warp row maxima
   static constexpr int kRowInvOff = kRedOff + NR * 16;     // float [64]: 1 / l per row (epilogue)
   // then the rotary table of the segment (rope_table_bytes, 0 without
-  // positions) and the tile starts of the work plan
+  // positions), or with score shaping float2 [64] (slope, offset) of the rows
+  // and int [64] first visible keys of the draft tokens, and the tile starts
+  // of the work plan
   static constexpr int kRopeOff = kRowInvOff + 256;
+  static constexpr int kModBytes = 64 * 8 + 64 * 4;
   static_assert(kQOff % 1024 == 0 && kQBytes % 1024 == 0, "UMMA operands need 1024-byte aligned swizzle atoms");
   static_assert(kBarOff % 8 == 0 && kRowMaskOff % 8 == 0 && kKeyMaskOff % 8 == 0, "8-byte alignment");
   static_assert(kRedOff % 16 == 0, "float4 array needs 16-byte alignment");
@@ -205,7 +208,7 @@ __device__ __forceinline__ void tmem_scale_cols(uint32_t taddr, const float *a) 
   }
 }
 
-template <int NR, bool kTma, bool kRope>
+template <int NR, bool kTma, bool kRope, bool kMod>
 __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
     verify_attn_tck_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
                            const __grid_constant__ CUtensorMap tmv) {
@@ -219,6 +222,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
   // NR <= 32: the row sums l are kept by the softmax threads (each over its own
   // keys, reduced once per segment part) instead of a ones-operand MMA per tile
   constexpr bool kRegL = NR <= 32;
+  static_assert(!(kRope && kMod), "the two share their shared-memory table");
   constexpr int kProducerWarp = 4, kMmaWarp = 5;
   constexpr int kBarQ = 1, kBarRed = 2, kBarSoft = 3, kBarEnd = 4;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -239,7 +243,9 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
   float4 *red = reinterpret_cast<float4 *>(smem + SM::kRedOff);
   float *row_inv = reinterpret_cast<float *>(smem + SM::kRowInvOff);
   float2 *rope_tab = reinterpret_cast<float2 *>(smem + SM::kRopeOff);
-  int *tstart = reinterpret_cast<int *>(smem + SM::kRopeOff + (kRope ? rope_table_bytes(p) : 0));
+  int *tstart = reinterpret_cast<int *>(smem + SM::kRopeOff + (kRope ? rope_table_bytes(p) : kMod ? SM::kModBytes : 0));
+  float2 *mod_row = reinterpret_cast<float2 *>(smem + SM::kRopeOff);       // (slope, offset) of row r
+  int *mod_first = reinterpret_cast<int *>(smem + SM::kRopeOff + 64 * 8);  // first visible key of token t
   constexpr bool use_tma = kTma;  // tiles by TMA boxes (dense, paged), else cp.async gathers
 
   const int tid = threadIdx.x;
@@ -262,13 +268,13 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  const CtaRange cr = plan_cta<TK>(p, tstart);  // contains __syncthreads
+  const CtaRange cr = plan_cta<TK, kMod>(p, tstart);  // contains __syncthreads
   if (c >= cr.G) return;
   const int t0 = cr.t0, t1 = cr.t1, s0 = cr.s0;
 
   if (warp == kProducerWarp || warp > kMmaWarp) {
     bool pok = true;
-    produce_tiles<__nv_bfloat16, D, NS, TK, 2, TkCfg<NR, kTma>::kProducers, kTma ? 1 : 0>(
+    produce_tiles<__nv_bfloat16, D, NS, TK, 2, TkCfg<NR, kTma>::kProducers, kTma ? 1 : 0, kMod>(
         p, &tmk, &tmv, tstart, cr, stages, full, empty, abort_flag, use_tma, pok,
         warp == kProducerWarp ? 0 : warp - kMmaWarp);
     return;
@@ -284,7 +290,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
   named_bar_sync(kBarEnd, kSoft + 32);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const float cl2 = p.scale * kLog2e;
+  const float cl2 = kMod ? 1.f : p.scale * kLog2e;  // shaped scores are in base-2 units already
   const int group = p.Hq / p.Hkv;
 
   bool ok = true;
@@ -347,7 +353,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
     };
 
     for (int s = s0; s < p.S && tstart[s] < t1; ++s) {
-      const Seg g = seg_info(p, s, false);
+      const Seg g = seg_info<kMod, TK>(p, s, false);
       const int lt0 = max(tstart[s], t0) - tstart[s];
       const int lt1 = min(tstart[s + 1], t1) - tstart[s];
       named_bar_sync(kBarQ, kSoft + 32);  // Q of this segment is in shared memory
@@ -395,7 +401,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
   // merged after its last tile
   int n_split = 0, ms[2] = {0, 0}, mslot[2] = {0, 0}, mnp[2] = {0, 0}, mpart[2] = {0, 0};
   for (int s = s0; s < p.S && tstart[s] < t1; ++s) {
-    const Seg g = seg_info(p, s, false);
+    const Seg g = seg_info<kMod, TK>(p, s, false);
     const int lt0 = max(tstart[s], t0) - tstart[s];
     const int lt1 = min(tstart[s + 1], t1) - tstart[s];
     const int first_cta = owner_cta(tstart[s], cr.total, cr.G);
@@ -486,14 +492,29 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
       if (tid < p.T) {
         const uint64_t gbits = group >= 64 ? ~0ull : ((1ull << group) - 1);
         uint64_t kmask = 0;
-        for (int t = 0; t < p.T; ++t)
-          if ((rowmask[t] >> tid) & 1ull) kmask |= gbits << (t * group);
+        const int koff = kMod ? mod_off(p.mod, p.T, g.b, tid, g.L) : 0;
+        for (int t = 0; t < p.T; ++t) {
+          bool see = (rowmask[t] >> tid) & 1ull;
+          if (kMod && p.mod.window > 0) see = see && mod_off(p.mod, p.T, g.b, t, g.L) - koff < p.mod.window;
+          if (see) kmask |= gbits << (t * group);
+        }
         keymask[tid] = kmask;
       }
       named_bar_sync(kBarSoft, kSoft);
       masks_ready = true;
     };
     if (NR <= 32 && has_draft) build_masks();
+    if constexpr (kMod) {
+      // (the previous segment's readers are past its epilogue's barriers)
+      if (tid < 64) {
+        const int t = tid / group, hq = g.hkv * group + tid % group;
+        mod_row[tid] = tid < p.R ? make_float2(mod_slope(p.mod, hq), (float)mod_off(p.mod, p.T, g.b, t, g.L))
+                                 : make_float2(0.f, 0.f);
+        if (tid < p.T)
+          mod_first[tid] = mod_first_slot(p.mod, g.b, mod_off(p.mod, p.T, g.b, tid, g.L), g.L) - g.base;
+      }
+      named_bar_sync(kBarSoft, kSoft);
+    }
 
     float mu[NR];  // reference max per row, log2 units
 #pragma unroll
@@ -509,12 +530,25 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
       const int st = it % NS;
       const uint32_t tS = tO + (2 + b) * NC;
       const int key = lt * TK + tid;
-      const bool masked = lt * TK + TK > g.n_prefix;
-      if (NR > 32 && masked && !masks_ready) build_masks();
+      const bool draft_tile = lt * TK + TK > g.n_prefix;
+      const bool masked = draft_tile || (kMod && lt * TK < g.hi);
+      if (NR > 32 && draft_tile && !masks_ready) build_masks();
       uint64_t km = ~0ull;  // rows that see this key
       if (masked) {
         if (key >= g.nkeys) km = 0;
         else if (key >= g.n_prefix) km = keymask[key - g.n_prefix];
+        else if (kMod && key < g.hi) {
+          const uint64_t gbits = group >= 64 ? ~0ull : ((1ull << group) - 1);
+          km = 0;
+          for (int t = 0; t < p.T; ++t)
+            if (key >= mod_first[t]) km |= gbits << (t * group);
+        }
+      }
+      float koff = 0.f;  // the key's position relative to L
+      if constexpr (kMod) {
+        koff = (float)(key - g.n_prefix);
+        if (p.mod.slopes != nullptr && key >= g.n_prefix && key < g.nkeys)
+          koff = (float)mod_off(p.mod, p.T, g.b, key - g.n_prefix, g.L);
       }
       wait_ok(s_full + b, (uint32_t)(jt >> 1) & 1u);
       // PV of tile jt-2 (same o_done barrier): waiting for every PV in order,
@@ -524,6 +558,22 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
       float x[NR];  // raw scores of this key, -inf where the row does not see it
       auto load_scores = [&]() {
         tmem_ld_f<NR>(tS, x);
+        if constexpr (kMod) {
+          if (p.mod.softcap > 0.f) {
+#pragma unroll
+            for (int r = 0; r < NR; ++r) x[r] = capped_tanh(x[r] * p.mod.in_mul, p.mod.out_mul);
+          } else {
+#pragma unroll
+            for (int r = 0; r < NR; ++r) x[r] *= p.mod.out_mul;
+          }
+          if (p.mod.slopes != nullptr) {
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              const float2 c = mod_row[r];
+              x[r] = fmaf(c.x, fabsf(c.y - koff), x[r]);
+            }
+          }
+        }
         if (masked) {
 #pragma unroll
           for (int r = 0; r < NR; ++r)
@@ -621,8 +671,9 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
           }
           put_p(cc, h, l);
         }
-        if (use_tma && key >= g.nkeys) {
-          // rows past the segment end: TMA brought whatever follows; zero V so 0 * V stays 0
+        if (kMod ? (p.R < 64 ? (km & ((1ull << p.R) - 1ull)) : km) == 0ull : (use_tma && key >= g.nkeys)) {
+          // rows past the segment end: TMA brought whatever follows; zero V so 0 * V
+          // stays 0 (with score shaping: every key that no row sees)
           wait_ok(full + st, (uint32_t)(it / NS) & 1u);
           uint8_t *vt = pk + Geo::kTileBytes;
 #pragma unroll
@@ -835,11 +886,13 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
 // ---------------------------------------------------------------------------
 template <int NR>
 static size_t tck_smem_bytes(const AttnParams &p) {
-  return 1024 + (size_t)TkSmem<NR>::kRopeOff + (size_t)rope_table_bytes(p) + (size_t)(p.S + 1) * 4;
+  return 1024 + (size_t)TkSmem<NR>::kRopeOff + (size_t)(p.mod.on ? TkSmem<NR>::kModBytes : rope_table_bytes(p)) +
+         (size_t)(p.S + 1) * 4;
 }
 
-// A kernel instance with the rotary embedding and one without: code that never
-// runs still costs the hot loop registers and schedule.
+// A kernel instance with the rotary embedding, one with score shaping and one
+// with neither: code that never runs still costs the hot loop registers and
+// schedule.
 
 size_t attn_tck_smem_required(const AttnParams &p) {
   return p.rows_pad <= 16 ? tck_smem_bytes<16>(p) : p.rows_pad <= 32 ? tck_smem_bytes<32>(p) : tck_smem_bytes<64>(p);
@@ -849,7 +902,9 @@ template <int NR, bool kTma>
 static cudaError_t launch_tck_t(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
                                 cudaStream_t stream) {
   const size_t smem = tck_smem_bytes<NR>(p);
-  auto kern = p.positions != nullptr ? verify_attn_tck_kernel<NR, kTma, true> : verify_attn_tck_kernel<NR, kTma, false>;
+  auto kern = p.mod.on                 ? verify_attn_tck_kernel<NR, kTma, false, true>
+              : p.positions != nullptr ? verify_attn_tck_kernel<NR, kTma, true, false>
+                                       : verify_attn_tck_kernel<NR, kTma, false, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   // cooperative: every CTA is resident, so the wait for a segment's parts ends

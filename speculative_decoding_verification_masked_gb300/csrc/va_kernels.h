@@ -9,6 +9,20 @@
 
 namespace va {
 
+constexpr float kModLog2e = 1.4426950408889634f;
+constexpr int kModMaxWindow = 1 << 23;
+
+// Score shaping of one call (va_mod.cuh); `on` = 0 for the calls without it.
+struct ModParams {
+  int on;
+  float softcap;           // 0: no cap
+  float in_mul, out_mul;   // capped: scale / cap and cap * log2 e; else out_mul = scale * log2 e
+  int window;              // 0: no window
+  const float *slopes;     // [Hq] or NULL
+  const int32_t *key_start;// [B] or NULL
+  const int32_t *token_pos;// [B][T] or NULL (L_b + t)
+};
+
 // Everything one attention launch needs; plain values and device pointers.
 struct AttnParams {
   // shape
@@ -56,6 +70,7 @@ struct AttnParams {
   float *lse_part, *o_part;
   uint64_t wait_ns;
   int test_drop_part;  // test hook: this CTA's parts of split segments never arrive (-1: off)
+  ModParams mod;
 };
 
 size_t attn_smem_required(const AttnParams &p);

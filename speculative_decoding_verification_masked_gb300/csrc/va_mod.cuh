@@ -1,0 +1,118 @@
+// Score shaping shared by the attention kernels and the accumulated-weight
+// pass: a tanh cap on the scores, a bias that falls with distance (a slope
+// per query head), a sliding window and a per-sequence document start.
+//
+//   s = scale q.k;  s = c tanh(s / c) if c > 0;  s = s - slope_h |d|,
+//   d = pos_q - pos_k,
+//   visible: d < window, and for a prefix slot j: j >= key_start_b.
+//
+// A prefix key's position is its slot; draft token t's is token_pos[b][t] (or
+// L_b + t).  Positions are used relative to L_b: offsets below 2^23 in
+// magnitude and prefix slots within 2^24 of L_b are exact in fp32, and farther
+// ones (which a window below 2^23 always hides) are off by 2^-24 of the
+// distance, the rounding of the bias itself.
+//
+// Scores leave here in base-2 units (times log2 e), so that the softmaxes'
+// exponent is 2^(s - m) with no further factor.
+#pragma once
+
+#include "va_common.cuh"
+#include "va_kernels.h"
+
+namespace va {
+
+constexpr int kModMaxOff = 1 << 23;
+
+// ---------------------------------------------------------------------------
+// tanh
+// ---------------------------------------------------------------------------
+// tanh(y) = y P(y^2) / Q(y^2), a rational approximation fitted to the relative
+// error on |y| <= 9.02 (reweighted least squares): 2.1e-8, 3.3e-7 as evaluated
+// in fp32.  Past 9.02, tanh rounds to 1 in fp32.  The hardware's one-instruction
+// tanh is off by 2^-11, which a cap of 50 would turn into 0.02 of a score;
+// 1 - 2 / (1 + e^2y) loses the small scores' digits the same way.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// cap2 * tanh(y): cap2 multiplies the numerator before the division.
+__device__ __forceinline__ float capped_tanh(float y, float cap2) {
+  y = fminf(fmaxf(y, -9.02f), 9.02f);
+  const float z = y * y;
+  float p = fmaf(1.33188971e-08f, z, 2.05833530e-05f);
+  p = fmaf(p, z, 3.49402661e-03f);
+  p = fmaf(p, z, 1.33797109e-01f);
+  p = fmaf(p, z, 1.0f);
+  float q = fmaf(7.76194668e-07f, z, 3.28308001e-04f);
+  q = fmaf(q, z, 2.58710440e-02f);
+  q = fmaf(q, z, 4.67130274e-01f);
+  q = fmaf(q, z, 1.0f);
+  return (cap2 * y) * p * rcp_approx(q);
+}
+
+// ---------------------------------------------------------------------------
+// positions and visibility
+// ---------------------------------------------------------------------------
+// Position of draft token t of sequence b relative to L_b (clamped).
+__device__ __forceinline__ int mod_off(const ModParams &m, int T, int b, int t, int L) {
+  if (m.token_pos == nullptr) return t;
+  const long long o = (long long)__ldg(m.token_pos + (size_t)b * T + t) - L;
+  return (int)max(-(long long)kModMaxOff, min((long long)kModMaxOff, o));
+}
+
+// First slot of the prefix that a row at offset `off` sees, in [0, L].
+__device__ __forceinline__ int mod_first_slot(const ModParams &m, int b, int off, int L) {
+  int lo = m.key_start != nullptr ? __ldg(m.key_start + b) : 0;
+  if (m.window > 0) lo = max(lo, L + off - m.window + 1);
+  return max(0, min(lo, L));
+}
+
+// First slot that any row of sequence b sees (lo) and the first that every row
+// sees (hi).  Called by a full warp.  An offset out of range is recorded.
+__device__ __forceinline__ void mod_range(const ModParams &m, int T, int b, int L, int *status, int &lo, int &hi) {
+  int omin = 0, omax = 0;
+  if (m.window > 0 || status != nullptr) {
+    if (m.token_pos == nullptr) {
+      omax = T - 1;
+    } else {
+      const int lane = threadIdx.x & 31;
+      omin = omax = mod_off(m, T, b, min(lane, T - 1), L);
+      if (lane + 32 < T) {
+        const int o = mod_off(m, T, b, lane + 32, L);
+        omin = min(omin, o);
+        omax = max(omax, o);
+      }
+      omin = __reduce_min_sync(0xffffffffu, omin);
+      omax = __reduce_max_sync(0xffffffffu, omax);
+      if (status != nullptr && (omin <= -kModMaxOff || omax >= kModMaxOff)) record_status(status, VA_ERR_DEVICE_BOUNDS);
+    }
+  }
+  lo = mod_first_slot(m, b, omin, L);
+  hi = mod_first_slot(m, b, omax, L);
+}
+
+// Draft token t's visibility row with the keys cleared that its window hides.
+__device__ __forceinline__ uint64_t mod_window_row(const ModParams &m, int T, int b, int t, int L, uint64_t row) {
+  if (m.window <= 0) return row;
+  const int o = mod_off(m, T, b, t, L);
+  for (int j = 0; j < T; ++j)
+    if (o - mod_off(m, T, b, j, L) >= m.window) row &= ~(1ull << j);
+  return row;
+}
+
+// Bias slope of query head hq in base-2 units, negated (0 without slopes).
+__device__ __forceinline__ float mod_slope(const ModParams &m, int hq) {
+  return m.slopes != nullptr ? -kModLog2e * __ldg(m.slopes + hq) : 0.f;
+}
+
+// A raw product q.k as a base-2 score: the cap, then the bias of a key at
+// distance d (fp32) for a head of (negated) slope ns.
+__device__ __forceinline__ float mod_score(const ModParams &m, float raw, float ns, float d) {
+  float s = m.softcap > 0.f ? capped_tanh(raw * m.in_mul, m.out_mul) : raw * m.out_mul;
+  if (m.slopes != nullptr) s = fmaf(ns, fabsf(d), s);
+  return s;
+}
+
+}  // namespace va

@@ -9,6 +9,7 @@
 
 #include "va_common.cuh"
 #include "va_kernels.h"
+#include "va_mod.cuh"
 
 namespace va {
 
@@ -44,8 +45,15 @@ struct Seg {
   int L;         // committed prefix length of the sequence
   int n_prefix;  // prefix keys of this segment (L, or the verify-set size)
   int nkeys;     // n_prefix + T
+  // score shaping only: the key stream starts at slot `base` (a multiple of the
+  // tile), its keys below `lo` are hidden from every row and those from `hi` on
+  // visible to all (both counted from base)
+  int base, lo, hi;
 };
 
+// kMod: the prefix is cut to what a window or a document start leaves visible
+// (called by full warps).
+template <bool kMod = false, int TK = 64>
 __device__ __forceinline__ Seg seg_info(const AttnParams &p, int s, bool record) {
   Seg g;
   g.rb = s % p.NRB;
@@ -66,6 +74,15 @@ __device__ __forceinline__ Seg seg_info(const AttnParams &p, int s, bool record)
     g.n_prefix = n;
   } else {
     g.n_prefix = L;
+  }
+  g.base = g.lo = g.hi = 0;
+  if constexpr (kMod) {
+    int lo, hi;
+    mod_range(p.mod, p.T, g.b, L, record ? p.status : nullptr, lo, hi);
+    g.base = lo & ~(TK - 1);
+    g.lo = lo - g.base;
+    g.hi = hi - g.base;
+    g.n_prefix = L - g.base;
   }
   g.nkeys = g.n_prefix + p.T;
   return g;
@@ -225,14 +242,15 @@ __device__ __forceinline__ uint64_t tile_vis64(int k0, int n_prefix, int nkeys, 
 // ---------------------------------------------------------------------------
 // producer: one warp moves K/V rows of each tile with bulk copies
 // ---------------------------------------------------------------------------
-template <typename Tin, int D>
+template <typename Tin, int D, bool kMod = false>
 __device__ __forceinline__ const Tin *key_row(const AttnParams &p, const Seg &g, int k, const Tin *base) {
   // segment-local key k -> cache row
   if (p.layout == VA_LAYOUT_PAGED) {
-    const int slot = k;  // logical slot: prefix 0..L-1, draft L..L+T-1
+    const int slot = kMod ? g.base + k : k;  // logical slot: prefix 0..L-1, draft L..L+T-1
     int page = __ldg(p.page_table + (size_t)g.b * p.max_pages + (slot >> p.page_shift));
     if (page < 0 || page >= p.num_pages) {
-      record_status(p.status, VA_ERR_DEVICE_BOUNDS);
+      // (the page entry of a key that no row sees may be anything)
+      if (!kMod || k >= g.lo) record_status(p.status, VA_ERR_DEVICE_BOUNDS);
       page = 0;
     }
     const size_t row = ((size_t)page << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
@@ -246,7 +264,7 @@ __device__ __forceinline__ const Tin *key_row(const AttnParams &p, const Seg &g,
       pos = 0;
     }
   } else {
-    pos = g.L + (k - g.n_prefix);  // dense: n_prefix == L, so pos == k
+    pos = g.L + (k - g.n_prefix);  // dense: pos == k (base + k with score shaping)
   }
   return base + (((size_t)g.b * p.len_cap + pos) * p.Hkv + g.hkv) * D;
 }
@@ -264,11 +282,19 @@ struct CtaRange {
 
 // Tiles of TK keys per segment, their exclusive scan into tstart[0..S], and
 // this CTA's range.  Called by every thread of the block (contains __syncthreads).
-template <int TK = kTK>
+template <int TK = kTK, bool kMod = false>
 __device__ __forceinline__ CtaRange plan_cta(const AttnParams &p, int *tstart) {
-  for (int s = threadIdx.x; s < p.S; s += blockDim.x) {
-    const Seg g = seg_info(p, s, true);
-    tstart[s] = (g.nkeys + TK - 1) / TK;
+  if constexpr (kMod) {  // a warp per sequence: its segments have the same keys
+    const int per = p.Hkv * p.NRB;
+    for (int b = threadIdx.x >> 5; b < p.B; b += blockDim.x >> 5) {
+      const Seg g = seg_info<true, TK>(p, b * per, true);
+      for (int i = threadIdx.x & 31; i < per; i += 32) tstart[b * per + i] = (g.nkeys + TK - 1) / TK;
+    }
+  } else {
+    for (int s = threadIdx.x; s < p.S; s += blockDim.x) {
+      const Seg g = seg_info(p, s, true);
+      tstart[s] = (g.nkeys + TK - 1) / TK;
+    }
   }
   __syncthreads();
   if ((threadIdx.x >> 5) == 0) warp_scan_inplace(tstart, p.S);
@@ -311,7 +337,7 @@ __device__ __forceinline__ CtaRange plan_cta(const AttnParams &p, int *tstart) {
 // cp.async gather only; -1 = chosen by use_tma): a kernel built for one way
 // carries none of the other's code, which measurably slows the warps that
 // share the kernel.
-template <typename Tin, int D, int NS, int TK = kTK, int MAXF = NS, int NPW = 1, int PATH = -1>
+template <typename Tin, int D, int NS, int TK = kTK, int MAXF = NS, int NPW = 1, int PATH = -1, bool kMod = false>
 __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensorMap *tmk, const CUtensorMap *tmv,
                                              const int *tstart, const CtaRange &cr, uint8_t *stages,
                                              uint64_t *full, uint64_t *empty, volatile int *abort_flag,
@@ -338,14 +364,14 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
     for (int j = 0; j < kRowSets; ++j) {
       if (j % NPW != pw) continue;
       const int k = ltt * TK + lane + 32 * j;
-      dst[j] = k < gg.nkeys ? key_row<Tin, D>(p, gg, k, kbase) : kbase;
+      dst[j] = k < gg.nkeys ? key_row<Tin, D, kMod>(p, gg, k, kbase) : kbase;
     }
   };
   if (!use_tma && cr.s0 < p.S && tstart[cr.s0] < cr.t1)
-    load_rows(seg_info(p, cr.s0, false), max(tstart[cr.s0], cr.t0) - tstart[cr.s0], rows);
+    load_rows(seg_info<kMod, TK>(p, cr.s0, false), max(tstart[cr.s0], cr.t0) - tstart[cr.s0], rows);
   int it = 0;
   for (int s = cr.s0; s < p.S && tstart[s] < cr.t1; ++s) {
-    const Seg g = seg_info(p, s, false);
+    const Seg g = seg_info<kMod, TK>(p, s, false);
     const int lt0 = max(tstart[s], cr.t0) - tstart[s];
     const int lt1 = min(tstart[s + 1], cr.t1) - tstart[s];
     for (int lt = lt0; lt < lt1; ++lt, ++it) {
@@ -378,12 +404,12 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
         if (lane == 0) mbar_arrive_expect_tx(full + st, (uint32_t)(nb * BR * 128 * C::kHalves * 2));
         __syncwarp();
         if (lane < nb) {
-          const int slot = k0 + lane * BR;
+          const int slot = (kMod ? g.base : 0) + k0 + lane * BR;
           int row;
           if (paged) {
             int page = __ldg(p.page_table + (size_t)g.b * p.max_pages + (slot >> p.page_shift));
             if (page < 0 || page >= p.num_pages) {
-              record_status(p.status, VA_ERR_DEVICE_BOUNDS);
+              if (!kMod || k0 + (lane + 1) * BR > g.lo) record_status(p.status, VA_ERR_DEVICE_BOUNDS);
               page = 0;
             }
             row = (page << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
@@ -406,7 +432,7 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
         if (lt + 1 < lt1) {
           load_rows(g, lt + 1, nrows);
         } else if (s + 1 < p.S && tstart[s + 1] < cr.t1) {
-          load_rows(seg_info(p, s + 1, false), max(tstart[s + 1], cr.t0) - tstart[s + 1], nrows);
+          load_rows(seg_info<kMod, TK>(p, s + 1, false), max(tstart[s + 1], cr.t0) - tstart[s + 1], nrows);
         } else {
           has_next = false;
         }
