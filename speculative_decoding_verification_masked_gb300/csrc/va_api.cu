@@ -452,11 +452,32 @@ va_status weight_common(const va_shape *shape, const va_score_mod *mod, const vo
   st = check_mod(mod != nullptr ? *mod : none, shape->scale, 1.f, false, p.mod);
   if (st != VA_OK) return st;
   p.mod.token_pos = nullptr;
+  p.mod.on = p.mod.softcap > 0.f || p.mod.window > 0 || p.mod.slopes != nullptr || p.mod.key_start != nullptr;
+  p.wait_ns = wait_limit_ns();
   return VA_OK;
 }
 
-va_status run_weight(const va::WeightParams &p, cudaStream_t stream) {
-  cudaError_t e = va::launch_accumulate_weight(p, stream);
+va_status run_weight(va::WeightParams &p, cudaStream_t stream) {
+  const int sms = device_sm_count(nullptr);
+  if (sms <= 0) return fail(VA_ERR_CUDA, "no usable CUDA device");
+  CUtensorMap tmk;
+  memset(&tmk, 0, sizeof tmk);
+  const int page = 1 << p.page_shift;
+  const bool paged = p.page_table != nullptr;
+  if (p.dtype == VA_DTYPE_BF16 && (!paged || page >= 8)) {
+    // as in the attention calls: boxes of a page (at most 64 rows) of the pool
+    const long long rows = paged ? (long long)p.num_pages * page : (long long)p.B * p.len_cap;
+    if (!paged && rows >= (1ll << 31)) return fail(VA_ERR_UNSUPPORTED, "B * max_cache_len must be below 2^31");
+    const int box = paged && page < 64 ? page : 64;
+    const bool good = rows < (1ll << 31) && encode_cache_map(&tmk, p.k, p.dtype, p.D, p.Hkv, rows, box);
+    if (!paged && !good) return fail(VA_ERR_CUDA, "could not encode the TMA tensor map of the cache");
+    if (good) p.tma_box = box;
+  }
+  const int keys = p.len_cap < p.stride ? p.len_cap : p.stride;
+  const long long tiles = (long long)p.B * p.Hkv * ((keys + 127) / 128);
+  if (tiles >= (1ll << 31)) return fail(VA_ERR_UNSUPPORTED, "problem too large (%lld key tiles)", tiles);
+  if (p.B > 65535 || p.Hkv > 65535) return fail(VA_ERR_UNSUPPORTED, "B and Hkv at most 65535");
+  cudaError_t e = va::launch_accumulate_weight(p, tmk, sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, "accumulated weight launch");
   return ok();
 }

@@ -15,6 +15,8 @@
 
 #include "va_common.cuh"
 #include "va_mod.cuh"
+#include "va_pipeline.cuh"
+#include "va_tcgen05.cuh"
 #include "va_weight.h"
 
 namespace va {
@@ -46,10 +48,10 @@ __device__ __forceinline__ const Tin *weight_key(const WeightParams &p, int b, i
   return static_cast<const Tin *>(p.k) + (row * p.Hkv + h) * p.D;
 }
 
-// One thread per key, its row in registers, query rows broadcast from shared
-// memory.
-template <typename Tin, int D>
+// fp32 (D = 64): one thread per key, its row in registers, query rows broadcast
+// from shared memory; FMA-bound.
 __global__ void __launch_bounds__(128) weight_simt_kernel(const WeightParams p) {
+  constexpr int D = 64;
   constexpr int RC = 16;  // query rows staged at once
   __shared__ float4 sq[RC][D / 4];
   __shared__ float slse[RC], sns[RC];
@@ -65,21 +67,14 @@ __global__ void __launch_bounds__(128) weight_simt_kernel(const WeightParams p) 
   const int lo = mod_first_slot(p.mod, b, 0, L);
   const bool live = j < L + a && j >= lo;
   float k[D];
-  const Tin *kr = live ? weight_key<Tin>(p, b, h, j, true) : nullptr;
+  const float *kr = live ? weight_key<float>(p, b, h, j, true) : nullptr;
 #pragma unroll
   for (int i = 0; i < D; ++i) k[i] = 0.f;
   if (kr != nullptr) {
 #pragma unroll
     for (int i = 0; i < D; i += 4) {
-      if constexpr (sizeof(Tin) == 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(kr + i));
-        k[i] = v.x, k[i + 1] = v.y, k[i + 2] = v.z, k[i + 3] = v.w;
-      } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(kr + i));
-        const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v.x));
-        const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v.y));
-        k[i] = x.x, k[i + 1] = x.y, k[i + 2] = y.x, k[i + 3] = y.y;
-      }
+      const float4 v = __ldg(reinterpret_cast<const float4 *>(kr + i));
+      k[i] = v.x, k[i + 1] = v.y, k[i + 2] = v.z, k[i + 3] = v.w;
     }
   }
   float acc = 0.f;
@@ -92,15 +87,8 @@ __global__ void __launch_bounds__(128) weight_simt_kernel(const WeightParams p) 
         const int i = r / group;
         const int t = p.path != nullptr ? __ldg(p.path + (size_t)b * p.T + i) : i;
         if (t >= 0 && t < p.T) {
-          const Tin *qr = static_cast<const Tin *>(p.q) + (((size_t)b * p.T + t) * p.Hq + h * group + r % group) * D;
-          if constexpr (sizeof(Tin) == 4) {
-            v = __ldg(reinterpret_cast<const float4 *>(qr) + c);
-          } else {
-            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(qr) + c);
-            const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.x));
-            const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.y));
-            v = make_float4(x.x, x.y, y.x, y.y);
-          }
+          const float *qr = static_cast<const float *>(p.q) + (((size_t)b * p.T + t) * p.Hq + h * group + r % group) * D;
+          v = __ldg(reinterpret_cast<const float4 *>(qr) + c);
         }
       }
       sq[e / (D / 4)][c] = v;
@@ -149,16 +137,412 @@ __global__ void __launch_bounds__(128) weight_simt_kernel(const WeightParams p) 
   }
 }
 
-cudaError_t launch_accumulate_weight(const WeightParams &p, cudaStream_t stream) {
-  const int keys = p.len_cap < p.stride ? p.len_cap : p.stride;
-  const dim3 grid((unsigned)((keys + 127) / 128), (unsigned)p.Hkv, (unsigned)p.B);
-  if (p.dtype == VA_DTYPE_FP32)
-    weight_simt_kernel<float, 64><<<grid, 128, 0, stream>>>(p);
-  else if (p.D == 64)
-    weight_simt_kernel<__nv_bfloat16, 64><<<grid, 128, 0, stream>>>(p);
-  else
-    weight_simt_kernel<__nv_bfloat16, 128><<<grid, 128, 0, stream>>>(p);
+// ---------------------------------------------------------------------------
+// bf16: the products on the 5th-generation tensor cores, keys on the TMEM lanes
+// ---------------------------------------------------------------------------
+//   S^T (128 keys x N rows) = K (128 x D) . Q^T      A = K tile, B = Q, both K-major
+// A thread owns one key of a tile, so the sum over the rows is the thread's own
+// and neither P nor a reduction leaves its registers: per score an FMA, an
+// exponential and an add.  K streams through a ring of TMA boxes (or cp.async
+// gathers), N is the number of accepted rows rounded up to 32.
+//
+// Bound by HBM (K once) while a kv-head has few rows; with 256 rows a tile's
+// 32,768 exponentials take about as long as its 32 KB.
+//
+// Roles (10 warps, one CTA per SM, a contiguous share of all 128-key tiles each):
+//   warps 0-3 / 4-7  the tiles of even / odd number: S from TMEM, exponentials,
+//                    row sum, the total's update; all eight stage Q and the
+//                    rows' lse when a kv-head begins
+//   warp 8           producer      warp 9  MMA issuer, owns TMEM (two S buffers)
+constexpr int kWtTile = 128;
+constexpr int kWtRows = 256;  // rows of one pass (N of the MMA)
+constexpr int kWtMaxStages = 6;
+constexpr int kWtThreads = 320;
+
+struct WtSeg {
+  int b, h;
+  int L, a;
+  int R;       // rows of this pass
+  int base;    // slot of the stream's first key, a multiple of the tile
+  int lo, hi;  // keys below lo no row sees, from hi (to L) every row does; from base
+  int nkeys;   // keys of the stream, from base; 0 = nothing to do
+};
+
+__device__ __forceinline__ WtSeg wt_seg(const WeightParams &p, int s, bool record) {
+  WtSeg g;
+  g.b = s / p.Hkv;
+  g.h = s % p.Hkv;
+  g.R = g.base = g.lo = g.hi = g.nkeys = 0;
+  if (!weight_seq(p, g.b, record, g.L, g.a)) return g;
+  const int rows = p.Hq / p.Hkv * g.a - p.row0;
+  g.R = max(0, min(rows, kWtRows));
+  const bool age = p.row0 == 0 && p.decay != 1.f;  // totals change where no row sees the key, too
+  if (g.R == 0) {
+    g.nkeys = age ? g.L : 0;
+    g.lo = g.hi = g.nkeys;  // nothing to load
+    return g;
+  }
+  const int lo = mod_first_slot(p.mod, g.b, 0, g.L), hi = mod_first_slot(p.mod, g.b, g.a - 1, g.L);
+  g.base = age ? 0 : lo & ~(kWtTile - 1);
+  g.lo = lo - g.base;
+  g.hi = hi - g.base;
+  g.nkeys = g.L + g.a - g.base;
+  return g;
+}
+
+struct WtSmem {  // offsets after the Q rows and the stages
+  static constexpr int kBars = 2 * kWtMaxStages + 5;  // full, empty, s_full[2], s_empty[2], drain
+  static constexpr int kMisc = (kBars * 8 + 15) & ~15;  // tmem base, abort flag
+  static constexpr int kLse = kMisc + 16;              // float [256]: -lse (-inf: no such row)
+  static constexpr int kSlope = kLse + kWtRows * 4;    // float [256]: -slope
+  static constexpr int kTok = kSlope + kWtRows * 4;    // float [256]: accepted rank of the row
+  static constexpr int kPlan = kTok + kWtRows * 4;     // int [S + 1]
+};
+
+template <int D, bool kTma, bool kMod>
+__global__ void __launch_bounds__(kWtThreads, 1)
+    weight_tc_kernel(const WeightParams p, const __grid_constant__ CUtensorMap tmk, int RQ, int NS) {
+  constexpr int TK = kWtTile;
+  constexpr int kHalves = D / 64;
+  constexpr int kStage = kHalves * TK * 128;
+  constexpr int kSoft = 256, kProducer = 8, kMma = 9;
+  constexpr int kBarQ = 1, kBarSoft = 2, kBarEnd = 3;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t *sQ = smem;  // [D/64 columns][RQ rows][128 B], 128-byte swizzle
+  uint8_t *stages = smem + kHalves * RQ * 128;
+  uint8_t *rest = stages + NS * kStage;
+  uint64_t *full = reinterpret_cast<uint64_t *>(rest);
+  uint64_t *empty = full + kWtMaxStages, *s_full = empty + kWtMaxStages, *s_empty = s_full + 2, *drain = s_full + 4;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rest + WtSmem::kMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(rest + WtSmem::kMisc + 4);
+  float *s_nlse = reinterpret_cast<float *>(rest + WtSmem::kLse);
+  float *s_slope = reinterpret_cast<float *>(rest + WtSmem::kSlope);
+  float *s_tok = reinterpret_cast<float *>(rest + WtSmem::kTok);
+  int *tstart = reinterpret_cast<int *>(rest + WtSmem::kPlan);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int S = p.B * p.Hkv;
+  const int group = p.Hq / p.Hkv;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full + i, kTma ? 1 : 32);
+      mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(s_empty + i, 128);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  for (int s = tid; s < S; s += kWtThreads)
+    tstart[s] = (wt_seg(p, s, blockIdx.x == 0 && p.row0 == 0 && s % p.Hkv == 0).nkeys + TK - 1) / TK;
+  __syncthreads();
+  if (warp == 0) warp_scan_inplace(tstart, S);
+  __syncthreads();
+  const long long total = tstart[S];
+  const int G = (int)min((long long)gridDim.x, total);
+  if ((int)blockIdx.x >= G) return;
+  const int t0 = (int)(blockIdx.x * total / G), t1 = (int)((blockIdx.x + 1) * total / G);
+  int s0 = 0;
+  for (int hi = S - 1; s0 < hi;) {
+    const int mid = (s0 + hi) >> 1;
+    if (tstart[mid + 1] > t0) hi = mid; else s0 = mid + 1;
+  }
+  bool ok = true;
+  auto wait_ok = [&](uint64_t *bar, uint32_t parity) { role_wait(bar, parity, ok, abort_flag, p.wait_ns, p.status); };
+  // a tile with keys some row sees (the others only age)
+  auto live = [](const WtSeg &g, int lt) { return g.R > 0 && lt * TK + TK > g.lo; };
+  // the next stage of the ring and the parity of its pass
+  struct Ring {
+    int st = 0;
+    uint32_t ph = 0;
+    __device__ void next(int n) {
+      if (++st == n) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+  };
+
+  if (warp == kProducer) {
+    const uint64_t policy = l2_evict_first_policy();
+    if (kTma && lane == 0) prefetch_tmap(&tmk);
+    Ring r;
+    int issued = 0;
+    for (int s = s0; s < S && tstart[s] < t1; ++s) {
+      const WtSeg g = wt_seg(p, s, false);
+      const int lt0 = max(tstart[s], t0) - tstart[s], lt1 = min(tstart[s + 1], t1) - tstart[s];
+      for (int lt = lt0; lt < lt1; ++lt) {
+        if (!live(g, lt)) continue;
+        wait_ok(empty + r.st, r.ph ^ 1u);
+        if (!ok) continue;
+        uint8_t *dst = stages + r.st * kStage;
+        const int k0 = lt * TK, slot0 = g.base + k0;
+        if constexpr (kTma) {
+          const int BR = p.tma_box, nbox = TK / BR;
+          const bool paged = p.page_table != nullptr;
+          const int nb = paged ? min(nbox, (g.nkeys - k0 + BR - 1) / BR) : nbox;
+          if (lane == 0) mbar_arrive_expect_tx(full + r.st, (uint32_t)(nb * BR * 128 * kHalves));
+          __syncwarp();
+          if (lane < nb) {
+            const int slot = slot0 + lane * BR;
+            int row = g.b * p.len_cap + slot;
+            if (paged) {
+              int page = __ldg(p.page_table + (size_t)g.b * p.max_pages + (slot >> p.page_shift));
+              if (page < 0 || page >= p.num_pages) {
+                if (k0 + (lane + 1) * BR > g.lo) record_status(p.status, VA_ERR_DEVICE_BOUNDS);
+                page = 0;
+              }
+              row = (page << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
+            }
+#pragma unroll
+            for (int c = 0; c < kHalves; ++c)
+              tma_load_3d(dst + c * TK * 128 + lane * BR * 128, &tmk, c * 64, g.h, row, full + r.st, policy);
+          }
+        } else {
+          // pages below 8 rows: lane l resolves rows l + 32 j, 16-byte copies
+          constexpr int CPR = D / 8, RPP = 32 / CPR;
+          const int cc = lane % CPR, rsub = lane / CPR;
+          for (int j = 0; j < TK / 32; ++j) {
+            const int k = k0 + lane + 32 * j;
+            const __nv_bfloat16 *row = nullptr;
+            if (k < g.nkeys) row = weight_key<__nv_bfloat16>(p, g.b, g.h, g.base + k, k >= g.lo);
+#pragma unroll
+            for (int i = 0; i < 32 / RPP; ++i) {
+              const int rl = i * RPP + rsub;
+              const uint64_t a = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(row), rl);
+              const void *src = a != 0 ? reinterpret_cast<const uint8_t *>(a) + cc * 16 : p.k;
+              cp_async_16(dst + swz<TK>(32 * j + rl, cc), src, a != 0 ? 16u : 0u);
+            }
+          }
+          cp_async_mbar_arrive(full + r.st);
+        }
+        r.next(NS);
+        ++issued;
+      }
+    }
+    if (!ok) {  // drain the copies in flight before leaving (bounded)
+      if constexpr (kTma) {
+        for (int j = 0; j < min(issued, NS); ++j) {
+          r.st = r.st == 0 ? NS - 1 : r.st - 1;
+          if (r.st == NS - 1) r.ph ^= 1u;
+          mbar_wait(full + r.st, r.ph, p.wait_ns >> 4);
+        }
+      } else {
+        cp_async_wait_all();
+      }
+    }
+    return;
+  }
+
+  if (warp == kMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  named_bar_sync(kBarEnd, kSoft + 32);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == kMma) {
+    Ring r;
+    int jt = 0;
+    const uint64_t dK0 = umma_sdesc(smem_u32(stages), 16, 1024), dQ0 = umma_sdesc(smem_u32(sQ), 16, 1024);
+    for (int s = s0; s < S && tstart[s] < t1; ++s) {
+      const WtSeg g = wt_seg(p, s, false);
+      const int lt0 = max(tstart[s], t0) - tstart[s], lt1 = min(tstart[s + 1], t1) - tstart[s];
+      if (lt0 >= lt1 || !live(g, lt1 - 1)) continue;
+      named_bar_sync(kBarQ, kSoft + 32);  // Q of this kv-head is in shared memory
+      const uint32_t idesc = umma_idesc(128, (g.R + 31) & ~31, 0, 0);
+      for (int lt = lt0; lt < lt1; ++lt) {
+        if (!live(g, lt)) continue;
+        const int b = jt & 1;
+        wait_ok(full + r.st, r.ph);
+        if (jt >= 2) wait_ok(s_empty + b, (uint32_t)((jt >> 1) - 1) & 1u);
+        if (ok) {
+          if constexpr (!kTma) fence_proxy_async_smem();
+          tc_fence_after();
+          const uint64_t dK = dK0 + (uint64_t)((r.st * kStage) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            umma_ss_warp(tmem + 256 * b, dK + (uint64_t)(((ks >> 2) * (TK * 128) + (ks & 3) * 32) >> 4),
+                         dQ0 + (uint64_t)(((ks >> 2) * (RQ * 128) + (ks & 3) * 32) >> 4), idesc, ks > 0 ? 1u : 0u);
+          umma_commit_warp(s_full + b);
+          umma_commit_warp(empty + r.st);
+        }
+        __syncwarp();
+        r.next(NS);
+        ++jt;
+      }
+    }
+    umma_commit_warp(drain);
+    mbar_wait(drain, 0u, p.wait_ns);
+    tc_fence_before();
+    named_bar_sync(kBarEnd, kSoft + 32);
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    return;
+  }
+
+  // ============================ sums over the rows ============================
+  const int wg = warp >> 2;            // takes the live tiles jt = wg mod 2
+  const int key_l = tid & 127;         // key of the tile = TMEM lane
+  const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 * wg;
+  int jt = 0;
+  for (int s = s0; s < S && tstart[s] < t1; ++s) {
+    const WtSeg g = wt_seg(p, s, false);
+    const int lt0 = max(tstart[s], t0) - tstart[s], lt1 = min(tstart[s + 1], t1) - tstart[s];
+    if (lt0 >= lt1) continue;
+    const int NP = (g.R + 31) & ~31;  // columns of S: whole 32-column loads
+    const bool any = live(g, lt1 - 1);  // (tiles turn live once)
+    if (any) {
+      named_bar_sync(kBarSoft, kSoft);  // every MMA that reads Q has completed (all tiles were waited for)
+      const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(p.q);
+      for (int e = tid; e < NP * (D / 8); e += kSoft) {
+        const int r = e / (D / 8), ch = e % (D / 8);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < g.R) {
+          const int i = (p.row0 + r) / group;
+          const int t = p.path != nullptr ? __ldg(p.path + (size_t)g.b * p.T + i) : i;
+          if (t >= 0 && t < p.T)
+            v = __ldg(reinterpret_cast<const uint4 *>(
+                          qb + (((size_t)g.b * p.T + t) * p.Hq + g.h * group + (p.row0 + r) % group) * D) + ch);
+        }
+        *reinterpret_cast<uint4 *>(sQ + (ch >> 3) * (RQ * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+      }
+      if (tid < NP) {
+        float nl = -INFINITY, ns = 0.f;
+        const int i = (p.row0 + tid) / group, hq = g.h * group + (p.row0 + tid) % group;
+        if (tid < g.R) {
+          const int t = p.path != nullptr ? __ldg(p.path + (size_t)g.b * p.T + i) : i;
+          if (t >= 0 && t < p.T) {
+            const float l = __ldg(p.lse + ((size_t)g.b * p.Hq + hq) * p.T + t);
+            nl = l == -INFINITY ? -INFINITY : -l;  // a row that saw no key adds nothing
+            if (kMod && p.mod.slopes != nullptr) ns = -__ldg(p.mod.slopes + hq);
+          } else {
+            record_status(p.status, VA_ERR_DEVICE_BOUNDS);
+          }
+        }
+        s_nlse[tid] = nl;
+        s_slope[tid] = ns;
+        s_tok[tid] = (float)i;
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      named_bar_sync(kBarSoft, kSoft);
+      named_bar_arrive(kBarQ, kSoft + 32);
+    }
+
+    float *w = p.weight + ((size_t)g.b * p.Hkv + g.h) * p.stride + g.base;
+    const int n_old = g.L - g.base;  // keys of the prefix
+    for (int lt = lt0; lt < lt1; ++lt) {
+      const int key = lt * TK + key_l;
+      if (!live(g, lt)) {
+        if ((lt & 1) == wg && key < g.nkeys) w[key] *= p.decay;
+        continue;
+      }
+      const int mine = (jt & 1) == wg;
+      const uint32_t ph = (uint32_t)(jt >> 1) & 1u;
+      ++jt;
+      if (!mine) continue;
+      // what the total keeps (row0 > 0: a later pass adds to the earlier ones')
+      float old = 0.f;
+      if (p.row0 > 0 ? key < g.nkeys : key < n_old && p.decay != 0.f) old = w[key];
+      const bool masked = lt * TK < g.hi || lt * TK + TK > n_old;
+      wait_ok(s_full + wg, ph);
+      tc_fence_after();
+      float acc0 = 0.f, acc1 = 0.f;
+      const float koff = (float)(key - n_old);
+      const float window = kMod && p.mod.window > 0 ? (float)p.mod.window : INFINITY;
+      const bool there = key >= g.lo && key < g.nkeys;
+      for (int c0 = 0; c0 < NP; c0 += 32) {
+        uint32_t u[32];
+        tmem_ld32(tS + c0, u);
+        tmem_ld_wait();
+        if (c0 + 32 >= NP) {
+          tc_fence_before();
+          mbar_arrive(s_empty + wg);
+        }
+#pragma unroll
+        for (int r = 0; r < 32; r += 2) {
+          const float2 nl = *reinterpret_cast<const float2 *>(s_nlse + c0 + r);
+          float2 d;
+          if (kMod && p.mod.softcap > 0.f)
+            d = add2(make_float2(capped_tanh(__uint_as_float(u[r]) * p.mod.in_mul, p.mod.out_mul),
+                                 capped_tanh(__uint_as_float(u[r + 1]) * p.mod.in_mul, p.mod.out_mul)), nl);
+          else
+            d = fma2(make_float2(__uint_as_float(u[r]), __uint_as_float(u[r + 1])),
+                     make_float2(p.mod.out_mul, p.mod.out_mul), nl);
+          if (kMod && p.mod.slopes != nullptr) {
+            const float2 ns = *reinterpret_cast<const float2 *>(s_slope + c0 + r);
+            const float2 tk = *reinterpret_cast<const float2 *>(s_tok + c0 + r);
+            d.x = fmaf(ns.x, fabsf(tk.x - koff), d.x);
+            d.y = fmaf(ns.y, fabsf(tk.y - koff), d.y);
+          }
+          if (masked) {
+            const float2 tk = *reinterpret_cast<const float2 *>(s_tok + c0 + r);
+            if (!(there && koff <= tk.x && tk.x - koff < window)) d.x = -INFINITY;
+            if (!(there && koff <= tk.y && tk.y - koff < window)) d.y = -INFINITY;
+          }
+          acc0 += ex2_approx(d.x * kModLog2e);
+          acc1 += ex2_approx(d.y * kModLog2e);
+        }
+      }
+      const float sum = acc0 + acc1;
+      if (ok && key < g.nkeys) w[key] = p.row0 > 0 ? old + sum : fmaf(p.decay, old, sum);
+    }
+  }
+  tc_fence_before();
+  named_bar_sync(kBarEnd, kSoft + 32);
+}
+
+template <int D, bool kTma, bool kMod>
+static cudaError_t launch_weight_tc(const WeightParams &p, const CUtensorMap &tmk, int grid, cudaStream_t stream) {
+  const int rows = p.Hq / p.Hkv * p.T - p.row0;
+  const int RQ = rows >= kWtRows ? kWtRows : (rows + 31) & ~31;
+  const size_t fixed = 1024 + (size_t)(D / 64) * RQ * 128 + WtSmem::kPlan + (size_t)(p.B * p.Hkv + 1) * 4;
+  const size_t stage = (size_t)(D / 64) * kWtTile * 128;
+  int NS = (int)((232448 - fixed) / stage);
+  if (NS > kWtMaxStages) NS = kWtMaxStages;
+  const size_t smem = fixed + NS * stage;
+  auto kern = weight_tc_kernel<D, kTma, kMod>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kWtThreads, smem, stream>>>(p, tmk, RQ, NS);
   return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t launch_weight_bf16(const WeightParams &p, const CUtensorMap &tmk, int grid, cudaStream_t stream) {
+  if (p.tma_box > 0)
+    return p.mod.on ? launch_weight_tc<D, true, true>(p, tmk, grid, stream)
+                    : launch_weight_tc<D, true, false>(p, tmk, grid, stream);
+  return p.mod.on ? launch_weight_tc<D, false, true>(p, tmk, grid, stream)
+                  : launch_weight_tc<D, false, false>(p, tmk, grid, stream);
+}
+
+// fp32: one thread per key (no TF32).  bf16: one pass of the tensor-core kernel
+// for every 256 rows of a kv-head; the later passes add to the totals.
+cudaError_t launch_accumulate_weight(const WeightParams &p, const CUtensorMap &tmk, int sms, cudaStream_t stream) {
+  const int keys = p.len_cap < p.stride ? p.len_cap : p.stride;
+  if (p.dtype == VA_DTYPE_FP32) {
+    const dim3 grid((unsigned)((keys + 127) / 128), (unsigned)p.Hkv, (unsigned)p.B);
+    weight_simt_kernel<<<grid, 128, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
+  const long long tiles = (long long)p.B * p.Hkv * ((keys + kWtTile - 1) / kWtTile);
+  const int grid = (int)(tiles < sms ? tiles : sms);
+  WeightParams q = p;
+  for (q.row0 = 0; q.row0 < p.Hq / p.Hkv * p.T; q.row0 += kWtRows) {
+    const cudaError_t e = p.D == 64 ? launch_weight_bf16<64>(q, tmk, grid, stream)
+                                    : launch_weight_bf16<128>(q, tmk, grid, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace va

@@ -24,9 +24,12 @@ struct WeightParams {
   float *weight;                 // [B][Hkv][stride]
   int stride;
   int *status;                   // may be NULL
-  ModParams mod;
+  ModParams mod;                 // in natural units; out_mul holds the scale also when off
+  int tma_box;                   // bf16: rows of one TMA box of the cache; 0 = gathered
+  int row0;                      // first packed row of this pass
+  uint64_t wait_ns;
 };
 
-cudaError_t launch_accumulate_weight(const WeightParams &p, cudaStream_t stream);
+cudaError_t launch_accumulate_weight(const WeightParams &p, const CUtensorMap &tmk, int sms, cudaStream_t stream);
 
 }  // namespace va
