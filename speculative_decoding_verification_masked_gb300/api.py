@@ -402,6 +402,8 @@ def _arg(t, name, shape, dtype, device):
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor or None")
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError("tensor arguments must live on the GPU")
     if t.device != device:
@@ -427,10 +429,13 @@ def _need(t, name, dim):
 def _run_on(device, stream, name, *args):
     """Call library function `name` with `device` current, on `stream` (that
     device's current stream by default); args end before the stream."""
-    f = getattr(lib(), name)
-    with torch.cuda.device(device):
-        s = torch.cuda.current_stream(device) if stream is None else stream
-        _check(f(*args, ctypes.c_void_p(s.cuda_stream)))
+    f = getattr(_lib or lib(), name)
+    s = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        _check(f(*args, s))
+    else:
+        with torch.cuda.device(device):
+            _check(f(*args, s))
 
 
 def _own(make, device, stream):

@@ -240,6 +240,22 @@ va_status check_mod(const va_score_mod &m, float scale, float unit, bool draft_m
   mp.softcap = m.softcap;
   mp.in_mul = m.softcap > 0.f ? scale / m.softcap : 0.f;
   mp.out_mul = (m.softcap > 0.f ? m.softcap : scale) * unit;
+  // tanh(y) / y as a polynomial of y^2 on |y| <= 0.75 (see cap_scores), with
+  // y = raw * in_mul, the cap and the unit folded in.  Coefficients that leave
+  // fp32's range (an extreme ratio of scale and cap) switch it off.
+  static const double poly[6] = {1.0,          -0.33332958817481995, 0.1332540661096573, -0.05334445461630821,
+                                 0.019582949578762054, -0.004716284107416868};
+  mp.small_lim = -1.f;
+  if (m.softcap > 0.f) {
+    const double in = (double)scale / m.softcap;
+    bool fits = true;
+    for (int k = 0; k < 6; ++k) {
+      const double c = poly[k] * pow(in, 2.0 * k) * scale * unit;
+      mp.small_c[k] = (float)c;
+      fits = fits && fabs(c) > 1e-36 && fabs(c) < 1e30;
+    }
+    if (fits) mp.small_lim = (float)(0.75 / in);
+  }
   mp.window = m.window;
   mp.slopes = m.slopes;
   mp.key_start = m.key_start;

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
     fence_mbar_init();
   }
   // ---- plan: tiles per segment, exclusive scan, this CTA's tile range ----
-  const CtaRange cr = plan_cta<kTK, kMod>(p, tstart);
+  const CtaRange cr = plan_cta<kTK, kMod>(p, tstart, reinterpret_cast<int4 *>(tstart + ((p.S + 1 + 3) & ~3)));
   if (c >= cr.G) return;
   const long long total = cr.total;
   const int G = cr.G;
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
   int rope_b = -1;  // sequence whose rotary table is in shared memory
 
   for (int s = s0; s < S && tstart[s] < t1; ++s) {
-    const Seg g = seg_info<kMod, kTK>(p, s, false);
+    const Seg g = seg_at<kMod, kTK>(p, s, cr);
     const int lt0 = max(tstart[s], t0) - tstart[s];
     const int lt1 = min(tstart[s + 1], t1) - tstart[s];
     const int first_cta = owner_cta(tstart[s], total, G);
@@ -142,11 +142,11 @@ __global__ void __launch_bounds__(kThreads, CPS)
       seen = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)seen) |
              (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(seen >> 32)) << 32;
     }
-    // V rows of tile lt that the consumers zero (0 * V must stay 0): TMA brought
+    // V rows of a tile that the consumers zero (0 * V must stay 0): TMA brought
     // whole boxes past the segment end; with score shaping, every key no row sees
-    auto zero_tile = [&](int lt) {
-      if (kMod) return lt * kTK < g.lo || lt * kTK + kTK > g.n_prefix;
-      return use_tma && lt * kTK + kTK > g.nkeys;
+    auto zero_tile = [&](int tile) {
+      if (kMod) return tile * kTK < g.lo || tile * kTK + kTK > g.n_prefix;
+      return use_tma && tile * kTK + kTK > g.nkeys;
     };
     auto zero_row = [&](int k) {
       if (kMod && (k < g.lo || (k >= g.n_prefix && k < g.nkeys && !((seen >> (k - g.n_prefix)) & 1ull)))) return true;
@@ -165,13 +165,13 @@ __global__ void __launch_bounds__(kThreads, CPS)
       named_bar_sync(kBarRope, kNWC * 32);
       rope_b = g.b;
     }
-    // the draft keys of tile lt, rotated in place by the consumer warps together
+    // the draft keys of a tile, rotated in place by the consumer warps together
     // before any of them reads the tile
-    auto rotate_draft = [&](int lt, int st) {
-      if (!kRope || lt * kTK + kTK <= g.n_prefix) return;
+    auto rotate_draft = [&](int tile, int st) {
+      if (!kRope || tile * kTK + kTK <= g.n_prefix) return;
       named_bar_sync(kBarRope, kNWC * 32);
-      const int r0 = max(0, g.n_prefix - lt * kTK), r1 = min(kTK, g.nkeys - lt * kTK);
-      rope_rotate_tile_rows<Tin, D, kTK>(stages + st * C::kStageBytes, r0, r1, lt * kTK + r0 - g.n_prefix, rope_tab,
+      const int r0 = max(0, g.n_prefix - tile * kTK), r1 = min(kTK, g.nkeys - tile * kTK);
+      rope_rotate_tile_rows<Tin, D, kTK>(stages + st * C::kStageBytes, r0, r1, tile * kTK + r0 - g.n_prefix, rope_tab,
                                          tid, kNWC * 32);
       named_bar_sync(kBarRope, kNWC * 32);
     };
@@ -250,19 +250,20 @@ __global__ void __launch_bounds__(kThreads, CPS)
 
       for (int lt = lt0; lt < lt1; ++lt, ++it) {
         const int st = it % NS;
+        const int tile = tile_of<kMod>(lt, lt0, lt1);
         const uint32_t ph = (uint32_t)(it / NS) & 1u;
         role_wait(full + st, ph, ok, abort_flag, p.wait_ns, p.status);
-        rotate_draft(lt, st);
+        rotate_draft(tile, st);
         if (ok) {
           const uint32_t ks_addr = smem_u32(stages + st * C::kStageBytes);
           const uint32_t vs_addr = ks_addr + C::kTileBytes;
           const int kb = kw * NK;
-          if (zero_tile(lt)) {
+          if (zero_tile(tile)) {
             // (P is exactly 0 there, but 0*NaN is not)
             uint8_t *vt = stages + st * C::kStageBytes + C::kTileBytes;
             for (int e = lane; e < NK * C::kChunks; e += 32) {
               const int r = kb + e / C::kChunks;
-              if (zero_row(lt * kTK + r)) *reinterpret_cast<uint4 *>(vt + swz(r, e % C::kChunks)) = make_uint4(0, 0, 0, 0);
+              if (zero_row(tile * kTK + r)) *reinterpret_cast<uint4 *>(vt + swz(r, e % C::kChunks)) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -284,9 +285,9 @@ __global__ void __launch_bounds__(kThreads, CPS)
             for (int nt = 0; nt < NT; ++nt) mma_bf16(sacc[nt], qa[2 * j + 1], bf[nt][2], bf[nt][3]);
           }
           // mask: keys past the segment end, and draft keys the row may not see
-          const int tile_k = lt * kTK + kb;
+          const int tile_k = tile * kTK + kb;
           if constexpr (kMod) {
-            const bool draft_tile = lt * kTK + kTK > g.n_prefix;
+            const bool draft_tile = tile * kTK + kTK > g.n_prefix;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
               }
             }
           }
-          if (lt * kTK + kTK > g.n_prefix) {
+          if (tile * kTK + kTK > g.n_prefix) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -510,17 +511,18 @@ __global__ void __launch_bounds__(kThreads, CPS)
       float m = -INFINITY, l = 0.f;
       for (int lt = lt0; lt < lt1; ++lt, ++it) {
         const int st = it % NS;
+        const int tile = tile_of<kMod>(lt, lt0, lt1);
         const uint32_t ph = (uint32_t)(it / NS) & 1u;
         role_wait(full + st, ph, ok, abort_flag, p.wait_ns, p.status);
-        rotate_draft(lt, st);
+        rotate_draft(tile, st);
         if (ok) {
           const uint8_t *kt = stages + st * C::kStageBytes;
           uint8_t *vt = stages + st * C::kStageBytes + C::kTileBytes;
-          if (zero_tile(lt)) {
+          if (zero_tile(tile)) {
             // zero V rows past the segment end (see the bf16 path); this warp's key half only
             for (int e = lane; e < 32 * C::kChunks; e += 32) {
               const int r = half * 32 + e / C::kChunks;
-              if (zero_row(lt * kTK + r)) *reinterpret_cast<uint4 *>(vt + swz(r, e % C::kChunks)) = make_uint4(0, 0, 0, 0);
+              if (zero_row(tile * kTK + r)) *reinterpret_cast<uint4 *>(vt + swz(r, e % C::kChunks)) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -538,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
               a = fmaf(qv[4 * i + 2], k4.z, a);
               a = fmaf(qv[4 * i + 3], k4.w, a);
             }
-            const int key = lt * kTK + half * 32 + kk;
+            const int key = tile * kTK + half * 32 + kk;
             bool vis = key < g.nkeys;
             if (vis && key >= g.n_prefix) vis = (rmask >> (key - g.n_prefix)) & 1ull;
             if constexpr (kMod) {
@@ -820,7 +822,7 @@ template <typename Tin, int D, int RG, int CPS>
 static size_t attn_smem_bytes(const AttnParams &p) {
   using C = Cfg<Tin, D, CPS>;
   return 1024 + (size_t)C::kStages * C::kStageBytes + C::kMergeBytes + 2 * C::kStages * 8 + 16 +
-         (size_t)((p.S + 1 + 3) & ~3) * 4 + (size_t)rope_table_bytes(p);
+         (size_t)((p.S + 1 + 3) & ~3) * 4 + (size_t)(p.mod.on ? kModCache * 16 : rope_table_bytes(p));
 }
 
 template <typename Tin, int D, int RG, int CPS = 1>

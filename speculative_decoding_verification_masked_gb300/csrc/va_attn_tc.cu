@@ -73,7 +73,9 @@ struct TcSmem {
   static constexpr int kLoFlagOff = kMiscOff + 16;          // int [2][2]: P residual written, per M-tile and buffer
   // then the rotary table of the segment (rope_table_bytes, 0 without
   // positions) and the tile starts of the work plan
-  static constexpr int kRopeOff = kLoFlagOff + 16;
+  // (with score shaping, instead of the rotary table, the ranges of the first sequences)
+  static constexpr int kRopeOff = (kLoFlagOff + 16 + 15) & ~15;
+  static_assert(kRopeOff % 16 == 0, "int4 array needs 16-byte alignment");
   static constexpr int kThreads = (5 * NMT + 2) * 32;
 };
 
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::kMiscOff + 4);
   volatile int *merge_ok = abort_flag + 1;
   float2 *rope_tab = reinterpret_cast<float2 *>(smem + SM::kRopeOff);
-  int *tstart = reinterpret_cast<int *>(smem + SM::kRopeOff + (kRope ? rope_table_bytes(p) : 0));
+  int *tstart = reinterpret_cast<int *>(smem + SM::kRopeOff + (kRope ? rope_table_bytes(p) : kMod ? kModCache * 16 : 0));
   volatile int *lo_flag = reinterpret_cast<volatile int *>(smem + SM::kLoFlagOff);
   constexpr bool use_tma = kTma;  // tiles by TMA boxes (dense, paged), else cp.async gathers
 
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  const CtaRange cr = plan_cta<kTK, kMod>(p, tstart);  // contains __syncthreads
+  const CtaRange cr = plan_cta<kTK, kMod>(p, tstart, reinterpret_cast<int4 *>(smem + SM::kRopeOff));  // contains __syncthreads
   if (c >= cr.G) return;
   const int t0 = cr.t0, t1 = cr.t1, s0 = cr.s0;
 
@@ -156,7 +158,9 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
   named_bar_sync(kBarEnd, kSoftThreads + kMmaThreads);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const float cl2 = kMod ? 1.f : p.scale * kLog2e;  // shaped scores are in base-2 units already
+  // scores stay raw until the exponential; capped or biased ones are in base-2 units already
+  const bool raw = !kMod || (p.mod.softcap == 0.f && p.mod.slopes == nullptr);
+  const float cl2 = raw ? p.scale * kLog2e : 1.f;
   const int group = p.Hq / p.Hkv;
 
   if (warp >= kMmaWarp0) {
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
     };
 
     for (int s = s0; s < p.S && tstart[s] < t1; ++s) {
-      const Seg g = seg_info<kMod, kTK>(p, s, false);
+      const Seg g = seg_at<kMod, kTK>(p, s, cr);
       const int lt0 = max(tstart[s], t0) - tstart[s];
       const int lt1 = min(tstart[s + 1], t1) - tstart[s];
       uint64_t seen = ~0ull;
@@ -271,7 +275,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
           // the softmax wrote the P residual of this tile too (set before its
           // arrive on p_full; rewritten only after this PV has completed)
           const bool exact = lo_flag[2 * mi + b] != 0;
-          acquire_stage(st, (uint32_t)(it / NS) & 1u, lt, g, seen);
+          acquire_stage(st, (uint32_t)(it / NS) & 1u, tile_of<kMod>(lt, lt0, lt1), g, seen);
           issue_pv(mi, b, st, lt == lt0, exact);
         }
         __syncwarp();
@@ -299,7 +303,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
   // split segments this CTA holds a part of (at most its first and its last)
   int n_split = 0, ms[2] = {0, 0}, mslot[2] = {0, 0}, mnp[2] = {0, 0}, mpart[2] = {0, 0};
   for (int s = s0; s < p.S && tstart[s] < t1; ++s) {
-    const Seg g = seg_info<kMod, kTK>(p, s, false);
+    const Seg g = seg_at<kMod, kTK>(p, s, cr);
     const int lt0 = max(tstart[s], t0) - tstart[s];
     const int lt1 = min(tstart[s + 1], t1) - tstart[s];
     const int first_cta = owner_cta(tstart[s], cr.total, cr.G);
@@ -417,27 +421,36 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j) sv[32 + j] = __uint_as_float(w[j]);
       }
-      const int k0 = lt * kTK;
+      const int k0 = tile_of<kMod>(lt, lt0, lt1) * kTK;
       const bool masked = k0 + kTK > g.n_prefix || (kMod && k0 < g.hi);
       if constexpr (kMod) {
-        if (p.mod.softcap > 0.f) {
-#pragma unroll
-          for (int j = 0; j < 64; ++j) sv[j] = capped_tanh(sv[j] * p.mod.in_mul, p.mod.out_mul);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 64; ++j) sv[j] *= p.mod.out_mul;
-        }
+        if (p.mod.softcap > 0.f) cap_scores<64>(p.mod, sv);
         if (p.mod.slopes != nullptr) {
-          const float d0 = qoff - (float)(k0 - g.n_prefix);
-          if (k0 + kTK <= g.n_prefix) {
+          const float mul = p.mod.softcap > 0.f ? 1.f : p.mod.out_mul;
+          const float d0 = qoff - (float)(k0 - g.n_prefix);  // distance of the tile's first key
+          if (k0 + kTK <= g.n_prefix && qoff >= 0.f) {
+            // the row is past every key: ns * (d0 - j), eight keys at a time
+            float2 step[4];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) sv[j] = fmaf(ns, fabsf(d0 - (float)j), sv[j]);
+            for (int q = 0; q < 4; ++q) step[q] = make_float2(-ns * (float)(2 * q), -ns * (float)(2 * q + 1));
+#pragma unroll
+            for (int j8 = 0; j8 < 64; j8 += 8) {
+              const float t8 = ns * (d0 - (float)j8);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int j = j8 + 2 * q;
+                const float2 y = fma2(make_float2(sv[j], sv[j + 1]), make_float2(mul, mul),
+                                      add2(make_float2(t8, t8), step[q]));
+                sv[j] = y.x;
+                sv[j + 1] = y.y;
+              }
+            }
           } else {
 #pragma unroll
             for (int j = 0; j < 64; ++j) {
               const int dk = k0 + j - g.n_prefix;  // draft key, or a prefix key below 0
               const float d = dk >= 0 && dk < p.T ? qoff - (float)mod_off(p.mod, p.T, g.b, dk, g.L) : d0 - (float)j;
-              sv[j] = fmaf(ns, fabsf(d), sv[j]);
+              sv[j] = fmaf(ns, fabsf(d), sv[j] * mul);
             }
           }
         }
@@ -624,7 +637,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
 // ---------------------------------------------------------------------------
 template <int NMT, int NS>
 static size_t tc_smem_bytes(const AttnParams &p) {
-  return 1024 + (size_t)TcSmem<NMT, NS>::kRopeOff + (size_t)rope_table_bytes(p) + (size_t)(p.S + 1) * 4;
+  return 1024 + (size_t)TcSmem<NMT, NS>::kRopeOff + (size_t)(p.mod.on ? kModCache * 16 : rope_table_bytes(p)) + (size_t)(p.S + 1) * 4;
 }
 
 constexpr size_t kTcSmemLimit = 232448;  // bytes of dynamic shared memory a CTA may have

@@ -81,10 +81,10 @@ struct TkSmem {
   static constexpr int kRowInvOff = kRedOff + NR * 16;     // float [64]: 1 / l per row (epilogue)
   // then the rotary table of the segment (rope_table_bytes, 0 without
   // positions), or with score shaping float2 [64] (slope, offset) of the rows
-  // and int [64] first visible keys of the draft tokens, and the tile starts
-  // of the work plan
+  // and int [64] first visible keys of the draft tokens and the ranges of the
+  // first sequences, and the tile starts of the work plan
   static constexpr int kRopeOff = kRowInvOff + 256;
-  static constexpr int kModBytes = 64 * 8 + 64 * 4;
+  static constexpr int kModBytes = 64 * 8 + 64 * 4 + kModCache * 16;
   static_assert(kQOff % 1024 == 0 && kQBytes % 1024 == 0, "UMMA operands need 1024-byte aligned swizzle atoms");
   static_assert(kBarOff % 8 == 0 && kRowMaskOff % 8 == 0 && kKeyMaskOff % 8 == 0, "8-byte alignment");
   static_assert(kRedOff % 16 == 0, "float4 array needs 16-byte alignment");
@@ -268,7 +268,8 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  const CtaRange cr = plan_cta<TK, kMod>(p, tstart);  // contains __syncthreads
+  const CtaRange cr = plan_cta<TK, kMod>(
+      p, tstart, reinterpret_cast<int4 *>(smem + SM::kRopeOff + 64 * 8 + 64 * 4));  // contains __syncthreads
   if (c >= cr.G) return;
   const int t0 = cr.t0, t1 = cr.t1, s0 = cr.s0;
 
@@ -290,7 +291,9 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
   named_bar_sync(kBarEnd, kSoft + 32);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const float cl2 = kMod ? 1.f : p.scale * kLog2e;  // shaped scores are in base-2 units already
+  // scores stay raw until the exponential; capped or biased ones are in base-2 units already
+  const bool raw = !kMod || (p.mod.softcap == 0.f && p.mod.slopes == nullptr);
+  const float cl2 = raw ? p.scale * kLog2e : 1.f;
   const int group = p.Hq / p.Hkv;
 
   bool ok = true;
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
     };
 
     for (int s = s0; s < p.S && tstart[s] < t1; ++s) {
-      const Seg g = seg_info<kMod, TK>(p, s, false);
+      const Seg g = seg_at<kMod, TK>(p, s, cr);
       const int lt0 = max(tstart[s], t0) - tstart[s];
       const int lt1 = min(tstart[s + 1], t1) - tstart[s];
       named_bar_sync(kBarQ, kSoft + 32);  // Q of this segment is in shared memory
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
   // merged after its last tile
   int n_split = 0, ms[2] = {0, 0}, mslot[2] = {0, 0}, mnp[2] = {0, 0}, mpart[2] = {0, 0};
   for (int s = s0; s < p.S && tstart[s] < t1; ++s) {
-    const Seg g = seg_info<kMod, TK>(p, s, false);
+    const Seg g = seg_at<kMod, TK>(p, s, cr);
     const int lt0 = max(tstart[s], t0) - tstart[s];
     const int lt1 = min(tstart[s + 1], t1) - tstart[s];
     const int first_cta = owner_cta(tstart[s], cr.total, cr.G);
@@ -504,6 +507,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
       masks_ready = true;
     };
     if (NR <= 32 && has_draft) build_masks();
+    bool ahead = true;  // score shaping: no token sits before the end of the prefix
     if constexpr (kMod) {
       // (the previous segment's readers are past its epilogue's barriers)
       if (tid < 64) {
@@ -513,7 +517,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
         if (tid < p.T)
           mod_first[tid] = mod_first_slot(p.mod, g.b, mod_off(p.mod, p.T, g.b, tid, g.L), g.L) - g.base;
       }
-      named_bar_sync(kBarSoft, kSoft);
+      ahead = !bar_red_or(kBarSoft, kSoft, tid < p.R && mod_row[tid].y < 0.f);
     }
 
     float mu[NR];  // reference max per row, log2 units
@@ -529,9 +533,10 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
       const int b = jt & 1;
       const int st = it % NS;
       const uint32_t tS = tO + (2 + b) * NC;
-      const int key = lt * TK + tid;
-      const bool draft_tile = lt * TK + TK > g.n_prefix;
-      const bool masked = draft_tile || (kMod && lt * TK < g.hi);
+      const int tile = tile_of<kMod>(lt, lt0, lt1);
+      const int key = tile * TK + tid;
+      const bool draft_tile = tile * TK + TK > g.n_prefix;
+      const bool masked = draft_tile || (kMod && tile * TK < g.hi);
       if (NR > 32 && draft_tile && !masks_ready) build_masks();
       uint64_t km = ~0ull;  // rows that see this key
       if (masked) {
@@ -545,6 +550,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
         }
       }
       float koff = 0.f;  // the key's position relative to L
+      const bool behind = kMod && !draft_tile && ahead;
       if constexpr (kMod) {
         koff = (float)(key - g.n_prefix);
         if (p.mod.slopes != nullptr && key >= g.n_prefix && key < g.nkeys)
@@ -559,18 +565,26 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
       auto load_scores = [&]() {
         tmem_ld_f<NR>(tS, x);
         if constexpr (kMod) {
-          if (p.mod.softcap > 0.f) {
-#pragma unroll
-            for (int r = 0; r < NR; ++r) x[r] = capped_tanh(x[r] * p.mod.in_mul, p.mod.out_mul);
-          } else {
-#pragma unroll
-            for (int r = 0; r < NR; ++r) x[r] *= p.mod.out_mul;
-          }
+          if (p.mod.softcap > 0.f) cap_scores<NR>(p.mod, x);
           if (p.mod.slopes != nullptr) {
+            const float mul = p.mod.softcap > 0.f ? 1.f : p.mod.out_mul;
+            if (behind) {
+              // every row is past the key: the bias is linear in the key's position
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-              const float2 c = mod_row[r];
-              x[r] = fmaf(c.x, fabsf(c.y - koff), x[r]);
+              for (int r = 0; r < NR; r += 2) {
+                const float4 c = *reinterpret_cast<const float4 *>(mod_row + r);
+                const float2 y = fma2(make_float2(x[r], x[r + 1]), make_float2(mul, mul),
+                                      make_float2(c.x * c.y, c.z * c.w));
+                const float2 s2 = fma2(make_float2(c.x, c.z), make_float2(-koff, -koff), y);
+                x[r] = s2.x;
+                x[r + 1] = s2.y;
+              }
+            } else {
+#pragma unroll
+              for (int r = 0; r < NR; ++r) {
+                const float2 c = mod_row[r];
+                x[r] = fmaf(c.x, fabsf(c.y - koff), x[r] * mul);
+              }
             }
           }
         }

@@ -51,15 +51,15 @@ struct Seg {
   int base, lo, hi;
 };
 
-// kMod: the prefix is cut to what a window or a document start leaves visible
-// (called by full warps).
+// kMod: the prefix is cut to what a window or a document start leaves visible;
+// `range` = {L, lo, hi} of the sequence when it is known already.
 template <bool kMod = false, int TK = 64>
-__device__ __forceinline__ Seg seg_info(const AttnParams &p, int s, bool record) {
+__device__ __forceinline__ Seg seg_info(const AttnParams &p, int s, bool record, const int4 *range = nullptr) {
   Seg g;
   g.rb = s % p.NRB;
   g.hkv = (s / p.NRB) % p.Hkv;
   g.b = s / (p.NRB * p.Hkv);
-  int L = __ldg(p.seqlens + g.b);
+  int L = kMod && range != nullptr ? range->x : __ldg(p.seqlens + g.b);
   if (L < 0 || L > p.len_cap - p.T) {
     if (record) record_status(p.status, VA_ERR_DEVICE_BOUNDS);
     L = L < 0 ? 0 : p.len_cap - p.T;
@@ -78,7 +78,12 @@ __device__ __forceinline__ Seg seg_info(const AttnParams &p, int s, bool record)
   g.base = g.lo = g.hi = 0;
   if constexpr (kMod) {
     int lo, hi;
-    mod_range(p.mod, p.T, g.b, L, record ? p.status : nullptr, lo, hi);
+    if (range != nullptr) {
+      lo = range->y;
+      hi = range->z;
+    } else {
+      mod_range(p.mod, p.T, g.b, L, record ? p.status : nullptr, lo, hi);
+    }
     g.base = lo & ~(TK - 1);
     g.lo = lo - g.base;
     g.hi = hi - g.base;
@@ -278,17 +283,42 @@ struct CtaRange {
   int G;            // CTAs the list is cut over (<= total)
   int t0, t1;       // this CTA's tiles [t0, t1)
   int s0;           // first segment touching t0
+  // score shaping: {L, lo, hi} of the kModCache sequences from b0 on
+  const int4 *range;
+  int b0;
 };
+
+constexpr int kModCache = 16;
+
+// Segment s of this CTA's share.
+template <bool kMod, int TK>
+__device__ __forceinline__ Seg seg_at(const AttnParams &p, int s, const CtaRange &cr) {
+  if constexpr (kMod) {
+    const int i = s / (p.NRB * p.Hkv) - cr.b0;
+    return seg_info<true, TK>(p, s, false, i < kModCache ? cr.range + i : nullptr);
+  } else {
+    return seg_info(p, s, false);
+  }
+}
+
+// Tile of the lt-th step over the tiles [lt0, lt1) of a segment part.  With
+// score shaping the nearest keys come first: a distance bias grows towards
+// them, so the softmax reference would move at every tile the other way round.
+template <bool kMod>
+__device__ __forceinline__ int tile_of(int lt, int lt0, int lt1) {
+  return kMod ? lt0 + lt1 - 1 - lt : lt;
+}
 
 // Tiles of TK keys per segment, their exclusive scan into tstart[0..S], and
 // this CTA's range.  Called by every thread of the block (contains __syncthreads).
+// With score shaping `range` is shared memory for kModCache entries.
 template <int TK = kTK, bool kMod = false>
-__device__ __forceinline__ CtaRange plan_cta(const AttnParams &p, int *tstart) {
-  if constexpr (kMod) {  // a warp per sequence: its segments have the same keys
-    const int per = p.Hkv * p.NRB;
-    for (int b = threadIdx.x >> 5; b < p.B; b += blockDim.x >> 5) {
-      const Seg g = seg_info<true, TK>(p, b * per, true);
-      for (int i = threadIdx.x & 31; i < per; i += 32) tstart[b * per + i] = (g.nkeys + TK - 1) / TK;
+__device__ __forceinline__ CtaRange plan_cta(const AttnParams &p, int *tstart, int4 *range = nullptr) {
+  const int per = p.Hkv * p.NRB;
+  if constexpr (kMod) {  // the segments of a sequence have the same keys
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+      const int n = (seg_info<true, TK>(p, b * per, true).nkeys + TK - 1) / TK;
+      for (int i = 0; i < per; ++i) tstart[b * per + i] = n;
     }
   } else {
     for (int s = threadIdx.x; s < p.S; s += blockDim.x) {
@@ -316,6 +346,15 @@ __device__ __forceinline__ CtaRange plan_cta(const AttnParams &p, int *tstart) {
       if (tstart[mid + 1] > r.t0) hi = mid; else lo = mid + 1;
     }
     r.s0 = lo;
+  }
+  if constexpr (kMod) {  // (the loads hit the first-level cache: made above)
+    r.range = range;
+    r.b0 = r.s0 / per;
+    if (threadIdx.x < kModCache && r.b0 + threadIdx.x < p.B) {
+      const Seg g = seg_info<true, TK>(p, (r.b0 + threadIdx.x) * per, false);
+      range[threadIdx.x] = make_int4(g.L, g.base + g.lo, g.base + g.hi, 0);
+    }
+    __syncthreads();
   }
   return r;
 }
@@ -367,11 +406,15 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
       dst[j] = k < gg.nkeys ? key_row<Tin, D, kMod>(p, gg, k, kbase) : kbase;
     }
   };
+  auto first_tile = [&](int s) {  // the tile this CTA's part of segment s starts with
+    const int lt0 = max(tstart[s], cr.t0) - tstart[s];
+    return tile_of<kMod>(lt0, lt0, min(tstart[s + 1], cr.t1) - tstart[s]);
+  };
   if (!use_tma && cr.s0 < p.S && tstart[cr.s0] < cr.t1)
-    load_rows(seg_info<kMod, TK>(p, cr.s0, false), max(tstart[cr.s0], cr.t0) - tstart[cr.s0], rows);
+    load_rows(seg_at<kMod, TK>(p, cr.s0, cr), first_tile(cr.s0), rows);
   int it = 0;
   for (int s = cr.s0; s < p.S && tstart[s] < cr.t1; ++s) {
-    const Seg g = seg_info<kMod, TK>(p, s, false);
+    const Seg g = seg_at<kMod, TK>(p, s, cr);
     const int lt0 = max(tstart[s], cr.t0) - tstart[s];
     const int lt1 = min(tstart[s + 1], cr.t1) - tstart[s];
     for (int lt = lt0; lt < lt1; ++lt, ++it) {
@@ -389,7 +432,7 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
       if (!ok) continue;
       uint8_t *kdst = stages + st * C::kStageBytes;
       uint8_t *vdst = kdst + C::kTileBytes;
-      const int k0 = lt * TK;
+      const int k0 = tile_of<kMod>(lt, lt0, lt1) * TK;
       if (use_tma) {
         // TMA boxes of BR rows x one kv-head x 128 bytes of the head dimension.
         // Dense: BR = 64 consecutive tokens; rows past the segment end arrive
@@ -430,9 +473,9 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
         const Tin *nrows[kRowSets];
         bool has_next = true;
         if (lt + 1 < lt1) {
-          load_rows(g, lt + 1, nrows);
+          load_rows(g, tile_of<kMod>(lt + 1, lt0, lt1), nrows);
         } else if (s + 1 < p.S && tstart[s + 1] < cr.t1) {
-          load_rows(seg_info<kMod, TK>(p, s + 1, false), max(tstart[s + 1], cr.t0) - tstart[s + 1], nrows);
+          load_rows(seg_at<kMod, TK>(p, s + 1, cr), first_tile(s + 1), nrows);
         } else {
           has_next = false;
         }

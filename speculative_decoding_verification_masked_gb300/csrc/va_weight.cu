@@ -467,16 +467,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           tc_fence_before();
           mbar_arrive(s_empty + wg);
         }
+        float x[32];
+#pragma unroll
+        for (int r = 0; r < 32; ++r) x[r] = __uint_as_float(u[r]);
+        if (kMod && p.mod.softcap > 0.f) cap_scores<32>(p.mod, x);
+        const float mul = kMod && p.mod.softcap > 0.f ? 1.f : p.mod.out_mul;
 #pragma unroll
         for (int r = 0; r < 32; r += 2) {
           const float2 nl = *reinterpret_cast<const float2 *>(s_nlse + c0 + r);
-          float2 d;
-          if (kMod && p.mod.softcap > 0.f)
-            d = add2(make_float2(capped_tanh(__uint_as_float(u[r]) * p.mod.in_mul, p.mod.out_mul),
-                                 capped_tanh(__uint_as_float(u[r + 1]) * p.mod.in_mul, p.mod.out_mul)), nl);
-          else
-            d = fma2(make_float2(__uint_as_float(u[r]), __uint_as_float(u[r + 1])),
-                     make_float2(p.mod.out_mul, p.mod.out_mul), nl);
+          float2 d = fma2(make_float2(x[r], x[r + 1]), make_float2(mul, mul), nl);
           if (kMod && p.mod.slopes != nullptr) {
             const float2 ns = *reinterpret_cast<const float2 *>(s_slope + c0 + r);
             const float2 tk = *reinterpret_cast<const float2 *>(s_tok + c0 + r);
