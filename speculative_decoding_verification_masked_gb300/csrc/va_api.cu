@@ -138,7 +138,8 @@ bool tck_enabled() {
   return !(e != nullptr && strcmp(e, "mma") == 0);
 }
 
-// (Calls with score shaping always take the tcgen05 kernels at d128.)
+// (Calls with score shaping always take the tcgen05 kernels at d128, and the
+// keys-on-lanes one at d64 up to 64 rows.)
 RowPlan row_plan(const va_shape &s, bool shaped = false) {
   RowPlan r;
   r.R = (s.Hq / s.Hkv) * s.T;
@@ -150,7 +151,7 @@ RowPlan row_plan(const va_shape &s, bool shaped = false) {
     r.use_tc = 1;
     r.RG = 4;
     r.rows_pad = r.R > 128 ? 256 : 128;
-  } else if (s.D == 128 && (shaped || tck_enabled())) {
+  } else if (shaped ? s.D == 128 || r.R <= 64 : s.D == 128 && tck_enabled()) {
     r.use_tc = 2;
     r.RG = 4;
     r.rows_pad = r.R <= 16 ? 16 : (r.R <= 32 ? 32 : 64);
@@ -236,7 +237,7 @@ va_status check_mod(const va_score_mod &m, float scale, float unit, bool draft_m
   if (draft_mask && (m.window > 0 || m.slopes != nullptr) && m.token_pos == nullptr)
     return fail(VA_ERR_INVALID_ARG, "a window or slopes with a tree or a mask need token_pos");
   memset(&mp, 0, sizeof mp);
-  mp.on = 1;
+  mp.on = m.softcap > 0.f || m.slopes != nullptr ? 2 : 1;
   mp.softcap = m.softcap;
   mp.in_mul = m.softcap > 0.f ? scale / m.softcap : 0.f;
   mp.out_mul = (m.softcap > 0.f ? m.softcap : scale) * unit;
@@ -468,7 +469,7 @@ va_status weight_common(const va_shape *shape, const va_score_mod *mod, const vo
   st = check_mod(mod != nullptr ? *mod : none, shape->scale, 1.f, false, p.mod);
   if (st != VA_OK) return st;
   p.mod.token_pos = nullptr;
-  p.mod.on = p.mod.softcap > 0.f || p.mod.window > 0 || p.mod.slopes != nullptr || p.mod.key_start != nullptr;
+  if (p.mod.softcap == 0.f && p.mod.window == 0 && p.mod.slopes == nullptr && p.mod.key_start == nullptr) p.mod.on = 0;
   p.wait_ns = wait_limit_ns();
   return VA_OK;
 }

@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
 
       for (int lt = lt0; lt < lt1; ++lt, ++it) {
         const int st = it % NS;
-        const int tile = tile_of<kMod>(lt, lt0, lt1);
+        const int tile = tile_of<kMod>(p, lt, lt0, lt1);
         const uint32_t ph = (uint32_t)(it / NS) & 1u;
         role_wait(full + st, ph, ok, abort_flag, p.wait_ns, p.status);
         rotate_draft(tile, st);
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
       float m = -INFINITY, l = 0.f;
       for (int lt = lt0; lt < lt1; ++lt, ++it) {
         const int st = it % NS;
-        const int tile = tile_of<kMod>(lt, lt0, lt1);
+        const int tile = tile_of<kMod>(p, lt, lt0, lt1);
         const uint32_t ph = (uint32_t)(it / NS) & 1u;
         role_wait(full + st, ph, ok, abort_flag, p.wait_ns, p.status);
         rotate_draft(tile, st);
@@ -830,11 +830,11 @@ static cudaError_t launch_attn_t(const AttnParams &p, const CUtensorMap &tmk, co
                                  cudaStream_t stream) {
   const size_t smem = attn_smem_bytes<Tin, D, RG, CPS>(p);
   // instances with the rotary embedding, with score shaping and with neither
-  // (code that never runs still costs the hot loop); d128 score shaping is left
-  // to the tcgen05 kernels
+  // (code that never runs still costs the hot loop); score shaping of d128 and of
+  // at most 64 rows of d64 is left to the tcgen05 kernels
   auto kern = p.positions != nullptr ? verify_attn_kernel<Tin, D, RG, CPS, true, false>
                                      : verify_attn_kernel<Tin, D, RG, CPS, false, false>;
-  if constexpr (D == 64) {
+  if constexpr (D == 64 && CPS == 1) {
     if (p.mod.on) kern = verify_attn_kernel<Tin, D, RG, CPS, false, true>;
   }
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

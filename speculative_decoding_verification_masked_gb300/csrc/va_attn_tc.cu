@@ -84,7 +84,9 @@ __device__ __forceinline__ uint32_t swz128(int r, int c) {
   return (uint32_t)((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-template <int NMT, bool kTma, bool kRope, bool kMod, int NS>
+// kMod: 0 without score shaping, 1 with a window or document start only, 2 with
+// a cap or slopes.
+template <int NMT, bool kTma, bool kRope, int kMod, int NS>
 __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
     verify_attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv) {
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::kMiscOff + 4);
   volatile int *merge_ok = abort_flag + 1;
   float2 *rope_tab = reinterpret_cast<float2 *>(smem + SM::kRopeOff);
-  int *tstart = reinterpret_cast<int *>(smem + SM::kRopeOff + (kRope ? rope_table_bytes(p) : kMod ? kModCache * 16 : 0));
+  int *tstart = reinterpret_cast<int *>(smem + SM::kRopeOff + (kRope ? rope_table_bytes(p) : kMod != 0 ? kModCache * 16 : 0));
   volatile int *lo_flag = reinterpret_cast<volatile int *>(smem + SM::kLoFlagOff);
   constexpr bool use_tma = kTma;  // tiles by TMA boxes (dense, paged), else cp.async gathers
 
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  const CtaRange cr = plan_cta<kTK, kMod>(p, tstart, reinterpret_cast<int4 *>(smem + SM::kRopeOff));  // contains __syncthreads
+  const CtaRange cr = plan_cta<kTK, kMod != 0>(p, tstart, reinterpret_cast<int4 *>(smem + SM::kRopeOff));  // contains __syncthreads
   if (c >= cr.G) return;
   const int t0 = cr.t0, t1 = cr.t1, s0 = cr.s0;
 
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
     bool pok = true;
     // at most NS-1 tiles in flight, and the second waits for the first: the
     // first tile of every CTA lands sooner when the kernel starts (-1 us)
-    produce_tiles<__nv_bfloat16, D, NS, kTK, NS - 1, 1, kTma ? 1 : 0, kMod>(p, &tmk, &tmv, tstart, cr, stages, full, empty,
+    produce_tiles<__nv_bfloat16, D, NS, kTK, NS - 1, 1, kTma ? 1 : 0, kMod != 0>(p, &tmk, &tmv, tstart, cr, stages, full, empty,
                                                                   abort_flag, use_tma, pok);
     return;
   }
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // scores stay raw until the exponential; capped or biased ones are in base-2 units already
-  const bool raw = !kMod || (p.mod.softcap == 0.f && p.mod.slopes == nullptr);
+  const bool raw = kMod != 2 || (p.mod.softcap == 0.f && p.mod.slopes == nullptr);
   const float cl2 = raw ? p.scale * kLog2e : 1.f;
   const int group = p.Hq / p.Hkv;
 
@@ -178,7 +180,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
     // draft keys some token sees)
     auto acquire_stage = [&](int st, uint32_t ph, int lt, const Seg &g, uint64_t seen) {
       wait_ok(full + st, ph);
-      if (kMod) {
+      if (kMod != 0) {
         if (ok && (lt * kTK < g.lo || lt * kTK + kTK > g.n_prefix)) {
           uint8_t *vt = stages + st * Geo::kStageBytes + Geo::kTileBytes;
           for (int e = lane; e < kTK * Geo::kChunks; e += 32) {
@@ -235,11 +237,11 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
     };
 
     for (int s = s0; s < p.S && tstart[s] < t1; ++s) {
-      const Seg g = seg_at<kMod, kTK>(p, s, cr);
+      const Seg g = seg_at<kMod != 0, kTK>(p, s, cr);
       const int lt0 = max(tstart[s], t0) - tstart[s];
       const int lt1 = min(tstart[s + 1], t1) - tstart[s];
       uint64_t seen = ~0ull;
-      if (kMod && !s_issuer && lt1 * kTK > g.n_prefix) {
+      if (kMod != 0 && !s_issuer && lt1 * kTK > g.n_prefix) {
         uint64_t lo, hi;
         draft_rows(p, draft_prefetch(p, g.b), lo, hi);
         seen = lane < p.T ? mod_window_row(p.mod, p.T, g.b, lane, g.L, lo) : 0ull;
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
           // the softmax wrote the P residual of this tile too (set before its
           // arrive on p_full; rewritten only after this PV has completed)
           const bool exact = lo_flag[2 * mi + b] != 0;
-          acquire_stage(st, (uint32_t)(it / NS) & 1u, tile_of<kMod>(lt, lt0, lt1), g, seen);
+          acquire_stage(st, (uint32_t)(it / NS) & 1u, (kMod == 2 ? tile_of<true>(p, lt, lt0, lt1) : lt), g, seen);
           issue_pv(mi, b, st, lt == lt0, exact);
         }
         __syncwarp();
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
   // split segments this CTA holds a part of (at most its first and its last)
   int n_split = 0, ms[2] = {0, 0}, mslot[2] = {0, 0}, mnp[2] = {0, 0}, mpart[2] = {0, 0};
   for (int s = s0; s < p.S && tstart[s] < t1; ++s) {
-    const Seg g = seg_at<kMod, kTK>(p, s, cr);
+    const Seg g = seg_at<kMod != 0, kTK>(p, s, cr);
     const int lt0 = max(tstart[s], t0) - tstart[s];
     const int lt1 = min(tstart[s + 1], t1) - tstart[s];
     const int first_cta = owner_cta(tstart[s], cr.total, cr.G);
@@ -392,13 +394,13 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
       draft_rows(p, dpre, tl, th);
       const uint64_t a = __shfl_sync(0xffffffffu, tl, t & 31), c2 = __shfl_sync(0xffffffffu, th, t & 31);
       rmask = t < 32 ? a : c2;
-      if (kMod) rmask = mod_window_row(p.mod, p.T, g.b, t, g.L, rmask);
+      if (kMod != 0) rmask = mod_window_row(p.mod, p.T, g.b, t, g.L, rmask);
     }
     float ns = 0.f, qoff = 0.f;  // score shaping: the row's (negated) slope and offset from L
     int first = 0;               // and the first key it sees
-    if constexpr (kMod) {
+    if constexpr (kMod != 0) {
       const int o = mod_off(p.mod, p.T, g.b, t, g.L);
-      ns = rvalid ? mod_slope(p.mod, hq) : 0.f;
+      ns = kMod == 2 && rvalid ? mod_slope(p.mod, hq) : 0.f;
       qoff = (float)o;
       first = mod_first_slot(p.mod, g.b, o, g.L) - g.base;
     }
@@ -421,9 +423,9 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j) sv[32 + j] = __uint_as_float(w[j]);
       }
-      const int k0 = tile_of<kMod>(lt, lt0, lt1) * kTK;
-      const bool masked = k0 + kTK > g.n_prefix || (kMod && k0 < g.hi);
-      if constexpr (kMod) {
+      const int k0 = (kMod == 2 ? tile_of<true>(p, lt, lt0, lt1) : lt) * kTK;
+      const bool masked = k0 + kTK > g.n_prefix || (kMod != 0 && k0 < g.hi);
+      if constexpr (kMod == 2) {
         if (p.mod.softcap > 0.f) cap_scores<64>(p.mod, sv);
         if (p.mod.slopes != nullptr) {
           const float mul = p.mod.softcap > 0.f ? 1.f : p.mod.out_mul;
@@ -457,7 +459,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
       }
       if (masked) {
         uint64_t vis = tile_vis64(k0, g.n_prefix, g.nkeys, rmask);
-        if (kMod && first > k0) vis &= first - k0 >= 64 ? 0ull : ~0ull << (first - k0);
+        if (kMod != 0 && first > k0) vis &= first - k0 >= 64 ? 0ull : ~0ull << (first - k0);
 #pragma unroll
         for (int j = 0; j < 64; ++j)
           if (!((vis >> j) & 1ull)) sv[j] = -INFINITY;
@@ -652,7 +654,7 @@ size_t attn_tc_smem_required(const AttnParams &p) {
   return p.rows_pad > 128 ? tc_smem_bytes<2, kTcStagesMin>(p) : tc_smem_bytes<1, kTcStagesMin>(p);
 }
 
-template <int NMT, bool kTma, bool kRope, bool kMod, int NS>
+template <int NMT, bool kTma, bool kRope, int kMod, int NS>
 static cudaError_t launch_tc_ns(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
                                 cudaStream_t stream) {
   const size_t smem = tc_smem_bytes<NMT, NS>(p);
@@ -679,17 +681,21 @@ static cudaError_t launch_tc_ns(const AttnParams &p, const CUtensorMap &tmk, con
 template <int NMT, bool kTma>
 static cudaError_t launch_tc_t(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
                                cudaStream_t stream) {
-  if (p.mod.on)
+  if (p.mod.on == 2)
     return tc_deep_ring<NMT>(p)
-               ? launch_tc_ns<NMT, kTma, false, true, kTcStagesMax>(p, tmk, tmv, grid, stream)
-               : launch_tc_ns<NMT, kTma, false, true, kTcStagesMin>(p, tmk, tmv, grid, stream);
+               ? launch_tc_ns<NMT, kTma, false, 2, kTcStagesMax>(p, tmk, tmv, grid, stream)
+               : launch_tc_ns<NMT, kTma, false, 2, kTcStagesMin>(p, tmk, tmv, grid, stream);
+  if (p.mod.on == 1)
+    return tc_deep_ring<NMT>(p)
+               ? launch_tc_ns<NMT, kTma, false, 1, kTcStagesMax>(p, tmk, tmv, grid, stream)
+               : launch_tc_ns<NMT, kTma, false, 1, kTcStagesMin>(p, tmk, tmv, grid, stream);
   if (p.positions != nullptr)
     return tc_deep_ring<NMT>(p)
-               ? launch_tc_ns<NMT, kTma, true, false, kTcStagesMax>(p, tmk, tmv, grid, stream)
-               : launch_tc_ns<NMT, kTma, true, false, kTcStagesMin>(p, tmk, tmv, grid, stream);
+               ? launch_tc_ns<NMT, kTma, true, 0, kTcStagesMax>(p, tmk, tmv, grid, stream)
+               : launch_tc_ns<NMT, kTma, true, 0, kTcStagesMin>(p, tmk, tmv, grid, stream);
   return tc_deep_ring<NMT>(p)
-             ? launch_tc_ns<NMT, kTma, false, false, kTcStagesMax>(p, tmk, tmv, grid, stream)
-             : launch_tc_ns<NMT, kTma, false, false, kTcStagesMin>(p, tmk, tmv, grid, stream);
+             ? launch_tc_ns<NMT, kTma, false, 0, kTcStagesMax>(p, tmk, tmv, grid, stream)
+             : launch_tc_ns<NMT, kTma, false, 0, kTcStagesMin>(p, tmk, tmv, grid, stream);
 }
 
 cudaError_t launch_attention_tc(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,

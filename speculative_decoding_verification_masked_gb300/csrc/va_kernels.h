@@ -12,7 +12,8 @@ namespace va {
 constexpr float kModLog2e = 1.4426950408889634f;
 constexpr int kModMaxWindow = 1 << 23;
 
-// Score shaping of one call (va_mod.cuh); `on` = 0 for the calls without it.
+// Score shaping of one call (va_mod.cuh); `on`: 0 without it, 1 when the scores
+// themselves are plain (window, document start), 2 with a cap or slopes.
 struct ModParams {
   int on;
   float softcap;           // 0: no cap

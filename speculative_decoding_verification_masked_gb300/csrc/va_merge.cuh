@@ -31,12 +31,11 @@ __device__ __forceinline__ int ld_acquire_gpu(const int *ptr) {
 // Exact log-sum-exp merge (LongSpec 2.C) of rows [r0, r1) of a split segment
 // of sequence b, kv-head hkv, whose row r is packed query row row_base + r,
 // from its np parts at slots slot0..slot0+np-1, by one warp of n_warps: LPR
-// lanes per row, each with 128/LPR columns, the lse and output loads of up to
+// lanes per row, each with D/LPR columns, the lse and output loads of up to
 // MB parts in flight at once, a running maximum across batches.
-template <int LPR, int MB>
+template <int LPR, int MB, int D = 128>
 __device__ __forceinline__ void merge_rows_warp(const AttnParams &p, int b, int hkv, int row_base, int slot0, int np,
                                                 int r0, int r1, int warp_id, int n_warps, int lane) {
-  constexpr int D = 128;
   constexpr int RPW = 32 / LPR;      // rows per warp pass
   constexpr int C4 = D / LPR / 4;    // float4 per lane and part
   const int sub = lane / LPR, li = lane % LPR;

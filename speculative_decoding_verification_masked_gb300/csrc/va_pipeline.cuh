@@ -302,11 +302,11 @@ __device__ __forceinline__ Seg seg_at(const AttnParams &p, int s, const CtaRange
 }
 
 // Tile of the lt-th step over the tiles [lt0, lt1) of a segment part.  With
-// score shaping the nearest keys come first: a distance bias grows towards
-// them, so the softmax reference would move at every tile the other way round.
+// slopes the nearest keys come first: the bias grows towards them, and the
+// softmax reference would move at every tile the other way round.
 template <bool kMod>
-__device__ __forceinline__ int tile_of(int lt, int lt0, int lt1) {
-  return kMod ? lt0 + lt1 - 1 - lt : lt;
+__device__ __forceinline__ int tile_of(const AttnParams &p, int lt, int lt0, int lt1) {
+  return kMod && p.mod.slopes != nullptr ? lt0 + lt1 - 1 - lt : lt;
 }
 
 // Tiles of TK keys per segment, their exclusive scan into tstart[0..S], and
@@ -376,7 +376,8 @@ __device__ __forceinline__ CtaRange plan_cta(const AttnParams &p, int *tstart, i
 // cp.async gather only; -1 = chosen by use_tma): a kernel built for one way
 // carries none of the other's code, which measurably slows the warps that
 // share the kernel.
-template <typename Tin, int D, int NS, int TK = kTK, int MAXF = NS, int NPW = 1, int PATH = -1, bool kMod = false>
+template <typename Tin, int D, int NS, int TK = kTK, int MAXF = NS, int NPW = 1, int PATH = -1, bool kMod = false,
+          int VOFF = StageGeom<Tin, D, TK>::kTileBytes>
 __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensorMap *tmk, const CUtensorMap *tmv,
                                              const int *tstart, const CtaRange &cr, uint8_t *stages,
                                              uint64_t *full, uint64_t *empty, volatile int *abort_flag,
@@ -408,7 +409,7 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
   };
   auto first_tile = [&](int s) {  // the tile this CTA's part of segment s starts with
     const int lt0 = max(tstart[s], cr.t0) - tstart[s];
-    return tile_of<kMod>(lt0, lt0, min(tstart[s + 1], cr.t1) - tstart[s]);
+    return tile_of<kMod>(p, lt0, lt0, min(tstart[s + 1], cr.t1) - tstart[s]);
   };
   if (!use_tma && cr.s0 < p.S && tstart[cr.s0] < cr.t1)
     load_rows(seg_at<kMod, TK>(p, cr.s0, cr), first_tile(cr.s0), rows);
@@ -430,9 +431,9 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
         ok = false;
       }
       if (!ok) continue;
-      uint8_t *kdst = stages + st * C::kStageBytes;
-      uint8_t *vdst = kdst + C::kTileBytes;
-      const int k0 = tile_of<kMod>(lt, lt0, lt1) * TK;
+      uint8_t *kdst = stages + st * (VOFF + C::kTileBytes);  // (VOFF: offset of the V tile in a stage)
+      uint8_t *vdst = kdst + VOFF;
+      const int k0 = tile_of<kMod>(p, lt, lt0, lt1) * TK;
       if (use_tma) {
         // TMA boxes of BR rows x one kv-head x 128 bytes of the head dimension.
         // Dense: BR = 64 consecutive tokens; rows past the segment end arrive
@@ -473,7 +474,7 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
         const Tin *nrows[kRowSets];
         bool has_next = true;
         if (lt + 1 < lt1) {
-          load_rows(g, tile_of<kMod>(lt + 1, lt0, lt1), nrows);
+          load_rows(g, tile_of<kMod>(p, lt + 1, lt0, lt1), nrows);
         } else if (s + 1 < p.S && tstart[s + 1] < cr.t1) {
           load_rows(seg_at<kMod, TK>(p, s + 1, cr), first_tile(s + 1), nrows);
         } else {

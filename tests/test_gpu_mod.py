@@ -43,6 +43,9 @@ FORMS = {
     "bf16 d128 320 rows pages of 64": ("bf16", 128, 40, 8, 1, 64),
     "bf16 d128 132 rows pages of 1": ("bf16", 128, 33, 4, 1, 1),
     "bf16 d64 12 rows": ("bf16", 64, 3, 8, 2, 0),
+    "bf16 d64 20 rows pages of 2": ("bf16", 64, 5, 4, 1, 2),
+    "bf16 d64 64 rows pages of 16": ("bf16", 64, 16, 4, 1, 16),
+    "bf16 d64 33 rows pages of 1": ("bf16", 64, 11, 3, 1, 1),
     "bf16 d64 80 rows pages of 8": ("bf16", 64, 20, 4, 1, 8),
     "fp32 d64 32 rows": ("fp32", 64, 8, 4, 1, 0),
     "fp32 d64 72 rows pages of 256": ("fp32", 64, 9, 8, 1, 256),
@@ -79,17 +82,17 @@ def test_no_rule_is_the_unshaped_call():
     assert (lse - ref_lse).abs().max() <= 1e-5
 
 
-@pytest.mark.parametrize("T,Hq,Hkv", [(8, 8, 2), (64, 4, 1)])
-def test_split_over_many_ctas(T, Hq, Hkv):
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(8, 8, 2, 128), (64, 4, 1, 128), (3, 8, 2, 64), (5, 8, 2, 64), (16, 8, 2, 64)])
+def test_split_over_many_ctas(T, Hq, Hkv, D):
     """A prefix long enough that one segment is cut over every CTA: partial
     results at very different biases are merged."""
-    c = shaped.make(5, [9000], T, Hq, Hkv, draft="tree", softcap=30.0, slopes=True, gain=2.0)
+    c = shaped.make(5, [9000], T, Hq, Hkv, D, draft="tree", softcap=30.0, slopes=True, gain=2.0)
     out, lse = shaped.run_attend(va, c)
     _check(c, out, lse)
 
 
 @pytest.mark.parametrize("T,Hq,Hkv,D,page", [(8, 8, 2, 128, 0), (8, 8, 2, 128, 16), (6, 8, 2, 128, 2),
-                                              (64, 4, 1, 128, 0), (5, 4, 1, 64, 8)])
+                                              (64, 4, 1, 128, 0), (5, 4, 1, 64, 8), (9, 6, 1, 64, 0), (24, 4, 1, 64, 0)])
 def test_hidden_keys_may_hold_anything(T, Hq, Hkv, D, page):
     """NaN and infinities in every K and V row that no row sees, and -1 in the
     page entries below the lowest visible slot."""
