@@ -13,6 +13,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "va_common.cuh"
 #include "va_mod.cuh"
 #include "va_pipeline.cuh"
@@ -439,6 +441,17 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 
     float *w = p.weight + ((size_t)g.b * p.Hkv + g.h) * p.stride + g.base;
     const int n_old = g.L - g.base;  // keys of the prefix
+    const float window = kMod && p.mod.window > 0 ? (float)p.mod.window : INFINITY;
+    auto total_of = [&](int key) {
+      return (p.row0 > 0 ? key < g.nkeys : key < n_old && p.decay != 0.f) ? w[key] : 0.f;
+    };
+    // S has been read: the MMA warp may write the buffer again
+    auto release = [&]() {
+      tc_fence_before();
+      mbar_arrive(s_empty + wg);
+    };
+    bool have_next = false;
+    float next_old = 0.f;
     for (int lt = lt0; lt < lt1; ++lt) {
       const int key = lt * TK + key_l;
       if (!live(g, lt)) {
@@ -449,49 +462,82 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       const uint32_t ph = (uint32_t)(jt >> 1) & 1u;
       ++jt;
       if (!mine) continue;
-      // what the total keeps (row0 > 0: a later pass adds to the earlier ones')
-      float old = 0.f;
-      if (p.row0 > 0 ? key < g.nkeys : key < n_old && p.decay != 0.f) old = w[key];
+      // what the total keeps (row0 > 0: a later pass adds to the earlier ones'),
+      // loaded while this warpgroup works on its tile before
+      const float old = have_next ? next_old : total_of(key);
+      have_next = lt + 2 < lt1;
+      next_old = have_next ? total_of(key + 2 * TK) : 0.f;
       const bool masked = lt * TK < g.hi || lt * TK + TK > n_old;
-      wait_ok(s_full + wg, ph);
-      tc_fence_after();
-      float acc0 = 0.f, acc1 = 0.f;
       const float koff = (float)(key - n_old);
-      const float window = kMod && p.mod.window > 0 ? (float)p.mod.window : INFINITY;
       const bool there = key >= g.lo && key < g.nkeys;
-      for (int c0 = 0; c0 < NP; c0 += 32) {
-        uint32_t u[32];
-        tmem_ld32(tS + c0, u);
-        tmem_ld_wait();
-        if (c0 + 32 >= NP) {
-          tc_fence_before();
-          mbar_arrive(s_empty + wg);
-        }
+      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      // adds the terms of 32 rows, S columns c0 ..; `edge`: rows that do not see the key are left out
+      auto rows32 = [&](const uint32_t (&u)[32], int c0, auto edge) {
         float x[32];
 #pragma unroll
         for (int r = 0; r < 32; ++r) x[r] = __uint_as_float(u[r]);
         if (kMod && p.mod.softcap > 0.f) cap_scores<32>(p.mod, x);
         const float mul = kMod && p.mod.softcap > 0.f ? 1.f : p.mod.out_mul;
+        if (kMod && p.mod.slopes != nullptr) {
 #pragma unroll
-        for (int r = 0; r < 32; r += 2) {
-          const float2 nl = *reinterpret_cast<const float2 *>(s_nlse + c0 + r);
-          float2 d = fma2(make_float2(x[r], x[r + 1]), make_float2(mul, mul), nl);
-          if (kMod && p.mod.slopes != nullptr) {
+          for (int r = 0; r < 32; r += 2) {
             const float2 ns = *reinterpret_cast<const float2 *>(s_slope + c0 + r);
             const float2 tk = *reinterpret_cast<const float2 *>(s_tok + c0 + r);
-            d.x = fmaf(ns.x, fabsf(tk.x - koff), d.x);
-            d.y = fmaf(ns.y, fabsf(tk.y - koff), d.y);
+            x[r] = fmaf(ns.x, fabsf(tk.x - koff), x[r] * mul);
+            x[r + 1] = fmaf(ns.y, fabsf(tk.y - koff), x[r + 1] * mul);
           }
-          if (masked) {
-            const float2 tk = *reinterpret_cast<const float2 *>(s_tok + c0 + r);
-            if (!(there && koff <= tk.x && tk.x - koff < window)) d.x = -INFINITY;
-            if (!(there && koff <= tk.y && tk.y - koff < window)) d.y = -INFINITY;
+        }
+        const float mul2nd = kMod && p.mod.slopes != nullptr ? 1.f : mul;
+#pragma unroll
+        for (int r = 0; r < 32; r += 4) {
+          const float4 nl = *reinterpret_cast<const float4 *>(s_nlse + c0 + r);
+          float2 d[2] = {fma2(make_float2(x[r], x[r + 1]), make_float2(mul2nd, mul2nd), make_float2(nl.x, nl.y)),
+                         fma2(make_float2(x[r + 2], x[r + 3]), make_float2(mul2nd, mul2nd), make_float2(nl.z, nl.w))};
+          if constexpr (decltype(edge)::value) {
+            const float4 tk = *reinterpret_cast<const float4 *>(s_tok + c0 + r);
+            if (!(there && koff <= tk.x && tk.x - koff < window)) d[0].x = -INFINITY;
+            if (!(there && koff <= tk.y && tk.y - koff < window)) d[0].y = -INFINITY;
+            if (!(there && koff <= tk.z && tk.z - koff < window)) d[1].x = -INFINITY;
+            if (!(there && koff <= tk.w && tk.w - koff < window)) d[1].y = -INFINITY;
           }
-          acc0 += ex2_approx(d.x * kModLog2e);
-          acc1 += ex2_approx(d.y * kModLog2e);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            // natural units so far: s - lse is small, and so exact, where the weight matters
+            d[q] = mul2(d[q], make_float2(kModLog2e, kModLog2e));
+            acc[q] = add2(acc[q], make_float2(ex2_approx(d[q].x), ex2_approx(d[q].y)));
+          }
+        }
+      };
+      wait_ok(s_full + wg, ph);
+      tc_fence_after();
+      uint32_t ua[32];
+      tmem_ld32(tS, ua);
+      if (masked || kMod) {  // (the cap and the bias leave no registers to load ahead)
+        for (int c0 = 0; c0 < NP; c0 += 32) {
+          if (c0 > 0) tmem_ld32(tS + c0, ua);
+          tmem_ld_wait32(ua);
+          if (c0 + 32 >= NP) release();
+          if (masked) rows32(ua, c0, std::true_type());
+          else if constexpr (kMod) rows32(ua, c0, std::false_type());
+        }
+      } else {
+        // the next columns are on their way from TMEM while these are summed
+        uint32_t ub[32];
+        tmem_ld_wait32(ua);
+        for (int c0 = 0; c0 < NP; c0 += 64) {
+          const bool two = c0 + 32 < NP, more = c0 + 64 < NP;
+          if (two) tmem_ld32(tS + c0 + 32, ub);
+          else release();
+          rows32(ua, c0, std::false_type());
+          if (!two) break;
+          tmem_ld_wait32(ub);
+          if (more) tmem_ld32(tS + c0 + 64, ua);
+          else release();
+          rows32(ub, c0 + 32, std::false_type());
+          if (more) tmem_ld_wait32(ua);
         }
       }
-      const float sum = acc0 + acc1;
+      const float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
       if (ok && key < g.nkeys) w[key] = p.row0 > 0 ? old + sum : fmaf(p.decay, old, sum);
     }
   }
