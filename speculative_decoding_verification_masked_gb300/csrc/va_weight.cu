@@ -151,15 +151,20 @@ __global__ void __launch_bounds__(128) weight_simt_kernel(const WeightParams p) 
 // Bound by HBM (K once) while a kv-head has few rows; with 256 rows a tile's
 // 32,768 exponentials take about as long as its 32 KB.
 //
-// Roles (10 warps, one CTA per SM, a contiguous share of all 128-key tiles each):
+// Roles (11 warps, one CTA per SM, a contiguous share of all 128-key tiles each):
 //   warps 0-3 / 4-7  the tiles of even / odd number: S from TMEM, exponentials,
 //                    row sum, the total's update; all eight stage Q and the
 //                    rows' lse when a kv-head begins
-//   warp 8           producer      warp 9  MMA issuer, owns TMEM (two S buffers)
+//   warps 8, 10      producers: a warp issues a TMA box every ~110 cycles, so the
+//                    sixteen of a tile of 16-row pages took one warp longer than
+//                    HBM takes for the tile (64 sequences: 150 us with one, 125
+//                    with two, 134 with three); boxes of 64 rows are left to one
+//                    (109 against 111 us), gathers take both
+//   warp 9           MMA issuer, owns TMEM (two S buffers)
 constexpr int kWtTile = 128;
 constexpr int kWtRows = 256;  // rows of one pass (N of the MMA)
 constexpr int kWtMaxStages = 6;
-constexpr int kWtThreads = 320;
+constexpr int kWtThreads = 352;
 
 struct WtSeg {
   int b, h;
@@ -201,7 +206,7 @@ struct WtSmem {  // offsets after the Q rows and the stages
   static constexpr int kPlan = kTok + kWtRows * 4;     // int [S + 1]
 };
 
-template <int D, bool kTma, bool kMod>
+template <int D, bool kTma, bool kMod, int kProducers>
 __global__ void __launch_bounds__(kWtThreads, 1)
     weight_tc_kernel(const WeightParams p, const __grid_constant__ CUtensorMap tmk, int RQ, int NS) {
   constexpr int TK = kWtTile;
@@ -228,7 +233,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full + i, kTma ? 1 : 32);
+      mbar_init(full + i, kTma ? kProducers : 32 * kProducers);
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -269,15 +274,28 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     }
   };
 
-  if (warp == kProducer) {
+  if (warp == kProducer || warp > kMma) {
+    const int pw = warp == kProducer ? 0 : warp - kMma;
+    if (pw >= kProducers) return;
     const uint64_t policy = l2_evict_first_policy();
     if (kTma && lane == 0) prefetch_tmap(&tmk);
     Ring r;
     int issued = 0;
+    const bool paged = p.page_table != nullptr;
+    // page entry of this lane's box of tile lt (TMA): fetched one tile ahead, or
+    // its latency would be the time of a tile
+    auto box_page = [&](const WtSeg &g, int lt) {
+      const int k = lt * TK + lane * p.tma_box;
+      if (!paged || lane >= TK / p.tma_box || k >= g.nkeys) return 0;
+      return __ldg(p.page_table + (size_t)g.b * p.max_pages + ((g.base + k) >> p.page_shift));
+    };
     for (int s = s0; s < S && tstart[s] < t1; ++s) {
       const WtSeg g = wt_seg(p, s, false);
       const int lt0 = max(tstart[s], t0) - tstart[s], lt1 = min(tstart[s + 1], t1) - tstart[s];
+      int page_next = kTma && lt0 < lt1 ? box_page(g, lt0) : 0;
       for (int lt = lt0; lt < lt1; ++lt) {
+        int page = page_next;
+        if (kTma && lt + 1 < lt1) page_next = box_page(g, lt + 1);
         if (!live(g, lt)) continue;
         wait_ok(empty + r.st, r.ph ^ 1u);
         if (!ok) continue;
@@ -285,15 +303,16 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         const int k0 = lt * TK, slot0 = g.base + k0;
         if constexpr (kTma) {
           const int BR = p.tma_box, nbox = TK / BR;
-          const bool paged = p.page_table != nullptr;
           const int nb = paged ? min(nbox, (g.nkeys - k0 + BR - 1) / BR) : nbox;
-          if (lane == 0) mbar_arrive_expect_tx(full + r.st, (uint32_t)(nb * BR * 128 * kHalves));
+          // two producers take a 128-byte column each (D 64: every other box)
+          constexpr bool two = kProducers == 2;
+          const int mine = !two ? nb * kHalves : kHalves == 2 ? nb : (nb + 1 - pw) / 2;
+          if (lane == 0) mbar_arrive_expect_tx(full + r.st, (uint32_t)(mine * BR * 128));
           __syncwarp();
-          if (lane < nb) {
+          if (lane < nb && (kHalves == 2 || !two || (lane & 1) == pw)) {
             const int slot = slot0 + lane * BR;
             int row = g.b * p.len_cap + slot;
             if (paged) {
-              int page = __ldg(p.page_table + (size_t)g.b * p.max_pages + (slot >> p.page_shift));
               if (page < 0 || page >= p.num_pages) {
                 if (k0 + (lane + 1) * BR > g.lo) record_status(p.status, VA_ERR_DEVICE_BOUNDS);
                 page = 0;
@@ -301,14 +320,16 @@ __global__ void __launch_bounds__(kWtThreads, 1)
               row = (page << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
             }
 #pragma unroll
-            for (int c = 0; c < kHalves; ++c)
+            for (int i = 0; i < (kHalves == 2 && two ? 1 : kHalves); ++i) {
+              const int c = kHalves == 2 && two ? pw : i;
               tma_load_3d(dst + c * TK * 128 + lane * BR * 128, &tmk, c * 64, g.h, row, full + r.st, policy);
+            }
           }
         } else {
           // pages below 8 rows: lane l resolves rows l + 32 j, 16-byte copies
           constexpr int CPR = D / 8, RPP = 32 / CPR;
           const int cc = lane % CPR, rsub = lane / CPR;
-          for (int j = 0; j < TK / 32; ++j) {
+          for (int j = pw; j < TK / 32; j += kProducers) {
             const int k = k0 + lane + 32 * j;
             const __nv_bfloat16 *row = nullptr;
             if (k < g.nkeys) row = weight_key<__nv_bfloat16>(p, g.b, g.h, g.base + k, k >= g.lo);
@@ -545,7 +566,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   named_bar_sync(kBarEnd, kSoft + 32);
 }
 
-template <int D, bool kTma, bool kMod>
+template <int D, bool kTma, bool kMod, int kProducers>
 static cudaError_t launch_weight_tc(const WeightParams &p, const CUtensorMap &tmk, int grid, cudaStream_t stream) {
   const int rows = p.Hq / p.Hkv * p.T - p.row0;
   const int RQ = rows >= kWtRows ? kWtRows : (rows + 31) & ~31;
@@ -554,7 +575,7 @@ static cudaError_t launch_weight_tc(const WeightParams &p, const CUtensorMap &tm
   int NS = (int)((232448 - fixed) / stage);
   if (NS > kWtMaxStages) NS = kWtMaxStages;
   const size_t smem = fixed + NS * stage;
-  auto kern = weight_tc_kernel<D, kTma, kMod>;
+  auto kern = weight_tc_kernel<D, kTma, kMod, kProducers>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   kern<<<grid, kWtThreads, smem, stream>>>(p, tmk, RQ, NS);
@@ -563,11 +584,14 @@ static cudaError_t launch_weight_tc(const WeightParams &p, const CUtensorMap &tm
 
 template <int D>
 static cudaError_t launch_weight_bf16(const WeightParams &p, const CUtensorMap &tmk, int grid, cudaStream_t stream) {
+  if (p.tma_box == 64)
+    return p.mod.on ? launch_weight_tc<D, true, true, 1>(p, tmk, grid, stream)
+                    : launch_weight_tc<D, true, false, 1>(p, tmk, grid, stream);
   if (p.tma_box > 0)
-    return p.mod.on ? launch_weight_tc<D, true, true>(p, tmk, grid, stream)
-                    : launch_weight_tc<D, true, false>(p, tmk, grid, stream);
-  return p.mod.on ? launch_weight_tc<D, false, true>(p, tmk, grid, stream)
-                  : launch_weight_tc<D, false, false>(p, tmk, grid, stream);
+    return p.mod.on ? launch_weight_tc<D, true, true, 2>(p, tmk, grid, stream)
+                    : launch_weight_tc<D, true, false, 2>(p, tmk, grid, stream);
+  return p.mod.on ? launch_weight_tc<D, false, true, 2>(p, tmk, grid, stream)
+                  : launch_weight_tc<D, false, false, 2>(p, tmk, grid, stream);
 }
 
 // fp32: one thread per key (no TF32).  bf16: one pass of the tensor-core kernel
