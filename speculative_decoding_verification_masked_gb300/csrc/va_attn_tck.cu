@@ -4,10 +4,14 @@
 
 namespace va {
 
-cudaError_t launch_attention_tck_shaped(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
-                                        cudaStream_t stream);
-cudaError_t launch_attention_tck_d64(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
-                                     cudaStream_t stream);
+cudaError_t launch_attention_tck_d128_range(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
+                                            cudaStream_t stream);
+cudaError_t launch_attention_tck_d128_score(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
+                                            cudaStream_t stream);
+cudaError_t launch_attention_tck_d64_range(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
+                                           cudaStream_t stream);
+cudaError_t launch_attention_tck_d64_score(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
+                                           cudaStream_t stream);
 
 size_t attn_tck_smem_required(const AttnParams &p) {
   if (p.D == 64)
@@ -21,8 +25,11 @@ size_t attn_tck_smem_required(const AttnParams &p) {
 
 cudaError_t launch_attention_tck(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
                                  cudaStream_t stream) {
-  if (p.D == 64) return launch_attention_tck_d64(p, tmk, tmv, grid, stream);
-  if (p.mod.on != 0) return launch_attention_tck_shaped(p, tmk, tmv, grid, stream);
+  if (p.mod.on != 0) {
+    auto launch = p.D == 64 ? (p.mod.on == 1 ? launch_attention_tck_d64_range : launch_attention_tck_d64_score)
+                            : (p.mod.on == 1 ? launch_attention_tck_d128_range : launch_attention_tck_d128_score);
+    return launch(p, tmk, tmv, grid, stream);
+  }
   return p.positions != nullptr ? launch_tck<128, true, 0>(p, tmk, tmv, grid, stream)
                                 : launch_tck<128, false, 0>(p, tmk, tmv, grid, stream);
 }

@@ -60,9 +60,11 @@ constexpr int kTkKeys = 128;  // keys per tile
 // producer warp that shares the cp.async gather of the paged / sparse layouts
 // (one warp's gather is limited by the copies it can keep in flight).  Seven
 // warps leave at most two per SM sub-partition, so 255 registers stay available.
-template <int NR, bool kTma>
+// kTma: 0 gathers, 1 TMA boxes, 2 TMA boxes issued by two producer warps (score
+// shaping, pages below 64 rows).
+template <int NR, int kTma>
 struct TkCfg {
-  static constexpr int kProducers = !kTma && NR <= 32 ? 2 : 1;
+  static constexpr int kProducers = kTma == 2 || (kTma == 0 && NR <= 32) ? 2 : 1;
   static constexpr int kThreads = (5 + kProducers) * 32;
 };
 
@@ -218,7 +220,7 @@ __device__ __forceinline__ void tmem_scale_cols(uint32_t taddr, const float *a) 
 
 // kMod: 0 without score shaping, 1 with a window or document start only (the
 // scores are the plain ones), 2 with a cap or slopes.
-template <int D, int NR, bool kTma, bool kRope, int kMod>
+template <int D, int NR, int kTma, bool kRope, int kMod>
 __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
     verify_attn_tck_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
                            const __grid_constant__ CUtensorMap tmv) {
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
   int *tstart = reinterpret_cast<int *>(smem + SM::kRopeOff + (kRope ? rope_table_bytes(p) : kMod != 0 ? SM::kModBytes : 0));
   float2 *mod_row = reinterpret_cast<float2 *>(smem + SM::kRopeOff);       // (slope, offset) of row r
   int *mod_first = reinterpret_cast<int *>(smem + SM::kRopeOff + 64 * 8);  // first visible key of token t
-  constexpr bool use_tma = kTma;  // tiles by TMA boxes (dense, paged), else cp.async gathers
+  constexpr bool use_tma = kTma != 0;  // tiles by TMA boxes (dense, paged), else cp.async gathers
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full + i, use_tma ? 1 : 32 * TkCfg<NR, kTma>::kProducers);
+      mbar_init(full + i, (use_tma ? 1 : 32) * TkCfg<NR, kTma>::kProducers);
       mbar_init(empty + i, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
 
   if (warp == kProducerWarp || warp > kMmaWarp) {
     bool pok = true;
-    produce_tiles<__nv_bfloat16, D, NS, TK, NS - 1, TkCfg<NR, kTma>::kProducers, kTma ? 1 : 0, kMod != 0, SM::kVOff>(
+    produce_tiles<__nv_bfloat16, D, NS, TK, NS - 1, TkCfg<NR, kTma>::kProducers, kTma, kMod != 0, SM::kVOff>(
         p, &tmk, &tmv, tstart, cr, stages, full, empty, abort_flag, use_tma, pok,
         warp == kProducerWarp ? 0 : warp - kMmaWarp);
     return;
@@ -929,7 +931,7 @@ static size_t tck_smem_bytes(const AttnParams &p) {
 
 // Launch of one instance.  Each translation unit that includes this file builds
 // the instances of the launchers it defines (they take long to compile).
-template <int D, int NR, bool kTma, bool kRope, int kMod>
+template <int D, int NR, int kTma, bool kRope, int kMod>
 static cudaError_t launch_tck_t(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
                                 cudaStream_t stream) {
   const size_t smem = tck_smem_bytes<D, NR>(p);
@@ -950,18 +952,20 @@ static cudaError_t launch_tck_t(const AttnParams &p, const CUtensorMap &tmk, con
   return cudaLaunchKernelEx(&cfg, kern, p, tmk, tmv);
 }
 
+template <int D, int NR, bool kRope, int kMod>
+static cudaError_t launch_tck_nr(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
+                                 cudaStream_t stream) {
+  if (p.tma_box == 0) return launch_tck_t<D, NR, 0, kRope, kMod>(p, tmk, tmv, grid, stream);
+  if (kMod == 0 || p.tma_box == 64) return launch_tck_t<D, NR, 1, kRope, kMod>(p, tmk, tmv, grid, stream);
+  return launch_tck_t<D, NR, kMod == 0 ? 1 : 2, kRope, kMod>(p, tmk, tmv, grid, stream);
+}
+
 template <int D, bool kRope, int kMod>
 static cudaError_t launch_tck(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
                               cudaStream_t stream) {
-  const bool tma = p.tma_box > 0;
-  if (p.rows_pad <= 16)
-    return tma ? launch_tck_t<D, 16, true, kRope, kMod>(p, tmk, tmv, grid, stream)
-               : launch_tck_t<D, 16, false, kRope, kMod>(p, tmk, tmv, grid, stream);
-  if (p.rows_pad <= 32)
-    return tma ? launch_tck_t<D, 32, true, kRope, kMod>(p, tmk, tmv, grid, stream)
-               : launch_tck_t<D, 32, false, kRope, kMod>(p, tmk, tmv, grid, stream);
-  return tma ? launch_tck_t<D, 64, true, kRope, kMod>(p, tmk, tmv, grid, stream)
-             : launch_tck_t<D, 64, false, kRope, kMod>(p, tmk, tmv, grid, stream);
+  return p.rows_pad <= 16   ? launch_tck_nr<D, 16, kRope, kMod>(p, tmk, tmv, grid, stream)
+         : p.rows_pad <= 32 ? launch_tck_nr<D, 32, kRope, kMod>(p, tmk, tmv, grid, stream)
+                            : launch_tck_nr<D, 64, kRope, kMod>(p, tmk, tmv, grid, stream);
 }
 
 }  // namespace va

@@ -372,7 +372,8 @@ __device__ __forceinline__ CtaRange plan_cta(const AttnParams &p, int *tstart, i
 //
 // NPW warps may share the gather (warp pw takes the row sets j = pw mod NPW,
 // and full[] then counts 32 * NPW arrivals); only warp 0 issues TMA boxes.
-// PATH fixes the way tiles arrive at compile time (1 = TMA boxes only, 0 =
+// PATH fixes the way tiles arrive at compile time (1 = TMA boxes only, 2 = TMA
+// boxes by two warps, K and V each, full[] then counting two arrivals, 0 =
 // cp.async gather only; -1 = chosen by use_tma): a kernel built for one way
 // carries none of the other's code, which measurably slows the warps that
 // share the kernel.
@@ -386,14 +387,17 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
   constexpr int kRowSets = TK / 32; // key rows per lane in the gather
   static_assert(kRowSets % NPW == 0, "row sets split evenly over the producer warps");
   const int lane = threadIdx.x & 31;
-  if constexpr (PATH >= 0) use_tma = PATH == 1;
-  if (use_tma && pw != 0) return 0;
+  if constexpr (PATH >= 0) use_tma = PATH >= 1;
+  if (use_tma && pw != 0 && PATH != 2) return 0;
+  // (a warp issues a TMA box every ~110 cycles: with boxes of 16 rows that takes
+  // longer than HBM takes for the tile)
+  const bool do_k = PATH != 2 || pw == 0, do_v = PATH != 2 || pw == 1;
   const uint64_t policy = l2_evict_first_policy();
   const Tin *kbase = static_cast<const Tin *>(p.k);
   const uintptr_t vdelta = reinterpret_cast<uintptr_t>(p.v) - reinterpret_cast<uintptr_t>(p.k);
   if (use_tma && lane == 0) {
-    prefetch_tmap(tmk);
-    prefetch_tmap(tmv);
+    if (do_k) prefetch_tmap(tmk);
+    if (do_v) prefetch_tmap(tmv);
   }
   // gather: the row addresses of the tile being issued; those of the next
   // tile are loaded before this tile's copies are issued, so their latency
@@ -418,7 +422,16 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
     const Seg g = seg_at<kMod, TK>(p, s, cr);
     const int lt0 = max(tstart[s], cr.t0) - tstart[s];
     const int lt1 = min(tstart[s + 1], cr.t1) - tstart[s];
+    // (PATH 2) the page entry of this lane's box, fetched one tile ahead
+    auto box_page = [&](int lt) {
+      const int k = tile_of<kMod>(p, lt, lt0, lt1) * TK + lane * p.tma_box;
+      if (p.layout != VA_LAYOUT_PAGED || lt >= lt1 || lane >= TK / p.tma_box || k >= g.nkeys) return 0;
+      return __ldg(p.page_table + (size_t)g.b * p.max_pages + (((kMod ? g.base : 0) + k) >> p.page_shift));
+    };
+    int page_next = PATH == 2 ? box_page(lt0) : 0;
     for (int lt = lt0; lt < lt1; ++lt, ++it) {
+      const int page_now = page_next;
+      if (PATH == 2) page_next = box_page(lt + 1);
       const int st = it % NS;
       const uint32_t ph = (uint32_t)(it / NS) & 1u;
       role_wait(empty + st, ph ^ 1u, ok, abort_flag, p.wait_ns, p.status);
@@ -445,13 +458,15 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
         const int nbox = TK / BR;  // boxes per 128-byte column (at most 16)
         const bool paged = p.layout == VA_LAYOUT_PAGED;
         const int nb = paged ? min(nbox, (g.nkeys - k0 + BR - 1) / BR) : nbox;
-        if (lane == 0) mbar_arrive_expect_tx(full + st, (uint32_t)(nb * BR * 128 * C::kHalves * 2));
+        if (lane == 0)
+          mbar_arrive_expect_tx(full + st, (uint32_t)(nb * BR * 128 * C::kHalves * (PATH == 2 ? 1 : 2)));
         __syncwarp();
         if (lane < nb) {
           const int slot = (kMod ? g.base : 0) + k0 + lane * BR;
           int row;
           if (paged) {
-            int page = __ldg(p.page_table + (size_t)g.b * p.max_pages + (slot >> p.page_shift));
+            int page = PATH == 2 ? page_now
+                                 : __ldg(p.page_table + (size_t)g.b * p.max_pages + (slot >> p.page_shift));
             if (page < 0 || page >= p.num_pages) {
               if (!kMod || k0 + (lane + 1) * BR > g.lo) record_status(p.status, VA_ERR_DEVICE_BOUNDS);
               page = 0;
@@ -463,8 +478,10 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
           const int off = lane * BR * 128;
 #pragma unroll
           for (int h = 0; h < C::kHalves; ++h) {
-            tma_load_3d(kdst + h * TK * 128 + off, tmk, h * (128 / (int)sizeof(Tin)), g.hkv, row, full + st, policy);
-            tma_load_3d(vdst + h * TK * 128 + off, tmv, h * (128 / (int)sizeof(Tin)), g.hkv, row, full + st, policy);
+            if (do_k)
+              tma_load_3d(kdst + h * TK * 128 + off, tmk, h * (128 / (int)sizeof(Tin)), g.hkv, row, full + st, policy);
+            if (do_v)
+              tma_load_3d(vdst + h * TK * 128 + off, tmv, h * (128 / (int)sizeof(Tin)), g.hkv, row, full + st, policy);
           }
         }
       } else {
