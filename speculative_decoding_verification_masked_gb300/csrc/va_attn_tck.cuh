@@ -62,10 +62,14 @@ constexpr int kTkKeys = 128;  // keys per tile
 // warps leave at most two per SM sub-partition, so 255 registers stay available.
 // kTma: 0 gathers, 1 TMA boxes, 2 TMA boxes issued by two producer warps (score
 // shaping, pages below 64 rows).
-template <int NR, int kTma>
+// Two softmax warpgroups share a tile's rows (score shaping, more than 16 rows):
+// each keeps half of them, so the two are two independent halves of the softmax
+// on the same S, P and O buffers, and a tile takes a thread half the work.
+template <int NR, int kTma, int kMod>
 struct TkCfg {
   static constexpr int kProducers = kTma == 2 || (kTma == 0 && NR <= 32) ? 2 : 1;
-  static constexpr int kThreads = (5 + kProducers) * 32;
+  static constexpr int kGroups = kMod != 0 && NR >= 32 ? 2 : 1;  // softmax warpgroups
+  static constexpr int kThreads = (4 * kGroups + 1 + kProducers) * 32;
 };
 
 // D = 64 (score shaping only): a stage is half the size, so the ring is twice as
@@ -221,7 +225,7 @@ __device__ __forceinline__ void tmem_scale_cols(uint32_t taddr, const float *a) 
 // kMod: 0 without score shaping, 1 with a window or document start only (the
 // scores are the plain ones), 2 with a cap or slopes.
 template <int D, int NR, int kTma, bool kRope, int kMod>
-__global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
+__global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
     verify_attn_tck_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
                            const __grid_constant__ CUtensorMap tmv) {
   using SM = TkSmem<D, NR>;
@@ -229,13 +233,16 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
   constexpr int TK = kTkKeys;
   constexpr int NS = SM::kStages;
   constexpr int NC = SM::kNC;
-  constexpr int kSoft = 128;
-  // NR <= 32: the row sums l are kept by the softmax threads (each over its own
+  using Cfg = TkCfg<NR, kTma, kMod>;
+  constexpr int WG = Cfg::kGroups;
+  constexpr int NW = NR / WG;  // rows of a softmax thread
+  constexpr int kSoft = 128 * WG;
+  // up to 32 rows a thread: the row sums l are kept by the softmax threads (each over its own
   // keys, reduced once per segment part) instead of a ones-operand MMA per tile
-  constexpr bool kRegL = NR <= 32;
+  constexpr bool kRegL = NW <= 32;
   static_assert(!(kRope && kMod != 0), "the two share their shared-memory table");
-  constexpr int kProducerWarp = 4, kMmaWarp = 5;
-  constexpr int kBarQ = 1, kBarRed = 2, kBarSoft = 3, kBarEnd = 4;
+  constexpr int kProducerWarp = 4 * WG, kMmaWarp = 4 * WG + 1;
+  constexpr int kBarQ = 1, kBarSoft = 3, kBarEnd = 4, kBarRed0 = 5;  // kBarRed0 + softmax warpgroup
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t *stages = smem;
@@ -266,7 +273,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full + i, (use_tma ? 1 : 32) * TkCfg<NR, kTma>::kProducers);
+      mbar_init(full + i, (use_tma ? 1 : 32) * Cfg::kProducers);
       mbar_init(empty + i, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -286,7 +293,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
 
   if (warp == kProducerWarp || warp > kMmaWarp) {
     bool pok = true;
-    produce_tiles<__nv_bfloat16, D, NS, TK, NS - 1, TkCfg<NR, kTma>::kProducers, kTma, kMod != 0, SM::kVOff>(
+    produce_tiles<__nv_bfloat16, D, NS, TK, NS - 1, Cfg::kProducers, kTma, kMod != 0, SM::kVOff>(
         p, &tmk, &tmv, tstart, cr, stages, full, empty, abort_flag, use_tma, pok,
         warp == kProducerWarp ? 0 : warp - kMmaWarp);
     return;
@@ -400,9 +407,14 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
   }
 
   // ================================== softmax ==================================
-  const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+  const int wg = WG == 1 ? 0 : warp >> 2;     // softmax warpgroup: rows [r_wg, r_wg + NW)
+  const int r_wg = wg * NW;
+  const int wq = WG == 1 ? warp : warp & 3;   // warp of the warpgroup
+  const int ktid = WG == 1 ? tid : tid & 127;  // key of the tile, and output column of the epilogue
+  const int kBarRed = kBarRed0 + wg;
+  const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
   const uint32_t tO = tmem + lane_base, tL = tO + SM::kLCol;
-  {  // the all-ones A operand of the row-sum MMA: 8 columns of bf16 pairs (1.0, 1.0)
+  if constexpr (WG == 1) {  // the all-ones A operand of the row-sum MMA: 8 columns of bf16 pairs (1.0, 1.0)
     uint32_t ones[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) ones[j] = 0x3F803F80u;
@@ -535,21 +547,21 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
       if (slopes || edge) ahead = !bar_red_or(kBarSoft, kSoft, slopes && tid < p.R && mod_row[tid].y < 0.f);
     }
 
-    float mu[NR];  // reference max per row, log2 units
+    float mu[NW];  // reference max per row, log2 units
 #pragma unroll
-    for (int r = 0; r < NR; ++r) mu[r] = -INFINITY;
+    for (int r = 0; r < NW; ++r) mu[r] = -INFINITY;
     // (kRegL) sums over this thread's keys of P (the fp32 weights, which the
     // bf16 hi + lo parts the PV MMA multiplies carry to ~2^-16)
-    float lsum[kRegL ? NR : 1];
+    float lsum[kRegL ? NW : 1];
 #pragma unroll
-    for (int r = 0; r < (kRegL ? NR : 1); ++r) lsum[r] = 0.f;
+    for (int r = 0; r < (kRegL ? NW : 1); ++r) lsum[r] = 0.f;
 
     for (int lt = lt0; lt < lt1; ++lt, ++it, ++jt) {
       const int b = jt & 1;
       const int st = it % NS;
-      const uint32_t tS = tO + (2 + b) * NC;
+      const uint32_t tS = tO + (2 + b) * NC + r_wg;
       const int tile = kMod == 2 ? tile_of<true>(p, lt, lt0, lt1) : lt;
-      const int key = tile * TK + tid;
+      const int key = tile * TK + ktid;
       const bool draft_tile = tile * TK + TK > g.n_prefix;
       const bool masked = draft_tile || (kMod != 0 && tile * TK < g.hi);
       if (NR > 32 && draft_tile && !masks_ready) build_masks();
@@ -564,6 +576,8 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
             if (key >= mod_first[t]) km |= gbits << (t * group);
         }
       }
+      const uint64_t km_all = km;
+      if constexpr (WG > 1) km >>= r_wg;
       float koff = 0.f;  // the key's position relative to L
       const bool behind = kMod == 2 && !draft_tile && ahead;
       if constexpr (kMod == 2) {
@@ -576,18 +590,18 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
       // two tiles late, keeps each barrier at most one phase ahead of its waiter
       if (jt >= 2) wait_ok(o_done + b, (uint32_t)((jt - 2) >> 1) & 1u);
       tc_fence_after();
-      float x[NR];  // raw scores of this key, -inf where the row does not see it
+      float x[NW];  // raw scores of this key, -inf where the row does not see it
       auto load_scores = [&]() {
-        tmem_ld_f<NR>(tS, x);
+        tmem_ld_f<NW>(tS, x);
         if constexpr (kMod == 2) {
-          if (p.mod.softcap > 0.f) cap_scores<NR>(p.mod, x);
+          if (p.mod.softcap > 0.f) cap_scores<NW>(p.mod, x);
           if (p.mod.slopes != nullptr) {
             const float mul = p.mod.softcap > 0.f ? 1.f : p.mod.out_mul;
             if (behind) {
               // every row is past the key: the bias is linear in the key's position
 #pragma unroll
-              for (int r = 0; r < NR; r += 2) {
-                const float4 c = *reinterpret_cast<const float4 *>(mod_row + r);
+              for (int r = 0; r < NW; r += 2) {
+                const float4 c = *reinterpret_cast<const float4 *>(mod_row + r_wg + r);
                 const float2 y = fma2(make_float2(x[r], x[r + 1]), make_float2(mul, mul),
                                       make_float2(c.x * c.y, c.z * c.w));
                 const float2 s2 = fma2(make_float2(c.x, c.z), make_float2(-koff, -koff), y);
@@ -596,8 +610,8 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
               }
             } else {
 #pragma unroll
-              for (int r = 0; r < NR; ++r) {
-                const float2 c = mod_row[r];
+              for (int r = 0; r < NW; ++r) {
+                const float2 c = mod_row[r_wg + r];
                 x[r] = fmaf(c.x, fabsf(c.y - koff), x[r] * mul);
               }
             }
@@ -605,7 +619,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
         }
         if (masked) {
 #pragma unroll
-          for (int r = 0; r < NR; ++r)
+          for (int r = 0; r < NW; ++r)
             if (!((km >> r) & 1ull)) x[r] = -INFINITY;
         }
       };
@@ -615,14 +629,14 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
         // vote below moves it to the exact maxima only when some score is more
         // than 2^8 above it (or key 0 is hidden from a row)
         // (at the edge of a window key 0 is mostly hidden, the tile's last key is not)
-        if (tid == (kMod != 0 && masked && !draft_tile ? TK - 1 : 0)) {
+        if (ktid == (kMod != 0 && masked && !draft_tile ? TK - 1 : 0)) {
 #pragma unroll
-          for (int r = 0; r < NR; ++r) reinterpret_cast<float *>(red)[r] = x[r] * cl2;
+          for (int r = 0; r < NW; ++r) reinterpret_cast<float *>(red + r_wg)[r] = x[r] * cl2;
         }
-        named_bar_sync(kBarRed, kSoft);
+        named_bar_sync(kBarRed, 128);
 #pragma unroll
-        for (int r = 0; r < NR; r += 4) {
-          const float4 m4 = reinterpret_cast<const float4 *>(red)[r >> 2];
+        for (int r = 0; r < NW; r += 4) {
+          const float4 m4 = red[r_wg + (r >> 2)];
           mu[r] = m4.x;
           mu[r + 1] = m4.y;
           mu[r + 2] = m4.z;
@@ -631,38 +645,39 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
       }
       float dmax = -INFINITY;  // (NaN where a row has seen nothing yet: ignored by fmaxf)
 #pragma unroll
-      for (int r = 0; r < NR; ++r) dmax = fmaxf(dmax, fmaf(x[r], cl2, -mu[r]));
-      if (bar_red_or(kBarRed, kSoft, dmax > 8.f)) {
+      for (int r = 0; r < NW; ++r) dmax = fmaxf(dmax, fmaf(x[r], cl2, -mu[r]));
+      if (bar_red_or(kBarRed, 128, dmax > 8.f)) {
         // some score passed its reference by more than 2^8: move the references
         // to the exact row maxima seen so far
-        WarpScatterMax<NR, 16>::run(x, lane);
-        if constexpr (NR >= 32) {
+        WarpScatterMax<NW, 16>::run(x, lane);
+        if constexpr (NW >= 32) {
 #pragma unroll
-          for (int j = 0; j < NR / 32; ++j) reinterpret_cast<float *>(red)[(j + (NR / 32) * lane) * 4 + warp] = x[j];
+          for (int j = 0; j < NW / 32; ++j)
+            reinterpret_cast<float *>(red + r_wg)[(j + (NW / 32) * lane) * 4 + wq] = x[j];
         } else {
-          if ((lane & (32 / NR - 1)) == 0) reinterpret_cast<float *>(red)[(lane / (32 / NR)) * 4 + warp] = x[0];
+          if ((lane & (32 / NW - 1)) == 0) reinterpret_cast<float *>(red + r_wg)[(lane / (32 / NW)) * 4 + wq] = x[0];
         }
-        named_bar_sync(kBarRed, kSoft);
+        named_bar_sync(kBarRed, 128);
         float *alpha = x;  // the scores are reloaded below
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const float4 m4 = red[r];
+        for (int r = 0; r < NW; ++r) {
+          const float4 m4 = red[r_wg + r];
           const float mnew = fmaxf(mu[r], fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)) * cl2);
           alpha[r] = mu[r] == -INFINITY ? 0.f : ex2_approx(mu[r] - mnew);
           mu[r] = mnew;
         }
         if constexpr (kRegL) {
 #pragma unroll
-          for (int r = 0; r < NR; ++r) lsum[r] *= alpha[r];
+          for (int r = 0; r < NW; ++r) lsum[r] *= alpha[r];
         }
         if (lt != lt0) {
           wait_ok(o_done + (b ^ 1), (uint32_t)((jt - 1) >> 1) & 1u);  // O and l hold every PV up to tile jt-1
           tc_fence_after();
-          tmem_scale_cols<NR>(tO, x);
-          tmem_scale_cols<NR>(tO + NR, x);
+          tmem_scale_cols<NW>(tO + r_wg, x);
+          tmem_scale_cols<NW>(tO + NR + r_wg, x);
           if constexpr (!kRegL) {
-            tmem_scale_cols<NR>(tL, x);
-            tmem_scale_cols<NR>(tL + NR, x);
+            tmem_scale_cols<NW>(tL, x);
+            tmem_scale_cols<NW>(tL + NR, x);
           }
           tmem_st_wait();
         }
@@ -672,17 +687,18 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
       // it): chunk cc of the hi part, and of the lo part NR/8 chunks further
       // (64 rows: in the second swizzle atom, 16 KB further)
       uint8_t *pk = stages + st * SM::kStageBytes;
-      const int sw = tid & 7;
-      auto put_p = [&](int cc, const uint32_t (&h)[4], const uint32_t (&l)[4]) {
-        *reinterpret_cast<uint4 *>(pk + tid * 128 + ((cc ^ sw) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+      const int sw = ktid & 7;
+      auto put_p = [&](int cw, const uint32_t (&h)[4], const uint32_t (&l)[4]) {
+        const int cc = r_wg / 8 + cw;
+        *reinterpret_cast<uint4 *>(pk + ktid * 128 + ((cc ^ sw) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
         if constexpr (NR <= 32)
-          *reinterpret_cast<uint4 *>(pk + tid * 128 + (((cc + NR / 8) ^ sw) << 4)) = make_uint4(l[0], l[1], l[2], l[3]);
+          *reinterpret_cast<uint4 *>(pk + ktid * 128 + (((cc + NR / 8) ^ sw) << 4)) = make_uint4(l[0], l[1], l[2], l[3]);
         else
-          *reinterpret_cast<uint4 *>(pk + TK * 128 + tid * 128 + ((cc ^ sw) << 4)) = make_uint4(l[0], l[1], l[2], l[3]);
+          *reinterpret_cast<uint4 *>(pk + TK * 128 + ktid * 128 + ((cc ^ sw) << 4)) = make_uint4(l[0], l[1], l[2], l[3]);
       };
       if (masked) {
 #pragma unroll
-        for (int cc = 0; cc < NR / 8; ++cc) {
+        for (int cc = 0; cc < NW / 8; ++cc) {
           uint32_t h[4], l[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -701,18 +717,19 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
           }
           put_p(cc, h, l);
         }
-        if (kMod != 0 ? (p.R < 64 ? (km & ((1ull << p.R) - 1ull)) : km) == 0ull : (use_tma && key >= g.nkeys)) {
+        if (kMod != 0 ? (p.R < 64 ? (km_all & ((1ull << p.R) - 1ull)) : km_all) == 0ull : (use_tma && key >= g.nkeys)) {
           // rows past the segment end: TMA brought whatever follows; zero V so 0 * V
           // stays 0 (with score shaping: every key that no row sees)
           wait_ok(full + st, (uint32_t)(it / NS) & 1u);
           uint8_t *vt = pk + SM::kVOff;
 #pragma unroll
-          for (int ch = 0; ch < D / 8; ++ch) *reinterpret_cast<uint4 *>(vt + swz<TK>(tid, ch)) = make_uint4(0, 0, 0, 0);
+          for (int c0 = 0; c0 < D / 8 / WG; ++c0)
+            *reinterpret_cast<uint4 *>(vt + swz<TK>(ktid, wg * (D / 8 / WG) + c0)) = make_uint4(0, 0, 0, 0);
         }
       } else {
         // every row sees every key of a prefix tile, so mu is finite here
 #pragma unroll
-        for (int cc = 0; cc < NR / 8; ++cc) {
+        for (int cc = 0; cc < NW / 8; ++cc) {
           uint32_t h[4], l[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -738,24 +755,24 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
     if (jt >= 2) wait_ok(o_done + (jt & 1), (uint32_t)((jt - 2) >> 1) & 1u);
     wait_ok(o_done + ((jt - 1) & 1), (uint32_t)((jt - 1) >> 1) & 1u);
     tc_fence_after();
-    constexpr int CH = NR < 32 ? NR : 32;  // columns per TMEM load
+    constexpr int CH = NW < 32 ? NW : 32;  // columns per TMEM load
     const size_t slot = (size_t)(s + c);
-    // per-row constants, once: thread r takes row r (l is the same on every
+    // per-row constants, once: thread r (of the warpgroup) takes its row r (l is the same on every
     // lane); its l and reference max are picked out of the register arrays by
     // predicated selects, so the rows are done by the threads in parallel
     float my_l = 0.f, my_mu = 0.f;
     if constexpr (kRegL) {
       // l: this thread's key sums, reduce-scattered over the warp (lane l gets
       // row l, or l / 2 for 16 rows), then the four warps' sums of each row
-      WarpScatterSum<NR, 16>::run(lsum, lane);
-      if ((lane & (32 / NR - 1)) == 0) reinterpret_cast<float *>(red)[(lane / (32 / NR)) * 4 + warp] = lsum[0];
+      WarpScatterSum<NW, 16>::run(lsum, lane);
+      if ((lane & (32 / NW - 1)) == 0) reinterpret_cast<float *>(red + r_wg)[(lane / (32 / NW)) * 4 + wq] = lsum[0];
       named_bar_sync(kBarSoft, kSoft);
-      if (tid < NR) {
-        const float4 l4 = red[tid];
+      if (ktid < NW) {
+        const float4 l4 = red[r_wg + ktid];
         my_l = (l4.x + l4.y) + (l4.z + l4.w);
       }
 #pragma unroll
-      for (int j = 0; j < NR; ++j) my_mu = tid == j ? mu[j] : my_mu;
+      for (int j = 0; j < NW; ++j) my_mu = ktid == j ? mu[j] : my_mu;
     } else {
 #pragma unroll
       for (int h = 0; h < NR / CH; ++h) {
@@ -768,8 +785,8 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
         }
       }
     }
-    if (tid < p.R) {
-      const int r = tid;
+    if (ktid < NW && r_wg + ktid < p.R) {
+      const int r = r_wg + ktid;
       const int t = r / group;
       const int hq = g.hkv * group + r % group;
       const float lse_nat = my_l > 0.f ? (my_mu + __log2f(my_l)) * kLn2 : -INFINITY;
@@ -785,19 +802,19 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
     // column d = tid of O / l for every row, staged row-major in the Q buffer
     // (free: every MMA of this part has completed) and written by bulk copies
     if (n_parts > 1) {
-      constexpr int HR = NR / 2;
-      if constexpr (NR <= 32) {
+      constexpr int HR = NW / 2;
+      if constexpr (NW <= 32) {
         // fp32 part: thread d stores column d of every row straight from TMEM
         // (a warp writes 128 contiguous bytes of a row)
-        float *orow = p.o_part + slot * p.rows_pad * D + tid;
+        float *orow = p.o_part + (slot * p.rows_pad + r_wg) * D + ktid;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           float ov[HR];
-          tmem_ld_hilo<HR>(tO + half * HR, NR, ov);
-          if (ok && (D == 128 || tid < D)) {
+          tmem_ld_hilo<HR>(tO + r_wg + half * HR, NR, ov);
+          if (ok && (D == 128 || ktid < D)) {
 #pragma unroll
             for (int j = 0; j < HR; j += 4) {
-              const float4 inv4 = *reinterpret_cast<const float4 *>(row_inv + half * HR + j);
+              const float4 inv4 = *reinterpret_cast<const float4 *>(row_inv + r_wg + half * HR + j);
               orow[(half * HR + j + 0) * D] = ov[j] * inv4.x;
               orow[(half * HR + j + 1) * D] = ov[j + 1] * inv4.y;
               orow[(half * HR + j + 2) * D] = ov[j + 2] * inv4.z;
@@ -857,17 +874,17 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
       // final bf16 rows: the group rows of one draft token are contiguous in out
       __nv_bfloat16 *stage_b = reinterpret_cast<__nv_bfloat16 *>(sQ);
 #pragma unroll
-      for (int h = 0; h < NR / CH; ++h) {
+      for (int h = 0; h < NW / CH; ++h) {
         float ov[CH];
-        tmem_ld_hilo<CH>(tO + h * CH, NR, ov);
+        tmem_ld_hilo<CH>(tO + r_wg + h * CH, NR, ov);
 #pragma unroll
         for (int j = 0; j < CH; j += 4) {
-          if (D < 128 && tid >= D) break;
-          const float4 inv4 = *reinterpret_cast<const float4 *>(row_inv + h * CH + j);
-          stage_b[(h * CH + j + 0) * D + tid] = __float2bfloat16_rn(ov[j] * inv4.x);
-          stage_b[(h * CH + j + 1) * D + tid] = __float2bfloat16_rn(ov[j + 1] * inv4.y);
-          stage_b[(h * CH + j + 2) * D + tid] = __float2bfloat16_rn(ov[j + 2] * inv4.z);
-          stage_b[(h * CH + j + 3) * D + tid] = __float2bfloat16_rn(ov[j + 3] * inv4.w);
+          if (D < 128 && ktid >= D) break;
+          const float4 inv4 = *reinterpret_cast<const float4 *>(row_inv + r_wg + h * CH + j);
+          stage_b[(r_wg + h * CH + j + 0) * D + ktid] = __float2bfloat16_rn(ov[j] * inv4.x);
+          stage_b[(r_wg + h * CH + j + 1) * D + ktid] = __float2bfloat16_rn(ov[j + 1] * inv4.y);
+          stage_b[(r_wg + h * CH + j + 2) * D + ktid] = __float2bfloat16_rn(ov[j + 2] * inv4.z);
+          stage_b[(r_wg + h * CH + j + 3) * D + ktid] = __float2bfloat16_rn(ov[j + 3] * inv4.w);
         }
       }
       fence_proxy_async_smem();
@@ -901,9 +918,9 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma>::kThreads, 1)
     if (*merge_ok) {
       const int r0 = mpart[k] * p.R / np, r1 = (mpart[k] + 1) * p.R / np;
       if (np <= 4)
-        merge_rows_warp<8, 4, D>(p, s / p.Hkv, s % p.Hkv, 0, mslot[k], np, r0, r1, warp, 4, lane);
+        merge_rows_warp<8, 4, D>(p, s / p.Hkv, s % p.Hkv, 0, mslot[k], np, r0, r1, warp, 4 * WG, lane);
       else
-        merge_rows_warp<D == 128 ? 32 : 16, 24, D>(p, s / p.Hkv, s % p.Hkv, 0, mslot[k], np, r0, r1, warp, 4, lane);
+        merge_rows_warp<D == 128 ? 32 : 16, 24, D>(p, s / p.Hkv, s % p.Hkv, 0, mslot[k], np, r0, r1, warp, 4 * WG, lane);
     }
     named_bar_sync(kBarSoft, kSoft);
     // leave: np arrivals and np departures wrap the counter back to zero
@@ -941,7 +958,7 @@ static cudaError_t launch_tck_t(const AttnParams &p, const CUtensorMap &tmk, con
   // cooperative: every CTA is resident, so the wait for a segment's parts ends
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(TkCfg<NR, kTma>::kThreads);
+  cfg.blockDim = dim3(TkCfg<NR, kTma, kMod>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
