@@ -121,9 +121,10 @@ __global__ void __launch_bounds__(kThreads, CPS)
 
   for (int s = s0; s < S && tstart[s] < t1; ++s) {
     const Seg g = seg_at<kMod, kTK>(p, s, cr);
-    const int lt0 = max(tstart[s], t0) - tstart[s];
-    const int lt1 = min(tstart[s + 1], t1) - tstart[s];
-    const int first_cta = owner_cta(tstart[s], total, G);
+    int lt0, lt1;
+    seg_tiles<kMod>(tstart, s, cr, lt0, lt1);
+    if (kMod && lt0 >= lt1) continue;
+    const int first_cta = owner_cta(tstart[s] + (kMod ? cr.cost : 0), total, G);
     const int n_parts = owner_cta(tstart[s + 1] - 1, total, G) - first_cta + 1;
     if (lt0 == 0 && tid == 0) {
       p.meta[s] = make_int2(s + first_cta, n_parts);

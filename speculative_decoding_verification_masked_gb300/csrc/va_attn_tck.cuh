@@ -375,8 +375,9 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
 
     for (int s = s0; s < p.S && tstart[s] < t1; ++s) {
       const Seg g = seg_at<kMod != 0, TK>(p, s, cr);
-      const int lt0 = max(tstart[s], t0) - tstart[s];
-      const int lt1 = min(tstart[s + 1], t1) - tstart[s];
+      int lt0, lt1;
+      seg_tiles<kMod != 0>(tstart, s, cr, lt0, lt1);
+      if (kMod != 0 && lt0 >= lt1) continue;
       named_bar_sync(kBarQ, kSoft + 32);  // Q of this segment is in shared memory
       wait_ok(full + it % NS, (uint32_t)(it / NS) & 1u);
       issue_s(jt & 1, it % NS, g, lt0);
@@ -428,9 +429,10 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
   int n_split = 0, ms[2] = {0, 0}, mslot[2] = {0, 0}, mnp[2] = {0, 0}, mpart[2] = {0, 0};
   for (int s = s0; s < p.S && tstart[s] < t1; ++s) {
     const Seg g = seg_at<kMod != 0, TK>(p, s, cr);
-    const int lt0 = max(tstart[s], t0) - tstart[s];
-    const int lt1 = min(tstart[s + 1], t1) - tstart[s];
-    const int first_cta = owner_cta(tstart[s], cr.total, cr.G);
+    int lt0, lt1;
+    seg_tiles<kMod != 0>(tstart, s, cr, lt0, lt1);
+    if (kMod != 0 && lt0 >= lt1) continue;
+    const int first_cta = owner_cta(tstart[s] + (kMod != 0 ? cr.cost : 0), cr.total, cr.G);
     const int n_parts = owner_cta(tstart[s + 1] - 1, cr.total, cr.G) - first_cta + 1;
     if (lt0 == 0 && tid == 0) p.meta[s] = make_int2(s + first_cta, n_parts);
 

@@ -286,9 +286,28 @@ struct CtaRange {
   // score shaping: {L, lo, hi} of the kModCache sequences from b0 on
   const int4 *range;
   int b0;
+  // and the tiles a segment counts for beyond its own (kSegCost, or 0), at its
+  // front in tstart
+  int cost;
 };
 
 constexpr int kModCache = 16;
+
+// What beginning and ending a segment costs, in tiles: stage Q, fill the
+// pipeline, write the rows out, about the time of four tiles.  Without it a CTA
+// of many short sequences gets as many tiles as one of a single long sequence
+// and takes several times as long (16 sequences of 3 to 4097 keys, d64: 41 us
+// against 26 us when all have 2050).
+constexpr int kSegCost = 4;
+
+// This CTA's tiles [lt0, lt1) of segment s (none when lt0 >= lt1: its range
+// ends inside the segment's cost).
+template <bool kMod>
+__device__ __forceinline__ void seg_tiles(const int *tstart, int s, const CtaRange &cr, int &lt0, int &lt1) {
+  const int first = tstart[s] + (kMod ? cr.cost : 0);
+  lt0 = max(first, cr.t0) - first;
+  lt1 = min(tstart[s + 1], cr.t1) - first;
+}
 
 // Segment s of this CTA's share.
 template <bool kMod, int TK>
@@ -331,6 +350,17 @@ __device__ __forceinline__ CtaRange plan_cta(const AttnParams &p, int *tstart, i
   __syncthreads();
   CtaRange r;
   r.total = tstart[p.S];
+  r.cost = 0;
+  if constexpr (kMod) {
+    // (with a tile a CTA or less there is nothing to balance)
+    if (r.total > gridDim.x) {
+      r.cost = kSegCost;
+      r.total += (long long)kSegCost * p.S;
+      __syncthreads();
+      for (int s = threadIdx.x; s <= p.S; s += blockDim.x) tstart[s] += kSegCost * s;
+      __syncthreads();
+    }
+  }
   // the list is cut over G <= total CTAs, so every CTA (and every part of a
   // segment) owns at least one tile; surplus CTAs of the grid have no work
   r.G = (int)min((long long)gridDim.x, r.total);
@@ -412,16 +442,23 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
     }
   };
   auto first_tile = [&](int s) {  // the tile this CTA's part of segment s starts with
-    const int lt0 = max(tstart[s], cr.t0) - tstart[s];
-    return tile_of<kMod>(p, lt0, lt0, min(tstart[s + 1], cr.t1) - tstart[s]);
+    int lt0, lt1;
+    seg_tiles<kMod>(tstart, s, cr, lt0, lt1);
+    return tile_of<kMod>(p, lt0, lt0, lt1);
   };
-  if (!use_tma && cr.s0 < p.S && tstart[cr.s0] < cr.t1)
+  auto has_tiles = [&](int s) {
+    int lt0, lt1;
+    seg_tiles<kMod>(tstart, s, cr, lt0, lt1);
+    return lt0 < lt1;
+  };
+  if (!use_tma && cr.s0 < p.S && tstart[cr.s0] < cr.t1 && has_tiles(cr.s0))
     load_rows(seg_at<kMod, TK>(p, cr.s0, cr), first_tile(cr.s0), rows);
   int it = 0;
   for (int s = cr.s0; s < p.S && tstart[s] < cr.t1; ++s) {
     const Seg g = seg_at<kMod, TK>(p, s, cr);
-    const int lt0 = max(tstart[s], cr.t0) - tstart[s];
-    const int lt1 = min(tstart[s + 1], cr.t1) - tstart[s];
+    int lt0, lt1;
+    seg_tiles<kMod>(tstart, s, cr, lt0, lt1);
+    if (kMod && lt0 >= lt1) continue;
     // (PATH 2) the page entry of this lane's box, fetched one tile ahead
     auto box_page = [&](int lt) {
       const int k = tile_of<kMod>(p, lt, lt0, lt1) * TK + lane * p.tma_box;
@@ -492,7 +529,7 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
         bool has_next = true;
         if (lt + 1 < lt1) {
           load_rows(g, tile_of<kMod>(p, lt + 1, lt0, lt1), nrows);
-        } else if (s + 1 < p.S && tstart[s + 1] < cr.t1) {
+        } else if (s + 1 < p.S && tstart[s + 1] < cr.t1 && has_tiles(s + 1)) {
           load_rows(seg_at<kMod, TK>(p, s + 1, cr), first_tile(s + 1), nrows);
         } else {
           has_next = false;
