@@ -75,23 +75,33 @@ __device__ __forceinline__ long long evict_row(const EvictParams &p, int b, int 
 
 __global__ void __launch_bounds__(kEvictThreads) evict_kv_kernel(const EvictParams p, int rows, int words, long long items) {
   extern __shared__ __align__(16) uint8_t smem[];  // K rows, V rows
-  __shared__ long long src[kEvictMaxRows], dst[kEvictMaxRows];  // cache rows; src -1: not moved
+  __shared__ long long src[kEvictMaxRows], dst[kEvictMaxRows];  // byte offsets in the caches; src -1: not moved
   __shared__ float sw[kEvictMaxRows];
   __shared__ int s_L, s_n, s_go;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int heads = p.B * p.Hkv;
-  const int cpr = p.row_bytes / 16;  // 16-byte columns of a row
+  // a thread keeps one 16-byte column and steps over the rows (threads past the
+  // last whole row of columns have none)
+  const int cpr = p.row_bytes / 16;
+  const int rstep = kEvictThreads / cpr;
+  const int r0 = tid / cpr < rstep ? tid / cpr : rows;
+  const int col = (tid % cpr) * 16;
   const EvictScratchView sc = evict_scratch(p);
-  uint8_t *bufs[2] = {smem, smem + rows * p.row_bytes};
-  uint8_t *caches[2] = {static_cast<uint8_t *>(p.k), static_cast<uint8_t *>(p.v)};
+  uint8_t *kbuf = smem + col, *vbuf = smem + rows * p.row_bytes + col;
+  uint8_t *kc = static_cast<uint8_t *>(p.k) + col, *vc = static_cast<uint8_t *>(p.v) + col;
 
+  // this thread's index of an item, loaded one item ahead
+  auto index_of = [&](long long it) {
+    const int j = (int)(it / heads) * rows + tid;
+    return it < items && tid < rows && j < p.max_indices ? __ldg(p.indices + (size_t)(it % heads) * p.max_indices + j) : -1;
+  };
+  int s_next = index_of(blockIdx.x);
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
     const int c = (int)(it / heads), bh = (int)(it % heads);
     const int b = bh / p.Hkv, h = bh % p.Hkv;
     const int j0 = c * rows;
-    const int32_t *idx = p.indices + (size_t)bh * p.max_indices;
-    int s = -1;
-    if (tid < rows && j0 + tid < p.max_indices) s = __ldg(idx + j0 + tid);
+    int s = s_next;
+    s_next = index_of(it + gridDim.x);
     if (warp == 0) {
       const int L = __ldg(p.seqlens + b);
       const int n = evict_count(p, b, L);
@@ -117,16 +127,18 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kv_kernel(const EvictPara
         record_status(p.status, VA_ERR_DEVICE_BOUNDS);
         s = j;
       }
-      const long long d = s != j ? evict_row(p, b, j) : -1;
-      src[tid] = d >= 0 ? evict_row(p, b, s) : -1;
-      dst[tid] = d;
+      const long long d = s != j ? evict_row(p, b, j) : -1, f = d >= 0 ? evict_row(p, b, s) : -1;
+      src[tid] = f >= 0 ? (f * p.Hkv + h) * p.row_bytes : -1;
+      dst[tid] = (d * p.Hkv + h) * p.row_bytes;
       if (w != nullptr) sw[tid] = w[s];
     }
     __syncthreads();
-    for (int e = tid; e < 2 * nr * cpr; e += kEvictThreads) {
-      const int x = e >= nr * cpr, r = (e - x * nr * cpr) / cpr, col = (e - x * nr * cpr) % cpr;
-      if (src[r] >= 0)
-        cp_async_16(bufs[x] + (r * cpr + col) * 16, caches[x] + (src[r] * p.Hkv + h) * p.row_bytes + col * 16, 16);
+#pragma unroll 4
+    for (int r = r0; r < nr; r += rstep) {
+      const long long o = src[r];
+      if (o < 0) continue;
+      cp_async_16(kbuf + r * p.row_bytes, kc + o, 16);
+      cp_async_16(vbuf + r * p.row_bytes, vc + o, 16);
     }
     cp_async_wait_all();
     __syncthreads();
@@ -154,11 +166,12 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kv_kernel(const EvictPara
     }
     __syncthreads();
     if (s_go) {
-      for (int e = tid; e < 2 * nr * cpr; e += kEvictThreads) {
-        const int x = e >= nr * cpr, r = (e - x * nr * cpr) / cpr, col = (e - x * nr * cpr) % cpr;
-        if (src[r] >= 0)
-          *reinterpret_cast<uint4 *>(caches[x] + (dst[r] * p.Hkv + h) * p.row_bytes + col * 16) =
-              *reinterpret_cast<const uint4 *>(bufs[x] + (r * cpr + col) * 16);
+#pragma unroll 4
+      for (int r = r0; r < nr; r += rstep) {
+        if (src[r] < 0) continue;
+        const long long o = dst[r];
+        *reinterpret_cast<uint4 *>(kc + o) = *reinterpret_cast<const uint4 *>(kbuf + r * p.row_bytes);
+        *reinterpret_cast<uint4 *>(vc + o) = *reinterpret_cast<const uint4 *>(vbuf + r * p.row_bytes);
       }
       if (w != nullptr && tid < nr) w[j0 + tid] = sw[tid];
     }
