@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
       const int k0 = (kMod == 2 ? tile_of<true>(p, lt, lt0, lt1) : lt) * kTK;
       const bool masked = k0 + kTK > g.n_prefix || (kMod != 0 && k0 < g.hi);
       if constexpr (kMod == 2) {
-        if (p.mod.softcap > 0.f) cap_scores<64>(p.mod, sv);
+        if (p.mod.softcap > 0.f) cap_scores<64, false>(p.mod, sv);
         if (p.mod.slopes != nullptr) {
           const float mul = p.mod.softcap > 0.f ? 1.f : p.mod.out_mul;
           const float d0 = qoff - (float)(k0 - g.n_prefix);  // distance of the tile's first key

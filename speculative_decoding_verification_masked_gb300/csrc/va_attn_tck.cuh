@@ -625,8 +625,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
             if (!((km >> r) & 1ull)) x[r] = -INFINITY;
         }
       };
-      load_scores();
-      if (lt == lt0) {
+      auto set_reference = [&]() {
         // first tile of this part: the scores of key 0 are the reference; the
         // vote below moves it to the exact maxima only when some score is more
         // than 2^8 above it (or key 0 is hidden from a row)
@@ -644,11 +643,14 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
           mu[r + 2] = m4.z;
           mu[r + 3] = m4.w;
         }
-      }
-      float dmax = -INFINITY;  // (NaN where a row has seen nothing yet: ignored by fmaxf)
+      };
+      auto passed_reference = [&]() {
+        float dmax = -INFINITY;  // (NaN where a row has seen nothing yet: ignored by fmaxf)
 #pragma unroll
-      for (int r = 0; r < NW; ++r) dmax = fmaxf(dmax, fmaf(x[r], cl2, -mu[r]));
-      if (bar_red_or(kBarRed, 128, dmax > 8.f)) {
+        for (int r = 0; r < NW; ++r) dmax = fmaxf(dmax, fmaf(x[r], cl2, -mu[r]));
+        return bar_red_or(kBarRed, 128, dmax > 8.f);
+      };
+      auto move_reference = [&]() {
         // some score passed its reference by more than 2^8: move the references
         // to the exact row maxima seen so far
         WarpScatterMax<NW, 16>::run(x, lane);
@@ -683,7 +685,26 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
           }
           tmem_st_wait();
         }
+      };
+      if constexpr (kMod == 2) {
+        // (one copy of the code that shapes the scores)
+        bool moved = false;
+#pragma unroll 1
+        while (true) {
+          load_scores();
+          if (moved) break;
+          if (lt == lt0) set_reference();
+          if (!passed_reference()) break;
+          move_reference();
+          moved = true;
+        }
+      } else {
         load_scores();
+        if (lt == lt0) set_reference();
+        if (passed_reference()) {
+          move_reference();
+          load_scores();
+        }
       }
       // P^T row of this key over the K tile of the stage (the S MMA is done with
       // it): chunk cc of the hi part, and of the lo part NR/8 chunks further

@@ -37,7 +37,22 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// cap2 * tanh(y): cap2 multiplies the numerator before the division.
+// cap2 * tanh of a pair; cap2 multiplies the numerators before the division.
+__device__ __forceinline__ float2 capped_tanh2(float2 y, float cap2) {
+  y.x = fminf(fmaxf(y.x, -9.02f), 9.02f);
+  y.y = fminf(fmaxf(y.y, -9.02f), 9.02f);
+  auto two = [](float c) { return make_float2(c, c); };
+  const float2 z = mul2(y, y);
+  float2 p = fma2(two(1.33188971e-08f), z, two(2.05833530e-05f));
+  p = fma2(p, z, two(3.49402661e-03f));
+  p = fma2(p, z, two(1.33797109e-01f));
+  p = fma2(p, z, two(1.0f));
+  float2 q = fma2(two(7.76194668e-07f), z, two(3.28308001e-04f));
+  q = fma2(q, z, two(2.58710440e-02f));
+  q = fma2(q, z, two(4.67130274e-01f));
+  q = fma2(q, z, two(1.0f));
+  return mul2(mul2(mul2(y, two(cap2)), p), make_float2(rcp_approx(q.x), rcp_approx(q.y)));
+}
 __device__ __forceinline__ float capped_tanh(float y, float cap2) {
   y = fminf(fmaxf(y, -9.02f), 9.02f);
   const float z = y * y;
@@ -56,8 +71,10 @@ __device__ __forceinline__ float capped_tanh(float y, float cap2) {
 // small (|y| <= 0.75, what a cap well above the usual scores leaves), tanh is an
 // odd polynomial of degree 11 (fitted like the above: 2.9e-8 relative, 1.5e-7 in
 // fp32) with the scale and the cap folded into its coefficients: seven packed
-// instructions for two scores and no division, against 32.
-template <int N>
+// instructions for two scores and no division, against nineteen.
+// (kPacked: the general case on pairs as well; off where 64 scores a thread leave
+// no room for aligned register pairs: the 256-row kernel lost 5% to it.)
+template <int N, bool kPacked = true>
 __device__ __forceinline__ void cap_scores(const ModParams &m, float (&x)[N]) {
   float top = 0.f;
 #pragma unroll
@@ -79,9 +96,16 @@ __device__ __forceinline__ void cap_scores(const ModParams &m, float (&x)[N]) {
       x[i] = q.x;
       x[i + 1] = q.y;
     }
-  } else {
+  } else if constexpr (!kPacked) {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = capped_tanh(x[i] * m.in_mul, m.out_mul);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 y = capped_tanh2(mul2(make_float2(x[i], x[i + 1]), make_float2(m.in_mul, m.in_mul)), m.out_mul);
+      x[i] = y.x;
+      x[i + 1] = y.y;
+    }
   }
 }
 
