@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(kThreads, CPS)
     uint64_t tl = 0, th = 0;
     if (has_draft && p.parent != nullptr) warp_tree_rows(p, g.b, tl, th);
     uint64_t seen = ~0ull;  // score shaping: the draft keys that some token sees
-    if (kMod && has_draft) {
+    // (without an explicit mask every token sees itself)
+    if (kMod && has_draft && p.mask != nullptr) {
       uint64_t lo, hi;
       draft_rows(p, draft_prefetch(p, g.b), lo, hi);
       seen = lane < p.T ? mod_window_row(p.mod, p.T, g.b, lane, g.L, lo) : 0ull;
@@ -541,14 +542,24 @@ __global__ void __launch_bounds__(kThreads, CPS)
               a = fmaf(qv[4 * i + 2], k4.z, a);
               a = fmaf(qv[4 * i + 3], k4.w, a);
             }
-            const int key = tile * kTK + half * 32 + kk;
-            bool vis = key < g.nkeys;
-            if (vis && key >= g.n_prefix) vis = (rmask >> (key - g.n_prefix)) & 1ull;
-            if constexpr (kMod) {
-              a = mod_score(p.mod, a, ns, qoff - key_off(key));
-              vis = vis && key >= first;
+            if constexpr (!kMod) {
+              const int key = tile * kTK + half * 32 + kk;
+              bool vis = key < g.nkeys;
+              if (vis && key >= g.n_prefix) vis = (rmask >> (key - g.n_prefix)) & 1ull;
+              a = vis ? a : -INFINITY;
             }
-            sc[kk] = vis ? a : -INFINITY;
+            sc[kk] = a;
+          }
+          if constexpr (kMod) {  // shape the scores, then hide keys
+#pragma unroll 2
+            for (int kk = 0; kk < 32; ++kk) {
+              const int key = tile * kTK + half * 32 + kk;
+              const float d = p.mod.slopes != nullptr ? qoff - key_off(key) : 0.f;
+              bool vis = key < g.nkeys && key >= first;
+              if (vis && key >= g.n_prefix) vis = (rmask >> (key - g.n_prefix)) & 1ull;
+              const float a = mod_score(p.mod, sc[kk], ns, d);
+              sc[kk] = vis ? a : -INFINITY;
+            }
           }
           float mx = m;
 #pragma unroll

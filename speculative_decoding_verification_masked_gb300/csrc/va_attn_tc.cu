@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
       seg_tiles<kMod != 0>(tstart, s, cr, lt0, lt1);
       if (kMod != 0 && lt0 >= lt1) continue;
       uint64_t seen = ~0ull;
-      if (kMod != 0 && !s_issuer && lt1 * kTK > g.n_prefix) {
+      // (without an explicit mask every token sees itself)
+      if (kMod != 0 && !s_issuer && p.mask != nullptr && lt1 * kTK > g.n_prefix) {
         uint64_t lo, hi;
         draft_rows(p, draft_prefetch(p, g.b), lo, hi);
         seen = lane < p.T ? mod_window_row(p.mod, p.T, g.b, lane, g.L, lo) : 0ull;
