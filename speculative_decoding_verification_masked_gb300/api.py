@@ -397,12 +397,12 @@ def verify_head_importance(q, k_cache, seqlens, heads, score=None, score_stride=
 # ----------------------------------------------------------------------------
 
 def _arg(t, name, shape, dtype, device):
-    """Device pointer of a contiguous tensor of this shape (None = any size), type and device; None stays None."""
+    """Device pointer of a contiguous tensor of this shape, type and device; None stays None."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor or None")
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == device and t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device.index and t.is_contiguous():
         return t.data_ptr()
     if not t.is_cuda:
         raise ValueError("tensor arguments must live on the GPU")
@@ -410,11 +410,21 @@ def _arg(t, name, shape, dtype, device):
         raise ValueError(f"{name} is on {t.device}, q or the cache on {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError("tensor arguments must be contiguous")
-    return t.data_ptr()
+    raise ValueError("tensor arguments must be contiguous")
+
+
+def _cache_args(layout, k, B, Hkv, D, table, device):
+    """Geometry arguments of a cache k: [cache length], or [pages, page size, table, table width]."""
+    n0, n1 = k.shape[:2]
+    if layout == "dense":
+        if n0 != B:
+            raise ValueError(f"the key cache: expected {B} sequences, got {n0}")
+        return [n1]
+    _need(table, "page_table", 2)
+    width = table.shape[1]
+    return [n0, n1, _arg(table, "page_table", (B, width), torch.int32, device), width]
 
 
 def _need(t, name, dim):
@@ -467,18 +477,17 @@ def _mod_call(layout, q, k, v, table, seqlens, mod, tree_parent, tree_mask, out,
     _need(q, "q", 4)
     _need(k, "the key cache", 4)
     B, T, Hq, D = q.shape
-    n0, n1, Hkv = k.shape[:3]
+    n0, n1, Hkv, _ = k.shape
     dev = q.device
     if not isinstance(mod, ScoreMod):
         raise TypeError("mod: expected a ScoreMod")
+    _need(v, "the value cache", 4)
+    _need(seqlens, "seqlens", 1)
     shape = _shape_of(q, Hkv, scale)
     out, lse = _outputs(q, out, lse)
-    cache = (B, None, Hkv, D) if layout == "dense" else (None, None, Hkv, D)
-    kv = [_arg(q, "q", (B, T, Hq, D), q.dtype, dev), _arg(k, "the key cache", cache, q.dtype, dev),
-          _arg(v, "the value cache", tuple(k.shape), q.dtype, dev)]
-    if seqlens is None or (layout == "paged" and table is None):
-        raise TypeError("seqlens and page_table must be tensors")
-    geo = [n1] if layout == "dense" else [n0, n1, _arg(table, "page_table", (B, None), torch.int32, dev), table.shape[1]]
+    kv = [_arg(q, "q", (B, T, Hq, D), q.dtype, dev), _arg(k, "the key cache", (n0, n1, Hkv, D), q.dtype, dev),
+          _arg(v, "the value cache", (n0, n1, Hkv, D), q.dtype, dev)]
+    geo = _cache_args(layout, k, B, Hkv, D, table, dev)
     m = mod.struct(B, T, Hq, dev)
     rest = [_arg(seqlens, "seqlens", (B,), torch.int32, dev), _arg(tree_parent, "tree_parent", (B, T), torch.int32, dev),
             _arg(tree_mask, "tree_mask", (B, T, (T + 31) // 32), torch.int32, dev),
@@ -520,22 +529,22 @@ def _weight_call(layout, q, k, table, seqlens, lse, weight, mod, path, n_accept,
     _need(k, "the key cache", 4)
     _need(weight, "weight", 3)
     B, T, Hq, D = q.shape
-    n0, n1, Hkv = k.shape[:3]
+    n0, n1, Hkv, _ = k.shape
     dev = q.device
     shape = _shape_of(q, Hkv, scale)
-    cache = (B, None, Hkv, D) if layout == "dense" else (None, None, Hkv, D)
-    if seqlens is None or lse is None or (layout == "paged" and table is None):
-        raise TypeError("seqlens, lse and page_table must be tensors")
+    _need(seqlens, "seqlens", 1)
+    _need(lse, "lse", 3)
     if mod is not None and not isinstance(mod, ScoreMod):
         raise TypeError("mod: expected a ScoreMod or None")
     m = mod.struct(B, T, Hq, dev) if mod is not None else None
-    geo = [n1] if layout == "dense" else [n0, n1, _arg(table, "page_table", (B, None), torch.int32, dev), table.shape[1]]
+    geo = _cache_args(layout, k, B, Hkv, D, table, dev)
+    stride = weight.shape[2]
     _run_on(dev, stream, f"verify_accumulate_weight_{layout}", ctypes.byref(shape),
             ctypes.byref(m) if m is not None else None, _arg(q, "q", (B, T, Hq, D), q.dtype, dev),
-            _arg(k, "the key cache", cache, q.dtype, dev), *geo, _arg(seqlens, "seqlens", (B,), torch.int32, dev),
+            _arg(k, "the key cache", (n0, n1, Hkv, D), q.dtype, dev), *geo, _arg(seqlens, "seqlens", (B,), torch.int32, dev),
             _arg(path, "path", (B, T), torch.int32, dev), _arg(n_accept, "n_accept", (B,), torch.int32, dev),
             _arg(lse, "lse", (B, Hq, T), torch.float32, dev), float(decay),
-            _arg(weight, "weight", (B, Hkv, None), torch.float32, dev), weight.shape[2], _status_ptr(workspace, dev))
+            _arg(weight, "weight", (B, Hkv, stride), torch.float32, dev), stride, _status_ptr(workspace, dev))
     return weight
 
 
@@ -571,18 +580,22 @@ def _evict_call(layout, k, v, table, seqlens, indices, n_indices, weight, seqlen
     n0, n1, Hkv, D = k.shape
     B = indices.shape[0]
     dev = k.device
-    if seqlens is None or n_indices is None or v is None or (layout == "paged" and table is None):
-        raise TypeError("the caches, seqlens, n_indices and page_table must be tensors")
+    _need(v, "the value cache", 4)
+    _need(seqlens, "seqlens", 1)
+    _need(n_indices, "n_indices", 2)
+    if weight is not None:
+        _need(weight, "weight", 3)
     if seqlens_out is None:
         seqlens_out = torch.empty(B, dtype=torch.int32, device=dev)
     shape = make_shape(B, 1, Hkv, Hkv, D, _dtype_code(k), 1.0)
-    cache = (B, None, Hkv, D) if layout == "dense" else (None, None, Hkv, D)
-    geo = [n1] if layout == "dense" else [n0, n1, _arg(table, "page_table", (B, None), torch.int32, dev), table.shape[1]]
-    args = [_arg(k, "the key cache", cache, k.dtype, dev), _arg(v, "the value cache", tuple(k.shape), k.dtype, dev),
+    geo = _cache_args(layout, k, B, Hkv, D, table, dev)
+    m, stride = indices.shape[2], weight.shape[2] if weight is not None else 0
+    args = [_arg(k, "the key cache", (n0, n1, Hkv, D), k.dtype, dev),
+            _arg(v, "the value cache", (n0, n1, Hkv, D), k.dtype, dev),
             *geo, _arg(seqlens, "seqlens", (B,), torch.int32, dev),
-            _arg(indices, "indices", (B, Hkv, None), torch.int32, dev),
-            _arg(n_indices, "n_indices", (B, Hkv), torch.int32, dev), indices.shape[2],
-            _arg(weight, "weight", (B, Hkv, None), torch.float32, dev), weight.shape[2] if weight is not None else 0,
+            _arg(indices, "indices", (B, Hkv, m), torch.int32, dev),
+            _arg(n_indices, "n_indices", (B, Hkv), torch.int32, dev), m,
+            _arg(weight, "weight", (B, Hkv, stride), torch.float32, dev), stride,
             _arg(seqlens_out, "seqlens_out", (B,), torch.int32, dev)]
     sc = scratch
     if sc is None:

@@ -500,7 +500,9 @@ va_status run_weight(va::WeightParams &p, cudaStream_t stream) {
 }
 
 va_status run_evict(const va::EvictParams &p, cudaStream_t stream) {
-  cudaError_t e = va::launch_evict_kv(p, stream);
+  const int sms = device_sm_count(nullptr);
+  if (sms <= 0) return fail(VA_ERR_CUDA, "no usable CUDA device");
+  cudaError_t e = va::launch_evict_kv(p, sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, "eviction launch");
   return ok();
 }

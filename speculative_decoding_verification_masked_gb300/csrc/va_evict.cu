@@ -17,6 +17,8 @@
 //
 // Bound by HBM: 2 x 2 x row bytes a kept row (K and V, read and written).
 // Chunks of 32 KB and up to six blocks an SM keep 190 KB an SM in flight.
+#include <mutex>
+
 #include "va_common.cuh"
 #include "va_evict.h"
 #include "va_kernels.h"
@@ -201,16 +203,25 @@ size_t evict_scratch_bytes(int B, int Hkv, int max_indices) {
   return 256 + align256(sizeof(unsigned) * (size_t)B * Hkv * evict_words(max_indices, evict_rows(1024)));
 }
 
-cudaError_t launch_evict_kv(const EvictParams &p, cudaStream_t stream) {
+cudaError_t launch_evict_kv(const EvictParams &p, int sms, cudaStream_t stream) {
   const int rows = evict_rows(p.row_bytes);
   const int words = evict_words(p.max_indices, rows);
   const size_t smem = 2 * (size_t)rows * p.row_bytes;
   const long long items = (long long)p.B * p.Hkv * ((p.max_indices + rows - 1) / rows);
-  int dev = 0, sms = 0, per_sm = 0;
+  int dev = 0, per_sm = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, evict_kv_kernel, kEvictThreads, smem);
   if (e != cudaSuccess) return e;
+  {  // blocks that fit an SM with this much shared memory, asked for once
+    static std::mutex mu;
+    static int cache[64][kEvictChunkBytes / 16 + 1];
+    std::lock_guard<std::mutex> lock(mu);
+    int &n = cache[dev & 63][smem / 32];
+    if (n == 0) {
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, evict_kv_kernel, kEvictThreads, smem);
+      if (e != cudaSuccess) return e;
+    }
+    per_sm = n;
+  }
   const long long most = (long long)sms * (per_sm < 1 ? 1 : per_sm);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items < most ? items : most));

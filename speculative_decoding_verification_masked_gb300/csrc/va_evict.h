@@ -28,6 +28,6 @@ struct EvictParams {
 
 size_t evict_scratch_bytes(int B, int Hkv, int max_indices);
 
-cudaError_t launch_evict_kv(const EvictParams &p, cudaStream_t stream);
+cudaError_t launch_evict_kv(const EvictParams &p, int sms, cudaStream_t stream);
 
 }  // namespace va
