@@ -415,6 +415,13 @@ def _arg(t, name, shape, dtype, device):
     raise ValueError("tensor arguments must be contiguous")
 
 
+def _req(t, name, shape, dtype, device):
+    """The same for an argument that has to be given."""
+    if t is None:
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    return _arg(t, name, shape, dtype, device)
+
+
 def _cache_args(layout, k, B, Hkv, D, table, device):
     """Geometry arguments of a cache k: [cache length], or [pages, page size, table, table width]."""
     n0, n1 = k.shape[:2]
@@ -448,13 +455,16 @@ def _run_on(device, stream, name, *args):
             _check(f(*args, s))
 
 
-def _own(make, device, stream):
-    """A workspace made for one call: its memory is not reused before the work on `stream` is done."""
-    with torch.cuda.device(device):
-        ws = make()
+def _made(make, device, stream):
+    """What make() allocates for a call on `stream`, from that stream's memory pool: neither
+    the memory's last user nor its next one overlaps with the call."""
     if stream is not None:
-        ws.buffer.record_stream(stream)
-    return ws
+        with torch.cuda.stream(stream):
+            return make()
+    if torch.cuda.current_device() == device.index:
+        return make()
+    with torch.cuda.device(device):
+        return make()
 
 
 class ScoreMod:
@@ -481,20 +491,19 @@ def _mod_call(layout, q, k, v, table, seqlens, mod, tree_parent, tree_mask, out,
     dev = q.device
     if not isinstance(mod, ScoreMod):
         raise TypeError("mod: expected a ScoreMod")
-    _need(v, "the value cache", 4)
-    _need(seqlens, "seqlens", 1)
     shape = _shape_of(q, Hkv, scale)
-    out, lse = _outputs(q, out, lse)
+    if out is None or lse is None:
+        out, lse = _made(lambda: _outputs(q, out, lse), dev, stream)
     kv = [_arg(q, "q", (B, T, Hq, D), q.dtype, dev), _arg(k, "the key cache", (n0, n1, Hkv, D), q.dtype, dev),
-          _arg(v, "the value cache", (n0, n1, Hkv, D), q.dtype, dev)]
+          _req(v, "the value cache", (n0, n1, Hkv, D), q.dtype, dev)]
     geo = _cache_args(layout, k, B, Hkv, D, table, dev)
     m = mod.struct(B, T, Hq, dev)
-    rest = [_arg(seqlens, "seqlens", (B,), torch.int32, dev), _arg(tree_parent, "tree_parent", (B, T), torch.int32, dev),
+    rest = [_req(seqlens, "seqlens", (B,), torch.int32, dev), _arg(tree_parent, "tree_parent", (B, T), torch.int32, dev),
             _arg(tree_mask, "tree_mask", (B, T, (T + 31) // 32), torch.int32, dev),
             _arg(out, "out", (B, T, Hq, D), q.dtype, dev), _arg(lse, "lse", (B, Hq, T), torch.float32, dev)]
     ws = workspace
     if ws is None:
-        ws = _own(lambda: Workspace.for_shape(shape, dev, stream), dev, stream)
+        ws = _made(lambda: Workspace.for_shape(shape, dev, stream), dev, stream)
     elif ws.buffer.device != dev:
         raise ValueError(f"workspace is on {ws.buffer.device}, q on {dev}")
     _run_on(dev, stream, f"verify_attn_{layout}_mod", ctypes.byref(shape), ctypes.byref(m), *kv, *geo, *rest, ws.ptr,
@@ -532,8 +541,6 @@ def _weight_call(layout, q, k, table, seqlens, lse, weight, mod, path, n_accept,
     n0, n1, Hkv, _ = k.shape
     dev = q.device
     shape = _shape_of(q, Hkv, scale)
-    _need(seqlens, "seqlens", 1)
-    _need(lse, "lse", 3)
     if mod is not None and not isinstance(mod, ScoreMod):
         raise TypeError("mod: expected a ScoreMod or None")
     m = mod.struct(B, T, Hq, dev) if mod is not None else None
@@ -541,9 +548,9 @@ def _weight_call(layout, q, k, table, seqlens, lse, weight, mod, path, n_accept,
     stride = weight.shape[2]
     _run_on(dev, stream, f"verify_accumulate_weight_{layout}", ctypes.byref(shape),
             ctypes.byref(m) if m is not None else None, _arg(q, "q", (B, T, Hq, D), q.dtype, dev),
-            _arg(k, "the key cache", (n0, n1, Hkv, D), q.dtype, dev), *geo, _arg(seqlens, "seqlens", (B,), torch.int32, dev),
+            _arg(k, "the key cache", (n0, n1, Hkv, D), q.dtype, dev), *geo, _req(seqlens, "seqlens", (B,), torch.int32, dev),
             _arg(path, "path", (B, T), torch.int32, dev), _arg(n_accept, "n_accept", (B,), torch.int32, dev),
-            _arg(lse, "lse", (B, Hq, T), torch.float32, dev), float(decay),
+            _req(lse, "lse", (B, Hq, T), torch.float32, dev), float(decay),
             _arg(weight, "weight", (B, Hkv, stride), torch.float32, dev), stride, _status_ptr(workspace, dev))
     return weight
 
@@ -580,26 +587,23 @@ def _evict_call(layout, k, v, table, seqlens, indices, n_indices, weight, seqlen
     n0, n1, Hkv, D = k.shape
     B = indices.shape[0]
     dev = k.device
-    _need(v, "the value cache", 4)
-    _need(seqlens, "seqlens", 1)
-    _need(n_indices, "n_indices", 2)
-    if weight is not None:
-        _need(weight, "weight", 3)
     if seqlens_out is None:
-        seqlens_out = torch.empty(B, dtype=torch.int32, device=dev)
+        seqlens_out = _made(lambda: torch.empty(B, dtype=torch.int32, device=dev), dev, stream)
     shape = make_shape(B, 1, Hkv, Hkv, D, _dtype_code(k), 1.0)
     geo = _cache_args(layout, k, B, Hkv, D, table, dev)
+    if weight is not None:
+        _need(weight, "weight", 3)
     m, stride = indices.shape[2], weight.shape[2] if weight is not None else 0
     args = [_arg(k, "the key cache", (n0, n1, Hkv, D), k.dtype, dev),
-            _arg(v, "the value cache", (n0, n1, Hkv, D), k.dtype, dev),
-            *geo, _arg(seqlens, "seqlens", (B,), torch.int32, dev),
+            _req(v, "the value cache", (n0, n1, Hkv, D), k.dtype, dev),
+            *geo, _req(seqlens, "seqlens", (B,), torch.int32, dev),
             _arg(indices, "indices", (B, Hkv, m), torch.int32, dev),
-            _arg(n_indices, "n_indices", (B, Hkv), torch.int32, dev), m,
+            _req(n_indices, "n_indices", (B, Hkv), torch.int32, dev), m,
             _arg(weight, "weight", (B, Hkv, stride), torch.float32, dev), stride,
             _arg(seqlens_out, "seqlens_out", (B,), torch.int32, dev)]
     sc = scratch
     if sc is None:
-        sc = _own(lambda: EvictScratch(B, Hkv, max(indices.shape[2], 1), dev, stream), dev, stream)
+        sc = _made(lambda: EvictScratch(B, Hkv, max(m, 1), dev, stream), dev, stream)
     elif sc.buffer.device != dev:
         raise ValueError(f"scratch is on {sc.buffer.device}, the cache on {dev}")
     _run_on(dev, stream, f"verify_evict_kv_{layout}", ctypes.byref(shape), *args, sc.ptr, sc.nbytes,

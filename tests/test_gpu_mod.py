@@ -200,3 +200,69 @@ def test_workspace_shared_with_the_unshaped_calls():
         va.verify_attn_dense(c.q.cuda(), c.k.cuda(), c.v.cuda(), shaped.dev(c.L), workspace=ws)
     va.verify_attn_check_status(ws)
     _check(c, out, lse)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(8, 8, 2, 128), (16, 8, 2, 128), (64, 4, 1, 128), (8, 8, 2, 64)])
+def test_timeout_then_recovery(T, Hq, Hkv, D):
+    """A lost part of a split segment ends in the documented error within the
+    wait limit, and a fresh workspace gives the right result again."""
+    c = shaped.make(5, [5000], T, Hq, Hkv, D, draft="tree", softcap=30.0, slopes=True)
+    shape = va.make_shape(1, T, Hq, Hkv, D, 0)
+    ws = va.Workspace.for_shape(shape)
+    L = va.api.lib()
+    assert L.verify_attn_test_inject(2_000_000, 0) == 0
+    try:
+        shaped.run_attend(va, c, workspace=ws)
+        with pytest.raises(va.VerifyAttnError) as ei:
+            va.verify_attn_check_status(ws)
+        assert ei.value.status == va.api.VA_ERR_TIMEOUT
+    finally:
+        assert L.verify_attn_test_inject(0, -1) == 0
+    ws = va.Workspace.for_shape(shape)
+    out, lse = shaped.run_attend(va, c, workspace=ws)
+    va.verify_attn_check_status(ws)
+    _check(c, out, lse)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with its own workspace."""
+    cs = [shaped.make(s, [3000, 40], 8, 8, 2, softcap=30.0, window=500) for s in (1, 2)]
+    args, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for c in cs:
+        ws = va.Workspace.for_shape(va.make_shape(2, 8, 8, 2, 128, 0))
+        args.append((c.q.cuda(), c.k.cuda(), c.v.cuda(), shaped.dev(c.L), shaped.mod_of(va, c), ws,
+                     torch.empty(2, 8, 8, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(2, 8, 8, device="cuda")))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (q, k, v, L, m, ws, out, lse), s in zip(args, streams):
+            va.verify_attn_dense_mod(q, k, v, L, m, out=out, lse=lse, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for c, a in zip(cs, args):
+        _check(c, a[6], a[7])
+
+
+def test_python_refusals():
+    """Tensors of another type, shape or order are refused before the call."""
+    c = shaped.make(1, [64], 4, 4, 2)
+    q, k, v, L, mod = c.q.cuda(), c.k.cuda(), c.v.cuda(), shaped.dev(c.L), shaped.mod_of(va, c)
+    call = va.verify_attn_dense_mod
+    with pytest.raises(TypeError):
+        call(q, k.float(), v, L, mod)
+    with pytest.raises(TypeError):
+        call(q, k, v, L.long(), mod)
+    with pytest.raises(TypeError):
+        call(q, k, v, L, None)
+    with pytest.raises(TypeError):
+        call(q, k, None, L, mod)
+    with pytest.raises(ValueError):
+        call(q, k[:, :-1], v, L, mod)
+    with pytest.raises(ValueError):
+        call(q, k, v, L, va.ScoreMod(slopes=torch.ones(3, device="cuda")))
+    with pytest.raises(ValueError):
+        call(q, k, v, L, va.ScoreMod(token_pos=L))
+    with pytest.raises(ValueError):
+        call(q.transpose(1, 2), k, v, L, mod)
+    with pytest.raises(ValueError):
+        call(torch.cat([q, q]), k, v, torch.cat([L, L]), mod)
+    with pytest.raises(ValueError):
+        call(q, k, v, L, mod, lse=torch.empty(1, 4, 5, device="cuda"))
