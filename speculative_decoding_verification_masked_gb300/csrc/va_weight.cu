@@ -153,18 +153,20 @@ __global__ void __launch_bounds__(128) weight_simt_kernel(const WeightParams p) 
 //
 // Roles (11 warps, one CTA per SM, a contiguous share of all 128-key tiles each):
 //   warps 0-3 / 4-7  the tiles of even / odd number: S from TMEM, exponentials,
-//                    row sum, the total's update; all eight stage Q and the
-//                    rows' lse when a kv-head begins
-//   warps 8, 10      producers: a warp issues a TMA box every ~110 cycles, so the
+//                    row sum, the total's update; all stage Q and the rows' lse
+//                    when a kv-head begins.  More than 160 rows without score
+//                    shaping: sixteen warps, two warpgroups to a tile with half of
+//                    its rows each (eight left the latency of the exponentials in
+//                    the open)
+//   warp 8           producer; two of them (8 and 10) for pages below 64 rows and
+//                    for gathers: a warp issues a TMA box every ~110 cycles, so the
 //                    sixteen of a tile of 16-row pages took one warp longer than
 //                    HBM takes for the tile (64 sequences: 150 us with one, 125
-//                    with two, 134 with three); boxes of 64 rows are left to one
-//                    (109 against 111 us), gathers take both
+//                    with two, 134 with three; boxes of 64 rows 109 against 111 us)
 //   warp 9           MMA issuer, owns TMEM (two S buffers)
 constexpr int kWtTile = 128;
 constexpr int kWtRows = 256;  // rows of one pass (N of the MMA)
 constexpr int kWtMaxStages = 6;
-constexpr int kWtThreads = 352;
 
 struct WtSeg {
   int b, h;
@@ -203,17 +205,21 @@ struct WtSmem {  // offsets after the Q rows and the stages
   static constexpr int kLse = kMisc + 16;              // float [256]: -lse (-inf: no such row)
   static constexpr int kSlope = kLse + kWtRows * 4;    // float [256]: -slope
   static constexpr int kTok = kSlope + kWtRows * 4;    // float [256]: accepted rank of the row
-  static constexpr int kPlan = kTok + kWtRows * 4;     // int [S + 1]
+  static constexpr int kPart = kTok + kWtRows * 4;     // float [2][2][128]: the second half's row sums
+  static constexpr int kPlan = kPart + 4 * 128 * 4;    // int [S + 1]
 };
 
-template <int D, bool kTma, bool kMod, int kProducers>
-__global__ void __launch_bounds__(kWtThreads, 1)
+// kGroups: warpgroups that sum (2, or 4 = two to a tile).
+template <int D, bool kTma, bool kMod, int kProducers, int kGroups>
+__global__ void __launch_bounds__((4 * kGroups + 3) * 32, 1)
     weight_tc_kernel(const WeightParams p, const __grid_constant__ CUtensorMap tmk, int RQ, int NS) {
   constexpr int TK = kWtTile;
   constexpr int kHalves = D / 64;
   constexpr int kStage = kHalves * TK * 128;
-  constexpr int kSoft = 256, kProducer = 8, kMma = 9;
-  constexpr int kBarQ = 1, kBarSoft = 2, kBarEnd = 3;
+  constexpr int kThreads = (4 * kGroups + 3) * 32;
+  constexpr int kSoft = 128 * kGroups, kProducer = 4 * kGroups, kMma = kProducer + 1;
+  constexpr int kPad = 16 * kGroups;  // S columns: whole 32-column loads of each half
+  constexpr int kBarQ = 1, kBarSoft = 2, kBarEnd = 3, kBarPair = 4;  // kBarPair + S buffer
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t *sQ = smem;  // [D/64 columns][RQ rows][128 B], 128-byte swizzle
@@ -238,13 +244,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(s_empty + i, 128);
+      mbar_init(s_empty + i, 64 * kGroups);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  for (int s = tid; s < S; s += kWtThreads)
+  for (int s = tid; s < S; s += kThreads)
     tstart[s] = (wt_seg(p, s, blockIdx.x == 0 && p.row0 == 0 && s % p.Hkv == 0).nkeys + TK - 1) / TK;
   __syncthreads();
   if (warp == 0) warp_scan_inplace(tstart, S);
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       const int lt0 = max(tstart[s], t0) - tstart[s], lt1 = min(tstart[s + 1], t1) - tstart[s];
       if (lt0 >= lt1 || !live(g, lt1 - 1)) continue;
       named_bar_sync(kBarQ, kSoft + 32);  // Q of this kv-head is in shared memory
-      const uint32_t idesc = umma_idesc(128, (g.R + 31) & ~31, 0, 0);
+      const uint32_t idesc = umma_idesc(128, (g.R + kPad - 1) & ~(kPad - 1), 0, 0);
       for (int lt = lt0; lt < lt1; ++lt) {
         if (!live(g, lt)) continue;
         const int b = jt & 1;
@@ -412,15 +418,16 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   }
 
   // ============================ sums over the rows ============================
-  const int wg = warp >> 2;            // takes the live tiles jt = wg mod 2
-  const int key_l = tid & 127;         // key of the tile = TMEM lane
-  const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 * wg;
+  const int wg = (warp >> 2) / (kGroups / 2);  // S buffer: takes the live tiles jt = wg mod 2
+  const int half = kGroups == 4 ? (warp >> 2) & 1 : 0;  // half of the rows
+  const int key_l = tid & 127;                 // key of the tile = TMEM lane
+  float *s_part = reinterpret_cast<float *>(rest + WtSmem::kPart) + wg * 128 + key_l;
   int jt = 0;
   for (int s = s0; s < S && tstart[s] < t1; ++s) {
     const WtSeg g = wt_seg(p, s, false);
     const int lt0 = max(tstart[s], t0) - tstart[s], lt1 = min(tstart[s + 1], t1) - tstart[s];
     if (lt0 >= lt1) continue;
-    const int NP = (g.R + 31) & ~31;  // columns of S: whole 32-column loads
+    const int NP = (g.R + kPad - 1) & ~(kPad - 1);  // columns of S
     const bool any = live(g, lt1 - 1);  // (tiles turn live once)
     if (any) {
       named_bar_sync(kBarSoft, kSoft);  // every MMA that reads Q has completed (all tiles were waited for)
@@ -473,10 +480,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     };
     bool have_next = false;
     float next_old = 0.f;
+    const int NH = kGroups == 4 ? NP / 2 : NP;  // this warpgroup's columns
+    const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 * wg + half * NH;
+    const float *w_nlse = s_nlse + half * NH, *w_slope = s_slope + half * NH, *w_tok = s_tok + half * NH;
     for (int lt = lt0; lt < lt1; ++lt) {
       const int key = lt * TK + key_l;
       if (!live(g, lt)) {
-        if ((lt & 1) == wg && key < g.nkeys) w[key] *= p.decay;
+        if ((lt & 1) == wg && half == 0 && key < g.nkeys) w[key] *= p.decay;
         continue;
       }
       const int mine = (jt & 1) == wg;
@@ -485,9 +495,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       if (!mine) continue;
       // what the total keeps (row0 > 0: a later pass adds to the earlier ones'),
       // loaded while this warpgroup works on its tile before
-      const float old = have_next ? next_old : total_of(key);
+      const float old = have_next ? next_old : half == 0 ? total_of(key) : 0.f;
       have_next = lt + 2 < lt1;
-      next_old = have_next ? total_of(key + 2 * TK) : 0.f;
+      next_old = have_next && half == 0 ? total_of(key + 2 * TK) : 0.f;
       const bool masked = lt * TK < g.hi || lt * TK + TK > n_old;
       const float koff = (float)(key - n_old);
       const bool there = key >= g.lo && key < g.nkeys;
@@ -502,8 +512,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         if (kMod && p.mod.slopes != nullptr) {
 #pragma unroll
           for (int r = 0; r < 32; r += 2) {
-            const float2 ns = *reinterpret_cast<const float2 *>(s_slope + c0 + r);
-            const float2 tk = *reinterpret_cast<const float2 *>(s_tok + c0 + r);
+            const float2 ns = *reinterpret_cast<const float2 *>(w_slope + c0 + r);
+            const float2 tk = *reinterpret_cast<const float2 *>(w_tok + c0 + r);
             x[r] = fmaf(ns.x, fabsf(tk.x - koff), x[r] * mul);
             x[r + 1] = fmaf(ns.y, fabsf(tk.y - koff), x[r + 1] * mul);
           }
@@ -511,11 +521,11 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         const float mul2nd = kMod && p.mod.slopes != nullptr ? 1.f : mul;
 #pragma unroll
         for (int r = 0; r < 32; r += 4) {
-          const float4 nl = *reinterpret_cast<const float4 *>(s_nlse + c0 + r);
+          const float4 nl = *reinterpret_cast<const float4 *>(w_nlse + c0 + r);
           float2 d[2] = {fma2(make_float2(x[r], x[r + 1]), make_float2(mul2nd, mul2nd), make_float2(nl.x, nl.y)),
                          fma2(make_float2(x[r + 2], x[r + 3]), make_float2(mul2nd, mul2nd), make_float2(nl.z, nl.w))};
           if constexpr (decltype(edge)::value) {
-            const float4 tk = *reinterpret_cast<const float4 *>(s_tok + c0 + r);
+            const float4 tk = *reinterpret_cast<const float4 *>(w_tok + c0 + r);
             if (!(there && koff <= tk.x && tk.x - koff < window)) d[0].x = -INFINITY;
             if (!(there && koff <= tk.y && tk.y - koff < window)) d[0].y = -INFINITY;
             if (!(there && koff <= tk.z && tk.z - koff < window)) d[1].x = -INFINITY;
@@ -533,20 +543,20 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       tc_fence_after();
       uint32_t ua[32];
       tmem_ld32(tS, ua);
-      if (masked || kMod) {  // (the cap and the bias leave no registers to load ahead)
-        for (int c0 = 0; c0 < NP; c0 += 32) {
+      if (masked || kMod || kGroups == 4) {  // (no registers to load ahead, or warps enough)
+        for (int c0 = 0; c0 < NH; c0 += 32) {
           if (c0 > 0) tmem_ld32(tS + c0, ua);
           tmem_ld_wait32(ua);
-          if (c0 + 32 >= NP) release();
+          if (c0 + 32 >= NH) release();
           if (masked) rows32(ua, c0, std::true_type());
-          else if constexpr (kMod) rows32(ua, c0, std::false_type());
+          else if constexpr (kMod || kGroups == 4) rows32(ua, c0, std::false_type());
         }
       } else {
         // the next columns are on their way from TMEM while these are summed
         uint32_t ub[32];
         tmem_ld_wait32(ua);
-        for (int c0 = 0; c0 < NP; c0 += 64) {
-          const bool two = c0 + 32 < NP, more = c0 + 64 < NP;
+        for (int c0 = 0; c0 < NH; c0 += 64) {
+          const bool two = c0 + 32 < NH, more = c0 + 64 < NH;
           if (two) tmem_ld32(tS + c0 + 32, ub);
           else release();
           rows32(ua, c0, std::false_type());
@@ -558,7 +568,16 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           if (more) tmem_ld_wait32(ua);
         }
       }
-      const float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+      float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+      if constexpr (kGroups == 4) {
+        // the halves' sums meet in shared memory, in the slot of the tile's parity:
+        // the slot is written again two tiles on, after the next barrier
+        float *slot = s_part + ((jt >> 1) & 1) * 256;
+        if (half == 1) *slot = sum;
+        named_bar_sync(kBarPair + wg, 256);
+        if (half == 1) continue;
+        sum += *slot;
+      }
       if (ok && key < g.nkeys) w[key] = p.row0 > 0 ? old + sum : fmaf(p.decay, old, sum);
     }
   }
@@ -566,32 +585,37 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   named_bar_sync(kBarEnd, kSoft + 32);
 }
 
-template <int D, bool kTma, bool kMod, int kProducers>
+template <int D, bool kTma, bool kMod, int kProducers, int kGroups>
 static cudaError_t launch_weight_tc(const WeightParams &p, const CUtensorMap &tmk, int grid, cudaStream_t stream) {
   const int rows = p.Hq / p.Hkv * p.T - p.row0;
-  const int RQ = rows >= kWtRows ? kWtRows : (rows + 31) & ~31;
+  const int pad = 16 * kGroups;
+  const int RQ = rows >= kWtRows ? kWtRows : (rows + pad - 1) & ~(pad - 1);
   const size_t fixed = 1024 + (size_t)(D / 64) * RQ * 128 + WtSmem::kPlan + (size_t)(p.B * p.Hkv + 1) * 4;
   const size_t stage = (size_t)(D / 64) * kWtTile * 128;
   int NS = (int)((232448 - fixed) / stage);
   if (NS > kWtMaxStages) NS = kWtMaxStages;
   const size_t smem = fixed + NS * stage;
-  auto kern = weight_tc_kernel<D, kTma, kMod, kProducers>;
+  auto kern = weight_tc_kernel<D, kTma, kMod, kProducers, kGroups>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kWtThreads, smem, stream>>>(p, tmk, RQ, NS);
+  kern<<<grid, (4 * kGroups + 3) * 32, smem, stream>>>(p, tmk, RQ, NS);
   return cudaGetLastError();
+}
+
+template <int D, bool kTma, int kProducers>
+static cudaError_t launch_weight_p(const WeightParams &p, const CUtensorMap &tmk, int grid, cudaStream_t stream) {
+  if (p.mod.on) return launch_weight_tc<D, kTma, true, kProducers, 2>(p, tmk, grid, stream);
+  // 8 x 128K keys, one warpgroup a tile against two: 160 rows 50.9 / 51.7 us, 192 rows
+  // 57.9 / 52.1, 256 rows 72.8 / 65.7
+  return p.Hq / p.Hkv * p.T - p.row0 > 160 ? launch_weight_tc<D, kTma, false, kProducers, 4>(p, tmk, grid, stream)
+                                           : launch_weight_tc<D, kTma, false, kProducers, 2>(p, tmk, grid, stream);
 }
 
 template <int D>
 static cudaError_t launch_weight_bf16(const WeightParams &p, const CUtensorMap &tmk, int grid, cudaStream_t stream) {
-  if (p.tma_box == 64)
-    return p.mod.on ? launch_weight_tc<D, true, true, 1>(p, tmk, grid, stream)
-                    : launch_weight_tc<D, true, false, 1>(p, tmk, grid, stream);
-  if (p.tma_box > 0)
-    return p.mod.on ? launch_weight_tc<D, true, true, 2>(p, tmk, grid, stream)
-                    : launch_weight_tc<D, true, false, 2>(p, tmk, grid, stream);
-  return p.mod.on ? launch_weight_tc<D, false, true, 2>(p, tmk, grid, stream)
-                  : launch_weight_tc<D, false, false, 2>(p, tmk, grid, stream);
+  return p.tma_box == 64  ? launch_weight_p<D, true, 1>(p, tmk, grid, stream)
+         : p.tma_box > 0  ? launch_weight_p<D, true, 2>(p, tmk, grid, stream)
+                          : launch_weight_p<D, false, 2>(p, tmk, grid, stream);
 }
 
 // fp32: one thread per key (no TF32).  bf16: one pass of the tensor-core kernel
