@@ -655,7 +655,8 @@ def rope_oracle_sample(B=4):
 # (dram__bytes_read.sum + dram__bytes_write.sum, the --set full capture of
 # `bench.py --profile <config>`), valid only while the sources that kernel is
 # built from hash to those captured.
-_HEADERS = ['va_common.cuh', 'va_pipeline.cuh', 'va_tcgen05.cuh', 'va_kernels.h', 'va_rope_fused.cuh', 'va_merge.cuh']
+_HEADERS = ['va_common.cuh', 'va_pipeline.cuh', 'va_mod.cuh', 'va_tcgen05.cuh', 'va_kernels.h', 'va_rope_fused.cuh',
+            'va_merge.cuh']
 KERNEL_SOURCES = {"tc": ["va_attn_tc.cu"] + _HEADERS, "tck": ["va_attn_tck.cu", "va_attn_tck.cuh"] + _HEADERS}
 PROFILED_TRAFFIC = {
     "tree": {"sources": "tc", "sha256": "5f3eb81cd915d48d4d7ded3a3450edc49e011db4a13bdb337279b5b9734ee886",

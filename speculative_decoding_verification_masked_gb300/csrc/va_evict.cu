@@ -16,7 +16,10 @@
 // words it was given.
 //
 // Bound by HBM: 2 x 2 x row bytes a kept row (K and V, read and written).
-// Chunks of 32 KB and up to six blocks an SM keep 190 KB an SM in flight.
+// Chunks of 32 KB and up to six blocks an SM keep 190 KB an SM in flight: 16
+// sequences cut to 8192 rows of 8 kv-heads (1.09 GB) take 199 us, 5.5 TB/s, 82%
+// of the measured copy rate.  Chunks of half that size took 207 to 218 us, blocks
+// of twice the threads 244 us; divisions in the copy loops had cost 268 us.
 #include <mutex>
 
 #include "va_common.cuh"
