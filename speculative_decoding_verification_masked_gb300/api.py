@@ -396,18 +396,22 @@ def verify_head_importance(q, k_cache, seqlens, heads, score=None, score_stride=
 # score shaping, accumulated attention weight, eviction
 # ----------------------------------------------------------------------------
 
-def _arg(t, name, shape, dtype, device):
-    """Device pointer of a contiguous tensor of this shape, type and device; None stays None."""
+_I32, _F32 = torch.int32, torch.float32
+
+
+def _arg(t, name, shape, dtype, dev):
+    """Device pointer of a contiguous tensor of this shape and type on GPU `dev`; None stays None."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor or None")
-    if t.dtype is dtype and t.shape == shape and t.get_device() == device.index and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name}: expected a torch.Tensor or None") from None
     if not t.is_cuda:
         raise ValueError("tensor arguments must live on the GPU")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, q or the cache on {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, q or the cache on cuda:{dev}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -415,55 +419,55 @@ def _arg(t, name, shape, dtype, device):
     raise ValueError("tensor arguments must be contiguous")
 
 
-def _req(t, name, shape, dtype, device):
+def _req(t, name, shape, dtype, dev):
     """The same for an argument that has to be given."""
     if t is None:
         raise TypeError(f"{name}: expected a torch.Tensor")
-    return _arg(t, name, shape, dtype, device)
+    return _arg(t, name, shape, dtype, dev)
 
 
-def _cache_args(layout, k, B, Hkv, D, table, device):
-    """Geometry arguments of a cache k: [cache length], or [pages, page size, table, table width]."""
-    n0, n1 = k.shape[:2]
-    if layout == "dense":
-        if n0 != B:
-            raise ValueError(f"the key cache: expected {B} sequences, got {n0}")
-        return [n1]
-    _need(table, "page_table", 2)
-    width = table.shape[1]
-    return [n0, n1, _arg(table, "page_table", (B, width), torch.int32, device), width]
-
-
-def _need(t, name, dim):
+def _sizes(t, name, dim):
+    """Sizes of a GPU tensor of `dim` dimensions."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError("tensor arguments must live on the GPU")
     if t.dim() != dim:
         raise ValueError(f"{name}: expected {dim} dimensions, got {list(t.shape)}")
+    return t.shape
 
 
-def _run_on(device, stream, name, *args):
-    """Call library function `name` with `device` current, on `stream` (that
-    device's current stream by default); args end before the stream."""
+def _cache_args(layout, n0, n1, B, table, dev):
+    """Geometry arguments of a cache: [cache length], or [pages, page size, table, table width]."""
+    if layout == "dense":
+        if n0 != B:
+            raise ValueError(f"the key cache: expected {B} sequences, got {n0}")
+        return (n1,)
+    width = _sizes(table, "page_table", 2)[1]
+    return n0, n1, _arg(table, "page_table", (B, width), _I32, dev), width
+
+
+def _run_on(dev, stream, name, *args):
+    """Call library function `name` with GPU `dev` current, on `stream` (that GPU's
+    current stream by default); args end before the stream."""
     f = getattr(_lib or lib(), name)
-    s = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
-        _check(f(*args, s))
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        status = f(*args, s)
     else:
-        with torch.cuda.device(device):
-            _check(f(*args, s))
+        with torch.cuda.device(dev):
+            status = f(*args, s)
+    if status != VA_OK:
+        _check(status)
 
 
-def _made(make, device, stream):
+def _made(make, dev, stream):
     """What make() allocates for a call on `stream`, from that stream's memory pool: neither
     the memory's last user nor its next one overlaps with the call."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return make()
-    if torch.cuda.current_device() == device.index:
-        return make()
-    with torch.cuda.device(device):
+    with torch.cuda.device(dev):
         return make()
 
 
@@ -477,37 +481,33 @@ class ScoreMod:
         self.softcap, self.window = float(softcap), int(window)
         self.slopes, self.key_start, self.token_pos = slopes, key_start, token_pos
 
-    def struct(self, B, T, Hq, device) -> VaScoreMod:
-        return VaScoreMod(self.softcap, self.window, _arg(self.slopes, "slopes", (Hq,), torch.float32, device),
-                          _arg(self.key_start, "key_start", (B,), torch.int32, device),
-                          _arg(self.token_pos, "token_pos", (B, T), torch.int32, device))
+    def struct(self, B, T, Hq, dev) -> VaScoreMod:
+        return VaScoreMod(self.softcap, self.window, _arg(self.slopes, "slopes", (Hq,), _F32, dev),
+                          _arg(self.key_start, "key_start", (B,), _I32, dev),
+                          _arg(self.token_pos, "token_pos", (B, T), _I32, dev))
 
 
 def _mod_call(layout, q, k, v, table, seqlens, mod, tree_parent, tree_mask, out, lse, workspace, scale, stream):
-    _need(q, "q", 4)
-    _need(k, "the key cache", 4)
-    B, T, Hq, D = q.shape
-    n0, n1, Hkv, _ = k.shape
-    dev = q.device
+    B, T, Hq, D = rows = _sizes(q, "q", 4)
+    n0, n1, Hkv, _ = _sizes(k, "the key cache", 4)
+    dev, dtype, cache = q.get_device(), q.dtype, (n0, n1, Hkv, D)
     if not isinstance(mod, ScoreMod):
         raise TypeError("mod: expected a ScoreMod")
-    shape = _shape_of(q, Hkv, scale)
+    shape = VaShape(B, T, Hq, Hkv, D, _dtype_code(q), D ** -0.5 if scale is None else scale, 0.0)
     if out is None or lse is None:
         out, lse = _made(lambda: _outputs(q, out, lse), dev, stream)
-    kv = [_arg(q, "q", (B, T, Hq, D), q.dtype, dev), _arg(k, "the key cache", (n0, n1, Hkv, D), q.dtype, dev),
-          _req(v, "the value cache", (n0, n1, Hkv, D), q.dtype, dev)]
-    geo = _cache_args(layout, k, B, Hkv, D, table, dev)
-    m = mod.struct(B, T, Hq, dev)
-    rest = [_req(seqlens, "seqlens", (B,), torch.int32, dev), _arg(tree_parent, "tree_parent", (B, T), torch.int32, dev),
-            _arg(tree_mask, "tree_mask", (B, T, (T + 31) // 32), torch.int32, dev),
-            _arg(out, "out", (B, T, Hq, D), q.dtype, dev), _arg(lse, "lse", (B, Hq, T), torch.float32, dev)]
     ws = workspace
     if ws is None:
-        ws = _made(lambda: Workspace.for_shape(shape, dev, stream), dev, stream)
-    elif ws.buffer.device != dev:
-        raise ValueError(f"workspace is on {ws.buffer.device}, q on {dev}")
-    _run_on(dev, stream, f"verify_attn_{layout}_mod", ctypes.byref(shape), ctypes.byref(m), *kv, *geo, *rest, ws.ptr,
-            ws.nbytes)
+        ws = _made(lambda: Workspace.for_shape(shape, q.device, stream), dev, stream)
+    elif ws.buffer.get_device() != dev:
+        raise ValueError(f"workspace is on {ws.buffer.device}, q on cuda:{dev}")
+    _run_on(dev, stream, "verify_attn_dense_mod" if layout == "dense" else "verify_attn_paged_mod",
+            ctypes.byref(shape), ctypes.byref(mod.struct(B, T, Hq, dev)), _arg(q, "q", rows, dtype, dev),
+            _arg(k, "the key cache", cache, dtype, dev), _req(v, "the value cache", cache, dtype, dev),
+            *_cache_args(layout, n0, n1, B, table, dev), _req(seqlens, "seqlens", (B,), _I32, dev),
+            _arg(tree_parent, "tree_parent", (B, T), _I32, dev),
+            _arg(tree_mask, "tree_mask", (B, T, (T + 31) // 32), _I32, dev), _arg(out, "out", rows, dtype, dev),
+            _arg(lse, "lse", (B, Hq, T), _F32, dev), ws.ptr, ws.nbytes)
     return out, lse
 
 
@@ -525,33 +525,29 @@ def verify_attn_paged_mod(q, k_pages, v_pages, page_table, seqlens, mod: ScoreMo
                      workspace, scale, stream)
 
 
-def _status_ptr(workspace, device):
+def _status_ptr(workspace, dev):
     if workspace is None:
         return None
-    if workspace.buffer.device != device:
-        raise ValueError(f"workspace is on {workspace.buffer.device}, the cache on {device}")
+    if workspace.buffer.get_device() != dev:
+        raise ValueError(f"workspace is on {workspace.buffer.device}, the cache on cuda:{dev}")
     return workspace.ptr
 
 
 def _weight_call(layout, q, k, table, seqlens, lse, weight, mod, path, n_accept, decay, scale, workspace, stream):
-    _need(q, "q", 4)
-    _need(k, "the key cache", 4)
-    _need(weight, "weight", 3)
-    B, T, Hq, D = q.shape
-    n0, n1, Hkv, _ = k.shape
-    dev = q.device
-    shape = _shape_of(q, Hkv, scale)
+    B, T, Hq, D = rows = _sizes(q, "q", 4)
+    n0, n1, Hkv, _ = _sizes(k, "the key cache", 4)
+    stride = _sizes(weight, "weight", 3)[2]
+    dev, dtype = q.get_device(), q.dtype
+    shape = VaShape(B, T, Hq, Hkv, D, _dtype_code(q), D ** -0.5 if scale is None else scale, 0.0)
     if mod is not None and not isinstance(mod, ScoreMod):
         raise TypeError("mod: expected a ScoreMod or None")
-    m = mod.struct(B, T, Hq, dev) if mod is not None else None
-    geo = _cache_args(layout, k, B, Hkv, D, table, dev)
-    stride = weight.shape[2]
-    _run_on(dev, stream, f"verify_accumulate_weight_{layout}", ctypes.byref(shape),
-            ctypes.byref(m) if m is not None else None, _arg(q, "q", (B, T, Hq, D), q.dtype, dev),
-            _arg(k, "the key cache", (n0, n1, Hkv, D), q.dtype, dev), *geo, _req(seqlens, "seqlens", (B,), torch.int32, dev),
-            _arg(path, "path", (B, T), torch.int32, dev), _arg(n_accept, "n_accept", (B,), torch.int32, dev),
-            _req(lse, "lse", (B, Hq, T), torch.float32, dev), float(decay),
-            _arg(weight, "weight", (B, Hkv, stride), torch.float32, dev), stride, _status_ptr(workspace, dev))
+    _run_on(dev, stream, "verify_accumulate_weight_dense" if layout == "dense" else "verify_accumulate_weight_paged",
+            ctypes.byref(shape), ctypes.byref(mod.struct(B, T, Hq, dev)) if mod is not None else None,
+            _arg(q, "q", rows, dtype, dev), _arg(k, "the key cache", (n0, n1, Hkv, D), dtype, dev),
+            *_cache_args(layout, n0, n1, B, table, dev), _req(seqlens, "seqlens", (B,), _I32, dev),
+            _arg(path, "path", (B, T), _I32, dev), _arg(n_accept, "n_accept", (B,), _I32, dev),
+            _req(lse, "lse", (B, Hq, T), _F32, dev), decay, _arg(weight, "weight", (B, Hkv, stride), _F32, dev), stride,
+            _status_ptr(workspace, dev))
     return weight
 
 
@@ -582,32 +578,24 @@ class EvictScratch(Workspace):
 
 
 def _evict_call(layout, k, v, table, seqlens, indices, n_indices, weight, seqlens_out, scratch, workspace, stream):
-    _need(k, "the key cache", 4)
-    _need(indices, "indices", 3)
-    n0, n1, Hkv, D = k.shape
-    B = indices.shape[0]
-    dev = k.device
+    n0, n1, Hkv, D = cache = _sizes(k, "the key cache", 4)
+    B, _, m = _sizes(indices, "indices", 3)
+    stride = _sizes(weight, "weight", 3)[2] if weight is not None else 0
+    dev, dtype = k.get_device(), k.dtype
     if seqlens_out is None:
-        seqlens_out = _made(lambda: torch.empty(B, dtype=torch.int32, device=dev), dev, stream)
-    shape = make_shape(B, 1, Hkv, Hkv, D, _dtype_code(k), 1.0)
-    geo = _cache_args(layout, k, B, Hkv, D, table, dev)
-    if weight is not None:
-        _need(weight, "weight", 3)
-    m, stride = indices.shape[2], weight.shape[2] if weight is not None else 0
-    args = [_arg(k, "the key cache", (n0, n1, Hkv, D), k.dtype, dev),
-            _req(v, "the value cache", (n0, n1, Hkv, D), k.dtype, dev),
-            *geo, _req(seqlens, "seqlens", (B,), torch.int32, dev),
-            _arg(indices, "indices", (B, Hkv, m), torch.int32, dev),
-            _req(n_indices, "n_indices", (B, Hkv), torch.int32, dev), m,
-            _arg(weight, "weight", (B, Hkv, stride), torch.float32, dev), stride,
-            _arg(seqlens_out, "seqlens_out", (B,), torch.int32, dev)]
+        seqlens_out = _made(lambda: torch.empty(B, dtype=_I32, device=k.device), dev, stream)
+    shape = VaShape(B, 1, Hkv, Hkv, D, _dtype_code(k), 1.0, 0.0)
     sc = scratch
     if sc is None:
-        sc = _made(lambda: EvictScratch(B, Hkv, max(m, 1), dev, stream), dev, stream)
-    elif sc.buffer.device != dev:
-        raise ValueError(f"scratch is on {sc.buffer.device}, the cache on {dev}")
-    _run_on(dev, stream, f"verify_evict_kv_{layout}", ctypes.byref(shape), *args, sc.ptr, sc.nbytes,
-            _status_ptr(workspace, dev))
+        sc = _made(lambda: EvictScratch(B, Hkv, max(m, 1), k.device, stream), dev, stream)
+    elif sc.buffer.get_device() != dev:
+        raise ValueError(f"scratch is on {sc.buffer.device}, the cache on cuda:{dev}")
+    _run_on(dev, stream, "verify_evict_kv_dense" if layout == "dense" else "verify_evict_kv_paged", ctypes.byref(shape),
+            _arg(k, "the key cache", cache, dtype, dev), _req(v, "the value cache", cache, dtype, dev),
+            *_cache_args(layout, n0, n1, B, table, dev), _req(seqlens, "seqlens", (B,), _I32, dev),
+            _arg(indices, "indices", (B, Hkv, m), _I32, dev), _req(n_indices, "n_indices", (B, Hkv), _I32, dev), m,
+            _arg(weight, "weight", (B, Hkv, stride), _F32, dev), stride,
+            _arg(seqlens_out, "seqlens_out", (B,), _I32, dev), sc.ptr, sc.nbytes, _status_ptr(workspace, dev))
     return seqlens_out
 
 
