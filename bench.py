@@ -659,14 +659,14 @@ _HEADERS = ['va_common.cuh', 'va_pipeline.cuh', 'va_mod.cuh', 'va_tcgen05.cuh', 
             'va_merge.cuh']
 KERNEL_SOURCES = {"tc": ["va_attn_tc.cu"] + _HEADERS, "tck": ["va_attn_tck.cu", "va_attn_tck.cuh"] + _HEADERS}
 PROFILED_TRAFFIC = {
-    "tree": {"sources": "tc", "sha256": "5f3eb81cd915d48d4d7ded3a3450edc49e011db4a13bdb337279b5b9734ee886",
-             "kernel": "verify_attn_tc_kernel<2, TMA>", "bytes": 541492736},
-    "chain": {"sources": "tck", "sha256": "82f27a4640fe712ccc1c3bc4dc5d7408724acaa1eecde6bd4dd2565ec887c29c",
-              "kernel": "verify_attn_tck_kernel<32, TMA>", "bytes": 138061568},
-    "sparse": {"sources": "tck", "sha256": "82f27a4640fe712ccc1c3bc4dc5d7408724acaa1eecde6bd4dd2565ec887c29c",
-               "kernel": "verify_attn_tck_kernel<32, gather>", "bytes": 141492480},
-    "paged": {"sources": "tck", "sha256": "82f27a4640fe712ccc1c3bc4dc5d7408724acaa1eecde6bd4dd2565ec887c29c",
-              "kernel": "verify_attn_tck_kernel<64, TMA>", "bytes": 1470916864},
+    "tree": {"sources": "tc", "sha256": "7b9f965fee8dbed1536d4f00c1fbb68915885b5aa3b4ee8984f4273cc8b5bed9",
+             "kernel": "verify_attn_tc_kernel<2, TMA>", "bytes": 541137664},
+    "chain": {"sources": "tck", "sha256": "5d86bd6ee620aa41a45863f1038d1da708a519247a893b79f457dd05351e46a0",
+              "kernel": "verify_attn_tck_kernel<128, 32, TMA>", "bytes": 137639680},
+    "sparse": {"sources": "tck", "sha256": "5d86bd6ee620aa41a45863f1038d1da708a519247a893b79f457dd05351e46a0",
+               "kernel": "verify_attn_tck_kernel<128, 32, gather>", "bytes": 140720896},
+    "paged": {"sources": "tck", "sha256": "5d86bd6ee620aa41a45863f1038d1da708a519247a893b79f457dd05351e46a0",
+              "kernel": "verify_attn_tck_kernel<128, 64, TMA>", "bytes": 1470595072},
 }
 
 
