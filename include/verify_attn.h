@@ -443,7 +443,8 @@ va_status verify_commit_kv_paged(const va_shape *shape, void *k_pages, void *v_p
  *     rotates), 16-byte aligned; lse [B][Hq][T]; path [B][T] int32 as
  *     verify_accept_greedy returns it (NULL: path[i] = i), n_accept [B] int32
  *     (NULL: T).  Rows with lse = -inf add nothing.
- *   decay in [0, 1]; weight fp32 [B][Hkv][weight_stride].
+ *   decay in [0, 1] (0: the old totals are not read, so they may hold
+ *     anything); weight fp32 [B][Hkv][weight_stride].
  *   Dense: k_cache [B][max_cache_len][Hkv][D].  Paged: as verify_attn_paged.
  * L_b + a must fit the cache and weight_stride, and path entries [0, T)
  * (device-checked: a bad sequence is left alone, a bad path entry adds

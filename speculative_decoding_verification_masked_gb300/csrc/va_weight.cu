@@ -8,6 +8,7 @@
 // chain.  With the rows' log-sum-exp known from the verification call,
 //   p(h, i, j) = exp(s(q[path[i]][h], k_j) - lse[h][path[i]]),  j <= L_b + i,
 //   w[g][j]    = (j < L_b ? decay * w[g][j] : 0) + sum over h of g and i of p.
+// With decay 0 the old totals are not read: they may be memory never written.
 // No softmax pass and no V: K is read once, every total by one thread, in a
 // fixed order (the result does not depend on the grid).
 #include <cuda_bf16.h>
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(128) weight_simt_kernel(const WeightParams p) 
   }
   if (j < L + a) {
     float *w = p.weight + ((size_t)b * p.Hkv + h) * p.stride + j;
-    *w = j < L ? fmaf(p.decay, *w, acc) : acc;
+    *w = j < L && p.decay != 0.f ? fmaf(p.decay, *w, acc) : acc;
   }
 }
 
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__((4 * kGroups + 3) * 32, 1)
     for (int lt = lt0; lt < lt1; ++lt) {
       const int key = lt * TK + key_l;
       if (!live(g, lt)) {
-        if ((lt & 1) == wg && half == 0 && key < g.nkeys) w[key] *= p.decay;
+        if ((lt & 1) == wg && half == 0 && key < g.nkeys) w[key] = p.decay != 0.f ? w[key] * p.decay : 0.f;
         continue;
       }
       const int mine = (jt & 1) == wg;

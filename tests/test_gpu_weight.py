@@ -123,6 +123,23 @@ def test_new_slots_start_from_nothing_and_stale_totals_may_be_nan():
     assert np.isnan(got[0, :, 133:]).all()
 
 
+@pytest.mark.parametrize("form", ["bf16 d128", "bf16 d64", "fp32 d64"])
+@pytest.mark.parametrize("kw", [dict(), dict(window=30)], ids=["plain", "window"])
+def test_decay_zero_does_not_read_the_old_totals(form, kw):
+    """Totals that were never written (NaN) are replaced, where rows see the key
+    and where none does, and in a step that accepts nothing."""
+    dtype, D, T, Hq, Hkv, page = FORMS[form]
+    c = shaped.make(5, [400, 60], T, Hq, Hkv, D, dtype, page, **kw)
+    path, acc, lse, weight = _inputs(c, 1, [4, 0])
+    weight[:] = 0.0
+    want = shaped.accumulate(c, path, acc, lse, 0.0, weight)
+    w = shaped.dev(weight)
+    for b, n in enumerate([400, 60]):
+        w[b, :, :n] = float("nan")
+    shaped.run_weight(va, c, shaped.dev(lse), w, path=shaped.dev(path), n_accept=shaped.dev(acc), decay=0.0)
+    _check(w.cpu().numpy(), want, c, acc, weight)
+
+
 @pytest.mark.parametrize("page", [0, 16, 2])
 def test_hidden_keys_and_rows_without_keys(page):
     """NaN keys below the window, -1 page entries there, and rows whose lse is
