@@ -241,21 +241,30 @@ va_status check_mod(const va_score_mod &m, float scale, float unit, bool draft_m
   mp.softcap = m.softcap;
   mp.in_mul = m.softcap > 0.f ? scale / m.softcap : 0.f;
   mp.out_mul = (m.softcap > 0.f ? m.softcap : scale) * unit;
-  // tanh(y) / y as a polynomial of y^2 on |y| <= 0.75 (see cap_scores), with
-  // y = raw * in_mul, the cap and the unit folded in.  Coefficients that leave
-  // fp32's range (an extreme ratio of scale and cap) switch it off.
-  static const double poly[6] = {1.0,          -0.33332958817481995, 0.1332540661096573, -0.05334445461630821,
-                                 0.019582949578762054, -0.004716284107416868};
-  mp.small_lim = -1.f;
-  if (m.softcap > 0.f) {
+  // tanh(y) / y as polynomials of y^2 on |y| <= 0.45 and 0.75 (see
+  // cap_scores), with y = raw * in_mul, the cap and the unit folded in.
+  // Coefficients that leave fp32's range (an extreme ratio of scale and cap)
+  // switch one off.
+  static const double poly4[4] = {0.9999997567324063, -0.33329467152321846, 0.13236368607993834, -0.046028179312785855};
+  static const double poly6[6] = {1.0,          -0.33332958817481995, 0.1332540661096573, -0.05334445461630821,
+                                  0.019582949578762054, -0.004716284107416868};
+  const struct {
+    const double *poly;
+    int n;
+    double lim;
+    float *c;
+  } small[2] = {{poly4, 4, 0.45, mp.small_c4}, {poly6, 6, 0.75, mp.small_c6}};
+  for (int i = 0; i < 2; ++i) {
+    mp.small_lim[i] = -1.f;
+    if (!(m.softcap > 0.f)) continue;
     const double in = (double)scale / m.softcap;
     bool fits = true;
-    for (int k = 0; k < 6; ++k) {
-      const double c = poly[k] * pow(in, 2.0 * k) * scale * unit;
-      mp.small_c[k] = (float)c;
+    for (int k = 0; k < small[i].n; ++k) {
+      const double c = small[i].poly[k] * pow(in, 2.0 * k) * scale * unit;
+      small[i].c[k] = (float)c;
       fits = fits && fabs(c) > 1e-36 && fabs(c) < 1e30;
     }
-    if (fits) mp.small_lim = (float)(0.75 / in);
+    if (fits) mp.small_lim[i] = (float)(small[i].lim / in);
   }
   mp.window = m.window;
   mp.slopes = m.slopes;

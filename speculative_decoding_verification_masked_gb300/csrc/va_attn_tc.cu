@@ -40,11 +40,17 @@
 // merges an equal share of the rows by their log-sum-exp.
 // Every wait is bounded; on timeout the CTA records VA_ERR_TIMEOUT, keeps the
 // barrier sequence of all roles intact, drains and frees TMEM.
-// With score shaping (va_mod.cuh) a row's 64 scores are capped and biased in its
-// thread's registers after they are loaded; the row's slope and offset are two
-// numbers, the keys' positions a ramp.  The cap's instructions come on top of a
-// softmax that is busy already: the 64-node tree over 128K keys takes 205 us
-// capped, 152 us with the same inputs and no cap.
+// With score shaping (va_mod.cuh) a row's scores are capped and biased in
+// registers after they are loaded; the row's slope and offset are two numbers, the
+// keys' positions a ramp.  The cap's instructions come on top of a softmax that is
+// busy already, and its code on top of a loop that nearly fills the instruction
+// caches.  So an M-tile has two softmax warpgroups then (20 warps in all), each
+// with 32 of a tile's 64 keys of every row and half of O's columns: half the code,
+// twice the warps.  They exchange the rows' maxima and sums at the vote's barrier.
+// 64-node tree over 128K keys, uncapped 152 us: capped at 30 210 us with one
+// warpgroup, 204 with two; at 15, where a third of the warps need the general
+// tanh, 537 and 231; 32 nodes (128 rows) 194 and 132; no cap but a document start at
+// 3/8 of the prefix 114 and 105.
 #include <cuda.h>
 #include <math.h>
 
@@ -66,6 +72,10 @@ constexpr int kTcStagesMax = 4;
 // ---------------------------------------------------------------------------
 // shared memory plan
 // ---------------------------------------------------------------------------
+// Softmax warpgroups of an M-tile: two for shaped scores, each with half of a
+// tile's keys.
+constexpr int tc_groups(int mod) { return mod != 0 ? 2 : 1; }
+
 template <int NMT, int NS>
 struct TcSmem {
   static constexpr int kQBytes = NMT * 2 * 128 * 128;  // NMT M-tiles x 2 columns x 128 rows x 128 B
@@ -78,10 +88,13 @@ struct TcSmem {
   static constexpr int kLoFlagOff = kMiscOff + 16;          // int [2][2]: P residual written, per M-tile and buffer
   // then the rotary table of the segment (rope_table_bytes, 0 without
   // positions) and the tile starts of the work plan
-  // (with score shaping, instead of the rotary table, the ranges of the first sequences)
+  // (with score shaping, instead of the rotary table, the ranges of the first
+  // sequences and what the two warpgroups of an M-tile tell each other: per tile
+  // parity, half and row, float2 {maximum, row sum})
   static constexpr int kRopeOff = (kLoFlagOff + 16 + 15) & ~15;
   static_assert(kRopeOff % 16 == 0, "int4 array needs 16-byte alignment");
-  static constexpr int kThreads = (5 * NMT + 2) * 32;
+  static constexpr int kModBytes = kModCache * 16 + 2 * 2 * NMT * 128 * 8;
+  static constexpr int threads(int mod) { return (4 * NMT * tc_groups(mod) + NMT + 2) * 32; }
 };
 
 // Offset of chunk c (16 B) of row r in a 128-row, 128B-swizzled Q tile pair.
@@ -92,16 +105,18 @@ __device__ __forceinline__ uint32_t swz128(int r, int c) {
 // kMod: 0 without score shaping, 1 with a window or document start only, 2 with
 // a cap or slopes.
 template <int NMT, bool kTma, bool kRope, int kMod, int NS>
-__global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
+__global__ void __launch_bounds__(TcSmem<NMT, NS>::threads(kMod), 1)
     verify_attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv) {
   using SM = TcSmem<NMT, NS>;
   using Geo = StageGeom<__nv_bfloat16, 128>;
   constexpr int D = 128;
-  constexpr int kSoftThreads = 128 * NMT;
-  constexpr int kProducerWarp = 4 * NMT;
-  constexpr int kMmaWarp0 = 4 * NMT + 1;  // PV issuer of M-tile i is warp kMmaWarp0 + i
-  constexpr int kSWarp = 5 * NMT + 1;     // S issuer of every M-tile
+  constexpr int kWG = tc_groups(kMod);  // softmax warpgroups of an M-tile
+  constexpr int N = kTK / kWG;          // keys of a tile that a softmax thread has
+  constexpr int kSoftThreads = 128 * NMT * kWG;
+  constexpr int kProducerWarp = 4 * NMT * kWG;
+  constexpr int kMmaWarp0 = kProducerWarp + 1;  // PV issuer of M-tile i is warp kMmaWarp0 + i
+  constexpr int kSWarp = kMmaWarp0 + NMT;       // S issuer of every M-tile
   constexpr int kMmaThreads = 32 * (NMT + 1);
   constexpr int kBarQ = 1, kBarSoft = 2, kBarEnd = 3, kBarVote = 4;  // kBarVote + M-tile
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -119,7 +134,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::kMiscOff + 4);
   volatile int *merge_ok = abort_flag + 1;
   float2 *rope_tab = reinterpret_cast<float2 *>(smem + SM::kRopeOff);
-  int *tstart = reinterpret_cast<int *>(smem + SM::kRopeOff + (kRope ? rope_table_bytes(p) : kMod != 0 ? kModCache * 16 : 0));
+  int *tstart = reinterpret_cast<int *>(smem + SM::kRopeOff + (kRope ? rope_table_bytes(p) : kMod != 0 ? SM::kModBytes : 0));
   volatile int *lo_flag = reinterpret_cast<volatile int *>(smem + SM::kLoFlagOff);
   constexpr bool use_tma = kTma;  // tiles by TMA boxes (dense, paged), else cp.async gathers
 
@@ -135,7 +150,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 128);
+      mbar_init(p_full + i, 128 * kWG);
       mbar_init(o_done + i, 1);
     }
     mbar_init(drain, NMT + 1);  // one commit per MMA-issuing warp
@@ -301,10 +316,14 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
   }
 
   // ============================ softmax warpgroups ============================
-  const int mi = warp >> 2;                 // M-tile of this warpgroup
+  const int mi = (warp >> 2) / kWG;         // M-tile of this warpgroup
+  const int half = (warp >> 2) % kWG;       // and, of two, its half of a tile's keys and of O's columns
   const int r = (warp & 3) * 32 + lane;     // row in the M-tile = TMEM lane
   const uint32_t lane_bits = (uint32_t)((warp & 3) * 32) << 16;
   const uint32_t tO = tmem + lane_bits + 128 * mi;
+  // (two warpgroups) slot of this row for tile parity 0 and half 0; the other half's
+  // is NMT * 128 on, the other parity's 2 * NMT * 128
+  float2 *xch = reinterpret_cast<float2 *>(smem + SM::kRopeOff + kModCache * 16) + mi * 128 + r;
   bool ok = true;
   auto wait_ok = [&](uint64_t *bar, uint32_t parity) { role_wait(bar, parity, ok, abort_flag, p.wait_ns, p.status); };
   int jt = 0;
@@ -414,14 +433,21 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
     }
     float m_used = -INFINITY;  // reference max of the exponentials (raw score units)
     float l = 0.f;
+    float l_other = 0.f;  // (two warpgroups) the other half's row sum, a tile behind
 
     for (int lt = lt0; lt < lt1; ++lt, ++jt) {
       const int b = jt & 1;
       const uint32_t tS = tmem + lane_bits + 256 + 64 * (2 * mi + b);
       wait_ok(s_full + 2 * mi + b, (uint32_t)(jt >> 1) & 1u);
       tc_fence_after();
-      float sv[64];
-      {  // both halves in flight before the one wait
+      float sv[N];
+      if constexpr (kWG == 2) {
+        uint32_t u[32];
+        tmem_ld32(tS + N * half, u);
+        tmem_ld_wait32(u);
+#pragma unroll
+        for (int j = 0; j < N; ++j) sv[j] = __uint_as_float(u[j]);
+      } else {  // both halves in flight before the one wait
         uint32_t u[32], w[32];
         tmem_ld32(tS, u);
         tmem_ld32(tS + 32, w);
@@ -429,22 +455,23 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j) sv[j] = __uint_as_float(u[j]);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) sv[32 + j] = __uint_as_float(w[j]);
+        for (int j = 0; j < 32; ++j) sv[N - 32 + j] = __uint_as_float(w[j]);
       }
       const int k0 = (kMod == 2 ? tile_of<true>(p, lt, lt0, lt1) : lt) * kTK;
       const bool masked = k0 + kTK > g.n_prefix || (kMod != 0 && k0 < g.hi);
       if constexpr (kMod == 2) {
-        if (p.mod.softcap > 0.f) cap_scores<64, false>(p.mod, sv);
+        if (p.mod.softcap > 0.f) cap_scores<N, true>(p.mod, sv);
         if (p.mod.slopes != nullptr) {
           const float mul = p.mod.softcap > 0.f ? 1.f : p.mod.out_mul;
-          const float d0 = qoff - (float)(k0 - g.n_prefix);  // distance of the tile's first key
-          if (k0 + kTK <= g.n_prefix && qoff >= 0.f) {
+          const int kh = k0 + N * half;
+          const float d0 = qoff - (float)(kh - g.n_prefix);  // distance of this half's first key
+          if (kh + N <= g.n_prefix && qoff >= 0.f) {
             // the row is past every key: ns * (d0 - j), eight keys at a time
             float2 step[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) step[q] = make_float2(-ns * (float)(2 * q), -ns * (float)(2 * q + 1));
 #pragma unroll
-            for (int j8 = 0; j8 < 64; j8 += 8) {
+            for (int j8 = 0; j8 < N; j8 += 8) {
               const float t8 = ns * (d0 - (float)j8);
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
@@ -457,8 +484,8 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 64; ++j) {
-              const int dk = k0 + j - g.n_prefix;  // draft key, or a prefix key below 0
+            for (int j = 0; j < N; ++j) {
+              const int dk = kh + j - g.n_prefix;  // draft key, or a prefix key below 0
               const float d = dk >= 0 && dk < p.T ? qoff - (float)mod_off(p.mod, p.T, g.b, dk, g.L) : d0 - (float)j;
               sv[j] = fmaf(ns, fabsf(d), sv[j] * mul);
             }
@@ -468,12 +495,22 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
       if (masked) {
         uint64_t vis = tile_vis64(k0, g.n_prefix, g.nkeys, rmask);
         if (kMod != 0 && first > k0) vis &= first - k0 >= 64 ? 0ull : ~0ull << (first - k0);
+        vis >>= N * half;
 #pragma unroll
-        for (int j = 0; j < 64; ++j)
+        for (int j = 0; j < N; ++j)
           if (!((vis >> j) & 1ull)) sv[j] = -INFINITY;
       }
       float mx;
-      {  // three-input maxima: 32 instructions, short dependency chains
+      // (three-input maxima: short dependency chains)
+      if constexpr (N == 32) {
+        float m10[10], m4[4];
+#pragma unroll
+        for (int q = 0; q < 10; ++q) m10[q] = max3f(sv[3 * q], sv[3 * q + 1], sv[3 * q + 2]);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) m4[q] = max3f(m10[3 * q], m10[3 * q + 1], m10[3 * q + 2]);
+        m4[3] = max3f(m10[9], sv[30], sv[31]);
+        mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]);
+      } else {
         float m22[22];
 #pragma unroll
         for (int q = 0; q < 21; ++q) m22[q] = max3f(sv[3 * q], sv[3 * q + 1], sv[3 * q + 2]);
@@ -483,6 +520,23 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
         for (int q = 0; q < 7; ++q) m8[q] = max3f(m22[3 * q], m22[3 * q + 1], m22[3 * q + 2]);
         m8[7] = m22[21];
         mx = max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+      }
+      bool lo = masked;  // P's residual is written (see below)
+      if constexpr (kWG == 2) {
+        // The halves of a row tell each other their maxima and sums, and vote on the
+        // residual, in one barrier.  (It also orders the other half's reads of S
+        // before P is written over it.)  The vote takes the reference from before this
+        // tile, which changes both its sides alike, and the other half's sum of a
+        // tile ago, which is at most its present one: it errs to the exact side.
+        float2 *x = xch + (jt & 1) * (2 * NMT * 128);
+        x[half * (NMT * 128)] = make_float2(mx, l);
+        const bool want = masked || m_used == -INFINITY || ex2_approx((mx - m_used) * cl2) * 15.f > l + l_other;
+        tc_fence_before();
+        lo = bar_red_or(kBarVote + mi, 256, want);
+        tc_fence_after();
+        const float2 other = x[(half ^ 1) * (NMT * 128)];
+        mx = fmaxf(mx, other.x);
+        l_other = other.y;
       }
       const float m_new = fmaxf(m_used, mx);
       // move the reference max only when it grew by more than 2^8 (exact either
@@ -497,41 +551,47 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
         if (need) {
           alpha = exp2f((m_used - m_new) * cl2);
           l *= alpha;
+          l_other *= alpha;
           m_used = m_new;
         }
       }
       const float mu = (m_used == -INFINITY) ? 0.f : m_used * cl2;
       // P's residual is needed where the tile's largest weight may exceed 1/16
       // of the row's weight up to and including it: 2^(mx - mu) > (l + 2^(mx - mu)) / 16
-      bool lo = masked;
-      if (!masked) lo = bar_red_or(kBarVote + mi, 128, ex2_approx(fmaf(mx, cl2, -mu)) * 15.f > l);
-      if (r == 0) lo_flag[2 * mi + b] = lo ? 1 : 0;
-      uint32_t ph[32];
+      if (kWG == 1 && !masked) lo = bar_red_or(kBarVote + mi, 128, ex2_approx(fmaf(mx, cl2, -mu)) * 15.f > l);
+      if (r == 0 && half == 0) lo_flag[2 * mi + b] = lo ? 1 : 0;
+      uint32_t ph[N / 2];
       // packed pairs: the scaled argument and the running sums take one
       // instruction per two scores
       const float2 cl2v = make_float2(cl2, cl2), nmu = make_float2(-mu, -mu);
       float2 ls2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       if (lo) {
         // P as bf16 hi + lo parts (a second set of MMAs adds the lo parts)
-        uint32_t pl[32];
+        uint32_t pl[N / 2];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < N / 2; ++j) {
           const float2 x = fma2(make_float2(sv[2 * j], sv[2 * j + 1]), cl2v, nmu);
           const float a = ex2_approx(x.x), bq = ex2_approx(x.y);
           ls2[j & 1] = add2(ls2[j & 1], make_float2(a, bq));
           split_bf16x2(a, bq, ph[j], pl[j]);
         }
-        tmem_st32(tS, ph);
-        tmem_st32(tS + 32, pl);
+        if constexpr (kWG == 2) {
+          tmem_st16(tS + 16 * half, ph);
+          tmem_st16(tS + 32 + 16 * half, pl);
+        } else {
+          tmem_st32(tS, ph);
+          tmem_st32(tS + 32, pl);
+        }
       } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < N / 2; ++j) {
           const float2 x = fma2(make_float2(sv[2 * j], sv[2 * j + 1]), cl2v, nmu);
           const float a = ex2_approx(x.x), bq = ex2_approx(x.y);
           ls2[j & 1] = add2(ls2[j & 1], make_float2(a, bq));
           ph[j] = pack_bf16(a, bq);
         }
-        tmem_st32(tS, ph);
+        if constexpr (kWG == 2) tmem_st16(tS + 16 * half, ph);
+        else tmem_st32(tS, ph);
       }
       const float ls = (ls2[0].x + ls2[1].x) + (ls2[0].y + ls2[1].y);
       l += ls;
@@ -541,7 +601,8 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
         wait_ok(o_done + 2 * mi + (b ^ 1), (uint32_t)((jt - 1) >> 1) & 1u);
         tc_fence_after();
 #pragma unroll
-        for (int cch = 0; cch < 4; ++cch) {
+        for (int ci = 0; ci < 4 / kWG; ++ci) {
+          const int cch = ci + half * (4 / kWG);
           uint32_t u[32];
           tmem_ld32(tO + 32 * cch, u);
           tmem_ld_wait();
@@ -559,12 +620,19 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
     if (jt >= 2) wait_ok(o_done + 2 * mi + (jt & 1), (uint32_t)((jt - 2) >> 1) & 1u);
     wait_ok(o_done + 2 * mi + ((jt - 1) & 1), (uint32_t)((jt - 1) >> 1) & 1u);
     tc_fence_after();
+    if constexpr (kWG == 2) {  // the row's sum is both halves'
+      float2 *x = xch + (jt & 1) * (2 * NMT * 128);
+      x[half * (NMT * 128)].y = l;
+      named_bar_sync(kBarVote + mi, 256);
+      l += x[(half ^ 1) * (NMT * 128)].y;
+    }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const float lse_nat = l > 0.f ? (m_used * cl2 + log2f(l)) * kLn2 : -INFINITY;
     const bool write = rvalid && ok;
     const uint32_t wrows = __ballot_sync(0xffffffffu, write);  // rows of this warp that are written
 #pragma unroll
-    for (int cch = 0; cch < 4; ++cch) {
+    for (int ci = 0; ci < 4 / kWG; ++ci) {
+      const int cch = ci + half * (4 / kWG);
       uint32_t u[32];
       tmem_ld32(tO + 32 * cch, u);
       tmem_ld_wait();
@@ -585,18 +653,21 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
         // the warp's 32 rows through a 32 x 33 float tile in the Q buffer (its
         // segment's S MMAs are all done): lane j then stores column j of each
         // row, so every store writes 128 contiguous bytes of one row
-        float *tr = reinterpret_cast<float *>(sQ) + warp * (32 * 33);
+        // (two warpgroups: 32 x 32, element (i, j) at j ^ i; the warps of an M-tile
+        // fill that M-tile's Q)
+        float *tr = reinterpret_cast<float *>(sQ) + warp * (kWG == 2 ? 32 * 32 : 32 * 33);
+        auto at = [](int i, int j) { return kWG == 2 ? i * 32 + (j ^ i) : i * 33 + j; };
 #pragma unroll
-        for (int j = 0; j < 32; ++j) tr[lane * 33 + j] = __uint_as_float(u[j]) * inv;
+        for (int j = 0; j < 32; ++j) tr[at(lane, j)] = __uint_as_float(u[j]) * inv;
         __syncwarp();
         float *op = p.o_part + ((size_t)(s + c) * p.rows_pad + mi * 128 + (warp & 3) * 32) * D + 32 * cch + lane;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          if ((wrows >> i) & 1u) op[(size_t)i * D] = tr[i * 33 + lane];
+          if ((wrows >> i) & 1u) op[(size_t)i * D] = tr[at(i, lane)];
         __syncwarp();
       }
     }
-    if (write) {
+    if (write && half == 0) {
       if (n_parts == 1)
         p.lse[((size_t)g.b * p.Hq + hq) * p.T + t] = lse_nat;
       else
@@ -629,10 +700,12 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
       const int rb = s % p.NRB, hkv = (s / p.NRB) % p.Hkv, b = s / (p.NRB * p.Hkv);
       const int nrows = min(p.rows_pad, p.R - rb * p.rows_pad);
       const int r0 = mpart[k] * nrows / np, r1 = (mpart[k] + 1) * nrows / np;
+      // (sixteen warps have fewer registers for parts in flight)
       if (np <= 4)
-        merge_rows_warp<8, 4>(p, b, hkv, rb * p.rows_pad, mslot[k], np, r0, r1, warp, 4 * NMT, lane);
+        merge_rows_warp<8, kWG == 2 ? 2 : 4>(p, b, hkv, rb * p.rows_pad, mslot[k], np, r0, r1, warp, kProducerWarp, lane);
       else
-        merge_rows_warp<32, 24>(p, b, hkv, rb * p.rows_pad, mslot[k], np, r0, r1, warp, 4 * NMT, lane);
+        merge_rows_warp<32, kWG == 2 ? 12 : 24>(p, b, hkv, rb * p.rows_pad, mslot[k], np, r0, r1, warp, kProducerWarp,
+                                               lane);
     }
     named_bar_sync(kBarSoft, kSoftThreads);
     // leave: np arrivals and np departures wrap the counter back to zero
@@ -647,7 +720,8 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::kThreads, 1)
 // ---------------------------------------------------------------------------
 template <int NMT, int NS>
 static size_t tc_smem_bytes(const AttnParams &p) {
-  return 1024 + (size_t)TcSmem<NMT, NS>::kRopeOff + (size_t)(p.mod.on ? kModCache * 16 : rope_table_bytes(p)) + (size_t)(p.S + 1) * 4;
+  return 1024 + (size_t)TcSmem<NMT, NS>::kRopeOff + (size_t)(p.mod.on ? TcSmem<NMT, NS>::kModBytes : rope_table_bytes(p)) +
+         (size_t)(p.S + 1) * 4;
 }
 
 constexpr size_t kTcSmemLimit = 232448;  // bytes of dynamic shared memory a CTA may have
@@ -672,7 +746,7 @@ static cudaError_t launch_tc_ns(const AttnParams &p, const CUtensorMap &tmk, con
   // cooperative: every CTA is resident, so the wait for a segment's parts ends
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(TcSmem<NMT, NS>::kThreads);
+  cfg.blockDim = dim3(TcSmem<NMT, NS>::threads(kMod));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

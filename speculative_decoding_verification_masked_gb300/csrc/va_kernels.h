@@ -18,8 +18,10 @@ struct ModParams {
   int on;
   float softcap;           // 0: no cap
   float in_mul, out_mul;   // capped: scale / cap and cap * log2 e; else out_mul = scale * log2 e
-  float small_lim;         // |raw product| up to which the polynomial below holds (-1: never)
-  float small_c[6];        // capped score = raw * (sum of small_c[k] raw^2k)
+  // the cap of small products as polynomials of 4 and 6 terms: capped score =
+  // raw * (sum of c[k] raw^2k) for |raw| up to lim (-1: never)
+  float small_lim[2];
+  float small_c4[4], small_c6[6];
   int window;              // 0: no window
   const float *slopes;     // [Hq] or NULL
   const int32_t *key_start;// [B] or NULL

@@ -67,38 +67,45 @@ __device__ __forceinline__ float capped_tanh(float y, float cap2) {
   return (cap2 * y) * p * rcp_approx(q);
 }
 
-// Caps N raw products of a thread in place.  Where every product of the warp is
-// small (|y| <= 0.75, what a cap well above the usual scores leaves), tanh is an
-// odd polynomial of degree 11 (fitted like the above: 2.9e-8 relative, 1.5e-7 in
-// fp32) with the scale and the cap folded into its coefficients: seven packed
-// instructions for two scores and no division, against nineteen.
-// (kPacked: the general case on pairs as well; off where 64 scores a thread leave
-// no room for aligned register pairs: the 256-row kernel lost 5% to it.)
-template <int N, bool kPacked = true>
+// raw * (sum of c[k] raw^2k) of N products in place.
+template <int N, int K>
+__device__ __forceinline__ void cap_small(const float (&c)[K], float (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 r = make_float2(x[i], x[i + 1]);
+    const float2 z = mul2(r, r);
+    float2 q = make_float2(c[K - 1], c[K - 1]);
+#pragma unroll
+    for (int k = K - 2; k >= 0; --k) q = fma2(q, z, make_float2(c[k], c[k]));
+    q = mul2(q, r);
+    x[i] = q.x;
+    x[i + 1] = q.y;
+  }
+}
+
+// Caps N raw products of a thread in place.  A cap well above the usual scores
+// leaves small |y|, where tanh is an odd polynomial, with the scale and the cap
+// folded into its coefficients and no division: where every product of the warp has
+// |y| <= 0.45, of degree 7, and (kMid) up to 0.75 of degree 11 (fitted like the
+// above: 2.4e-7 and 2.9e-8 relative; 3.2e-7 and 1.6e-7 in fp32).  A packed
+// instruction keeps the FMA pipe for two cycles, and on 256 rows each one of a pair
+// costs 8 us of a tree over 128K keys: five or seven against nineteen.
+// Code costs as well: warps at different places of more code than the instruction
+// caches hold wait for it.  With 64 scores a thread the 256-row tree took 537 us
+// where a tile's warps went different ways and 212 where they did not (32 scores:
+// 231 and 204), and the keys-on-lanes kernel loses more by the second polynomial
+// than it gains (64 rows, scores past 0.45: 335 us with it, 314 without; the
+// weights of 256 rows 164 and 200).
+template <int N, bool kMid>
 __device__ __forceinline__ void cap_scores(const ModParams &m, float (&x)[N]) {
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < N; i += 2) top = max3f(top, fabsf(x[i]), fabsf(x[i + 1]));
-  if (__all_sync(0xffffffffu, top <= m.small_lim)) {
-    const float2 c0 = make_float2(m.small_c[0], m.small_c[0]), c1 = make_float2(m.small_c[1], m.small_c[1]),
-                 c2 = make_float2(m.small_c[2], m.small_c[2]), c3 = make_float2(m.small_c[3], m.small_c[3]),
-                 c4 = make_float2(m.small_c[4], m.small_c[4]), c5 = make_float2(m.small_c[5], m.small_c[5]);
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const float2 r = make_float2(x[i], x[i + 1]);
-      const float2 z = mul2(r, r);
-      float2 q = fma2(c5, z, c4);
-      q = fma2(q, z, c3);
-      q = fma2(q, z, c2);
-      q = fma2(q, z, c1);
-      q = fma2(q, z, c0);
-      q = mul2(q, r);
-      x[i] = q.x;
-      x[i + 1] = q.y;
-    }
-  } else if constexpr (!kPacked) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = capped_tanh(x[i] * m.in_mul, m.out_mul);
+  top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // (none is negative)
+  if (top <= m.small_lim[0]) {
+    cap_small<N>(m.small_c4, x);
+  } else if (kMid && top <= m.small_lim[1]) {
+    cap_small<N>(m.small_c6, x);
   } else {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
