@@ -132,6 +132,46 @@ def test_draft_keys_that_nobody_sees_may_hold_anything():
     compare(out, lse, {"out": ro, "lse": rl})
 
 
+@pytest.mark.parametrize("reach", [1e-4, 0.1, 0.44, 0.74, 1.5, 30.0])
+@pytest.mark.parametrize("cap", [0.5, 50.0, 1e6])
+@pytest.mark.parametrize("dtype,D,T,Hq,Hkv", [("bf16", 128, 1, 2, 2), ("bf16", 128, 5, 8, 2), ("bf16", 128, 16, 8, 2),
+                                              ("bf16", 128, 25, 4, 1), ("bf16", 128, 64, 4, 1), ("bf16", 64, 8, 8, 2),
+                                              ("bf16", 64, 24, 4, 1), ("fp32", 64, 8, 4, 1)])
+def test_every_part_of_the_cap(dtype, D, T, Hq, Hkv, cap, reach):
+    """Scores |s| / cap up to `reach`, each alone in its row (a window of one) and
+    an exact product (one element of q is not zero), so that lse is the capped
+    score.  The cap is good to 3.3e-7 of it, and y, its units and the way back
+    round five times: 1e-6 of it, and 1e-6 for the row's sum (2^0 and log2 of it).
+    The weight of such a key, exp(s - lse), is 1 to the same error and lse's
+    rounding."""
+    g = torch.Generator().manual_seed(T)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    B = 3
+    L = torch.tensor([0, 70, 200], dtype=torch.int32)
+    q = torch.zeros(B, T, Hq, D)
+    col = torch.randint(D, (B, T, Hq), generator=g)
+    q.scatter_(3, col[..., None], 2.0)
+    k = ((torch.rand(B, 200 + T, Hkv, D, generator=g) * 2 - 1) * (reach * cap / 2)).to(dt)
+    v = torch.randn(B, 200 + T, Hkv, D, generator=g).to(dt)
+    pos = L[:, None] + torch.arange(T, dtype=torch.int32)
+    own = k.double()[torch.arange(B)[:, None], pos.long()]  # [B][T][Hkv][D]: each token's own key
+    raw = 2.0 * own.repeat_interleave(Hq // Hkv, 2).gather(3, col[..., None])[..., 0]
+    s = (cap * torch.tanh(raw / cap)).transpose(1, 2)  # [B][Hq][T]
+    mod = va.ScoreMod(softcap=cap, window=1, token_pos=pos.cuda())
+    out, lse = va.verify_attn_dense_mod(q.to(dt).cuda(), k.cuda(), v.cuda(), L.cuda(), mod, scale=1.0)
+    err = (lse.cpu().double() - s).abs()
+    assert (err <= 1e-6 * s.abs() + 1e-6).all(), float((err / (s.abs() + 1)).max())
+    vals = v[torch.arange(B)[:, None], pos.long()].repeat_interleave(Hq // Hkv, 2)
+    assert (out.cpu().float() - vals.float()).abs().max() <= 2 ** -8 * 6
+    if cap > 100.0:  # (lse's own rounding is too much of exp's argument)
+        return
+    w = torch.zeros(B, Hkv, 200 + T, device="cuda")
+    va.verify_accumulate_weight_dense(q.to(dt).cuda(), k.cuda(), L.cuda(), s.float().contiguous().cuda(), w, mod=mod,
+                                      scale=1.0)
+    got = w.cpu()[torch.arange(B)[:, None], :, pos.long()] / (Hq // Hkv)  # [B][T][Hkv]
+    assert (got - 1).abs().max() <= 2e-6 * cap + 2e-6
+
+
 def test_large_scores_stay_at_the_cap():
     """Products far past the cap, both signs, and the largest finite ones: all
     weights of a row are then 0 or equal."""
