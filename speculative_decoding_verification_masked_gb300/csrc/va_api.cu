@@ -478,7 +478,6 @@ va_status weight_common(const va_shape *shape, const va_score_mod *mod, const vo
   st = check_mod(mod != nullptr ? *mod : none, shape->scale, 1.f, false, p.mod);
   if (st != VA_OK) return st;
   p.mod.token_pos = nullptr;
-  if (p.mod.softcap == 0.f && p.mod.window == 0 && p.mod.slopes == nullptr && p.mod.key_start == nullptr) p.mod.on = 0;
   p.wait_ns = wait_limit_ns();
   return VA_OK;
 }

@@ -157,8 +157,8 @@ __global__ void __launch_bounds__(128) weight_simt_kernel(const WeightParams p) 
 // Roles (11 warps, one CTA per SM, a contiguous share of all 128-key tiles each):
 //   warps 0-3 / 4-7  the tiles of even / odd number: S from TMEM, exponentials,
 //                    row sum, the total's update; all stage Q and the rows' lse
-//                    when a kv-head begins.  More than 160 rows without score
-//                    shaping: sixteen warps, two warpgroups to a tile with half of
+//                    when a kv-head begins.  More than 160 rows without a cap
+//                    or slopes: sixteen warps, two warpgroups to a tile with half of
 //                    its rows each (eight left the latency of the exponentials in
 //                    the open)
 //   warp 8           producer; two of them (8 and 10) for pages below 64 rows and
@@ -212,7 +212,9 @@ struct WtSmem {  // offsets after the Q rows and the stages
   static constexpr int kPlan = kPart + 4 * 128 * 4;    // int [S + 1]
 };
 
-// kGroups: warpgroups that sum (2, or 4 = two to a tile).
+// kMod: a cap or slopes (a window or a document start needs no code of its own in
+// the tiles that every row sees).  kGroups: warpgroups that sum (2, or 4 = two to
+// a tile).
 template <int D, bool kTma, bool kMod, int kProducers, int kGroups>
 __global__ void __launch_bounds__((4 * kGroups + 3) * 32, 1)
     weight_tc_kernel(const WeightParams p, const __grid_constant__ CUtensorMap tmk, int RQ, int NS) {
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__((4 * kGroups + 3) * 32, 1)
 
     float *w = p.weight + ((size_t)g.b * p.Hkv + g.h) * p.stride + g.base;
     const int n_old = g.L - g.base;  // keys of the prefix
-    const float window = kMod && p.mod.window > 0 ? (float)p.mod.window : INFINITY;
+    const float window = p.mod.window > 0 ? (float)p.mod.window : INFINITY;
     auto total_of = [&](int key) {
       return (p.row0 > 0 ? key < g.nkeys : key < n_old && p.decay != 0.f) ? w[key] : 0.f;
     };
@@ -607,7 +609,8 @@ static cudaError_t launch_weight_tc(const WeightParams &p, const CUtensorMap &tm
 
 template <int D, bool kTma, int kProducers>
 static cudaError_t launch_weight_p(const WeightParams &p, const CUtensorMap &tmk, int grid, cudaStream_t stream) {
-  if (p.mod.on) return launch_weight_tc<D, kTma, true, kProducers, 2>(p, tmk, grid, stream);
+  // (a cap or slopes leave four warpgroups too few registers: 256 rows capped 138 / 238 us)
+  if (p.mod.on == 2) return launch_weight_tc<D, kTma, true, kProducers, 2>(p, tmk, grid, stream);
   // 8 x 128K keys, one warpgroup a tile against two: 160 rows 50.9 / 51.7 us, 192 rows
   // 57.9 / 52.1, 256 rows 72.8 / 65.7
   return p.Hq / p.Hkv * p.T - p.row0 > 160 ? launch_weight_tc<D, kTma, false, kProducers, 4>(p, tmk, grid, stream)
