@@ -138,8 +138,8 @@ bool tck_enabled() {
   return !(e != nullptr && strcmp(e, "mma") == 0);
 }
 
-// (Calls with score shaping always take the tcgen05 kernels at d128, and the
-// keys-on-lanes one at d64 up to 64 rows.)
+// (bf16 calls with score shaping always take the tcgen05 kernels, d64 the
+// keys-on-lanes one.)
 RowPlan row_plan(const va_shape &s, bool shaped = false) {
   RowPlan r;
   r.R = (s.Hq / s.Hkv) * s.T;
@@ -151,7 +151,7 @@ RowPlan row_plan(const va_shape &s, bool shaped = false) {
     r.use_tc = 1;
     r.RG = 4;
     r.rows_pad = r.R > 128 ? 256 : 128;
-  } else if (shaped ? s.D == 128 || r.R <= 64 : s.D == 128 && tck_enabled()) {
+  } else if (shaped || (s.D == 128 && tck_enabled())) {
     r.use_tc = 2;
     r.RG = 4;
     r.rows_pad = r.R <= 16 ? 16 : (r.R <= 32 ? 32 : 64);

@@ -199,18 +199,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint64_t m = has_draft ? draft_row(p, g.b, trow[h], tl, th) : 0ull;
-        rmask[h] = kMod && has_draft ? mod_window_row(p.mod, p.T, g.b, trow[h], g.L, m) : m;
-      }
-      float ns[2] = {0.f, 0.f}, qoff[2] = {0.f, 0.f};  // score shaping, per row: slope, offset from L,
-      int first[2] = {0, 0};                           // first visible key
-      if constexpr (kMod) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int o = mod_off(p.mod, p.T, g.b, trow[h], g.L);
-          ns[h] = rvalid[h] ? mod_slope(p.mod, g.hkv * group + rr[h] % group) : 0.f;
-          qoff[h] = (float)o;
-          first[h] = mod_first_slot(p.mod, g.b, o, g.L) - g.base;
-        }
+        rmask[h] = m;
       }
       {
         const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(p.q);
@@ -288,19 +277,6 @@ __global__ void __launch_bounds__(kThreads, CPS)
           }
           // mask: keys past the segment end, and draft keys the row may not see
           const int tile_k = tile * kTK + kb;
-          if constexpr (kMod) {
-            const bool draft_tile = tile * kTK + kTK > g.n_prefix;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int key = tile_k + nt * 8 + 2 * tq + (e & 1);
-                const float d = qoff[e >> 1] - (draft_tile ? key_off(key) : (float)(key - g.n_prefix));
-                sacc[nt][e] = mod_score(p.mod, sacc[nt][e], ns[e >> 1], d);
-                if (key < first[e >> 1]) sacc[nt][e] = -INFINITY;
-              }
-            }
-          }
           if (tile * kTK + kTK > g.n_prefix) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -842,11 +818,11 @@ static cudaError_t launch_attn_t(const AttnParams &p, const CUtensorMap &tmk, co
                                  cudaStream_t stream) {
   const size_t smem = attn_smem_bytes<Tin, D, RG, CPS>(p);
   // instances with the rotary embedding, with score shaping and with neither
-  // (code that never runs still costs the hot loop); score shaping of d128 and of
-  // at most 64 rows of d64 is left to the tcgen05 kernels
+  // (code that never runs still costs the hot loop); score shaping of bf16 is
+  // left to the tcgen05 kernels
   auto kern = p.positions != nullptr ? verify_attn_kernel<Tin, D, RG, CPS, true, false>
                                      : verify_attn_kernel<Tin, D, RG, CPS, false, false>;
-  if constexpr (D == 64 && CPS == 1) {
+  if constexpr (std::is_same<Tin, float>::value) {
     if (p.mod.on) kern = verify_attn_kernel<Tin, D, RG, CPS, false, true>;
   }
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -112,7 +112,9 @@ struct TkSmem {
   // and int [64] first visible keys of the draft tokens and the ranges of the
   // first sequences, and the tile starts of the work plan
   static constexpr int kRopeOff = kRowInvOff + 256;
-  static constexpr int kModBytes = 64 * 8 + 64 * 4 + kModCache * 16;
+  // (d 64, 64 rows: and uint64 [64] rows of the draft tokens)
+  static constexpr int kTokRowsOff = 64 * 8 + 64 * 4 + kModCache * 16;
+  static constexpr int kModBytes = kTokRowsOff + (D == 64 && NR == 64 ? 64 * 8 : 0);
   static_assert(kQOff % 1024 == 0 && kQBytes % 1024 == 0, "UMMA operands need 1024-byte aligned swizzle atoms");
   static_assert(kBarOff % 8 == 0 && kRowMaskOff % 8 == 0 && kKeyMaskOff % 8 == 0, "8-byte alignment");
   static_assert(kRedOff % 16 == 0, "float4 array needs 16-byte alignment");
@@ -250,6 +252,9 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
   using Cfg = TkCfg<NR, kTma, kMod>;
   constexpr int WG = Cfg::kGroups;
   constexpr int NW = NR / WG;  // rows of a softmax thread
+  // d 64: more than 64 rows come as blocks of 64, each a segment of its own (d 128
+  // has the kernel with the rows on the lanes for them)
+  constexpr bool kBlocks = D == 64 && NR == 64 && kMod != 0;
   constexpr int kSoft = 128 * WG;
   // up to 32 rows a thread: the row sums l are kept by the softmax threads (each over its own
   // keys, reduced once per segment part) instead of a ones-operand MMA per tile
@@ -278,6 +283,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
   int *tstart = reinterpret_cast<int *>(smem + SM::kRopeOff + (kRope ? rope_table_bytes(p) : kMod != 0 ? SM::kModBytes : 0));
   float2 *mod_row = reinterpret_cast<float2 *>(smem + SM::kRopeOff);       // (slope, offset) of row r
   int *mod_first = reinterpret_cast<int *>(smem + SM::kRopeOff + 64 * 8);  // first visible key of token t
+  uint64_t *tok_rows = reinterpret_cast<uint64_t *>(smem + SM::kRopeOff + SM::kTokRowsOff);
   constexpr bool use_tma = kTma != 0;  // tiles by TMA boxes (dense, paged), else cp.async gathers
 
   const int tid = threadIdx.x;
@@ -449,6 +455,17 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
     const int first_cta = owner_cta(tstart[s] + (kMod != 0 ? cr.cost : 0), cr.total, cr.G);
     const int n_parts = owner_cta(tstart[s + 1] - 1, cr.total, cr.G) - first_cta + 1;
     if (lt0 == 0 && tid == 0) p.meta[s] = make_int2(s + first_cta, n_parts);
+    // the packed rows [base, base + R) of the kv-head
+    const int base = kBlocks ? g.rb * NR : 0, R = kBlocks ? min(NR, p.R - base) : p.R;
+    // bit r: this segment's row r is one of draft token t
+    auto token_rows = [&](int t) -> uint64_t {
+      if constexpr (kBlocks) {
+        const int lo = max(t * group - base, 0), hi = min((t + 1) * group - base, 64);
+        return hi <= lo ? 0ull : (hi - lo >= 64 ? ~0ull : (1ull << (hi - lo)) - 1) << lo;
+      } else {
+        return (group >= 64 ? ~0ull : (1ull << group) - 1) << (t * group);
+      }
+    };
 
     // ---- Q of this segment into shared memory: [2 columns][NR rows][128 B], 128B swizzle ----
     // (the previous segment's MMAs have completed: its epilogue waited for the last one)
@@ -497,9 +514,9 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
         const int e = tid + u * kSoft;
         const int row = e / kCh;
         v[u] = make_uint4(0, 0, 0, 0);
-        if (row < p.R) {
-          const int t = row / group;
-          const int hq = g.hkv * group + row % group;
+        if (row < R) {
+          const int t = (base + row) / group;
+          const int hq = g.hkv * group + (base + row) % group;
           v[u] = __ldg(reinterpret_cast<const uint4 *>(qb + (((size_t)g.b * p.T + t) * p.Hq + hq) * D) + (e % kCh));
         }
       }
@@ -533,13 +550,12 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
       }
       named_bar_sync(kBarSoft, kSoft);
       if (tid < p.T) {
-        const uint64_t gbits = group >= 64 ? ~0ull : ((1ull << group) - 1);
         uint64_t kmask = 0;
         const int koff = kMod != 0 ? mod_off(p.mod, p.T, g.b, tid, g.L) : 0;
         for (int t = 0; t < p.T; ++t) {
           bool see = (rowmask[t] >> tid) & 1ull;
           if (kMod != 0 && p.mod.window > 0) see = see && mod_off(p.mod, p.T, g.b, t, g.L) - koff < p.mod.window;
-          if (see) kmask |= gbits << (t * group);
+          if (see) kmask |= kBlocks ? tok_rows[t] : token_rows(t);
         }
         keymask[tid] = kmask;
       }
@@ -553,14 +569,16 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
     bool ahead = true;  // no token sits before the end of the prefix
     if constexpr (kMod != 0) {
       const bool slopes = kMod == 2 && p.mod.slopes != nullptr, edge = lt0 * TK < g.hi;
+      // (the masks of the draft keys come later, behind a barrier of their own)
+      if (kBlocks && (edge || has_draft) && tid < p.T) tok_rows[tid] = token_rows(tid);
       if (slopes && tid < 64) {
-        const int t = tid / group, hq = g.hkv * group + tid % group;
-        mod_row[tid] = tid < p.R ? make_float2(mod_slope(p.mod, hq), (float)mod_off(p.mod, p.T, g.b, t, g.L))
+        const int t = (base + tid) / group, hq = g.hkv * group + (base + tid) % group;
+        mod_row[tid] = tid < R ? make_float2(mod_slope(p.mod, hq), (float)mod_off(p.mod, p.T, g.b, t, g.L))
                                  : make_float2(0.f, 0.f);
       }
       if (edge && tid < p.T)
         mod_first[tid] = mod_first_slot(p.mod, g.b, mod_off(p.mod, p.T, g.b, tid, g.L), g.L) - g.base;
-      if (slopes || edge) ahead = !bar_red_or(kBarSoft, kSoft, slopes && tid < p.R && mod_row[tid].y < 0.f);
+      if (slopes || edge) ahead = !bar_red_or(kBarSoft, kSoft, slopes && tid < R && mod_row[tid].y < 0.f);
     }
 
     float mu[NW];  // reference max per row, log2 units
@@ -586,10 +604,9 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
         if (key >= g.nkeys) km = 0;
         else if (key >= g.n_prefix) km = keymask[key - g.n_prefix];
         else if (kMod != 0 && key < g.hi) {
-          const uint64_t gbits = group >= 64 ? ~0ull : ((1ull << group) - 1);
           km = 0;
           for (int t = 0; t < p.T; ++t)
-            if (key >= mod_first[t]) km |= gbits << (t * group);
+            if (key >= mod_first[t]) km |= kBlocks ? tok_rows[t] : token_rows(t);
         }
       }
       const uint64_t km_all = km;
@@ -754,7 +771,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
           }
           put_p(cc, h, l);
         }
-        if (kMod != 0 ? (p.R < 64 ? (km_all & ((1ull << p.R) - 1ull)) : km_all) == 0ull : (use_tma && key >= g.nkeys)) {
+        if (kMod != 0 ? (R < 64 ? (km_all & ((1ull << R) - 1ull)) : km_all) == 0ull : (use_tma && key >= g.nkeys)) {
           // rows past the segment end: TMA brought whatever follows; zero V so 0 * V
           // stays 0 (with score shaping: every key that no row sees)
           wait_ok(full + st, (uint32_t)(it / NS) & 1u);
@@ -822,10 +839,10 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
         }
       }
     }
-    if (ktid < NW && r_wg + ktid < p.R) {
+    if (ktid < NW && r_wg + ktid < R) {
       const int r = r_wg + ktid;
-      const int t = r / group;
-      const int hq = g.hkv * group + r % group;
+      const int t = (base + r) / group;
+      const int hq = g.hkv * group + (base + r) % group;
       const float lse_nat = my_l > 0.f ? (my_mu + __log2f(my_l)) * kLn2 : -INFINITY;
       row_inv[r] = my_l > 0.f ? __fdividef(1.f, my_l) : 0.f;
       if (ok) {
@@ -928,15 +945,18 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
       named_bar_sync(kBarSoft, kSoft);
       if (ok && tid < p.T) {
         const int t = tid;
-        __nv_bfloat16 *dst =
-            static_cast<__nv_bfloat16 *>(p.out) + (((size_t)g.b * p.T + t) * p.Hq + g.hkv * group) * D;
-        const __nv_bfloat16 *src = stage_b + (size_t)t * group * D;
-        if (p.out_align16) {
-          bulk_store_s2g(dst, src, (uint32_t)(group * D * 2));
+        const int r0 = kBlocks ? max(t * group - base, 0) : t * group;  // its rows of the segment
+        const int n = kBlocks ? min((t + 1) * group - base, R) - r0 : group;
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
+                             (((size_t)g.b * p.T + t) * p.Hq + g.hkv * group + (base + r0 - t * group)) * D;
+        const __nv_bfloat16 *src = stage_b + (size_t)r0 * D;
+        if (kBlocks && n <= 0) {
+        } else if (p.out_align16) {
+          bulk_store_s2g(dst, src, (uint32_t)(n * D * 2));
           bulk_commit();
           bulk_wait_read_all();
         } else {
-          for (int e = 0; e < group * D; ++e) dst[e] = src[e];
+          for (int e = 0; e < n * D; ++e) dst[e] = src[e];
         }
       }
       named_bar_sync(kBarSoft, kSoft);
@@ -953,11 +973,14 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
     if (tid == 0) *merge_ok = wait_parts_arrived(p, s, np) ? 1 : 0;
     named_bar_sync(kBarSoft, kSoft);  // thread 0's acquire, then the barrier, orders the reads below
     if (*merge_ok) {
-      const int r0 = mpart[k] * p.R / np, r1 = (mpart[k] + 1) * p.R / np;
+      const int seg = kBlocks ? s / p.NRB : s, base = kBlocks ? s % p.NRB * NR : 0;
+      const int R = kBlocks ? min(NR, p.R - base) : p.R;
+      const int r0 = mpart[k] * R / np, r1 = (mpart[k] + 1) * R / np;
       if (np <= 4)
-        merge_rows_warp<8, 4, D>(p, s / p.Hkv, s % p.Hkv, 0, mslot[k], np, r0, r1, warp, 4 * WG, lane);
+        merge_rows_warp<8, 4, D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k], np, r0, r1, warp, 4 * WG, lane);
       else
-        merge_rows_warp<D == 128 ? 32 : 16, 24, D>(p, s / p.Hkv, s % p.Hkv, 0, mslot[k], np, r0, r1, warp, 4 * WG, lane);
+        merge_rows_warp<D == 128 ? 32 : 16, 24, D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k], np, r0, r1, warp, 4 * WG,
+                                                   lane);
     }
     named_bar_sync(kBarSoft, kSoft);
     // leave: np arrivals and np departures wrap the counter back to zero

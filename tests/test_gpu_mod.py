@@ -91,6 +91,22 @@ def test_split_over_many_ctas(T, Hq, Hkv, D):
     _check(c, out, lse)
 
 
+@pytest.mark.parametrize("rule", ["all", "cap", "window", "none"])
+@pytest.mark.parametrize("T,Hq,Hkv,page,L", [(17, 8, 2, 0, [9000]), (40, 3, 1, 16, [300, 0, 77]), (64, 8, 1, 2, [130, 65]),
+                                             (1, 96, 1, 0, [2000, 1]), (3, 70, 1, 64, [129, 4000]),
+                                             (64, 10, 2, 0, [0, 600])])
+def test_d64_blocks_of_rows(rule, T, Hq, Hkv, page, L):
+    """d 64 above 64 rows: blocks of 64, which may begin and end inside a token's heads."""
+    kw = dict(RULES[rule])
+    if "start" in kw:
+        kw["start"] = [0, 64, 3][:len(L)]
+    c = shaped.make(3 * T + Hq, L, T, Hq, Hkv, 64, "bf16", page, ["tree", "block", "empty"][T % 3], **kw)
+    ws = va.Workspace.for_shape(va.make_shape(c.B, T, Hq, Hkv, 64, 0))
+    out, lse = shaped.run_attend(va, c, workspace=ws)
+    va.verify_attn_check_status(ws)
+    _check(c, out, lse)
+
+
 @pytest.mark.parametrize("T,Hq,Hkv,D,page", [(8, 8, 2, 128, 0), (8, 8, 2, 128, 16), (6, 8, 2, 128, 2),
                                               (64, 4, 1, 128, 0), (5, 4, 1, 64, 8), (9, 6, 1, 64, 0), (24, 4, 1, 64, 0)])
 def test_hidden_keys_may_hold_anything(T, Hq, Hkv, D, page):
