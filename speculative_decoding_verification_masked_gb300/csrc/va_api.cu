@@ -145,8 +145,8 @@ RowPlan row_plan(const va_shape &s, bool shaped = false) {
   r.R = (s.Hq / s.Hkv) * s.T;
   r.use_tc = 0;
   if (s.dtype == VA_DTYPE_FP32) {
-    r.RG = 4;
-    r.rows_pad = 64;
+    r.RG = shaped && r.R <= 32 ? (r.R <= 16 ? 1 : 2) : 4;
+    r.rows_pad = 16 * r.RG;
   } else if (s.D == 128 && r.R > 64) {
     r.use_tc = 1;
     r.RG = 4;

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
   using C = Cfg<Tin, D, CPS>;
   constexpr int NS = C::kStages;
   constexpr int KW = C::kF32 ? 2 : kNWC / RG;  // key-split warps per row group
-  constexpr int RPS = C::kF32 ? 64 : 16 * RG;  // packed rows per segment
+  constexpr int RPS = C::kF32 && !kMod ? 64 : 16 * RG;  // packed rows per segment
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // the 128-byte swizzle pattern repeats every 1024 bytes: stages start 1024-aligned
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -440,9 +440,16 @@ __global__ void __launch_bounds__(kThreads, CPS)
       named_bar_sync(1, kNWC * 32);
     } else {
       // ------------------------------ fp32 SIMT path ------------------------------
-      // thread = (row r in 0..63, key half); D == 64
-      const int r = tid & 63;
-      const int half = tid >> 6;
+      // thread = (row r in 0..63, key half); D == 64.  With score shaping r is one
+      // of 16, 32 or 64 rows; below 64 the thread has every KG-th key, so that a
+      // segment of few rows leaves no thread without work (12 sequences of 470 to 888
+      // keys, 16 rows a kv-head, capped: 98.7 us on 64 rows, 35.8 on 16).
+      constexpr int KG = 128 / RPS;  // key groups
+      constexpr int NK = 64 / KG;    // keys of a thread and tile
+      const int r = tid & (RPS - 1);
+      const int half = tid / RPS;
+      constexpr bool kSpread = RPS < 64;
+      auto key_at = [&](int kk) { return kSpread ? kk * KG + half : half * NK + kk; };
       const int rrow = g.rb * RPS + r;
       const bool rv = rrow < p.R;
       const int t = rv ? rrow / group : 0;
@@ -497,18 +504,21 @@ __global__ void __launch_bounds__(kThreads, CPS)
           const uint8_t *kt = stages + st * C::kStageBytes;
           uint8_t *vt = stages + st * C::kStageBytes + C::kTileBytes;
           if (zero_tile(tile)) {
-            // zero V rows past the segment end (see the bf16 path); this warp's key half only
-            for (int e = lane; e < 32 * C::kChunks; e += 32) {
-              const int r = half * 32 + e / C::kChunks;
+            // zero V rows past the segment end (see the bf16 path); those this warp reads only
+            // (RPS = 16: its two key groups are neighbours)
+            constexpr int kGW = RPS == 16 ? 2 : 1;  // key groups of a warp
+            for (int e = lane; e < kGW * NK * C::kChunks; e += 32) {
+              const int i = e / C::kChunks;
+              const int r = kSpread ? i / kGW * KG + warp * 32 / RPS + i % kGW : half * 32 + i;
               if (zero_row(tile * kTK + r)) *reinterpret_cast<uint4 *>(vt + swz(r, e % C::kChunks)) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
           }
-          float sc[32];
+          float sc[NK];
 #pragma unroll 4
-          for (int kk = 0; kk < 32; ++kk) {
-            const int kr = half * 32 + kk;
+          for (int kk = 0; kk < NK; ++kk) {
+            const int kr = key_at(kk);
             float a = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -528,8 +538,8 @@ __global__ void __launch_bounds__(kThreads, CPS)
           }
           if constexpr (kMod) {  // shape the scores, then hide keys
 #pragma unroll 2
-            for (int kk = 0; kk < 32; ++kk) {
-              const int key = tile * kTK + half * 32 + kk;
+            for (int kk = 0; kk < NK; ++kk) {
+              const int key = tile * kTK + key_at(kk);
               const float d = p.mod.slopes != nullptr ? qoff - key_off(key) : 0.f;
               bool vis = key < g.nkeys && key >= first;
               if (vis && key >= g.n_prefix) vis = (rmask >> (key - g.n_prefix)) & 1ull;
@@ -539,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
           }
           float mx = m;
 #pragma unroll
-          for (int kk = 0; kk < 32; ++kk) mx = fmaxf(mx, sc[kk]);
+          for (int kk = 0; kk < NK; ++kk) mx = fmaxf(mx, sc[kk]);
           const float alpha = (mx == -INFINITY) ? 1.f : exp2f((m - mx) * cl2);
           const float mu = (mx == -INFINITY) ? 0.f : mx * cl2;
           m = mx;
@@ -547,10 +557,10 @@ __global__ void __launch_bounds__(kThreads, CPS)
 #pragma unroll
           for (int i = 0; i < 64; ++i) o[i] *= alpha;
 #pragma unroll 4
-          for (int kk = 0; kk < 32; ++kk) {
+          for (int kk = 0; kk < NK; ++kk) {
             const float pv = exp2f(fmaf(sc[kk], cl2, -mu));
             ls += pv;
-            const int vrow = half * 32 + kk;
+            const int vrow = key_at(kk);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float4 v4 = *reinterpret_cast<const float4 *>(vt + swz(vrow, i));
@@ -565,31 +575,48 @@ __global__ void __launch_bounds__(kThreads, CPS)
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + st);
       }
-      // merge the two key halves of each row through shared memory
+      // merge the key groups of each row through shared memory
       float *mine = merge + (size_t)tid * 66;
 #pragma unroll
       for (int i = 0; i < 64; ++i) mine[i] = o[i];
       mine[64] = m;
       mine[65] = l;
       named_bar_sync(1, kNWC * 32);
-      const float *a0 = merge + (size_t)r * 66;
-      const float *a1 = merge + (size_t)(r + 64) * 66;
-      const float M = fmaxf(a0[64], a1[64]);
-      const float w0 = (M == -INFINITY || a0[64] == -INFINITY) ? 0.f : exp2f((a0[64] - M) * cl2);
-      const float w1 = (M == -INFINITY || a1[64] == -INFINITY) ? 0.f : exp2f((a1[64] - M) * cl2);
-      const float Lsum = w0 * a0[65] + w1 * a1[65];
+      const float *a0 = merge + (size_t)r * 66;  // group j's at j * RPS * 66
+      float M = a0[64];
+#pragma unroll
+      for (int j = 1; j < KG; ++j) M = fmaxf(M, a0[j * RPS * 66 + 64]);
+      float w[KG], Lsum = 0.f;
+#pragma unroll
+      for (int j = 0; j < KG; ++j) {
+        const float mj = a0[j * RPS * 66 + 64];
+        w[j] = (M == -INFINITY || mj == -INFINITY) ? 0.f : exp2f((mj - M) * cl2);
+      }
+      if constexpr (KG == 2) {
+        Lsum = w[0] * a0[65] + w[1] * a0[RPS * 66 + 65];
+      } else {
+#pragma unroll
+        for (int j = 0; j < KG; ++j) Lsum = fmaf(w[j], a0[j * RPS * 66 + 65], Lsum);
+      }
       const float inv = Lsum > 0.f ? 1.f / Lsum : 0.f;
       const float lse_nat = Lsum > 0.f ? (M * cl2 + log2f(Lsum)) * kLn2 : -INFINITY;
       if (rv && ok) {
-        if (n_parts == 1) {
-          float *ob = static_cast<float *>(p.out) + (((size_t)g.b * p.T + t) * p.Hq + hq) * 64;
-          for (int d = half * 32; d < half * 32 + 32; ++d) ob[d] = (w0 * a0[d] + w1 * a1[d]) * inv;
-          if (half == 0) p.lse[((size_t)g.b * p.Hq + hq) * p.T + t] = lse_nat;
-        } else {
-          const int slot = s + c;
-          float *op = p.o_part + ((size_t)slot * p.rows_pad + r) * 64;
-          for (int d = half * 32; d < half * 32 + 32; ++d) op[d] = (w0 * a0[d] + w1 * a1[d]) * inv;
-          if (half == 0) p.lse_part[(size_t)slot * p.rows_pad + r] = lse_nat;
+        const int slot = s + c;
+        float *op = n_parts == 1 ? static_cast<float *>(p.out) + (((size_t)g.b * p.T + t) * p.Hq + hq) * 64
+                                 : p.o_part + ((size_t)slot * p.rows_pad + r) * 64;
+        for (int d = half * NK; d < half * NK + NK; ++d) {
+          if constexpr (KG == 2) {
+            op[d] = (w[0] * a0[d] + w[1] * a0[RPS * 66 + d]) * inv;
+          } else {
+            float x = 0.f;
+#pragma unroll
+            for (int j = 0; j < KG; ++j) x = fmaf(w[j], a0[j * RPS * 66 + d], x);
+            op[d] = x * inv;
+          }
+        }
+        if (half == 0) {
+          if (n_parts == 1) p.lse[((size_t)g.b * p.Hq + hq) * p.T + t] = lse_nat;
+          else p.lse_part[(size_t)slot * p.rows_pad + r] = lse_nat;
         }
       }
       named_bar_sync(1, kNWC * 32);
@@ -823,7 +850,10 @@ static cudaError_t launch_attn_t(const AttnParams &p, const CUtensorMap &tmk, co
   auto kern = p.positions != nullptr ? verify_attn_kernel<Tin, D, RG, CPS, true, false>
                                      : verify_attn_kernel<Tin, D, RG, CPS, false, false>;
   if constexpr (std::is_same<Tin, float>::value) {
-    if (p.mod.on) kern = verify_attn_kernel<Tin, D, RG, CPS, false, true>;
+    if (p.mod.on)
+      kern = p.RG == 1   ? verify_attn_kernel<Tin, D, 1, CPS, false, true>
+             : p.RG == 2 ? verify_attn_kernel<Tin, D, 2, CPS, false, true>
+                         : verify_attn_kernel<Tin, D, RG, CPS, false, true>;
   }
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;

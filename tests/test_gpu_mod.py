@@ -92,6 +92,29 @@ def test_split_over_many_ctas(T, Hq, Hkv, D):
 
 
 @pytest.mark.parametrize("rule", ["all", "cap", "window", "none"])
+@pytest.mark.parametrize("T,Hq,Hkv,page", [(1, 1, 1, 0), (4, 4, 1, 1), (8, 4, 2, 16), (6, 10, 2, 0), (8, 8, 1, 4),
+                                           (16, 9, 1, 0)])
+def test_fp32_rows_and_key_groups(rule, T, Hq, Hkv, page):
+    """fp32 with 1 to 144 rows of a kv-head: 16, 32 and 64 rows a segment, whose keys
+    eight, four and two threads of a row share; NaN in the K and V rows that nobody sees."""
+    kw = dict(RULES[rule])
+    L = [0, 1, 63, 64, 65, 200, 1500]
+    if "start" in kw:
+        kw["start"] = [0, 1, 40, 64, 0, 100, 1400]
+    c = shaped.make(5 * T + Hq, L, T, Hq, Hkv, 64, "fp32", page, ["tree", "block", "empty", "chain"][T % 4], **kw)
+    ro, rl = shaped.attend(c)
+    if not page:
+        for b, n in enumerate(L):
+            c.k[b, n + T:], c.v[b, n + T:] = float("nan"), float("inf")
+            lo = max(int(c.start[b]), int(c.pos[b].min()) - c.window + 1 if c.window else 0, 0)
+            c.k[b, :min(lo, n)], c.v[b, :min(lo, n)] = float("nan"), float("nan")
+    ws = va.Workspace.for_shape(va.make_shape(c.B, T, Hq, Hkv, 64, 2))
+    out, lse = shaped.run_attend(va, c, workspace=ws)
+    va.verify_attn_check_status(ws)
+    compare(out, lse, {"out": ro, "lse": rl}, tol_out=1e-4, tol_lse=1e-4)
+
+
+@pytest.mark.parametrize("rule", ["all", "cap", "window", "none"])
 @pytest.mark.parametrize("T,Hq,Hkv,page,L", [(17, 8, 2, 0, [9000]), (40, 3, 1, 16, [300, 0, 77]), (64, 8, 1, 2, [130, 65]),
                                              (1, 96, 1, 0, [2000, 1]), (3, 70, 1, 64, [129, 4000]),
                                              (64, 10, 2, 0, [0, 600])])
