@@ -1,6 +1,7 @@
 // Verification attention on the 5th-generation tensor cores with the KEYS on
 // the TMEM lanes, for segments of at most 64 packed query rows (GQA group x T
-// draft tokens; a chain of 8 drafts with group 4 gives 32 rows).  One MMA has
+// draft tokens; a chain of 8 drafts with group 4 gives 32 rows; d 64 with score
+// shaping comes in blocks of 64 rows above that).  One MMA has
 // M = 128, so rather than padding 32 query rows to 128 the products are taken
 // transposed, with a 128-key tile as the M side:
 //
@@ -45,8 +46,8 @@
 // With score shaping (va_mod.cuh) the raw products a softmax thread has loaded
 // are capped and biased in its registers before anything else looks at them; a
 // thread owns one key, so the key's position is one number and the rows' slopes
-// and offsets are broadcast from shared memory.  What the cap adds, seven packed
-// instructions for two scores, made the four softmax warps the bound; above 16
+// and offsets are broadcast from shared memory.  What the cap adds, five packed
+// instructions for two scores at least, made the four softmax warps the bound; above 16
 // rows there are therefore eight (TkCfg), and the 1024-key window of 64 paged
 // sequences went from 126 to 93 us, the capped 8-token chain over 32K from 39.7
 // to 34.7 us.  What bounds them now: HBM for long prefixes (single tokens over

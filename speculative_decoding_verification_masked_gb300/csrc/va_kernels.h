@@ -38,7 +38,8 @@ struct AttnParams {
   int S;       // segments = B * Hkv * NRB
   int rows_pad;// rows per segment slot in the partial buffers
   int use_tc;  // tcgen05 kernels (bf16, D 128): 1 = rows on TMEM lanes (more than 64
-              // packed rows), 2 = keys on TMEM lanes (at most 64), 3 = rows on TMEM
+              // packed rows), 2 = keys on TMEM lanes (at most 64; D 64 with score shaping,
+              // too, in blocks of 64 rows), 3 = rows on TMEM
               // lanes, two M-tiles of 128-key TMA tiles (more than 128 rows, dense or
               // paged with pages of 8 rows or more); 0 = mma.sync kernel
   int cps;     // CTAs of the attention kernel resident per SM (1 or 2)
