@@ -444,14 +444,14 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::threads(kMod), 1)
       if constexpr (kWG == 2) {
         uint32_t u[32];
         tmem_ld32(tS + N * half, u);
-        tmem_ld_wait32(u);
+        tmem_ld_wait(u);
 #pragma unroll
         for (int j = 0; j < N; ++j) sv[j] = __uint_as_float(u[j]);
       } else {  // both halves in flight before the one wait
         uint32_t u[32], w[32];
         tmem_ld32(tS, u);
         tmem_ld32(tS + 32, w);
-        tmem_ld_wait();
+        tmem_ld_wait(u, w);
 #pragma unroll
         for (int j = 0; j < 32; ++j) sv[j] = __uint_as_float(u[j]);
 #pragma unroll
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::threads(kMod), 1)
           const int cch = ci + half * (4 / kWG);
           uint32_t u[32];
           tmem_ld32(tO + 32 * cch, u);
-          tmem_ld_wait();
+          tmem_ld_wait(u);
 #pragma unroll
           for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * alpha);
           tmem_st32(tO + 32 * cch, u);
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::threads(kMod), 1)
       const int cch = ci + half * (4 / kWG);
       uint32_t u[32];
       tmem_ld32(tO + 32 * cch, u);
-      tmem_ld_wait();
+      tmem_ld_wait(u);
       if (n_parts == 1) {
         if (!write) continue;
         uint4 *ob = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +

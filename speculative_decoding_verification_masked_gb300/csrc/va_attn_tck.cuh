@@ -182,13 +182,13 @@ __device__ __forceinline__ void tmem_ld_f(uint32_t taddr, float (&x)[NR]) {
   if constexpr (NR == 8) {
     uint32_t u[8];
     tmem_ld8(taddr, u);
-    tmem_ld_wait();
+    tmem_ld_wait(u);
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(u[j]);
   } else if constexpr (NR == 16) {
     uint32_t u[16];
     tmem_ld16(taddr, u);
-    tmem_ld_wait();
+    tmem_ld_wait(u);
 #pragma unroll
     for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(u[j]);
   } else {
@@ -196,7 +196,7 @@ __device__ __forceinline__ void tmem_ld_f(uint32_t taddr, float (&x)[NR]) {
     for (int h = 0; h < NR / 32; ++h) {
       uint32_t u[32];
       tmem_ld32(taddr + 32 * h, u);
-      tmem_ld_wait();
+      tmem_ld_wait(u);
 #pragma unroll
       for (int j = 0; j < 32; ++j) x[32 * h + j] = __uint_as_float(u[j]);
     }
@@ -219,7 +219,7 @@ __device__ __forceinline__ void tmem_scale_cols(uint32_t taddr, const float *a) 
   if constexpr (NR == 16) {
     uint32_t u[16];
     tmem_ld16(taddr, u);
-    tmem_ld_wait();
+    tmem_ld_wait(u);
 #pragma unroll
     for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * a[j]);
     tmem_st16(taddr, u);
@@ -230,7 +230,7 @@ __device__ __forceinline__ void tmem_scale_cols(uint32_t taddr, const float *a) 
     for (int h = 0; h < NR / 16; ++h) {
       uint32_t u[16];
       tmem_ld16(taddr + 16 * h, u);
-      tmem_ld_wait();
+      tmem_ld_wait(u);
 #pragma unroll
       for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * a[16 * h + j]);
       tmem_st16(taddr + 16 * h, u);

@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(TpSmem::kThreads, 1)
         uint32_t u[4][32];
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, u[q]);
-        tmem_ld_wait();
+        tmem_ld_wait(u[0], u[1], u[2], u[3]);
         if (masked) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(TpSmem::kThreads, 1)
         uint32_t u[2][32];
         tmem_ld32(tS + 64 * h, u[0]);
         tmem_ld32(tS + 64 * h + 32, u[1]);
-        tmem_ld_wait();
+        tmem_ld_wait(u[0], u[1]);
 #pragma unroll
         for (int cq = 0; cq < 2; ++cq) {
           if (masked) {
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(TpSmem::kThreads, 1)
         for (int cch = 0; cch < 4; ++cch) {
           uint32_t u[32];
           tmem_ld32(tO + 32 * cch, u);
-          tmem_ld_wait();
+          tmem_ld_wait(u);
 #pragma unroll
           for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * alpha);
           tmem_st32(tO + 32 * cch, u);
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(TpSmem::kThreads, 1)
     for (int cch = 0; cch < 4; ++cch) {
       uint32_t u[32];
       tmem_ld32(tO + 32 * cch, u);
-      tmem_ld_wait();
+      tmem_ld_wait(u);
       if (!write) continue;
       if (n_parts == 1) {
         __nv_bfloat16 *orow = static_cast<__nv_bfloat16 *>(p.out) + (((size_t)g.b * p.T + t) * p.Hq + hq) * D + 32 * cch;

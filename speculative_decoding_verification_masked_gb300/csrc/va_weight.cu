@@ -551,7 +551,7 @@ __global__ void __launch_bounds__((4 * kGroups + 3) * 32, 1)
       if (masked || kMod || kGroups == 4) {  // (no registers to load ahead, or warps enough)
         for (int c0 = 0; c0 < NH; c0 += 32) {
           if (c0 > 0) tmem_ld32(tS + c0, ua);
-          tmem_ld_wait32(ua);
+          tmem_ld_wait(ua);
           if (c0 + 32 >= NH) release();
           if (masked) rows32(ua, c0, std::true_type());
           else if constexpr (kMod || kGroups == 4) rows32(ua, c0, std::false_type());
@@ -559,18 +559,18 @@ __global__ void __launch_bounds__((4 * kGroups + 3) * 32, 1)
       } else {
         // the next columns are on their way from TMEM while these are summed
         uint32_t ub[32];
-        tmem_ld_wait32(ua);
+        tmem_ld_wait(ua);
         for (int c0 = 0; c0 < NH; c0 += 64) {
           const bool two = c0 + 32 < NH, more = c0 + 64 < NH;
           if (two) tmem_ld32(tS + c0 + 32, ub);
           else release();
           rows32(ua, c0, std::false_type());
           if (!two) break;
-          tmem_ld_wait32(ub);
+          tmem_ld_wait(ub);
           if (more) tmem_ld32(tS + c0 + 64, ua);
           else release();
           rows32(ub, c0 + 32, std::false_type());
-          if (more) tmem_ld_wait32(ua);
+          if (more) tmem_ld_wait(ua);
         }
       }
       float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
