@@ -391,7 +391,7 @@ va_status run_attention(const Common &c, int layout, const void *k, const void *
   if (tiles_cap >= (1ll << 31)) return fail(VA_ERR_UNSUPPORTED, "problem too large (%lld key tiles)", tiles_cap);
   const long long ctas = (long long)rp.cps * sms;
   const int grid = (int)(tiles_cap < ctas ? tiles_cap : ctas);
-  if (va::attn_smem_required(p) > 232448) return fail(VA_ERR_UNSUPPORTED, "shared memory plan too large");
+  if (va::attn_smem_required(p) > (size_t)va::kSmemLimit) return fail(VA_ERR_UNSUPPORTED, "shared memory plan too large");
   cudaError_t e = va::launch_attention(p, tmk, tmv, grid < 1 ? 1 : grid, stream);
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   return ok();

@@ -855,7 +855,7 @@ static cudaError_t launch_attn_t(const AttnParams &p, const CUtensorMap &tmk, co
              : p.RG == 2 ? verify_attn_kernel<Tin, D, 2, CPS, false, true>
                          : verify_attn_kernel<Tin, D, RG, CPS, false, true>;
   }
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem(kern);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, smem, stream>>>(p, tmk, tmv);
   return cudaGetLastError();

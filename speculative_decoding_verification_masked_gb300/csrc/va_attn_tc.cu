@@ -724,12 +724,10 @@ static size_t tc_smem_bytes(const AttnParams &p) {
          (size_t)(p.S + 1) * 4;
 }
 
-constexpr size_t kTcSmemLimit = 232448;  // bytes of dynamic shared memory a CTA may have
-
 // the ring depth an instance gets: the largest that fits the plan
 template <int NMT>
 static bool tc_deep_ring(const AttnParams &p) {
-  return tc_smem_bytes<NMT, kTcStagesMax>(p) <= kTcSmemLimit;
+  return tc_smem_bytes<NMT, kTcStagesMax>(p) <= (size_t)kSmemLimit;
 }
 
 size_t attn_tc_smem_required(const AttnParams &p) {
@@ -741,7 +739,7 @@ static cudaError_t launch_tc_ns(const AttnParams &p, const CUtensorMap &tmk, con
                                 cudaStream_t stream) {
   const size_t smem = tc_smem_bytes<NMT, NS>(p);
   auto kern = verify_attn_tc_kernel<NMT, kTma, kRope, kMod, NS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem(kern);
   if (e != cudaSuccess) return e;
   // cooperative: every CTA is resident, so the wait for a segment's parts ends
   cudaLaunchConfig_t cfg = {};

@@ -1014,7 +1014,7 @@ static cudaError_t launch_tck_t(const AttnParams &p, const CUtensorMap &tmk, con
                                 cudaStream_t stream) {
   const size_t smem = tck_smem_bytes<D, NR>(p);
   auto kern = verify_attn_tck_kernel<D, NR, kTma, kRope, kMod>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem(kern);
   if (e != cudaSuccess) return e;
   // cooperative: every CTA is resident, so the wait for a segment's parts ends
   cudaLaunchConfig_t cfg = {};

@@ -646,7 +646,7 @@ cudaError_t launch_attention_tcp(const AttnParams &p, const CUtensorMap &tmk, co
                                  cudaStream_t stream) {
   const size_t smem = attn_tcp_smem_required(p);
   auto kern = p.positions != nullptr ? verify_attn_tcp_kernel<true> : verify_attn_tcp_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem(kern);
   if (e != cudaSuccess) return e;
   // cooperative: every CTA is resident, so the wait for a segment's parts ends
   cudaLaunchConfig_t cfg = {};

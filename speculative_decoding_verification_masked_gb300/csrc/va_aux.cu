@@ -624,7 +624,7 @@ cudaError_t launch_build_index(int B, int Hkv, const int32_t *seqlens, const flo
   p.status = status;
   p.radix_only = radix_only ? 1 : 0;
   const size_t smem = build_index_smem_bytes();
-  cudaError_t e = cudaFuncSetAttribute(build_index_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem(build_index_kernel, (int)smem);
   if (e != cudaSuccess) return e;
   build_index_kernel<<<B * Hkv, kIdxThreads, smem, stream>>>(p);
   return cudaGetLastError();

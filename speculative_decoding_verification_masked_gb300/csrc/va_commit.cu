@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(128) commit_kv_kernel(const CommitParams p) {
 cudaError_t launch_commit_kv(const CommitParams &p, cudaStream_t stream) {
   const size_t smem = (size_t)p.T * p.row_bytes;
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(commit_kv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(commit_kv_kernel, kSmemLimit - 256);  // (64 ints of static shared memory)
     if (e != cudaSuccess) return e;
   }
   commit_kv_kernel<<<dim3((unsigned)p.B, (unsigned)p.Hkv, 2), 128, smem, stream>>>(p);

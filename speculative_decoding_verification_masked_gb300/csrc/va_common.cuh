@@ -33,6 +33,18 @@ constexpr size_t kSplitCountOff = 64;
 constexpr size_t kSplitDoneOff = 128;
 constexpr int kMaxSegments = 2048;
 
+// Dynamic shared memory a CTA may have (with no static shared memory beside it).
+constexpr int kSmemLimit = 232448;
+
+// Lets `kern` be launched with up to `bytes` of dynamic shared memory.  The limit
+// belongs to the kernel and the process, not to a launch: always the same value, so
+// that calls of other sizes on other host threads cannot lower it before a launch.
+// (It does not change how many CTAs fit an SM; the launch's own size does.)
+template <typename Kern>
+inline cudaError_t allow_smem(Kern *kern, int bytes = kSmemLimit) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 __host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 constexpr size_t kMergeCntOff = kHeaderBytes;

@@ -597,11 +597,11 @@ static cudaError_t launch_weight_tc(const WeightParams &p, const CUtensorMap &tm
   const int RQ = rows >= kWtRows ? kWtRows : (rows + pad - 1) & ~(pad - 1);
   const size_t fixed = 1024 + (size_t)(D / 64) * RQ * 128 + WtSmem::kPlan + (size_t)(p.B * p.Hkv + 1) * 4;
   const size_t stage = (size_t)(D / 64) * kWtTile * 128;
-  int NS = (int)((232448 - fixed) / stage);
+  int NS = (int)((kSmemLimit - fixed) / stage);
   if (NS > kWtMaxStages) NS = kWtMaxStages;
   const size_t smem = fixed + NS * stage;
   auto kern = weight_tc_kernel<D, kTma, kMod, kProducers, kGroups>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem(kern);
   if (e != cudaSuccess) return e;
   kern<<<grid, (4 * kGroups + 3) * 32, smem, stream>>>(p, tmk, RQ, NS);
   return cudaGetLastError();

@@ -1,4 +1,5 @@
 """Calls from host threads other than the first one."""
+import sys
 import threading
 
 import pytest
@@ -11,6 +12,8 @@ pytestmark = pytest.mark.gpu
 
 if not torch.cuda.is_available():  # collected on CPU-only machines, skipped there
     pytest.skip("no CUDA device", allow_module_level=True)
+
+CALLS = 4000
 
 
 def _attend(B, T, Hq, Hkv, D, dtype, plain=False):
@@ -91,3 +94,85 @@ def test_first_call_of_a_thread(job):
     s.synchronize()
     for got, ref in zip(outs, want):
         assert torch.equal(got, ref)
+
+
+class _Recorder:
+    """Stands in for the loaded library: notes a call's function and arguments."""
+
+    def __init__(self, real):
+        self.real, self.seen = real, None
+
+    def __getattr__(self, name):
+        f = getattr(self.real, name)
+
+        def note(*args):
+            self.seen = (f, args)
+            return 0
+
+        return note
+
+
+def _c_call(call, stream):
+    """The C call behind a Python call, to be made again and again with little around it."""
+    real = va.api.lib()
+    rec = _Recorder(real)
+    va.api._lib = rec
+    try:
+        call(stream)
+    finally:
+        va.api._lib = real
+    return rec.seen
+
+
+# one kernel instance each, with different needs of shared memory (sequences, rows)
+PAIRS = {
+    "keys on lanes": lambda: (_attend(1, 8, 8, 2, 128, "bf16"), _attend(8, 8, 32, 8, 128, "bf16")),
+    "keys on lanes, d64": lambda: (_attend(1, 4, 4, 1, 64, "bf16"), _attend(8, 4, 32, 8, 64, "bf16")),
+    "rows on lanes": lambda: (_attend(1, 64, 4, 1, 128, "bf16"), _attend(8, 64, 32, 8, 128, "bf16")),
+    "fp32": lambda: (_attend(1, 8, 4, 1, 64, "fp32"), _attend(8, 8, 32, 8, 64, "fp32")),
+    "plain": lambda: (_attend(1, 8, 8, 2, 128, "bf16", True), _attend(8, 8, 32, 8, 128, "bf16", True)),
+    "plain, d64": lambda: (_attend(1, 4, 4, 1, 64, "bf16", True), _attend(8, 4, 32, 8, 64, "bf16", True)),
+    "plain, rows on lanes": lambda: (_attend(1, 64, 4, 1, 128, "bf16", True), _attend(8, 64, 32, 8, 128, "bf16", True)),
+    "weights": lambda: (_weigh(1, 8, 8, 2, 128), _weigh(8, 32, 32, 8, 128)),
+    "commit": lambda: (_commit(2, 64, 256), _commit(2, 49, 256)),
+}
+
+
+@pytest.mark.parametrize("pair", PAIRS)
+def test_two_threads_of_one_kernel(pair):
+    """What a launch sets on a kernel belongs to the process, not to the call: calls of
+    different sizes at the same time all succeed and give what a lone call gives."""
+    jobs = PAIRS[pair]()
+    want, work = [], []
+    for call, outs in jobs:
+        call(None)
+        torch.cuda.synchronize()
+        want.append([x.clone() for x in outs])
+        s = torch.cuda.Stream()
+        work.append((*_c_call(call, s), s))
+    errors = []
+
+    def run(f, args, s):
+        for i in range(CALLS):
+            status = f(*args)
+            if status != 0:
+                errors.append((i, status, va.api.lib().verify_attn_last_error().decode()))
+                break
+            if i % 200 == 199:
+                s.synchronize()
+        s.synchronize()
+
+    old = sys.getswitchinterval()
+    sys.setswitchinterval(1e-5)
+    try:
+        threads = [threading.Thread(target=run, args=w) for w in work]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(old)
+    assert not errors, errors[0]
+    for (_, outs), w in zip(jobs, want):
+        for got, ref in zip(outs, w):
+            assert torch.equal(got, ref)
