@@ -96,12 +96,17 @@ __device__ __forceinline__ void cap_small(const float (&c)[K], float (&x)[N]) {
 // 231 and 204), and the keys-on-lanes kernel loses more by the second polynomial
 // than it gains (64 rows, scores past 0.45: 335 us with it, 314 without; the
 // weights of 256 rows 164 and 200).
+// The form decides the last bits, so it may depend on nothing that no row sees: a
+// thread whose key is hidden from every row (`hidden`) has no say, and where a thread
+// has keys of both kinds (`mixed`) the general form is taken without asking.
 template <int N, bool kMid>
-__device__ __forceinline__ void cap_scores(const ModParams &m, float (&x)[N]) {
+__device__ __forceinline__ void cap_scores(const ModParams &m, float (&x)[N], bool hidden, bool mixed) {
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < N; i += 2) top = max3f(top, fabsf(x[i]), fabsf(x[i + 1]));
+  if (hidden) top = 0.f;
   top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // (none is negative)
+  if (mixed) top = INFINITY;
   if (top <= m.small_lim[0]) {
     cap_small<N>(m.small_c4, x);
   } else if (kMid && top <= m.small_lim[1]) {
