@@ -37,6 +37,18 @@ va_status verify_attn_selftest_wait_timeout(void *workspace, unsigned long long 
 va_status verify_attn_test_inject(unsigned long long wait_ns, int drop_part);
 
 /*
+ * The same for the waits between the roles of a block.  Until called again,
+ * every later attention and accumulated-weight launch of the process (a) uses
+ * wait_ns as the limit of each bounded device wait, as above, and (b) if cta >=
+ * 0, lets CTA number cta of the tcgen05 kernels keep from its softmax warps (or
+ * the warps that sum) that scores are ready: they wait until the limit runs
+ * out, VA_ERR_TIMEOUT is recorded, and every role of that block runs to its end
+ * without waiting any more (cta < 0: off).  Nothing on the GPU faults or hangs;
+ * the call's outputs are undefined.
+ */
+va_status verify_attn_test_stall(unsigned long long wait_ns, int cta);
+
+/*
  * Path of verify_build_index for the tests.  mode 0 (the default): each
  * top-k selection first tries the one-pass sampled-threshold select and falls
  * back to the radix select over all keys when the sample cannot decide;

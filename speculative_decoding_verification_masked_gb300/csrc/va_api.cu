@@ -61,11 +61,17 @@ uint64_t wait_limit_ns() {
   return v;
 }
 
-// Test hook (verify_attn_testing.h): a wait limit and a dropped part for the
-// next attention calls of the process.
+// Test hooks (verify_attn_testing.h): a wait limit, a dropped part and a stalled
+// CTA for the next calls of the process.
 std::atomic<unsigned long long> g_test_wait_ns{0};
 std::atomic<int> g_test_drop_part{-1};
+std::atomic<int> g_test_stall{-1};
 std::atomic<int> g_test_index_radix{0};  // verify_attn_test_index_path
+
+uint64_t call_wait_ns() {
+  const unsigned long long t = g_test_wait_ns.load();
+  return t != 0 ? t : wait_limit_ns();
+}
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -353,9 +359,9 @@ va_status run_attention(const Common &c, int layout, const void *k, const void *
   p.merge_cnt = reinterpret_cast<int2 *>(ws + wl.mcnt_off);
   p.lse_part = reinterpret_cast<float *>(ws + wl.lse_off);
   p.o_part = reinterpret_cast<float *>(ws + wl.o_off);
-  p.wait_ns = wait_limit_ns();
+  p.wait_ns = call_wait_ns();
   p.test_drop_part = g_test_drop_part.load();
-  if (const unsigned long long tw = g_test_wait_ns.load()) p.wait_ns = tw;
+  p.test_stall = g_test_stall.load();
 
   CUtensorMap tmk, tmv;
   memset(&tmk, 0, sizeof tmk);
@@ -484,7 +490,8 @@ va_status weight_common(const va_shape *shape, const va_score_mod *mod, const vo
   st = check_mod(mod != nullptr ? *mod : none, shape->scale, 1.f, false, p.mod);
   if (st != VA_OK) return st;
   p.mod.token_pos = nullptr;
-  p.wait_ns = wait_limit_ns();
+  p.wait_ns = call_wait_ns();
+  p.test_stall = g_test_stall.load();
   return VA_OK;
 }
 
@@ -1046,6 +1053,13 @@ va_status verify_attn_test_inject(unsigned long long wait_ns, int drop_part) {
   if (wait_ns > 100000000ull) return fail(VA_ERR_INVALID_ARG, "wait_ns must be at most 0.1 s");
   g_test_wait_ns.store(wait_ns);
   g_test_drop_part.store(drop_part < 0 ? -1 : drop_part);
+  return ok();
+}
+
+va_status verify_attn_test_stall(unsigned long long wait_ns, int cta) {
+  if (wait_ns > 100000000ull) return fail(VA_ERR_INVALID_ARG, "wait_ns must be at most 0.1 s");
+  g_test_wait_ns.store(wait_ns);
+  g_test_stall.store(cta < 0 ? -1 : cta);
   return ok();
 }
 

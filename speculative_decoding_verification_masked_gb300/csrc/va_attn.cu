@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
         const int st = it % NS;
         const int tile = tile_of<kMod>(p, lt, lt0, lt1);
         const uint32_t ph = (uint32_t)(it / NS) & 1u;
-        role_wait(full + st, ph, ok, abort_flag, p.wait_ns, p.status);
+        warp_role_wait(full + st, ph, ok, abort_flag, p.wait_ns, p.status);
         rotate_draft(tile, st);
         if (ok) {
           const uint32_t ks_addr = smem_u32(stages + st * C::kStageBytes);
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, CPS)
         const int st = it % NS;
         const int tile = tile_of<kMod>(p, lt, lt0, lt1);
         const uint32_t ph = (uint32_t)(it / NS) & 1u;
-        role_wait(full + st, ph, ok, abort_flag, p.wait_ns, p.status);
+        warp_role_wait(full + st, ph, ok, abort_flag, p.wait_ns, p.status);
         rotate_draft(tile, st);
         if (ok) {
           const uint8_t *kt = stages + st * C::kStageBytes;

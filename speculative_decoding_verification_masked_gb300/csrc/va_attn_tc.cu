@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::threads(kMod), 1)
       mbar_init(empty + i, NMT);  // one arrive per M-tile issuer
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(s_full + i, 1);
+      mbar_init(s_full + i, c == p.test_stall ? kNever : 1);
       mbar_init(p_full + i, 128 * kWG);
       mbar_init(o_done + i, 1);
     }
@@ -193,6 +193,9 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::threads(kMod), 1)
     const uint32_t id_o = umma_idesc(128, 128, 0, 1);
     int it = 0, jt = 0;
     bool ok = true;
+    // (a role that has given up waits no more but goes on issuing, so that no lane leaves
+    // the warp that elects an issuer: the MMAs stay inside the buffers and nobody keeps
+    // their results)
     auto wait_ok = [&](uint64_t *bar, uint32_t parity) { role_wait(bar, parity, ok, abort_flag, p.wait_ns, p.status); };
     // make stage `st` of tile lt ready for the MMAs: wait for it; on the dense
     // path zero the V rows past the segment end (TMA brought whole boxes)
@@ -228,7 +231,6 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::threads(kMod), 1)
     const uint64_t dV0 = umma_sdesc(smem_u32(stages) + Geo::kTileBytes, 8192, 1024);
     constexpr uint64_t kStageStep = Geo::kStageBytes >> 4;
     auto issue_s = [&](int i, int b, int st) {  // S_i(b) = Q_i K^T
-      if (!ok) return;
       tc_fence_after();
       const uint64_t dK = dK0 + (uint64_t)st * kStageStep;
       const uint32_t dS = tmem + 256 + 64 * (2 * i + b);
@@ -241,7 +243,6 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::threads(kMod), 1)
       umma_commit_warp(s_full + 2 * i + b);
     };
     auto issue_pv = [&](int i, int b, int st, bool first, bool exact) {  // O_i += P_i V
-      if (!ok) return;
       tc_fence_after();
       const uint64_t dV = dV0 + (uint64_t)st * kStageStep;
       const uint32_t aP = tmem + 256 + 64 * (2 * i + b);  // P hi; the residual 32 columns on
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::threads(kMod), 1)
             if (jt >= 2) wait_ok(o_done + 2 * i + b, (uint32_t)((jt - 2) >> 1) & 1u);
             if (i == 0) {
               wait_ok(full + st, (uint32_t)(it / NS) & 1u);
-              if (kRope && ok && lt * kTK + kTK > g.n_prefix) {
+              if (kRope && lt * kTK + kTK > g.n_prefix) {
                 // the draft keys of this tile, rotated in place before the S MMAs read them
                 const int r0 = max(0, g.n_prefix - lt * kTK), r1 = min(kTK, g.nkeys - lt * kTK);
                 rope_rotate_tile_rows<__nv_bfloat16, D, kTK>(stages + st * Geo::kStageBytes, r0, r1,
@@ -409,7 +410,9 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::threads(kMod), 1)
       }
       fence_proxy_async_smem();
     }
-    named_bar_arrive(kBarQ, kSoftThreads + kMmaThreads);
+    // (a wait, not an arrival alone: after a wait has run out nothing else keeps the
+    // softmax from a second arrival before the issuers' first, which would never end)
+    named_bar_sync(kBarQ, kSoftThreads + kMmaThreads);
 
     const int rr = g.rb * p.rows_pad + mi * 128 + r;
     const bool rvalid = rr < p.R;

@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
       mbar_init(empty + i, 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(s_full + b, 1);
+      mbar_init(s_full + b, c == p.test_stall ? kNever : 1);
       mbar_init(p_full + b, kSoft);
     }
     mbar_init(o_done + 0, 1);
@@ -339,6 +339,8 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
   auto wait_ok = [&](uint64_t *bar, uint32_t parity) { role_wait(bar, parity, ok, abort_flag, p.wait_ns, p.status); };
 
   if (warp == kMmaWarp) {
+    // (after giving up, too, this warp goes on issuing: no lane may leave the warp that
+    // elects an issuer; the MMAs stay inside the buffers and nobody keeps their results)
     // ================================ MMA issuer ================================
     const uint32_t id_s = umma_idesc(128, NR, 0, 0);
     const uint32_t id_o = umma_idesc(128, 2 * NR, 1, 1);  // N = [P_hi | P_lo]
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
     const uint64_t dP0 = umma_sdesc(smem_u32(stages), TK * 128, 1024);
     constexpr uint64_t kStageStep = SM::kStageBytes >> 4;
     auto issue_s = [&](int b, int st, const Seg &g, int lt) {  // S^T(b) = K Q^T
-      if (kRope && ok && lt * TK + TK > g.n_prefix) {
+      if (kRope && lt * TK + TK > g.n_prefix) {
         // the draft keys of this tile, rotated in place before the MMA reads them
         const int r0 = max(0, g.n_prefix - lt * TK), r1 = min(TK, g.nkeys - lt * TK);
         rope_rotate_tile_rows_bf16_call<D, TK>(stages + st * SM::kStageBytes, r0, r1, lt * TK + r0 - g.n_prefix,
@@ -365,7 +367,6 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
       }
-      if (!ok) return;
       tc_fence_after();
       const uint64_t dK = dK0 + (uint64_t)st * kStageStep;
       const uint32_t dS = tmem + (2 + b) * NC;
@@ -378,7 +379,6 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
       umma_commit_warp(s_full + b);
     };
     auto issue_pv = [&](int st, int b, bool first) {  // [O_hi|O_lo]^T += V^T [P_hi|P_lo]^T
-      if (!ok) return;
       tc_fence_after();
       const uint64_t dV = dV0 + (uint64_t)st * kStageStep;
       const uint64_t dP = dP0 + (uint64_t)st * kStageStep;
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
       fence_proxy_async_smem();
     }
     tc_fence_before();
-    named_bar_arrive(kBarQ, kSoft + 32);
+    named_bar_sync(kBarQ, kSoft + 32);  // (a wait: keeps the roles in step after a wait has run out)
 
     // ---- draft visibility, when this part holds draft keys: per draft key
     // dk, the packed rows r = t * group + h of the tokens t that see it.  Up to

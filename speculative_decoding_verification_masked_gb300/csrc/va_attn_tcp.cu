@@ -145,12 +145,11 @@ __device__ __forceinline__ void tp_produce(const AttnParams &p, const CUtensorMa
       }
     }
   }
-  if (!ok) {
-    // drain the boxes this warp issued before leaving (bounded)
-    for (int j = max(0, it - kTpSlots); j < it; ++j) {
-      mbar_wait(kfull + (j % kTpSlots), (uint32_t)(j / kTpSlots) & 1u, p.wait_ns >> 4);
-      mbar_wait(vfull + (j % kTpSlots), (uint32_t)(j / kTpSlots) & 1u, p.wait_ns >> 4);
-    }
+  // the boxes this warp issued land before it leaves (bounded), so that the block
+  // cannot end before them
+  for (int j = max(0, it - kTpSlots); j < it; ++j) {
+    mbar_wait(kfull + (j % kTpSlots), (uint32_t)(j / kTpSlots) & 1u, p.wait_ns >> 4);
+    mbar_wait(vfull + (j % kTpSlots), (uint32_t)(j / kTpSlots) & 1u, p.wait_ns >> 4);
   }
 }
 
@@ -197,7 +196,7 @@ __global__ void __launch_bounds__(TpSmem::kThreads, 1)
       mbar_init(vempty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full + i, 1);
+      mbar_init(s_full + i, c == p.test_stall ? kNever : 1);
       mbar_init(p_full + i, 128);
       mbar_init(o_done + i, 1);
     }
@@ -410,7 +409,7 @@ __global__ void __launch_bounds__(TpSmem::kThreads, 1)
       fence_proxy_async_smem();
     }
     tc_fence_before();
-    named_bar_arrive(kBarQ, kSoft + 32);
+    named_bar_sync(kBarQ, kSoft + 32);  // (a wait: keeps the roles in step after a wait has run out)
 
     const int rr = g.rb * p.rows_pad + mi * 128 + r;
     const bool rvalid = rr < p.R;

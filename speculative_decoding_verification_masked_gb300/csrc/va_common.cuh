@@ -85,6 +85,9 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
   return t;
 }
 
+// Arrivals of a barrier that a test keeps from completing (verify_attn_test_stall).
+constexpr int kNever = 1 << 16;
+
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
 }
@@ -142,6 +145,18 @@ __device__ __forceinline__ void role_wait(uint64_t *bar, uint32_t parity, bool &
     *abort_flag = 1;
     ok = false;
   }
+}
+
+// role_wait of a warp with instructions for all its lanes behind the wait.  ok is the
+// same on every lane, before and after: a phase that completes while the role gives up
+// may show on some lanes only, and such an instruction must not be reached by a part
+// of the warp.  (The vote takes ~1% where a tile waits for it: the roles that can do
+// without use role_wait.)
+__device__ __forceinline__ void warp_role_wait(uint64_t *bar, uint32_t parity, bool &ok, volatile int *abort_flag,
+                                               uint64_t limit_ns, int *status) {
+  if (__all_sync(0xffffffffu, !ok || mbar_try_wait(bar, parity))) return;
+  role_wait(bar, parity, ok, abort_flag, limit_ns, status);
+  ok = __all_sync(0xffffffffu, ok);
 }
 
 // One tiled TMA box of a 3-D tensor map (coordinates innermost first) into

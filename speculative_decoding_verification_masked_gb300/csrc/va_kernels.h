@@ -76,6 +76,7 @@ struct AttnParams {
   float *lse_part, *o_part;
   uint64_t wait_ns;
   int test_drop_part;  // test hook: this CTA's parts of split segments never arrive (-1: off)
+  int test_stall;      // test hook: this CTA's softmax is never told that scores are ready (-1: off)
   ModParams mod;
 };
 

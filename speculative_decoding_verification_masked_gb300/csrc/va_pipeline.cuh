@@ -480,6 +480,9 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
         *abort_flag = 1;
         ok = false;
       }
+      // the gather passes row addresses between the lanes: all of them go on, or none
+      // (TMA lanes are independent; a lane that has left is not waited for)
+      if (!use_tma) ok = __all_sync(0xffffffffu, ok);
       if (!ok) continue;
       uint8_t *kdst = stages + st * (VOFF + C::kTileBytes);  // (VOFF: offset of the V tile in a stage)
       uint8_t *vdst = kdst + VOFF;
@@ -562,13 +565,12 @@ __device__ __forceinline__ int produce_tiles(const AttnParams &p, const CUtensor
       }
     }
   }
-  if (!ok) {
-    // drain the copies this warp issued before leaving (bounded)
-    if (use_tma) {
-      for (int j = max(0, it - NS); j < it; ++j) mbar_wait(full + (j % NS), (uint32_t)(j / NS) & 1u, p.wait_ns >> 4);
-    } else {
-      cp_async_wait_all();
-    }
+  // the copies this warp issued land before it leaves (bounded), so that the block
+  // cannot end before them: once a wait has run out no other role waits for a tile
+  if (use_tma) {
+    for (int j = max(0, it - NS); j < it; ++j) mbar_wait(full + (j % NS), (uint32_t)(j / NS) & 1u, p.wait_ns >> 4);
+  } else {
+    cp_async_wait_all();
   }
   return it;
 }

@@ -248,7 +248,7 @@ __global__ void __launch_bounds__((4 * kGroups + 3) * 32, 1)
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full + i, 1);
+      mbar_init(s_full + i, (int)blockIdx.x == p.test_stall ? kNever : 1);
       mbar_init(s_empty + i, 64 * kGroups);
     }
     mbar_init(drain, 1);
@@ -309,6 +309,8 @@ __global__ void __launch_bounds__((4 * kGroups + 3) * 32, 1)
         if (kTma && lt + 1 < lt1) page_next = box_page(g, lt + 1);
         if (!live(g, lt)) continue;
         wait_ok(empty + r.st, r.ph ^ 1u);
+        // the gather passes row addresses between the lanes: all of them go on, or none
+        if constexpr (!kTma) ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
         uint8_t *dst = stages + r.st * kStage;
         const int k0 = lt * TK, slot0 = g.base + k0;
@@ -358,16 +360,16 @@ __global__ void __launch_bounds__((4 * kGroups + 3) * 32, 1)
         ++issued;
       }
     }
-    if (!ok) {  // drain the copies in flight before leaving (bounded)
-      if constexpr (kTma) {
-        for (int j = 0; j < min(issued, NS); ++j) {
-          r.st = r.st == 0 ? NS - 1 : r.st - 1;
-          if (r.st == NS - 1) r.ph ^= 1u;
-          mbar_wait(full + r.st, r.ph, p.wait_ns >> 4);
-        }
-      } else {
-        cp_async_wait_all();
+    // the copies this warp issued land before it leaves (bounded), so that the block
+    // cannot end before them
+    if constexpr (kTma) {
+      for (int j = 0; j < min(issued, NS); ++j) {
+        r.st = r.st == 0 ? NS - 1 : r.st - 1;
+        if (r.st == NS - 1) r.ph ^= 1u;
+        mbar_wait(full + r.st, r.ph, p.wait_ns >> 4);
       }
+    } else {
+      cp_async_wait_all();
     }
     return;
   }
@@ -397,17 +399,16 @@ __global__ void __launch_bounds__((4 * kGroups + 3) * 32, 1)
         const int b = jt & 1;
         wait_ok(full + r.st, r.ph);
         if (jt >= 2) wait_ok(s_empty + b, (uint32_t)((jt >> 1) - 1) & 1u);
-        if (ok) {
-          if constexpr (!kTma) fence_proxy_async_smem();
-          tc_fence_after();
-          const uint64_t dK = dK0 + (uint64_t)((r.st * kStage) >> 4);
+        // (after giving up, too: no lane may leave the warp that elects an issuer)
+        if constexpr (!kTma) fence_proxy_async_smem();
+        tc_fence_after();
+        const uint64_t dK = dK0 + (uint64_t)((r.st * kStage) >> 4);
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            umma_ss_warp(tmem + 256 * b, dK + (uint64_t)(((ks >> 2) * (TK * 128) + (ks & 3) * 32) >> 4),
-                         dQ0 + (uint64_t)(((ks >> 2) * (RQ * 128) + (ks & 3) * 32) >> 4), idesc, ks > 0 ? 1u : 0u);
-          umma_commit_warp(s_full + b);
-          umma_commit_warp(empty + r.st);
-        }
+        for (int ks = 0; ks < D / 16; ++ks)
+          umma_ss_warp(tmem + 256 * b, dK + (uint64_t)(((ks >> 2) * (TK * 128) + (ks & 3) * 32) >> 4),
+                       dQ0 + (uint64_t)(((ks >> 2) * (RQ * 128) + (ks & 3) * 32) >> 4), idesc, ks > 0 ? 1u : 0u);
+        umma_commit_warp(s_full + b);
+        umma_commit_warp(empty + r.st);
         __syncwarp();
         r.next(NS);
         ++jt;
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__((4 * kGroups + 3) * 32, 1)
       fence_proxy_async_smem();
       tc_fence_before();
       named_bar_sync(kBarSoft, kSoft);
-      named_bar_arrive(kBarQ, kSoft + 32);
+      named_bar_sync(kBarQ, kSoft + 32);  // (a wait: keeps the roles in step after a wait has run out)
     }
 
     float *w = p.weight + ((size_t)g.b * p.Hkv + g.h) * p.stride + g.base;

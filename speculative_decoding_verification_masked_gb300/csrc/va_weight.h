@@ -28,6 +28,7 @@ struct WeightParams {
   int tma_box;                   // bf16: rows of one TMA box of the cache; 0 = gathered
   int row0;                      // first packed row of this pass
   uint64_t wait_ns;
+  int test_stall;                // test hook: as in AttnParams
 };
 
 cudaError_t launch_accumulate_weight(const WeightParams &p, const CUtensorMap &tmk, int sms, cudaStream_t stream);
