@@ -488,6 +488,11 @@ va_status verify_accumulate_weight_paged(const va_shape *shape, const va_score_m
  * a bad index or page leaves its row in place; both are recorded as
  * VA_ERR_DEVICE_BOUNDS in `workspace` (may be NULL), and the kept rows of that
  * sequence are then undefined.
+ * The blocks of a call wait for one another, bounded: if a wait runs out
+ * (VA_ERR_TIMEOUT in `workspace`) some rows are not moved.  seqlens_out is then
+ * L_b for every sequence, slots 0 .. n-1 of K, V and weight (n the kept rows)
+ * are undefined, later slots keep what they hold, and scratch is as before the
+ * call.
  */
 size_t verify_evict_kv_scratch_size(int B, int Hkv, int max_indices);
 

@@ -32,6 +32,8 @@ va_status verify_attn_selftest_wait_timeout(void *workspace, unsigned long long 
  * segment parts it computed, as if that message were lost:
  * the other parts of those segments then wait for it until the limit runs
  * out, record VA_ERR_TIMEOUT and finish without merging (drop_part < 0: off).
+ * Eviction launches take both too: their block number drop_part does not
+ * announce the chunks it has read, and the blocks that write over them give up.
  * Nothing on the GPU faults or hangs; the call's outputs are undefined.
  */
 va_status verify_attn_test_inject(unsigned long long wait_ns, int drop_part);

@@ -568,7 +568,8 @@ va_status evict_common(const va_shape *shape, void *k, void *v, const int32_t *s
   p.seqlens_out = seqlens_out;
   p.scratch = scratch;
   p.status = static_cast<int *>(workspace);
-  p.wait_ns = wait_limit_ns();
+  p.wait_ns = call_wait_ns();
+  p.test_drop = g_test_drop_part.load();
   return VA_OK;
 }
 

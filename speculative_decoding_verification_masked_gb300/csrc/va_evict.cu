@@ -13,7 +13,8 @@
 // ascending order, so the lowest unfinished chunk never waits for one that is
 // not running; the wait is bounded all the same.  "Read" is one bit a chunk in
 // the caller's scratch, 32 chunks a word; the last block to leave clears the
-// words it was given.
+// words it was given.  Where a wait has run out some chunks are not written, and the
+// last block takes the new lengths back: no sequence is reported as cut.
 //
 // Bound by HBM: 2 x 2 x row bytes a kept row (K and V, read and written).
 // Chunks of 32 KB and up to six blocks an SM keep 190 KB an SM in flight: 16
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kv_kernel(const EvictPara
     // announce, then wait for the lower chunks of this kv-head
     if (warp == 0) {
       unsigned *bits = sc.bits + (size_t)bh * words;
-      if (lane == 0) red_release_or(bits + (c >> 5), 1u << (c & 31));
+      if (lane == 0 && (int)blockIdx.x != p.test_drop) red_release_or(bits + (c >> 5), 1u << (c & 31));
       bool all = true;
       for (int g = lane; g <= c >> 5; g += 32) {
         const unsigned need = g < (c >> 5) ? ~0u : (1u << (c & 31)) - 1u;
@@ -182,7 +183,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kv_kernel(const EvictPara
     }
     __syncthreads();
   }
-  // the last block out clears the bits for the next call
+  // the last block out clears the bits for the next call, and takes the lengths back
+  // if a wait ran out (every block's are written by its thread 0, before this count)
   if (tid == 0) {
     __threadfence();
     s_go = atomicAdd(sc.done, 1u) == gridDim.x - 1;
@@ -190,6 +192,9 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kv_kernel(const EvictPara
   __syncthreads();
   if (s_go) {
     __threadfence();
+    if (*reinterpret_cast<volatile int *>(sc.gave_up) != 0)
+      for (int b = tid; b < p.B; b += kEvictThreads) p.seqlens_out[b] = __ldg(p.seqlens + b);
+    __syncthreads();
     const size_t total = (size_t)heads * words;
     for (size_t i = tid; i < total; i += kEvictThreads) sc.bits[i] = 0u;
     if (tid == 0) {

@@ -24,6 +24,7 @@ struct EvictParams {
   void *scratch;                 // evict_scratch_bytes, zero between calls
   int *status;                   // may be NULL
   uint64_t wait_ns;
+  int test_drop;                 // test hook: this block announces nothing (-1: off)
 };
 
 size_t evict_scratch_bytes(int B, int Hkv, int max_indices);
