@@ -248,7 +248,8 @@ typedef struct {
  * verify_attn_dense and verify_attn_paged with score shaping: the same layouts,
  * draft masks, workspace, outputs and errors.  q and the draft keys are taken
  * as stored (rotated by verify_rope_draft_* where the model rotates).  A row
- * that sees no key gets out = 0 and lse = -inf.  mod must not be NULL.
+ * that sees no key gets out = 0 and lse = -inf, one with a NaN in q NaN for both.
+ * mod must not be NULL.
  */
 va_status verify_attn_dense_mod(const va_shape *shape, const va_score_mod *mod, const void *q, const void *k_cache,
                                 const void *v_cache, int max_cache_len, const int32_t *seqlens,

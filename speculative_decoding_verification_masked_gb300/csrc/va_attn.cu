@@ -598,8 +598,9 @@ __global__ void __launch_bounds__(kThreads, CPS)
 #pragma unroll
         for (int j = 0; j < KG; ++j) Lsum = fmaf(w[j], a0[j * RPS * 66 + 65], Lsum);
       }
-      const float inv = Lsum > 0.f ? 1.f / Lsum : 0.f;
-      const float lse_nat = Lsum > 0.f ? (M * cl2 + log2f(Lsum)) * kLn2 : -INFINITY;
+      const bool some = kMod ? mod_row_seen(Lsum) : Lsum > 0.f;
+      const float inv = some ? 1.f / Lsum : 0.f;
+      const float lse_nat = some ? (M * cl2 + log2f(Lsum)) * kLn2 : -INFINITY;
       if (rv && ok) {
         const int slot = s + c;
         float *op = n_parts == 1 ? static_cast<float *>(p.out) + (((size_t)g.b * p.T + t) * p.Hq + hq) * 64
@@ -760,7 +761,7 @@ __device__ __forceinline__ void merge_split_row(const AttnParams &p, int4 e, int
     }
     float m = M;
 #pragma unroll
-    for (int j = 0; j < kSplitBatch; ++j) m = fmaxf(m, ls[j]);
+    for (int j = 0; j < kSplitBatch; ++j) m = max_nan(m, ls[j]);  // (a part may be NaN)
     if (m == -INFINITY) continue;  // no part so far saw a key
     const float a = M == -INFINITY ? 0.f : __expf(M - m);
     L *= a;
@@ -779,13 +780,13 @@ __device__ __forceinline__ void merge_split_row(const AttnParams &p, int4 e, int
     }
     M = m;
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L != 0.f ? 1.f / L : 0.f;
   OutT *out = static_cast<OutT *>(p.out) + (((size_t)b * p.T + t) * p.Hq + hq) * D + 4 * li;
   store_out<OutT>(out + 0, acc.x * inv);
   store_out<OutT>(out + 1, acc.y * inv);
   store_out<OutT>(out + 2, acc.z * inv);
   store_out<OutT>(out + 3, acc.w * inv);
-  if (li == 0) p.lse[((size_t)b * p.Hq + hq) * p.T + t] = L > 0.f ? M + __logf(L) : -INFINITY;
+  if (li == 0) p.lse[((size_t)b * p.Hq + hq) * p.T + t] = L != 0.f ? M + __logf(L) : -INFINITY;
 }
 
 template <typename OutT>

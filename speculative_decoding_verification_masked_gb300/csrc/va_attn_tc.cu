@@ -629,8 +629,9 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::threads(kMod), 1)
       named_bar_sync(kBarVote + mi, 256);
       l += x[(half ^ 1) * (NMT * 128)].y;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const float lse_nat = l > 0.f ? (m_used * cl2 + log2f(l)) * kLn2 : -INFINITY;
+    const bool seen = kMod != 0 ? mod_row_seen(l) : l > 0.f;
+    const float inv = seen ? 1.f / l : 0.f;
+    const float lse_nat = seen ? (m_used * cl2 + log2f(l)) * kLn2 : -INFINITY;
     const bool write = rvalid && ok;
     const uint32_t wrows = __ballot_sync(0xffffffffu, write);  // rows of this warp that are written
 #pragma unroll

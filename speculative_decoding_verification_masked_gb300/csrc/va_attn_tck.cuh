@@ -844,8 +844,9 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
       const int r = r_wg + ktid;
       const int t = (base + r) / group;
       const int hq = g.hkv * group + (base + r) % group;
-      const float lse_nat = my_l > 0.f ? (my_mu + __log2f(my_l)) * kLn2 : -INFINITY;
-      row_inv[r] = my_l > 0.f ? __fdividef(1.f, my_l) : 0.f;
+      const bool seen = kMod != 0 ? mod_row_seen(my_l) : my_l > 0.f;
+      const float lse_nat = seen ? (my_mu + __log2f(my_l)) * kLn2 : -INFINITY;
+      row_inv[r] = seen ? __fdividef(1.f, my_l) : 0.f;
       if (ok) {
         if (n_parts == 1)
           p.lse[((size_t)g.b * p.Hq + hq) * p.T + t] = lse_nat;

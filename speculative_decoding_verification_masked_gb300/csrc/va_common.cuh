@@ -287,6 +287,12 @@ __device__ __forceinline__ float2 sub2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+// The larger value; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 // Largest of three (one instruction on sm_100+).
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;

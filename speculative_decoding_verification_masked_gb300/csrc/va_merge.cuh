@@ -30,7 +30,7 @@ __device__ __forceinline__ int ld_acquire_gpu(const int *ptr) {
 
 // Exact log-sum-exp merge (LongSpec 2.C) of rows [r0, r1) of a split segment
 // of sequence b, kv-head hkv, whose row r is packed query row row_base + r,
-// from its np parts at slots slot0..slot0+np-1, by one warp of n_warps: LPR
+// (a part whose lse is NaN makes the row NaN), from its np parts at slots slot0..slot0+np-1, by one warp of n_warps: LPR
 // lanes per row, each with D/LPR columns, the lse and output loads of up to
 // MB parts in flight at once, a running maximum across batches.
 template <int LPR, int MB, int D = 128>
@@ -65,7 +65,7 @@ __device__ __forceinline__ void merge_rows_warp(const AttnParams &p, int b, int 
       }
       float m = M;
 #pragma unroll
-      for (int j = 0; j < MB; ++j) m = fmaxf(m, ls[j]);
+      for (int j = 0; j < MB; ++j) m = max_nan(m, ls[j]);
       if (m == -INFINITY) continue;  // no part so far saw a key
       const float a = M == -INFINITY ? 0.f : __expf(M - m);
       L *= a;
@@ -91,14 +91,14 @@ __device__ __forceinline__ void merge_rows_warp(const AttnParams &p, int b, int 
       M = m;
     }
     if (!act) continue;
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L != 0.f ? 1.f / L : 0.f;
     const int t = (row_base + row) / group, hq = hkv * group + (row_base + row) % group;
     uint2 *dst = reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) +
                                            (((size_t)b * p.T + t) * p.Hq + hq) * D + li * C4 * 4);
 #pragma unroll
     for (int c = 0; c < C4; ++c)
       dst[c] = make_uint2(pack_bf16(acc[c].x * inv, acc[c].y * inv), pack_bf16(acc[c].z * inv, acc[c].w * inv));
-    if (li == 0) p.lse[((size_t)b * p.Hq + hq) * p.T + t] = L > 0.f ? M + __logf(L) : -INFINITY;
+    if (li == 0) p.lse[((size_t)b * p.Hq + hq) * p.T + t] = L != 0.f ? M + __logf(L) : -INFINITY;
   }
 }
 

@@ -37,10 +37,18 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// y cut to where the approximation holds; NaN stays NaN.
+__device__ __forceinline__ float cut_tanh_arg(float y) {
+  float d;
+  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}"
+      : "=f"(d) : "f"(y), "f"(-9.02f), "f"(9.02f));
+  return d;
+}
+
 // cap2 * tanh of a pair; cap2 multiplies the numerators before the division.
 __device__ __forceinline__ float2 capped_tanh2(float2 y, float cap2) {
-  y.x = fminf(fmaxf(y.x, -9.02f), 9.02f);
-  y.y = fminf(fmaxf(y.y, -9.02f), 9.02f);
+  y.x = cut_tanh_arg(y.x);
+  y.y = cut_tanh_arg(y.y);
   auto two = [](float c) { return make_float2(c, c); };
   const float2 z = mul2(y, y);
   float2 p = fma2(two(1.33188971e-08f), z, two(2.05833530e-05f));
@@ -54,7 +62,7 @@ __device__ __forceinline__ float2 capped_tanh2(float2 y, float cap2) {
   return mul2(mul2(mul2(y, two(cap2)), p), make_float2(rcp_approx(q.x), rcp_approx(q.y)));
 }
 __device__ __forceinline__ float capped_tanh(float y, float cap2) {
-  y = fminf(fmaxf(y, -9.02f), 9.02f);
+  y = cut_tanh_arg(y);
   const float z = y * y;
   float p = fmaf(1.33188971e-08f, z, 2.05833530e-05f);
   p = fmaf(p, z, 3.49402661e-03f);
@@ -124,6 +132,10 @@ __device__ __forceinline__ void cap_scores(const ModParams &m, float (&x)[N], bo
 // ---------------------------------------------------------------------------
 // positions and visibility
 // ---------------------------------------------------------------------------
+// Whether a row's sum of weights holds a key.  NaN scores (a NaN in q) count, so that
+// such a row's out and lse come out as NaN.
+__device__ __forceinline__ bool mod_row_seen(float l) { return l != 0.f; }
+
 // Position of draft token t of sequence b relative to L_b (clamped).
 __device__ __forceinline__ int mod_off(const ModParams &m, int T, int b, int t, int L) {
   if (m.token_pos == nullptr) return t;
