@@ -468,7 +468,8 @@ va_status verify_accumulate_weight_paged(const va_shape *shape, const va_score_m
  * to slot j, j < n_indices[b][h]; later slots keep what they hold.  The new
  * length is seqlens_out[b] = n_indices[b][0].  Every kv-head keeps its own
  * rows, so slot j may hold another token in each; distances (va_score_mod) then
- * count kept rows.
+ * count kept rows.  A window or slopes over such a cache are therefore not those
+ * of a model that counts tokens: it evicts without them, or not at all.
  *   indices [B][Hkv][max_indices] and n_indices [B][Hkv] int32 as
  *     verify_build_index writes them (with the accumulated weight as its
  *     scores): strictly increasing entries in [0, L_b), the same n in every
