@@ -331,8 +331,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // scores stay raw until the exponential; capped or biased ones are in base-2 units already
-  const bool raw = kMod != 2 || (p.mod.softcap == 0.f && p.mod.slopes == nullptr);
-  const float cl2 = raw ? p.scale * kLog2e : 1.f;
+  const float cl2 = kMod == 2 ? 1.f : p.scale * kLog2e;
   const int group = p.Hq / p.Hkv;
 
   bool ok = true;

@@ -27,8 +27,9 @@ constexpr int kModMaxOff = 1 << 23;
 // tanh
 // ---------------------------------------------------------------------------
 // tanh(y) = y P(y^2) / Q(y^2), a rational approximation fitted to the relative
-// error on |y| <= 9.02 (reweighted least squares): 2.1e-8, 3.3e-7 as evaluated
-// in fp32.  Past 9.02, tanh rounds to 1 in fp32.  The hardware's one-instruction
+// error on |y| <= 9.02 (reweighted least squares): 5.8e-8 with the coefficients
+// below, 3.7e-7 with every step rounded to fp32 and the reciprocal too, whose
+// approximation may add 6e-8.  Past 9.02, tanh rounds to 1 in fp32.  The hardware's one-instruction
 // tanh is off by 2^-11, which a cap of 50 would turn into 0.02 of a score;
 // 1 - 2 / (1 + e^2y) loses the small scores' digits the same way.
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -95,7 +96,7 @@ __device__ __forceinline__ void cap_small(const float (&c)[K], float (&x)[N]) {
 // leaves small |y|, where tanh is an odd polynomial, with the scale and the cap
 // folded into its coefficients and no division: where every product of the warp has
 // |y| <= 0.45, of degree 7, and (kMid) up to 0.75 of degree 11 (fitted like the
-// above: 2.4e-7 and 2.9e-8 relative; 3.2e-7 and 1.6e-7 in fp32).  A packed
+// above: 2.5e-7 and 6.4e-8 relative; 3.3e-7 and 1.6e-7 in fp32).  A packed
 // instruction keeps the FMA pipe for two cycles, and on 256 rows each one of a pair
 // costs 8 us of a tree over 128K keys: five or seven against nineteen.
 // Code costs as well: warps at different places of more code than the instruction
