@@ -237,7 +237,8 @@ va_status check_common(const Common &c) {
 // Checks a call's score shaping and turns it into kernel parameters.  The
 // scores come out in units of `unit` (log2 e: base 2).  `draft_mask`: the call
 // has a tree or a mask, whose tokens' positions are not those of a chain.
-va_status check_mod(const va_score_mod &m, float scale, float unit, bool draft_mask, va::ModParams &mp) {
+// `fine`: the cap as the weights need it.
+va_status check_mod(const va_score_mod &m, float scale, float unit, bool draft_mask, bool fine, va::ModParams &mp) {
   if (m.softcap != 0.f && !(m.softcap >= 1e-6f && m.softcap <= 1e6f))
     return fail(VA_ERR_INVALID_ARG, "softcap=%g must be 0 or in [1e-6, 1e6]", (double)m.softcap);
   if (m.softcap != 0.f && !isfinite(scale / m.softcap))
@@ -253,19 +254,22 @@ va_status check_mod(const va_score_mod &m, float scale, float unit, bool draft_m
   mp.softcap = m.softcap;
   mp.in_mul = m.softcap > 0.f ? scale / m.softcap : 0.f;
   mp.out_mul = (m.softcap > 0.f ? m.softcap : scale) * unit;
-  // tanh(y) / y as polynomials of y^2 on |y| <= 0.45 and 0.75 (see
+  // tanh(y) / y as polynomials of y^2 on |y| <= 0.45 (`fine`: 0.55) and 0.75 (see
   // cap_scores), with y = raw * in_mul, the cap and the unit folded in.
   // Coefficients that leave fp32's range (an extreme ratio of scale and cap)
   // switch one off.
   static const double poly4[4] = {0.9999997567324063, -0.33329467152321846, 0.13236368607993834, -0.046028179312785855};
-  static const double poly6[6] = {1.0,          -0.33332958817481995, 0.1332540661096573, -0.05334445461630821,
-                                  0.019582949578762054, -0.004716284107416868};
+  static const double poly5[5] = {0.9999999676555539, -0.3333279510369555, 0.133188778641548, -0.052589361543509544,
+                                  0.01631550484988293};
+  static const double poly6[6] = {0.9999999710305179,   -0.33332958938071583, 0.1332540659736949,
+                                  -0.05334445358700722, 0.01958294971043087,  -0.0047162840144022765};
   const struct {
     const double *poly;
     int n;
     double lim;
     float *c;
-  } small[2] = {{poly4, 4, 0.45, mp.small_c4}, {poly6, 6, 0.75, mp.small_c6}};
+  } small[2] = {{fine ? poly5 : poly4, fine ? 5 : 4, fine ? 0.55 : 0.45, mp.small_c},
+                {poly6, 6, 0.75, mp.small_c6}};
   for (int i = 0; i < 2; ++i) {
     mp.small_lim[i] = -1.f;
     if (!(m.softcap > 0.f)) continue;
@@ -294,7 +298,7 @@ va_status run_attention(const Common &c, int layout, const void *k, const void *
   va::ModParams mp;
   memset(&mp, 0, sizeof mp);
   if (mod != nullptr) {
-    const va_status st = check_mod(*mod, s.scale, va::kModLog2e, c.parent != nullptr || c.mask != nullptr, mp);
+    const va_status st = check_mod(*mod, s.scale, va::kModLog2e, c.parent != nullptr || c.mask != nullptr, false, mp);
     if (st != VA_OK) return st;
   }
   const int sms = device_sm_count(&dev);
@@ -487,7 +491,7 @@ va_status weight_common(const va_shape *shape, const va_score_mod *mod, const vo
   p.status = static_cast<int *>(workspace);
   const va_score_mod none = {0.f, 0, nullptr, nullptr, nullptr};
   // natural units; accepted row i sits at L_b + i, so no token_pos
-  st = check_mod(mod != nullptr ? *mod : none, shape->scale, 1.f, false, p.mod);
+  st = check_mod(mod != nullptr ? *mod : none, shape->scale, 1.f, false, true, p.mod);
   if (st != VA_OK) return st;
   p.mod.token_pos = nullptr;
   p.wait_ns = call_wait_ns();

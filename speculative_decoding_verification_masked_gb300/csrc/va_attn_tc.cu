@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(TcSmem<NMT, NS>::threads(kMod), 1)
       const int k0 = (kMod == 2 ? tile_of<true>(p, lt, lt0, lt1) : lt) * kTK;
       const bool masked = k0 + kTK > g.n_prefix || (kMod != 0 && k0 < g.hi);
       if constexpr (kMod == 2) {
-        if (p.mod.softcap > 0.f) cap_scores<N, true>(p.mod, sv, false, masked);
+        if (p.mod.softcap > 0.f) cap_scores<N, true, false>(p.mod, sv, false, masked);
         if (p.mod.slopes != nullptr) {
           const float mul = p.mod.softcap > 0.f ? 1.f : p.mod.out_mul;
           const int kh = k0 + N * half;

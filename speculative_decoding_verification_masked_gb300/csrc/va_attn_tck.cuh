@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(TkCfg<NR, kTma, kMod>::kThreads, 1)
       auto load_scores = [&]() {
         tmem_ld_f<NW>(tS, x);
         if constexpr (kMod == 2) {
-          if (p.mod.softcap > 0.f) cap_scores<NW, false>(p.mod, x, km_all == 0ull, false);
+          if (p.mod.softcap > 0.f) cap_scores<NW, false, false>(p.mod, x, km_all == 0ull, false);
           if (p.mod.slopes != nullptr) {
             const float mul = p.mod.softcap > 0.f ? 1.f : p.mod.out_mul;
             if (behind) {

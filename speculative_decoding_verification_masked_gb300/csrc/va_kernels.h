@@ -18,10 +18,10 @@ struct ModParams {
   int on;
   float softcap;           // 0: no cap
   float in_mul, out_mul;   // capped: scale / cap and cap * log2 e; else out_mul = scale * log2 e
-  // the cap of small products as polynomials of 4 and 6 terms: capped score =
+  // the cap of small products as two polynomials: capped score =
   // raw * (sum of c[k] raw^2k) for |raw| up to lim (-1: never)
   float small_lim[2];
-  float small_c4[4], small_c6[6];
+  float small_c[5], small_c6[6];  // (4 terms for attention, 5 for the weights)
   int window;              // 0: no window
   const float *slopes;     // [Hq] or NULL
   const int32_t *key_start;// [B] or NULL

@@ -78,7 +78,7 @@ __device__ __forceinline__ float capped_tanh(float y, float cap2) {
 
 // raw * (sum of c[k] raw^2k) of N products in place.
 template <int N, int K>
-__device__ __forceinline__ void cap_small(const float (&c)[K], float (&x)[N]) {
+__device__ __forceinline__ void cap_small(const float *c, float (&x)[N]) {
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
     const float2 r = make_float2(x[i], x[i + 1]);
@@ -96,9 +96,12 @@ __device__ __forceinline__ void cap_small(const float (&c)[K], float (&x)[N]) {
 // leaves small |y|, where tanh is an odd polynomial, with the scale and the cap
 // folded into its coefficients and no division: where every product of the warp has
 // |y| <= 0.45, of degree 7, and (kMid) up to 0.75 of degree 11 (fitted like the
-// above: 2.5e-7 and 6.4e-8 relative; 3.3e-7 and 1.6e-7 in fp32).  A packed
+// above: 2.5e-7 and 2.9e-8 relative; 3.3e-7 and 1.6e-7 in fp32).  A packed
 // instruction keeps the FMA pipe for two cycles, and on 256 rows each one of a pair
 // costs 8 us of a tree over 128K keys: five or seven against nineteen.
+// The weights take one more term (kFine: |y| <= 0.55, degree 9, 3.2e-8; 1.4e-7 in
+// fp32): exp(s - lse) shows a score's last digits, and with four terms the weights of a
+// chain were off by 3.8e-6, twice what fp32 tanh leaves.
 // Code costs as well: warps at different places of more code than the instruction
 // caches hold wait for it.  With 64 scores a thread the 256-row tree took 537 us
 // where a tile's warps went different ways and 212 where they did not (32 scores:
@@ -108,7 +111,7 @@ __device__ __forceinline__ void cap_small(const float (&c)[K], float (&x)[N]) {
 // The form decides the last bits, so it may depend on nothing that no row sees: a
 // thread whose key is hidden from every row (`hidden`) has no say, and where a thread
 // has keys of both kinds (`mixed`) the general form is taken without asking.
-template <int N, bool kMid>
+template <int N, bool kMid, bool kFine>
 __device__ __forceinline__ void cap_scores(const ModParams &m, float (&x)[N], bool hidden, bool mixed) {
   float top = 0.f;
 #pragma unroll
@@ -117,9 +120,9 @@ __device__ __forceinline__ void cap_scores(const ModParams &m, float (&x)[N], bo
   top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // (none is negative)
   if (mixed) top = INFINITY;
   if (top <= m.small_lim[0]) {
-    cap_small<N>(m.small_c4, x);
+    cap_small<N, kFine ? 5 : 4>(m.small_c, x);
   } else if (kMid && top <= m.small_lim[1]) {
-    cap_small<N>(m.small_c6, x);
+    cap_small<N, 6>(m.small_c6, x);
   } else {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {

@@ -513,7 +513,7 @@ __global__ void __launch_bounds__((4 * kGroups + 3) * 32, 1)
         float x[32];
 #pragma unroll
         for (int r = 0; r < 32; ++r) x[r] = __uint_as_float(u[r]);
-        if (kMod && p.mod.softcap > 0.f) cap_scores<32, true>(p.mod, x, !there, false);
+        if (kMod && p.mod.softcap > 0.f) cap_scores<32, true, true>(p.mod, x, !there, false);
         const float mul = kMod && p.mod.softcap > 0.f ? 1.f : p.mod.out_mul;
         if (kMod && p.mod.slopes != nullptr) {
 #pragma unroll
