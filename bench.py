@@ -659,14 +659,14 @@ _HEADERS = ['va_common.cuh', 'va_pipeline.cuh', 'va_mod.cuh', 'va_tcgen05.cuh', 
             'va_merge.cuh']
 KERNEL_SOURCES = {"tc": ["va_attn_tc.cu"] + _HEADERS, "tck": ["va_attn_tck.cu", "va_attn_tck.cuh"] + _HEADERS}
 PROFILED_TRAFFIC = {
-    "tree": {"sources": "tc", "sha256": "5b7edc3b25a3d77a60d85b1415d48ea7726a24c2ab691d0221c86acedbe10da7",
-             "kernel": "verify_attn_tc_kernel<2, TMA>", "bytes": 541476096},
-    "chain": {"sources": "tck", "sha256": "2e39f091483386e3283659cd5205870075cedf9e7cf89ed0c5c8876c9dc63cdd",
-              "kernel": "verify_attn_tck_kernel<128, 32, TMA>", "bytes": 137700608},
-    "sparse": {"sources": "tck", "sha256": "2e39f091483386e3283659cd5205870075cedf9e7cf89ed0c5c8876c9dc63cdd",
-               "kernel": "verify_attn_tck_kernel<128, 32, gather>", "bytes": 141008896},
-    "paged": {"sources": "tck", "sha256": "2e39f091483386e3283659cd5205870075cedf9e7cf89ed0c5c8876c9dc63cdd",
-              "kernel": "verify_attn_tck_kernel<128, 64, TMA>", "bytes": 1470697472},
+    "tree": {"sources": "tc", "sha256": "cd212dcfc4330700094765a269c57c1e244352e368298fa5932e651fe940f722",
+             "kernel": "verify_attn_tc_kernel<2, TMA>", "bytes": 541424896},
+    "chain": {"sources": "tck", "sha256": "ca669ac3fa53988905cf1703fe684493208bb616ebeb0dd52b8adcff48c5af4e",
+              "kernel": "verify_attn_tck_kernel<128, 32, TMA>", "bytes": 137643008},
+    "sparse": {"sources": "tck", "sha256": "ca669ac3fa53988905cf1703fe684493208bb616ebeb0dd52b8adcff48c5af4e",
+               "kernel": "verify_attn_tck_kernel<128, 32, gather>", "bytes": 140987904},
+    "paged": {"sources": "tck", "sha256": "ca669ac3fa53988905cf1703fe684493208bb616ebeb0dd52b8adcff48c5af4e",
+              "kernel": "verify_attn_tck_kernel<128, 64, TMA>", "bytes": 1471213568},
 }
 
 

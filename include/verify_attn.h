@@ -449,7 +449,8 @@ va_status verify_commit_kv_paged(const va_shape *shape, void *k_pages, void *v_p
  *   Dense: k_cache [B][max_cache_len][Hkv][D].  Paged: as verify_attn_paged.
  * L_b + a must fit the cache and weight_stride, and path entries [0, T)
  * (device-checked: a bad sequence is left alone, a bad path entry adds
- * nothing; VA_ERR_DEVICE_BOUNDS in `workspace`, which may be NULL).
+ * nothing; VA_ERR_DEVICE_BOUNDS in `workspace`, which may be NULL).  If a
+ * bounded wait runs out (VA_ERR_TIMEOUT) the totals are undefined.
  */
 va_status verify_accumulate_weight_dense(const va_shape *shape, const va_score_mod *mod, const void *q,
                                          const void *k_cache, int max_cache_len, const int32_t *seqlens,

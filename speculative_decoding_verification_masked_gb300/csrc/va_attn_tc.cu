@@ -47,9 +47,9 @@
 // caches.  So an M-tile has two softmax warpgroups then (20 warps in all), each
 // with 32 of a tile's 64 keys of every row and half of O's columns: half the code,
 // twice the warps.  They exchange the rows' maxima and sums at the vote's barrier.
-// 64-node tree over 128K keys, uncapped 152 us: capped at 30 210 us with one
-// warpgroup, 204 with two; at 15, where a third of the warps need the general
-// tanh, 537 and 231; 32 nodes (128 rows) 194 and 132; no cap but a document start at
+// 64-node tree over 128K keys, uncapped 153 us: capped at 30 210 us with one
+// warpgroup, 198 with two; at 15, where a third of the warps need the general
+// tanh, 537 and 222; 32 nodes (128 rows) 194 and 135; no cap but a document start at
 // 3/8 of the prefix 114 and 105.
 #include <cuda.h>
 #include <math.h>

@@ -105,9 +105,9 @@ __device__ __forceinline__ void cap_small(const float *c, float (&x)[N]) {
 // Code costs as well: warps at different places of more code than the instruction
 // caches hold wait for it.  With 64 scores a thread the 256-row tree took 537 us
 // where a tile's warps went different ways and 212 where they did not (32 scores:
-// 231 and 204), and the keys-on-lanes kernel loses more by the second polynomial
+// 222 and 198), and the keys-on-lanes kernel loses more by the second polynomial
 // than it gains (64 rows, scores past 0.45: 335 us with it, 314 without; the
-// weights of 256 rows 164 and 200).
+// weights of 256 rows 164 and 200, and 167 with the term more).
 // The form decides the last bits, so it may depend on nothing that no row sees: a
 // thread whose key is hidden from every row (`hidden`) has no say, and where a thread
 // has keys of both kinds (`mixed`) the general form is taken without asking.

@@ -9,8 +9,9 @@
 //   p(h, i, j) = exp(s(q[path[i]][h], k_j) - lse[h][path[i]]),  j <= L_b + i,
 //   w[g][j]    = (j < L_b ? decay * w[g][j] : 0) + sum over h of g and i of p.
 // With decay 0 the old totals are not read: they may be memory never written.
-// No softmax pass and no V: K is read once, every total by one thread, in a
-// fixed order (the result does not depend on the grid).
+// No softmax pass and no V: K is read once for every 256 rows of a kv-head (the
+// totals too), every total by one thread, in a fixed order (the result does not
+// depend on the grid).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -610,7 +611,8 @@ static cudaError_t launch_weight_tc(const WeightParams &p, const CUtensorMap &tm
 
 template <int D, bool kTma, int kProducers>
 static cudaError_t launch_weight_p(const WeightParams &p, const CUtensorMap &tmk, int grid, cudaStream_t stream) {
-  // (a cap or slopes leave four warpgroups too few registers: 256 rows capped 138 / 238 us)
+  // (a cap or slopes leave four warpgroups too few registers: 256 rows capped 138 / 238 us;
+  // 142 with the term that the weights' cap has more)
   if (p.mod.on == 2) return launch_weight_tc<D, kTma, true, kProducers, 2>(p, tmk, grid, stream);
   // 8 x 128K keys, one warpgroup a tile against two: 160 rows 50.9 / 51.7 us, 192 rows
   // 57.9 / 52.1, 256 rows 72.8 / 65.7
