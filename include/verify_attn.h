@@ -510,6 +510,99 @@ va_status verify_evict_kv_paged(const va_shape *shape, void *k_pages, void *v_pa
                                 int weight_stride, int32_t *seqlens_out, void *scratch, size_t scratch_bytes,
                                 void *workspace, va_stream stream);
 
+/*
+ * RMS norm of every query and key head and the rotary embedding, in one pass
+ * over a projection's output, out of place or in place.  For every row x (one
+ * head of one token), in fp32 and rounded once:
+ *   y = x / sqrt(mean(x^2) + eps) * weight       (the head's weight given)
+ *   y rotated as verify_rope_draft_* rotates     (positions given)
+ * with q_weight for the query heads and k_weight for the key heads, each [D] of
+ * the element type; NULL leaves those rows unnormed.  positions [B][T] int32,
+ * any value; NULL rotates nothing.  Angles are good to 2^-25 of a turn at any
+ * position, to 2^-34 below 2^20.
+ *   shape: B, T, Hq, Hkv, D, dtype bf16 or fp32 and rope_base (read with
+ *     positions); any T with B * T < 2^31; D a multiple of 16, at most 256; Hq
+ *     and Hkv need not divide.  scale is not used.
+ *   q, k and the outputs are rows of D elements, 16-byte aligned; head h of
+ *     token t of sequence b starts (b * batch stride + t * token stride + h * D)
+ *     elements from the pointer, strides in elements and such that every row is
+ *     16-byte aligned (q and k may lie side by side in one projection's output).
+ *     An output may be its own input, with the same strides; any other overlap
+ *     of outputs and inputs is undefined.
+ */
+typedef struct {
+  const void *ptr;      /* written where it is an output */
+  int64_t batch_stride; /* elements from token t of one sequence to that of the next */
+  int64_t token_stride; /* elements from one token to the next */
+} va_rows;
+
+va_status verify_norm_rope(const va_shape *shape, const va_rows *q, const va_rows *k, const void *q_weight,
+                           const void *k_weight, float eps, const int32_t *positions, const va_rows *q_out,
+                           const va_rows *k_out, va_stream stream);
+
+/*
+ * Caches held in 8 or 4 bits.  A quantised row is one token of one kv-head, a
+ * run of verify_kv_row_bytes() bytes:
+ *   VA_KV_E4M3  D codes in e4m3, the row scale s (fp32), 12 zero bytes
+ *               (D 128: 144 bytes, D 64: 80);  x = code * s
+ *   VA_KV_E2M1  D/2 bytes of codes in e2m1 (element 2j in the low half of byte
+ *               j), D/16 group scales g in e4m3, s (fp32), zeros to a multiple
+ *               of 16 (D 128: 80 bytes, D 64: 48);  x = code * g * s, g that of
+ *               the element's group of 16
+ * With amax the row's largest magnitude, s = 2^e for the least e >= -126 with
+ * amax <= 448 * 2^e (e4m3) or amax <= 6 * 448 * 2^e (e2m1); g is the largest
+ * magnitude of the group / (6 s), and a code x / s or x / (g s), each rounded to
+ * the nearest representable value, ties to even, saturating (g = 0: code 0).
+ * These roundings are exact: the bytes are the same for every call.  A row that
+ * holds an infinity or a NaN has s = NaN and reads back as NaN.
+ *   Caches take the place of K and V caches of rows of D elements:
+ *   dense [B][max_cache_len][Hkv][row bytes], pages [num_pages][page_size][Hkv]
+ *   [row bytes], both 16-byte aligned.  verify_commit_kv_* and verify_evict_kv_*
+ *   move such rows when called with dtype bf16 and D = row bytes / 2.
+ */
+typedef enum { VA_KV_E4M3 = 0, VA_KV_E2M1 = 1 } va_kv_format;
+
+/* Bytes of a quantised row; 0 for an unknown format or a D other than 64 or 128. */
+size_t verify_kv_row_bytes(va_kv_format format, int D);
+
+/*
+ * Rows of K and V quantised into such a cache: row t < n_tokens[b] of sequence b
+ * goes to slot seqlens[b] + t.  Other slots keep what they hold.  Use: append the
+ * draft rows (normed and rotated, verify_norm_rope) or a chunk of a prompt.
+ *   shape: B (<= 65535), T, Hkv, D (64 or 128), dtype bf16 or fp32 (Hq and scale
+ *     are not used); any T with T * Hkv < 2^30.
+ *   k, v: as in verify_norm_rope.  n_tokens [B] int32 in [0, T], or NULL: T.
+ *   Dense: seqlens[b] + n_tokens[b] <= max_cache_len.  Paged: as verify_attn_paged.
+ * A sequence that does not fit is left alone and a row whose page entry is out of
+ * range is not written; both are recorded as VA_ERR_DEVICE_BOUNDS in `workspace`
+ * (may be NULL).
+ */
+va_status verify_quantize_kv_dense(const va_shape *shape, va_kv_format format, const va_rows *k, const va_rows *v,
+                                   void *k_cache, void *v_cache, int max_cache_len, const int32_t *seqlens,
+                                   const int32_t *n_tokens, void *workspace, va_stream stream);
+
+va_status verify_quantize_kv_paged(const va_shape *shape, va_kv_format format, const va_rows *k, const va_rows *v,
+                                   void *k_pages, void *v_pages, int num_pages, int page_size,
+                                   const int32_t *page_table, int max_pages_per_seq, const int32_t *seqlens,
+                                   const int32_t *n_tokens, void *workspace, va_stream stream);
+
+/*
+ * A range of slots read back: row t < n_tokens[b] of the outputs of sequence b is
+ * slot start[b] + t in shape->dtype, rounded to nearest (bf16 and fp32 hold every
+ * value exactly but where it leaves their range); later rows of the outputs keep
+ * what they hold.  Arguments, limits and errors as above (k and v are written; the
+ * rows of a bad sequence or page are not).
+ */
+va_status verify_dequantize_kv_dense(const va_shape *shape, va_kv_format format, const void *k_cache,
+                                     const void *v_cache, int max_cache_len, const int32_t *start,
+                                     const int32_t *n_tokens, const va_rows *k, const va_rows *v, void *workspace,
+                                     va_stream stream);
+
+va_status verify_dequantize_kv_paged(const va_shape *shape, va_kv_format format, const void *k_pages,
+                                     const void *v_pages, int num_pages, int page_size, const int32_t *page_table,
+                                     int max_pages_per_seq, const int32_t *start, const int32_t *n_tokens,
+                                     const va_rows *k, const va_rows *v, void *workspace, va_stream stream);
+
 /* Wait for `stream`, read and clear the device status word of `workspace`.
  * Returns VA_OK or the first device-side error recorded since the last check.
  * After VA_ERR_TIMEOUT the workspace needs verify_attn_workspace_init() before

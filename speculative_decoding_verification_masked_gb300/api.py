@@ -41,6 +41,10 @@ class VaShape(ctypes.Structure):
                 ("rope_base", ctypes.c_float)]
 
 
+class VaRows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -78,6 +82,12 @@ _SIGS = {
     "verify_evict_kv_dense": (_I, [ctypes.POINTER(VaShape), _P, _P, _I, _P, _P, _P, _I, _P, _I, _P, _P, _SZ, _P, _P]),
     "verify_evict_kv_paged": (_I, [ctypes.POINTER(VaShape), _P, _P, _I, _I, _P, _I, _P, _P, _P, _I, _P, _I, _P, _P,
                                    _SZ, _P, _P]),
+    "verify_norm_rope": (_I, [_P, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P]),
+    "verify_kv_row_bytes": (_SZ, [_I, _I]),
+    "verify_quantize_kv_dense": (_I, [_P, _I, _P, _P, _P, _P, _I, _P, _P, _P, _P]),
+    "verify_quantize_kv_paged": (_I, [_P, _I, _P, _P, _P, _P, _I, _I, _P, _I, _P, _P, _P, _P]),
+    "verify_dequantize_kv_dense": (_I, [_P, _I, _P, _P, _I, _P, _P, _P, _P, _P, _P]),
+    "verify_dequantize_kv_paged": (_I, [_P, _I, _P, _P, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P]),
     "verify_attn_check_status": (_I, [_P, _P]),
     "verify_attn_last_error": (ctypes.c_char_p, []),
     "verify_attn_version": (ctypes.c_char_p, []),
@@ -302,10 +312,21 @@ def verify_accept_greedy(parent, draft_tokens, target_next, path=None, n_accept=
     return path, n_accept, bonus
 
 
+def _bf16_rows(cache):
+    """A cache whose rows are moved as they are: quantised rows (uint8) as bf16 rows of half as many elements."""
+    if isinstance(cache, torch.Tensor) and cache.dtype == torch.uint8 and cache.dim() == 4:
+        if cache.shape[-1] % 16 != 0 or not cache.is_contiguous():
+            raise ValueError("caches held in 8 or 4 bits must be contiguous, in rows of 16-byte multiples")
+        return cache.view(torch.bfloat16)
+    return cache
+
+
 def verify_commit_kv_dense(k_cache, v_cache, seqlens, path, n_accept, seqlens_out=None,
                            workspace: Workspace = None, stream=None):
     """Move the accepted draft rows of k_cache / v_cache [B][len][Hkv][D] in
-    place to the slots after each prefix; returns seqlens + n_accept."""
+    place to the slots after each prefix; returns seqlens + n_accept.  (Here and
+    in the eviction a cache may hold quantised rows, uint8 [..][kv_row_bytes].)"""
+    k_cache, v_cache = _bf16_rows(k_cache), _bf16_rows(v_cache)
     B, cap, Hkv, D = k_cache.shape
     T = path.shape[1]
     if seqlens_out is None:
@@ -320,6 +341,7 @@ def verify_commit_kv_dense(k_cache, v_cache, seqlens, path, n_accept, seqlens_ou
 def verify_commit_kv_paged(k_pages, v_pages, page_table, seqlens, path, n_accept, seqlens_out=None,
                            workspace: Workspace = None, stream=None):
     """The same commit through a page table; pages [P][page][Hkv][D]."""
+    k_pages, v_pages = _bf16_rows(k_pages), _bf16_rows(v_pages)
     P, ps, Hkv, D = k_pages.shape
     B, max_pages = page_table.shape
     T = path.shape[1]
@@ -579,6 +601,7 @@ class EvictScratch(Workspace):
 
 
 def _evict_call(layout, k, v, table, seqlens, indices, n_indices, weight, seqlens_out, scratch, workspace, stream):
+    k, v = _bf16_rows(k), _bf16_rows(v)
     n0, n1, Hkv, D = cache = _sizes(k, "the key cache", 4)
     B, _, m = _sizes(indices, "indices", 3)
     stride = _sizes(weight, "weight", 3)[2] if weight is not None else 0
@@ -614,6 +637,129 @@ def verify_evict_kv_paged(k_pages, v_pages, page_table, seqlens, indices, n_indi
     """The same eviction through a page table; pages [P][page][Hkv][D]."""
     return _evict_call("paged", k_pages, v_pages, page_table, seqlens, indices, n_indices, weight, seqlens_out,
                        scratch, workspace, stream)
+
+
+# ----------------------------------------------------------------------------
+# norm with rotation, caches held in 8 or 4 bits
+# ----------------------------------------------------------------------------
+
+KV_FORMATS = {"e4m3": 0, "e2m1": 1}
+
+
+def kv_row_bytes(fmt, D) -> int:
+    """Bytes of a quantised row (one token of one kv-head): caches of format `fmt`
+    ("e4m3" or "e2m1") are uint8 [B][len][Hkv][kv_row_bytes], or pages of such rows."""
+    n = int(lib().verify_kv_row_bytes(_format(fmt), int(D)))
+    if n == 0:
+        raise ValueError(f"caches held in {fmt} take D = 64 or 128, not {D}")
+    return n
+
+
+def _format(fmt) -> int:
+    try:
+        return KV_FORMATS[fmt]
+    except (KeyError, TypeError):
+        raise ValueError(f"unknown cache format {fmt!r}; use 'e4m3' or 'e2m1'") from None
+
+
+def _rows(t, name, shape, dtype, dev) -> VaRows:
+    """Rows of D elements of a [B][T][heads][D] tensor: heads side by side, any
+    batch and token stride (a part of a projection's output)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must live on the GPU")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the others on cuda:{dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+    B, T, H, D = shape
+    sb, st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return VaRows(t.data_ptr(), sb if B > 1 else 0, st if T > 1 else 0)
+
+
+def verify_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, eps=1e-6, rope_base=10000.0, q_out=None,
+                     k_out=None, stream=None):
+    """RMS norm of every head of q [B][T][Hq][D] and k [B][T][Hkv][D] (weights [D];
+    None: no norm) and the rotation at positions int32 [B][T] (None: no rotation),
+    in one pass.  q and k may be parts of one projection's output; returns (q_out,
+    k_out), contiguous unless given (an output may be its own input)."""
+    B, T, Hq, D = _sizes(q, "q", 4)
+    Hkv = _sizes(k, "k", 4)[2]
+    dev, dtype = q.get_device(), q.dtype
+    shape = VaShape(B, T, Hq, Hkv, D, _dtype_code(q), 1.0, rope_base)
+    sq, sk = (B, T, Hq, D), (B, T, Hkv, D)
+    if q_out is None or k_out is None:
+        new = _made(lambda: [torch.empty(s, dtype=dtype, device=q.device) if o is None else o
+                             for s, o in ((sq, q_out), (sk, k_out))], dev, stream)
+        q_out, k_out = new
+    _run_on(dev, stream, "verify_norm_rope", ctypes.byref(shape), ctypes.byref(_rows(q, "q", sq, dtype, dev)),
+            ctypes.byref(_rows(k, "k", sk, dtype, dev)), _arg(q_weight, "q_weight", (D,), dtype, dev),
+            _arg(k_weight, "k_weight", (D,), dtype, dev), eps, _arg(positions, "positions", (B, T), _I32, dev),
+            ctypes.byref(_rows(q_out, "q_out", sq, dtype, dev)), ctypes.byref(_rows(k_out, "k_out", sk, dtype, dev)))
+    return q_out, k_out
+
+
+def _quant_call(what, layout, k, v, k_cache, v_cache, table, start, fmt, n_tokens, workspace, stream):
+    B, T, Hkv, D = rows = _sizes(k, "k", 4)
+    n0, n1, _, _ = _sizes(k_cache, "the key cache", 4)
+    dev, dtype = k.get_device(), k.dtype
+    shape = VaShape(B, T, Hkv, Hkv, D, _dtype_code(k), 1.0, 0.0)
+    code, cache = _format(fmt), (n0, n1, Hkv, kv_row_bytes(fmt, D))
+    plain = ctypes.byref(_rows(k, "k", rows, dtype, dev)), ctypes.byref(_rows(v, "v", rows, dtype, dev))
+    caches = (_arg(k_cache, "the key cache", cache, torch.uint8, dev),
+              _req(v_cache, "the value cache", cache, torch.uint8, dev), *_cache_args(layout, n0, n1, B, table, dev))
+    first = _req(start, "start" if what == "dequantize" else "seqlens", (B,), _I32, dev)
+    count = _arg(n_tokens, "n_tokens", (B,), _I32, dev)
+    args = (*plain, *caches, first, count) if what == "quantize" else (*caches, first, count, *plain)
+    _run_on(dev, stream, f"verify_{what}_kv_{layout}", ctypes.byref(shape), code, *args, _status_ptr(workspace, dev))
+
+
+def verify_quantize_kv_dense(k, v, k_cache, v_cache, seqlens, fmt, n_tokens=None, workspace: Workspace = None,
+                             stream=None):
+    """Quantise rows k, v [B][T][Hkv][D] into caches held in `fmt`, uint8
+    [B][len][Hkv][kv_row_bytes], at slots seqlens[b] + t for t < n_tokens[b] (None: T)."""
+    _quant_call("quantize", "dense", k, v, k_cache, v_cache, None, seqlens, fmt, n_tokens, workspace, stream)
+
+
+def verify_quantize_kv_paged(k, v, k_pages, v_pages, page_table, seqlens, fmt, n_tokens=None,
+                             workspace: Workspace = None, stream=None):
+    """The same through a page table; pages uint8 [P][page][Hkv][kv_row_bytes]."""
+    _quant_call("quantize", "paged", k, v, k_pages, v_pages, page_table, seqlens, fmt, n_tokens, workspace, stream)
+
+
+def _read_back(layout, k_cache, v_cache, table, start, fmt, n, dtype, n_tokens, k_out, v_out, workspace, stream):
+    _, _, Hkv, nbytes = _sizes(k_cache, "the key cache", 4)
+    B = _sizes(start, "start", 1)[0]
+    if k_out is None or v_out is None:
+        if n is None:
+            raise TypeError("n: the number of slots is needed without k_out and v_out")
+        D = {kv_row_bytes(fmt, d): d for d in (64, 128)}.get(nbytes)
+        if D is None:
+            raise ValueError(f"the key cache: rows of {nbytes} bytes are no {fmt} rows")
+        # (rows past n_tokens stay as they are made: zero)
+        k_out, v_out = _made(lambda: [torch.zeros(B, n, Hkv, D, dtype=dtype, device=k_cache.device) if o is None else o
+                                      for o in (k_out, v_out)], k_cache.get_device(), stream)
+    _quant_call("dequantize", layout, k_out, v_out, k_cache, v_cache, table, start, fmt, n_tokens, workspace, stream)
+    return k_out, v_out
+
+
+def verify_dequantize_kv_dense(k_cache, v_cache, start, fmt, n=None, dtype=torch.bfloat16, n_tokens=None, k_out=None,
+                               v_out=None, workspace: Workspace = None, stream=None):
+    """Read slots start[b] .. start[b] + n - 1 of caches held in `fmt` back (only the
+    first n_tokens[b] of them, if given); returns (k, v) [B][n][Hkv][D]."""
+    return _read_back("dense", k_cache, v_cache, None, start, fmt, n, dtype, n_tokens, k_out, v_out, workspace, stream)
+
+
+def verify_dequantize_kv_paged(k_pages, v_pages, page_table, start, fmt, n=None, dtype=torch.bfloat16, n_tokens=None,
+                               k_out=None, v_out=None, workspace: Workspace = None, stream=None):
+    """The same through a page table."""
+    return _read_back("paged", k_pages, v_pages, page_table, start, fmt, n, dtype, n_tokens, k_out, v_out, workspace,
+                      stream)
 
 
 def verify_attn_check_status(workspace: Workspace, stream=None):

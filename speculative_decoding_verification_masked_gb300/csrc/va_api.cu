@@ -17,6 +17,7 @@
 #include "va_kernels.h"
 #include "va_commit.h"
 #include "va_evict.h"
+#include "va_quant.h"
 #include "va_score.h"
 #include "va_rope.h"
 #include "va_weight.h"
@@ -640,6 +641,67 @@ va_status rope_common(const va_shape *shape, void *q, void *k, const int32_t *se
   rp.status = static_cast<int *>(workspace);
   return VA_OK;
 }
+
+// Rows of a [B][T][heads][D] tensor: every row 16-byte aligned; where they are
+// written, no two in one place.
+va_status check_rows(const va_rows *r, const char *name, const va_shape &s, int heads, bool written, va::TokenRows &out) {
+  const int elem = s.dtype == VA_DTYPE_BF16 ? 2 : 4;
+  if (r == nullptr || r->ptr == nullptr) return fail(VA_ERR_INVALID_ARG, "%s must not be NULL", name);
+  if (!aligned(r->ptr, 16) || r->batch_stride % (16 / elem) != 0 || r->token_stride % (16 / elem) != 0)
+    return fail(VA_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned", name);
+  const int64_t lim = (int64_t)1 << 40;
+  if (r->batch_stride < 0 || r->token_stride < 0 || r->batch_stride > lim || r->token_stride > lim)
+    return fail(VA_ERR_INVALID_ARG, "%s: strides must be in [0, 2^40]", name);
+  if (written) {
+    const int64_t row = (int64_t)heads * s.D, tok = s.T > 1 ? r->token_stride : row, bat = s.B > 1 ? r->batch_stride : row;
+    const bool apart = tok >= row && bat >= row &&
+                       (s.T == 1 || s.B == 1 || bat / s.T >= tok || tok / s.B >= bat);
+    if (!apart) return fail(VA_ERR_INVALID_ARG, "%s: the strides put rows in one place", name);
+  }
+  out = {r->ptr, (long long)r->batch_stride, (long long)r->token_stride};
+  return VA_OK;
+}
+
+va_status quant_common(const va_shape *shape, va_kv_format format, const va_rows *k, const va_rows *v,
+                       const void *k_cache, const void *v_cache, const int32_t *start, const int32_t *n_tokens,
+                       void *workspace, bool write, va::QuantParams &p) {
+  if (shape == nullptr) return fail(VA_ERR_INVALID_ARG, "shape is NULL");
+  const va_shape &s = *shape;
+  if (s.B < 1 || s.T < 1 || s.Hkv < 1) return fail(VA_ERR_INVALID_ARG, "B, T and Hkv must be >= 1");
+  if (s.dtype != VA_DTYPE_BF16 && s.dtype != VA_DTYPE_FP32) return fail(VA_ERR_INVALID_ARG, "unknown dtype %d", (int)s.dtype);
+  if (format != VA_KV_E4M3 && format != VA_KV_E2M1) return fail(VA_ERR_INVALID_ARG, "unknown cache format %d", (int)format);
+  if (s.D != 64 && s.D != 128) return fail(VA_ERR_UNSUPPORTED, "D=%d; 64 and 128 are supported", s.D);
+  if (s.B > 65535 || (long long)s.T * s.Hkv >= (1ll << 30))
+    return fail(VA_ERR_UNSUPPORTED, "B <= 65535 and T * Hkv < 2^30 are supported");
+  memset(&p, 0, sizeof p);
+  va_status st = check_rows(k, "k", s, s.Hkv, !write, p.k);
+  if (st == VA_OK) st = check_rows(v, "v", s, s.Hkv, !write, p.v);
+  if (st != VA_OK) return st;
+  if (k_cache == nullptr || v_cache == nullptr || start == nullptr)
+    return fail(VA_ERR_INVALID_ARG, "the caches and the first slots must not be NULL");
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return fail(VA_ERR_INVALID_ARG, "caches must be 16-byte aligned");
+  if (!aligned(start, 4) || !aligned(n_tokens, 4))
+    return fail(VA_ERR_INVALID_ARG, "the first slots and n_tokens must be 4-byte aligned");
+  if (workspace != nullptr && !aligned(workspace, 256)) return fail(VA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  p.B = s.B;
+  p.T = s.T;
+  p.Hkv = s.Hkv;
+  p.D = s.D;
+  p.fp32 = s.dtype == VA_DTYPE_FP32 ? 1 : 0;
+  p.format = format;
+  p.k_cache = const_cast<void *>(k_cache);
+  p.v_cache = const_cast<void *>(v_cache);
+  p.start = start;
+  p.n_tokens = n_tokens;
+  p.status = static_cast<int *>(workspace);
+  return VA_OK;
+}
+
+va_status run_quant(const va::QuantParams &p, bool write, cudaStream_t stream) {
+  cudaError_t e = write ? va::launch_quantize_kv(p, stream) : va::launch_dequantize_kv(p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, write ? "quantising launch" : "read-back launch");
+  return ok();
+}
 }  // namespace
 
 extern "C" {
@@ -798,6 +860,100 @@ va_status verify_commit_kv_dense(const va_shape *shape, void *k_cache, void *v_c
   cudaError_t e = va::launch_commit_kv(cp, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "commit launch");
   return ok();
+}
+
+va_status verify_norm_rope(const va_shape *shape, const va_rows *q, const va_rows *k, const void *q_weight,
+                           const void *k_weight, float eps, const int32_t *positions, const va_rows *q_out,
+                           const va_rows *k_out, va_stream stream) {
+  if (shape == nullptr) return fail(VA_ERR_INVALID_ARG, "shape is NULL");
+  const va_shape &s = *shape;
+  if (s.B < 1 || s.T < 1 || s.Hq < 1 || s.Hkv < 1 || s.D < 1)
+    return fail(VA_ERR_INVALID_ARG, "bad shape (B=%d T=%d Hq=%d Hkv=%d D=%d)", s.B, s.T, s.Hq, s.Hkv, s.D);
+  if (s.dtype != VA_DTYPE_BF16 && s.dtype != VA_DTYPE_FP32) return fail(VA_ERR_INVALID_ARG, "unknown dtype %d", (int)s.dtype);
+  if (s.D > 256 || s.D % 16 != 0) return fail(VA_ERR_UNSUPPORTED, "D=%d; multiples of 16 up to 256 are supported", s.D);
+  if ((long long)s.B * s.T >= (1ll << 31) || (long long)s.Hq + s.Hkv > 65536)
+    return fail(VA_ERR_UNSUPPORTED, "B * T < 2^31 and Hq + Hkv <= 65536 are supported");
+  va::NormParams p;
+  memset(&p, 0, sizeof p);
+  va_status st = check_rows(q, "q", s, s.Hq, false, p.q);
+  if (st == VA_OK) st = check_rows(k, "k", s, s.Hkv, false, p.k);
+  if (st == VA_OK) st = check_rows(q_out, "q_out", s, s.Hq, true, p.q_out);
+  if (st == VA_OK) st = check_rows(k_out, "k_out", s, s.Hkv, true, p.k_out);
+  if (st != VA_OK) return st;
+  if (!aligned(q_weight, 16) || !aligned(k_weight, 16)) return fail(VA_ERR_INVALID_ARG, "weights must be 16-byte aligned");
+  if (!aligned(positions, 4)) return fail(VA_ERR_INVALID_ARG, "positions must be 4-byte aligned");
+  if ((q_weight != nullptr || k_weight != nullptr) && !(eps >= 0.f && isfinite(eps)))
+    return fail(VA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  p.B = s.B;
+  p.T = s.T;
+  p.Hq = s.Hq;
+  p.Hkv = s.Hkv;
+  p.D = s.D;
+  p.fp32 = s.dtype == VA_DTYPE_FP32 ? 1 : 0;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.eps = eps;
+  p.positions = positions;
+  if (positions != nullptr) {
+    if (!(s.rope_base > 0.f) || !isfinite(s.rope_base)) return fail(VA_ERR_INVALID_ARG, "rope_base must be finite and > 0");
+    for (int i = 0; i < s.D / 2; ++i) {
+      const double turns = fmod(pow((double)s.rope_base, -(double)(2 * i) / s.D) / 6.283185307179586, 1.0);
+      p.turns[i] = (uint64_t)ldexp(turns, 64);
+    }
+  }
+  cudaError_t e = va::launch_norm_rope(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "norm and rotation launch");
+  return ok();
+}
+
+size_t verify_kv_row_bytes(va_kv_format format, int D) {
+  if (D != 64 && D != 128) return 0;
+  return format == VA_KV_E4M3 ? (size_t)D + 16 : format == VA_KV_E2M1 ? (size_t)D / 2 + 16 : 0;
+}
+
+va_status verify_quantize_kv_dense(const va_shape *shape, va_kv_format format, const va_rows *k, const va_rows *v,
+                                   void *k_cache, void *v_cache, int max_cache_len, const int32_t *seqlens,
+                                   const int32_t *n_tokens, void *workspace, va_stream stream) {
+  va::QuantParams p;
+  va_status st = quant_common(shape, format, k, v, k_cache, v_cache, seqlens, n_tokens, workspace, true, p);
+  if (st != VA_OK) return st;
+  if (max_cache_len < 1) return fail(VA_ERR_INVALID_ARG, "max_cache_len must be >= 1");
+  p.len_cap = max_cache_len;
+  return run_quant(p, true, (cudaStream_t)stream);
+}
+
+va_status verify_quantize_kv_paged(const va_shape *shape, va_kv_format format, const va_rows *k, const va_rows *v,
+                                   void *k_pages, void *v_pages, int num_pages, int page_size,
+                                   const int32_t *page_table, int max_pages_per_seq, const int32_t *seqlens,
+                                   const int32_t *n_tokens, void *workspace, va_stream stream) {
+  va::QuantParams p;
+  va_status st = quant_common(shape, format, k, v, k_pages, v_pages, seqlens, n_tokens, workspace, true, p);
+  if (st == VA_OK) st = check_pages(p, page_table, num_pages, page_size, max_pages_per_seq, 1);
+  if (st != VA_OK) return st;
+  return run_quant(p, true, (cudaStream_t)stream);
+}
+
+va_status verify_dequantize_kv_dense(const va_shape *shape, va_kv_format format, const void *k_cache,
+                                     const void *v_cache, int max_cache_len, const int32_t *start,
+                                     const int32_t *n_tokens, const va_rows *k, const va_rows *v, void *workspace,
+                                     va_stream stream) {
+  va::QuantParams p;
+  va_status st = quant_common(shape, format, k, v, k_cache, v_cache, start, n_tokens, workspace, false, p);
+  if (st != VA_OK) return st;
+  if (max_cache_len < 1) return fail(VA_ERR_INVALID_ARG, "max_cache_len must be >= 1");
+  p.len_cap = max_cache_len;
+  return run_quant(p, false, (cudaStream_t)stream);
+}
+
+va_status verify_dequantize_kv_paged(const va_shape *shape, va_kv_format format, const void *k_pages,
+                                     const void *v_pages, int num_pages, int page_size, const int32_t *page_table,
+                                     int max_pages_per_seq, const int32_t *start, const int32_t *n_tokens,
+                                     const va_rows *k, const va_rows *v, void *workspace, va_stream stream) {
+  va::QuantParams p;
+  va_status st = quant_common(shape, format, k, v, k_pages, v_pages, start, n_tokens, workspace, false, p);
+  if (st == VA_OK) st = check_pages(p, page_table, num_pages, page_size, max_pages_per_seq, 1);
+  if (st != VA_OK) return st;
+  return run_quant(p, false, (cudaStream_t)stream);
 }
 
 size_t verify_head_importance_scratch_size(int B, int T, int n_heads, int max_cache_len) {
