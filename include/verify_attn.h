@@ -603,6 +603,27 @@ va_status verify_dequantize_kv_paged(const va_shape *shape, va_kv_format format,
                                      int max_pages_per_seq, const int32_t *start, const int32_t *n_tokens,
                                      const va_rows *k, const va_rows *v, void *workspace, va_stream stream);
 
+/*
+ * verify_attn_dense and verify_attn_paged over such a cache: the same draft masks,
+ * lengths, workspace (verify_attn_workspace_size), outputs and errors; bf16 q and
+ * out.  The draft rows are in the cache already (verify_quantize_kv_*).  Scores,
+ * sums and the merge are fp32; a weight is rounded to half precision (relative
+ * 2^-12) before it multiplies its value row.  B * Hkv * ceil(Hq/Hkv*T / 64) <= 2048.
+ * A row that sees no key gets out = 0 and lse = -inf, one that holds a NaN, or sees
+ * a key whose row scale is NaN, NaN for both.  What a key that no row sees holds
+ * does not matter.
+ */
+va_status verify_attn_dense_quant(const va_shape *shape, va_kv_format format, const void *q, const void *k_cache,
+                                  const void *v_cache, int max_cache_len, const int32_t *seqlens,
+                                  const int32_t *tree_parent, const uint32_t *tree_mask, void *out, float *lse,
+                                  void *workspace, size_t ws_bytes, va_stream stream);
+
+va_status verify_attn_paged_quant(const va_shape *shape, va_kv_format format, const void *q, const void *k_pages,
+                                  const void *v_pages, int num_pages, int page_size, const int32_t *page_table,
+                                  int max_pages_per_seq, const int32_t *seqlens, const int32_t *tree_parent,
+                                  const uint32_t *tree_mask, void *out, float *lse, void *workspace, size_t ws_bytes,
+                                  va_stream stream);
+
 /* Wait for `stream`, read and clear the device status word of `workspace`.
  * Returns VA_OK or the first device-side error recorded since the last check.
  * After VA_ERR_TIMEOUT the workspace needs verify_attn_workspace_init() before

@@ -82,6 +82,8 @@ _SIGS = {
     "verify_evict_kv_dense": (_I, [ctypes.POINTER(VaShape), _P, _P, _I, _P, _P, _P, _I, _P, _I, _P, _P, _SZ, _P, _P]),
     "verify_evict_kv_paged": (_I, [ctypes.POINTER(VaShape), _P, _P, _I, _I, _P, _I, _P, _P, _P, _I, _P, _I, _P, _P,
                                    _SZ, _P, _P]),
+    "verify_attn_dense_quant": (_I, [_P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "verify_attn_paged_quant": (_I, [_P, _I, _P, _P, _P, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "verify_norm_rope": (_I, [_P, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P]),
     "verify_kv_row_bytes": (_SZ, [_I, _I]),
     "verify_quantize_kv_dense": (_I, [_P, _I, _P, _P, _P, _P, _I, _P, _P, _P, _P]),
@@ -760,6 +762,43 @@ def verify_dequantize_kv_paged(k_pages, v_pages, page_table, start, fmt, n=None,
     """The same through a page table."""
     return _read_back("paged", k_pages, v_pages, page_table, start, fmt, n, dtype, n_tokens, k_out, v_out, workspace,
                       stream)
+
+
+def _attn_quant(layout, q, k, v, table, seqlens, fmt, tree_parent, tree_mask, out, lse, workspace, scale, stream):
+    B, T, Hq, D = rows = _sizes(q, "q", 4)
+    n0, n1, Hkv, _ = _sizes(k, "the key cache", 4)
+    dev, dtype = q.get_device(), q.dtype
+    shape = VaShape(B, T, Hq, Hkv, D, _dtype_code(q), D ** -0.5 if scale is None else scale, 0.0)
+    code, cache = _format(fmt), (n0, n1, Hkv, kv_row_bytes(fmt, D))
+    if out is None or lse is None:
+        out, lse = _made(lambda: _outputs(q, out, lse), dev, stream)
+    ws = workspace
+    if ws is None:
+        ws = _made(lambda: Workspace.for_shape(shape, q.device, stream), dev, stream)
+    elif ws.buffer.get_device() != dev:
+        raise ValueError(f"workspace is on {ws.buffer.device}, q on cuda:{dev}")
+    _run_on(dev, stream, "verify_attn_dense_quant" if layout == "dense" else "verify_attn_paged_quant",
+            ctypes.byref(shape), code, _arg(q, "q", rows, dtype, dev), _arg(k, "the key cache", cache, torch.uint8, dev),
+            _req(v, "the value cache", cache, torch.uint8, dev), *_cache_args(layout, n0, n1, B, table, dev),
+            _req(seqlens, "seqlens", (B,), _I32, dev), _arg(tree_parent, "tree_parent", (B, T), _I32, dev),
+            _arg(tree_mask, "tree_mask", (B, T, (T + 31) // 32), _I32, dev), _arg(out, "out", rows, dtype, dev),
+            _arg(lse, "lse", (B, Hq, T), _F32, dev), ws.ptr, ws.nbytes)
+    return out, lse
+
+
+def verify_attn_dense_quant(q, k_cache, v_cache, seqlens, fmt, tree_parent=None, tree_mask=None, out=None, lse=None,
+                            workspace: Workspace = None, scale=None, stream=None):
+    """verify_attn_dense over caches held in `fmt` ("e4m3" or "e2m1"), uint8
+    [B][len][Hkv][kv_row_bytes]; returns (out [B][T][Hq][D], lse [B][Hq][T])."""
+    return _attn_quant("dense", q, k_cache, v_cache, None, seqlens, fmt, tree_parent, tree_mask, out, lse, workspace,
+                       scale, stream)
+
+
+def verify_attn_paged_quant(q, k_pages, v_pages, page_table, seqlens, fmt, tree_parent=None, tree_mask=None, out=None,
+                            lse=None, workspace: Workspace = None, scale=None, stream=None):
+    """verify_attn_paged over pages of quantised rows, uint8 [P][page][Hkv][kv_row_bytes]."""
+    return _attn_quant("paged", q, k_pages, v_pages, page_table, seqlens, fmt, tree_parent, tree_mask, out, lse,
+                       workspace, scale, stream)
 
 
 def verify_attn_check_status(workspace: Workspace, stream=None):

@@ -16,6 +16,7 @@
 #include "va_common.cuh"
 #include "va_kernels.h"
 #include "va_commit.h"
+#include "va_attn_quant.h"
 #include "va_evict.h"
 #include "va_quant.h"
 #include "va_score.h"
@@ -117,6 +118,25 @@ bool encode_cache_map(CUtensorMap *m, const void *base, va_dtype dt, int D, int 
   // a host thread that has not touched the GPU yet has no current context, which the
   // driver's call needs: selecting the thread's device makes its primary context current
   int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode() == CUDA_SUCCESS;
+}
+
+// 3-D map over a cache of quantised rows [rows][Hkv][row_bytes]: boxes of box_rows tokens x one
+// kv-head x the whole row, as they are.
+bool encode_rows_map(CUtensorMap *m, const void *base, int row_bytes, int Hkv, long long rows, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)row_bytes, (cuuint64_t)Hkv, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)Hkv * row_bytes};
+  const cuuint32_t box[3] = {(cuuint32_t)row_bytes, 1, (cuuint32_t)box_rows};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  auto encode = [&] {
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  if (encode() == CUDA_SUCCESS) return true;
+  int dev = 0;  // (no context current on this thread yet: as above)
   return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode() == CUDA_SUCCESS;
 }
 
@@ -290,6 +310,53 @@ va_status check_mod(const va_score_mod &m, float scale, float unit, bool draft_m
   return VA_OK;
 }
 
+// The parameters every attention kernel takes from the call.
+void fill_attn(va::AttnParams &p, const Common &c, int layout, const void *k, const void *v, int len_cap, int num_pages,
+               int page_size, const int32_t *page_table, int max_pages) {
+  const va_shape &s = *c.shape;
+  p.B = s.B;
+  p.T = s.T;
+  p.Hq = s.Hq;
+  p.Hkv = s.Hkv;
+  p.D = s.D;
+  p.scale = s.scale;
+  p.dtype = s.dtype;
+  p.layout = layout;
+  p.q = c.q;
+  p.k = k;
+  p.v = v;
+  p.len_cap = len_cap;
+  p.num_pages = num_pages;
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < page_size) ++p.page_shift;
+  p.max_pages = max_pages;
+  p.page_table = page_table;
+  p.seqlens = c.seqlens;
+  p.parent = c.parent;
+  p.mask = c.mask;
+  p.mask_words = (s.T + 31) / 32;
+  p.out = c.out;
+  p.out_align16 = aligned(c.out, 16) ? 1 : 0;
+  p.lse = c.lse;
+  p.wait_ns = call_wait_ns();
+  p.test_drop_part = g_test_drop_part.load();
+  p.test_stall = g_test_stall.load();
+}
+
+// The workspace's parts, for the row plan in p.
+void fill_workspace(va::AttnParams &p, void *workspace, int slots) {
+  const va::WsLayout wl = va::ws_layout(p.S, slots, p.rows_pad, p.D);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  p.status = reinterpret_cast<int *>(ws);
+  p.meta = reinterpret_cast<int2 *>(ws + wl.meta_off);
+  p.split_list = reinterpret_cast<int4 *>(ws + wl.split_off);
+  p.split_count = reinterpret_cast<int *>(ws + va::kSplitCountOff);
+  p.split_done = reinterpret_cast<int *>(ws + va::kSplitDoneOff);
+  p.merge_cnt = reinterpret_cast<int2 *>(ws + wl.mcnt_off);
+  p.lse_part = reinterpret_cast<float *>(ws + wl.lse_off);
+  p.o_part = reinterpret_cast<float *>(ws + wl.o_off);
+}
+
 va_status run_attention(const Common &c, int layout, const void *k, const void *v, int len_cap, int num_pages,
                         int page_size, const int32_t *page_table, int max_pages, const int32_t *indices,
                         const int32_t *n_indices, int max_indices, cudaStream_t stream,
@@ -311,12 +378,8 @@ va_status run_attention(const Common &c, int layout, const void *k, const void *
 
   va::AttnParams p;
   memset(&p, 0, sizeof p);
+  fill_attn(p, c, layout, k, v, len_cap, num_pages, page_size, page_table, max_pages);
   p.mod = mp;
-  p.B = s.B;
-  p.T = s.T;
-  p.Hq = s.Hq;
-  p.Hkv = s.Hkv;
-  p.D = s.D;
   p.R = rp.R;
   p.RG = rp.RG;
   p.NRB = rp.NRB;
@@ -324,25 +387,9 @@ va_status run_attention(const Common &c, int layout, const void *k, const void *
   p.rows_pad = rp.rows_pad;
   p.use_tc = rp.use_tc;
   p.cps = rp.cps;
-  p.scale = s.scale;
-  p.dtype = s.dtype;
-  p.layout = layout;
-  p.q = c.q;
-  p.k = k;
-  p.v = v;
-  p.len_cap = len_cap;
-  p.num_pages = num_pages;
-  p.page_shift = 0;
-  while ((1 << p.page_shift) < page_size) ++p.page_shift;
-  p.max_pages = max_pages;
-  p.page_table = page_table;
-  p.seqlens = c.seqlens;
   p.indices = indices;
   p.n_indices = n_indices;
   p.max_indices = max_indices;
-  p.parent = c.parent;
-  p.mask = c.mask;
-  p.mask_words = (s.T + 31) / 32;
   p.positions = c.positions;
   if (c.positions != nullptr) {
     for (int i = 0; i < s.D / 2; ++i) {
@@ -351,22 +398,7 @@ va_status run_attention(const Common &c, int layout, const void *k, const void *
       p.rope_flo[i] = (float)(f - (double)p.rope_fhi[i]);
     }
   }
-  p.out = c.out;
-  p.out_align16 = aligned(c.out, 16) ? 1 : 0;
-  p.lse = c.lse;
-  const va::WsLayout wl = va::ws_layout(rp.S, rp.S + rp.cps * sms, rp.rows_pad, s.D);
-  uint8_t *ws = static_cast<uint8_t *>(c.ws);
-  p.status = reinterpret_cast<int *>(ws);
-  p.meta = reinterpret_cast<int2 *>(ws + wl.meta_off);
-  p.split_list = reinterpret_cast<int4 *>(ws + wl.split_off);
-  p.split_count = reinterpret_cast<int *>(ws + va::kSplitCountOff);
-  p.split_done = reinterpret_cast<int *>(ws + va::kSplitDoneOff);
-  p.merge_cnt = reinterpret_cast<int2 *>(ws + wl.mcnt_off);
-  p.lse_part = reinterpret_cast<float *>(ws + wl.lse_off);
-  p.o_part = reinterpret_cast<float *>(ws + wl.o_off);
-  p.wait_ns = call_wait_ns();
-  p.test_drop_part = g_test_drop_part.load();
-  p.test_stall = g_test_stall.load();
+  fill_workspace(p, c.ws, rp.S + rp.cps * sms);
 
   CUtensorMap tmk, tmv;
   memset(&tmk, 0, sizeof tmk);
@@ -408,14 +440,95 @@ va_status run_attention(const Common &c, int layout, const void *k, const void *
   return ok();
 }
 
+// Attention over a cache held in 8 or 4 bits (dense or paged).
+va_status run_attention_quant(const Common &c, va_kv_format format, int layout, const void *k, const void *v, int len_cap,
+                              int num_pages, int page_size, const int32_t *page_table, int max_pages,
+                              cudaStream_t stream) {
+  const va_shape &s = *c.shape;
+  const int sms = device_sm_count(nullptr);
+  if (sms <= 0) return fail(VA_ERR_CUDA, "no usable CUDA device");
+  va::AttnParams p;
+  memset(&p, 0, sizeof p);
+  fill_attn(p, c, layout, k, v, len_cap, num_pages, page_size, page_table, max_pages);
+  p.R = (s.Hq / s.Hkv) * s.T;
+  p.rows_pad = va::quant_block_rows(p.R);
+  p.RG = 4;
+  p.NRB = (p.R + p.rows_pad - 1) / p.rows_pad;
+  p.cps = 1;
+  const long long segments = (long long)s.B * s.Hkv * p.NRB;
+  if (segments > kMaxSegments)
+    return fail(VA_ERR_UNSUPPORTED, "B*Hkv*row_blocks = %lld exceeds %d", segments, kMaxSegments);
+  p.S = (int)segments;
+  const size_t need = va::ws_layout(p.S, p.S + sms, p.rows_pad, s.D).total;
+  if (c.ws_bytes < need) return fail(VA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", c.ws_bytes, need);
+  fill_workspace(p, c.ws, p.S + sms);
+
+  const int row = (int)verify_kv_row_bytes(format, s.D);
+  const long long rows = layout == VA_LAYOUT_DENSE ? (long long)s.B * len_cap : (long long)num_pages * page_size;
+  CUtensorMap tmk, tmv;
+  memset(&tmk, 0, sizeof tmk);
+  memset(&tmv, 0, sizeof tmv);
+  if (layout == VA_LAYOUT_DENSE) {
+    if (rows >= (1ll << 31)) return fail(VA_ERR_UNSUPPORTED, "B * max_cache_len must be below 2^31");
+    if (!encode_rows_map(&tmk, k, row, s.Hkv, rows, 128) || !encode_rows_map(&tmv, v, row, s.Hkv, rows, 128))
+      return fail(VA_ERR_CUDA, "could not encode the TMA tensor maps of the cache");
+    p.tma_box = 128;
+  } else if (page_size >= 8) {
+    // one box a page (at most 128 rows), on a 128-byte boundary of the ring.  Smaller
+    // pages, or a pool the map cannot describe, are gathered.
+    const int box = page_size < 128 ? page_size : 128;
+    if (rows < (1ll << 31) && encode_rows_map(&tmk, k, row, s.Hkv, rows, box) &&
+        encode_rows_map(&tmv, v, row, s.Hkv, rows, box))
+      p.tma_box = box;
+  }
+  const long long tiles_cap = (long long)p.S * (((long long)len_cap + 127) / 128);
+  if (tiles_cap >= (1ll << 31)) return fail(VA_ERR_UNSUPPORTED, "problem too large (%lld key tiles)", tiles_cap);
+  const int grid = (int)(tiles_cap < sms ? tiles_cap : sms);
+  auto launch = format == VA_KV_E4M3
+                    ? (s.D == 128 ? va::launch_attention_e4m3_d128 : va::launch_attention_e4m3_d64)
+                    : (s.D == 128 ? va::launch_attention_e2m1_d128 : va::launch_attention_e2m1_d64);
+  cudaError_t e = launch(p, tmk, tmv, grid < 1 ? 1 : grid, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+  return ok();
+}
+
+// The arguments of a dense or paged cache behind an attention call.
+va_status check_dense(const Common &c, const void *k, const void *v, int max_cache_len) {
+  if (k == nullptr || v == nullptr) return fail(VA_ERR_INVALID_ARG, "k_cache and v_cache must not be NULL");
+  if (!aligned(k, 16) || !aligned(v, 16)) return fail(VA_ERR_INVALID_ARG, "caches must be 16-byte aligned");
+  if (max_cache_len < c.shape->T)
+    return fail(VA_ERR_INVALID_ARG, "max_cache_len=%d is smaller than T=%d", max_cache_len, c.shape->T);
+  return VA_OK;
+}
+
+va_status check_paged(const Common &c, const void *k, const void *v, int num_pages, int page_size,
+                      const int32_t *page_table, int max_pages_per_seq) {
+  if (k == nullptr || v == nullptr || page_table == nullptr)
+    return fail(VA_ERR_INVALID_ARG, "k_pages, v_pages and page_table must not be NULL");
+  if (!aligned(k, 16) || !aligned(v, 16)) return fail(VA_ERR_INVALID_ARG, "pages must be 16-byte aligned");
+  if (page_size < 1 || page_size > 1024 || (page_size & (page_size - 1)) != 0)
+    return fail(VA_ERR_INVALID_ARG, "page_size=%d must be a power of two in [1, 1024]", page_size);
+  if (num_pages < 1 || max_pages_per_seq < 1) return fail(VA_ERR_INVALID_ARG, "num_pages and max_pages_per_seq must be >= 1");
+  const long long cap = (long long)max_pages_per_seq * page_size;
+  if (cap < c.shape->T) return fail(VA_ERR_INVALID_ARG, "max_pages_per_seq*page_size is smaller than T");
+  if (cap >= (1ll << 30)) return fail(VA_ERR_UNSUPPORTED, "max_pages_per_seq*page_size too large");
+  return VA_OK;
+}
+
+// The shape of a call over quantised rows: bf16 queries.
+va_status check_quant(const Common &c, va_kv_format format) {
+  va_status st = check_common(c);
+  if (st != VA_OK) return st;
+  if (format != VA_KV_E4M3 && format != VA_KV_E2M1) return fail(VA_ERR_INVALID_ARG, "unknown cache format %d", (int)format);
+  if (c.shape->dtype != VA_DTYPE_BF16) return fail(VA_ERR_UNSUPPORTED, "caches held in 8 or 4 bits take bf16 queries");
+  return VA_OK;
+}
+
 va_status attn_dense(const Common &c, const void *k_cache, const void *v_cache, int max_cache_len,
                      const va_score_mod *mod, cudaStream_t stream) {
   va_status st = check_common(c);
+  if (st == VA_OK) st = check_dense(c, k_cache, v_cache, max_cache_len);
   if (st != VA_OK) return st;
-  if (k_cache == nullptr || v_cache == nullptr) return fail(VA_ERR_INVALID_ARG, "k_cache and v_cache must not be NULL");
-  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return fail(VA_ERR_INVALID_ARG, "caches must be 16-byte aligned");
-  if (max_cache_len < c.shape->T)
-    return fail(VA_ERR_INVALID_ARG, "max_cache_len=%d is smaller than T=%d", max_cache_len, c.shape->T);
   return run_attention(c, VA_LAYOUT_DENSE, k_cache, v_cache, max_cache_len, 0, 1, nullptr, 0, nullptr, nullptr, 0,
                        stream, mod);
 }
@@ -423,18 +536,10 @@ va_status attn_dense(const Common &c, const void *k_cache, const void *v_cache, 
 va_status attn_paged(const Common &c, const void *k_pages, const void *v_pages, int num_pages, int page_size,
                      const int32_t *page_table, int max_pages_per_seq, const va_score_mod *mod, cudaStream_t stream) {
   va_status st = check_common(c);
+  if (st == VA_OK) st = check_paged(c, k_pages, v_pages, num_pages, page_size, page_table, max_pages_per_seq);
   if (st != VA_OK) return st;
-  if (k_pages == nullptr || v_pages == nullptr || page_table == nullptr)
-    return fail(VA_ERR_INVALID_ARG, "k_pages, v_pages and page_table must not be NULL");
-  if (!aligned(k_pages, 16) || !aligned(v_pages, 16)) return fail(VA_ERR_INVALID_ARG, "pages must be 16-byte aligned");
-  if (page_size < 1 || page_size > 1024 || (page_size & (page_size - 1)) != 0)
-    return fail(VA_ERR_INVALID_ARG, "page_size=%d must be a power of two in [1, 1024]", page_size);
-  if (num_pages < 1 || max_pages_per_seq < 1) return fail(VA_ERR_INVALID_ARG, "num_pages and max_pages_per_seq must be >= 1");
-  const long long cap = (long long)max_pages_per_seq * page_size;
-  if (cap < c.shape->T) return fail(VA_ERR_INVALID_ARG, "max_pages_per_seq*page_size is smaller than T");
-  if (cap >= (1ll << 30)) return fail(VA_ERR_UNSUPPORTED, "max_pages_per_seq*page_size too large");
-  return run_attention(c, VA_LAYOUT_PAGED, k_pages, v_pages, (int)cap, num_pages, page_size, page_table,
-                       max_pages_per_seq, nullptr, nullptr, 0, stream, mod);
+  return run_attention(c, VA_LAYOUT_PAGED, k_pages, v_pages, max_pages_per_seq * page_size, num_pages, page_size,
+                       page_table, max_pages_per_seq, nullptr, nullptr, 0, stream, mod);
 }
 
 }  // namespace
@@ -860,6 +965,31 @@ va_status verify_commit_kv_dense(const va_shape *shape, void *k_cache, void *v_c
   cudaError_t e = va::launch_commit_kv(cp, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "commit launch");
   return ok();
+}
+
+va_status verify_attn_dense_quant(const va_shape *shape, va_kv_format format, const void *q, const void *k_cache,
+                                  const void *v_cache, int max_cache_len, const int32_t *seqlens,
+                                  const int32_t *tree_parent, const uint32_t *tree_mask, void *out, float *lse,
+                                  void *workspace, size_t ws_bytes, va_stream stream) {
+  const Common c{shape, q, seqlens, tree_parent, tree_mask, nullptr, out, lse, workspace, ws_bytes};
+  va_status st = check_quant(c, format);
+  if (st == VA_OK) st = check_dense(c, k_cache, v_cache, max_cache_len);
+  if (st != VA_OK) return st;
+  return run_attention_quant(c, format, VA_LAYOUT_DENSE, k_cache, v_cache, max_cache_len, 0, 1, nullptr, 0,
+                             (cudaStream_t)stream);
+}
+
+va_status verify_attn_paged_quant(const va_shape *shape, va_kv_format format, const void *q, const void *k_pages,
+                                  const void *v_pages, int num_pages, int page_size, const int32_t *page_table,
+                                  int max_pages_per_seq, const int32_t *seqlens, const int32_t *tree_parent,
+                                  const uint32_t *tree_mask, void *out, float *lse, void *workspace, size_t ws_bytes,
+                                  va_stream stream) {
+  const Common c{shape, q, seqlens, tree_parent, tree_mask, nullptr, out, lse, workspace, ws_bytes};
+  va_status st = check_quant(c, format);
+  if (st == VA_OK) st = check_paged(c, k_pages, v_pages, num_pages, page_size, page_table, max_pages_per_seq);
+  if (st != VA_OK) return st;
+  return run_attention_quant(c, format, VA_LAYOUT_PAGED, k_pages, v_pages, max_pages_per_seq * page_size, num_pages,
+                             page_size, page_table, max_pages_per_seq, (cudaStream_t)stream);
 }
 
 va_status verify_norm_rope(const va_shape *shape, const va_rows *q, const va_rows *k, const void *q_weight,

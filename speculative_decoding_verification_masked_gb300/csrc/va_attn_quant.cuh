@@ -1,0 +1,878 @@
+// Verification attention over a cache held in 8 or 4 bits (va_quant.cuh), on the
+// 5th-generation tensor cores with the KEYS on the TMEM lanes.  For blocks of NR
+// packed query rows (GQA group x draft tokens) and tiles of 128 keys:
+//
+//   S^T (128 keys x NR) = K (128 x d) . Q^T     A = K in TMEM, B = Q, K-major
+//   O^T (d x NR)       += V^T . P^T             A = V tile, MN-major; B = P^T, MN-major
+//
+// K and V become halves on their way: a code times its group scale has at most six
+// significant bits and lies in 2^-18 .. 2^12, so that is exact, and the row scale, a
+// power of two, stays out of the operands.  It multiplies a key's scores (one key is
+// one thread), and a key's P for the value row.  Nothing of a row is read twice.
+//
+// Roundings.  Q is scaled by one power of two for the block, its largest element to
+// 2^14 .. 2^15, and rounded to half: an element keeps all its bits down to 2^-32 of the
+// largest and is off by 2^-40 of it at most.  P is rounded to half: relative 2^-12,
+// an eighth of the half step that the bf16 output is rounded by.  Weights are
+// 2^6 at the row's reference and at most 2^14; P times the ratio of the key's value
+// scale to the largest one seen is exact but below 2^-14, where it is off by 2^-25.
+// Scores, row sums, O and the merge are fp32.
+//
+// The softmax reference of a row moves as in the bf16 kernel of this orientation, when
+// a score exceeds it by more than 2^8, and with it the largest value scale.
+//
+// Roles, one CTA per SM, persistent over the stream-K cut of all tiles, cooperative:
+//   softmax    NR/32 warpgroups (one for 16 rows); a thread owns a key and up to 32 rows
+//   K          a warpgroup: a thread takes its key's row from the ring, makes halves
+//              and stores them to TMEM (two buffers)
+//   V          a warpgroup: the same into a swizzled tile in shared memory (two buffers)
+//   producers  two warps, K and V each: TMA boxes of whole rows (dense; pages of 8 rows
+//              and more), or 16-byte cp.async gathers
+//   issuer     a warp: MMAs, TMEM
+// K needs no shared memory this way: the tile's 32 KB of halves would be written once
+// and read once, at 128 bytes a cycle as long as HBM takes for a whole 4-bit tile.
+//
+// Barriers of tile j (buffer j % 2, scales j % 4):
+//   full_k/v[stage]   the ring's rows have landed;  empty_k/v[stage] they are in registers
+//   k_full[j % 4]     K in TMEM and its scales in shared memory
+//   vs_full[j % 4]    V's scales;  v_full[j % 2] V's tile
+//   s_full[j % 2]     S of the tile (and its K buffer is free)
+//   p_full[j % 2]     P written, S read;  o_done[j % 2] PV done (P and V buffers free)
+// A scale buffer is written again for tile j + 4, behind the wait for PV of tile j + 1 (V)
+// or S of tile j + 2 (K), both of which come after the softmax of tile j.
+// Every wait is bounded; a role that gives up goes on without waiting.
+#pragma once
+
+#include <cuda.h>
+#include <math.h>
+
+#include "va_attn_quant.h"
+#include "va_common.cuh"
+#include "va_kernels.h"
+#include "va_merge.cuh"
+#include "va_pipeline.cuh"
+#include "va_quant.cuh"
+#include "va_rowreduce.cuh"
+#include "va_tcgen05.cuh"
+
+namespace va {
+
+constexpr int kTqKeys = 128;    // keys per tile
+constexpr int kTqStages = 8;    // most stages of the ring
+constexpr float kTqBias = 6.f;  // log2 of the weight at the reference
+constexpr float kTqMove = 8.f;  // a score this far above the reference moves it
+
+template <int NR>
+struct TqCfg {
+  static constexpr int kGroups = NR > 32 ? NR / 32 : 1;  // softmax warpgroups
+  static constexpr int kSoft = 128 * kGroups;
+  // (the last warpgroup: two producers, the issuer, and a warp without work)
+  static constexpr int kKWarp = 4 * kGroups, kVWarp = kKWarp + 4, kProducer = kVWarp + 4, kMmaWarp = kProducer + 2;
+  static constexpr int kThreads = (kProducer + 4) * 32;
+  // Registers a thread: the launch's, and what the warpgroups divide them into.
+  static constexpr int kRegsLaunch = kGroups == 1 ? 128 : 96;
+  static constexpr int kRegsSoft = kGroups == 1 ? 208 : 136, kRegsKv = kGroups == 1 ? 104 : 72,
+                       kRegsRest = kGroups == 1 ? 96 : 64;
+  static_assert(kGroups * kRegsSoft + 2 * kRegsKv + kRegsRest <= (kGroups + 3) * kRegsLaunch, "within the launch's registers");
+  static_assert(kThreads * kRegsLaunch <= 65536, "a block's registers");
+};
+
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int FMT, int D, int NR>
+struct TqSmem {
+  static constexpr int kRow = QRow<FMT, D>::kBytes;
+  static constexpr int kRaw = kTqKeys * kRow;              // K (or V) rows of a stage
+  static constexpr int kVBytes = (D / 64) * kTqKeys * 128; // V tile in halves
+  // (d 64: the PV MMA keeps M = 128; its lanes 64 .. 127 multiply the 16 KB that follow
+  // the tile, inside the plan, and nobody reads them)
+  static constexpr int kPOff = 2 * kVBytes;                // P^T: per key a 128-byte row
+  static constexpr int kQOff = kPOff + 2 * kTqKeys * 128;
+  static constexpr int kQBytes = (D / 64) * NR * 128;
+  static constexpr int kBarOff = kQOff + kQBytes;
+  static constexpr int kNumBars = 4 * kTqStages + 4 + 4 + 2 + 2 + 2 + 2 + 1;
+  static constexpr int kMiscOff = (kBarOff + kNumBars * 8 + 15) & ~15;  // tmem base, abort flag, merge flag
+  static constexpr int kRowMaskOff = kMiscOff + 16;      // u64 [64]: draft visibility rows
+  static constexpr int kKeyMaskOff = kRowMaskOff + 512;  // u64 [64]: per draft key, rows that see it
+  static constexpr int kRedOff = kKeyMaskOff + 512;      // float4 [NR]: per-warp row maxima
+  static constexpr int kVRedOff = kRedOff + NR * 16;     // float [16]: per-warp largest value scales, Q maxima
+  static constexpr int kRowInvOff = kVRedOff + 64;       // float [NR]
+  static constexpr int kKsOff = kRowInvOff + NR * 4;     // float [4][128]
+  static constexpr int kVsOff = kKsOff + 4 * 512;        // float [4][128]
+  static constexpr int kRingOff = (kVsOff + 4 * 512 + 127) & ~127;
+  static constexpr int kNC = NR < 32 ? 32 : NR;          // TMEM columns per region
+  // O at 0, S at NC and 2NC, K at 3NC and 3NC + D/2
+  static constexpr int kKCol = 3 * kNC;
+  static constexpr int kTmemCols = kKCol + D <= 256 ? 256 : 512;
+  static_assert(kKCol + D <= 512, "TMEM plan");
+  static_assert(kQOff % 1024 == 0 && kPOff % 1024 == 0 && kQBytes % 1024 == 0, "swizzle atoms");
+  static_assert(kRowInvOff % 16 == 0 && kKsOff % 16 == 0, "vector loads");
+  // d 64: what the unused lanes of the second V buffer read is the P buffers
+  static_assert(D == 128 || kPOff + 16384 <= kQOff, "unused lanes stay inside");
+};
+
+// Instruction descriptor of kind::f16 with half operands and fp32 accumulation.
+__host__ __device__ constexpr uint32_t umma_idesc_half(int M, int N, int a_mn_major, int b_mn_major) {
+  return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+
+// 16 bytes of codes as halves, two to a register: 32 values of e2m1 (groups 2c and 2c + 1
+// of the row's group scales) or 16 of e4m3.
+template <int FMT>
+struct CodeChunk {
+  static constexpr int kRegs = FMT == VA_KV_E4M3 ? 8 : 16;
+};
+template <int FMT>
+__device__ __forceinline__ void codes_to_halves(const uint4 &v, uint32_t two_groups, uint32_t (&h)[CodeChunk<FMT>::kRegs]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (FMT == VA_KV_E4M3) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = half2_bits(e4m3x2_to_half2(w[i / 2] >> (16 * (i & 1)) & 0xffffu));
+  } else {
+    const __half2 g = e4m3x2_to_half2(two_groups & 0xffffu);
+    const __half2 g0 = __low2half2(g), g1 = __high2half2(g);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      h[i] = half2_bits(__hmul2(e2m1x2_to_half2(w[i / 4] >> (8 * (i & 3)) & 0xffu), i < 8 ? g0 : g1));
+  }
+}
+
+// Two group scales of chunk c out of a row's tail, and the row scale.
+template <int FMT, int D>
+__device__ __forceinline__ uint32_t tail_groups(const uint4 &tail, int c) {
+  if constexpr (FMT == VA_KV_E4M3) return 0u;
+  const uint32_t w = c < 2 ? tail.x : tail.y;
+  return w >> (16 * (c & 1));
+}
+template <int FMT, int D>
+__device__ __forceinline__ float tail_scale(const uint4 &tail) {
+  return __uint_as_float(FMT == VA_KV_E4M3 ? tail.x : D == 128 ? tail.z : tail.y);
+}
+
+// ---------------------------------------------------------------------------
+// producer: one warp fills the K (or V) half of the ring with raw rows
+// ---------------------------------------------------------------------------
+template <int FMT, int D, bool kTma>
+__device__ __forceinline__ void produce_raw(const AttnParams &p, const CUtensorMap *tm, const uint8_t *cache,
+                                            const int *tstart, const CtaRange &cr, uint8_t *ring, uint64_t *full,
+                                            uint64_t *empty, volatile int *abort_flag) {
+  constexpr int RB = QRow<FMT, D>::kBytes;
+  constexpr int TK = kTqKeys;
+  const int lane = threadIdx.x & 31;
+  const uint64_t policy = l2_evict_first_policy();
+  if (kTma && lane == 0) prefetch_tmap(tm);
+  const bool paged = p.layout == VA_LAYOUT_PAGED;
+  // the row of key k (gather)
+  auto row_of = [&](const Seg &g, int k) -> const uint8_t * {
+    size_t row;
+    if (paged) {
+      int page = __ldg(p.page_table + (size_t)g.b * p.max_pages + (k >> p.page_shift));
+      if (page < 0 || page >= p.num_pages) {
+        record_status(p.status, VA_ERR_DEVICE_BOUNDS);
+        page = 0;
+      }
+      row = ((size_t)page << p.page_shift) + (k & ((1 << p.page_shift) - 1));
+    } else {
+      row = (size_t)g.b * p.len_cap + k;
+    }
+    return cache + (row * p.Hkv + g.hkv) * RB;
+  };
+  bool ok = true;
+  int st = 0, it = 0;
+  uint32_t ph = 0;
+  for (int s = cr.s0; s < p.S && tstart[s] < cr.t1; ++s) {
+    const Seg g = seg_info(p, s, false);
+    int lt0, lt1;
+    seg_tiles<false>(tstart, s, cr, lt0, lt1);
+    // the page entry of this lane's box, fetched one tile ahead
+    const int BR = p.tma_box;
+    auto box_page = [&](int lt) {
+      const int k = lt * TK + lane * BR;
+      if (!kTma || !paged || lt >= lt1 || lane >= TK / BR || k >= g.nkeys) return 0;
+      return __ldg(p.page_table + (size_t)g.b * p.max_pages + (k >> p.page_shift));
+    };
+    int page_next = box_page(lt0);
+    for (int lt = lt0; lt < lt1; ++lt, ++it) {
+      const int page_now = page_next;
+      page_next = box_page(lt + 1);
+      warp_role_wait(empty + st, ph ^ 1u, ok, abort_flag, p.wait_ns, p.status);
+      if (ok) {
+        uint8_t *dst = ring + (size_t)st * (2 * TK * RB);
+        const int k0 = lt * TK;
+        if constexpr (kTma) {
+          // dense: one box; rows past the segment's end arrive too (other tokens, or
+          // zeros past the cache) and are masked.  Paged: a box a page; boxes that
+          // start past the end are not loaded.
+          const int nb = paged ? min(TK / BR, (g.nkeys - k0 + BR - 1) / BR) : 1;
+          if (lane == 0) mbar_arrive_expect_tx(full + st, (uint32_t)(nb * BR * RB));
+          __syncwarp();
+          if (lane < nb) {
+            int row;
+            if (paged) {
+              int page = page_now;
+              if (page < 0 || page >= p.num_pages) {
+                record_status(p.status, VA_ERR_DEVICE_BOUNDS);
+                page = 0;
+              }
+              row = (page << p.page_shift) + ((k0 + lane * BR) & ((1 << p.page_shift) - 1));
+            } else {
+              row = g.b * p.len_cap + k0;
+            }
+            tma_load_3d(dst + lane * BR * RB, tm, 0, g.hkv, row, full + st, policy);
+          }
+        } else {
+          constexpr int CPR = RB / 16;  // 16-byte chunks of a row
+#pragma unroll
+          for (int j = 0; j < TK / 32; ++j) {
+            const int k = k0 + 32 * j + lane;
+            const uint8_t *mine = k < g.nkeys ? row_of(g, k) : cache;
+#pragma unroll
+            for (int i = 0; i < CPR; ++i) {
+              const int e = 32 * i + lane, r = e / CPR, c = e % CPR;
+              const uintptr_t a = (uintptr_t)__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine), r);
+              cp_async_16(dst + (32 * j + r) * RB + c * 16, reinterpret_cast<const void *>(a + 16 * c),
+                          k0 + 32 * j + r < g.nkeys ? 16u : 0u);
+            }
+          }
+          cp_async_mbar_arrive(full + st);
+        }
+      }
+      if (++st == p.stages) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+  }
+  // the copies this warp issued land before it leaves (bounded)
+  if constexpr (kTma) {
+    for (int j = max(0, it - p.stages); j < it; ++j)
+      mbar_wait(full + j % p.stages, (uint32_t)(j / p.stages) & 1u, p.wait_ns >> 4);
+  } else {
+    cp_async_wait_all();
+  }
+}
+
+template <int FMT, int D, int NR, bool kTma>
+__global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
+    verify_attn_quant_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
+                             const __grid_constant__ CUtensorMap tmv) {
+  using SM = TqSmem<FMT, D, NR>;
+  using Cfg = TqCfg<NR>;
+  constexpr int TK = kTqKeys, NC = SM::kNC, WG = Cfg::kGroups, kSoft = Cfg::kSoft, RB = SM::kRow;
+  constexpr int NW = NR / WG;  // rows of a softmax thread
+  constexpr int kChunks = QRow<FMT, D>::kCodeBytes / 16, kRegs = CodeChunk<FMT>::kRegs;
+  constexpr int kBarQ = 1, kBarSoft = 3, kBarEnd = 4, kBarRed0 = 5;  // kBarRed0 + softmax warpgroup
+  constexpr int kEndThreads = kSoft + 256 + 32;                      // all but the producers
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t *sV = smem, *sP = smem + SM::kPOff, *sQ = smem + SM::kQOff, *ring = smem + SM::kRingOff;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SM::kBarOff);
+  uint64_t *full = bars, *empty = bars + 2 * kTqStages;  // [K, V][stage]
+  uint64_t *k_full = bars + 4 * kTqStages, *vs_full = k_full + 4, *v_full = vs_full + 4, *s_full = v_full + 2,
+           *p_full = s_full + 2, *o_done = p_full + 2, *drain = o_done + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::kMiscOff);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::kMiscOff + 4);
+  uint64_t *rowmask = reinterpret_cast<uint64_t *>(smem + SM::kRowMaskOff);
+  uint64_t *keymask = reinterpret_cast<uint64_t *>(smem + SM::kKeyMaskOff);
+  float4 *red = reinterpret_cast<float4 *>(smem + SM::kRedOff);
+  float *vred = reinterpret_cast<float *>(smem + SM::kVRedOff);
+  float *row_inv = reinterpret_cast<float *>(smem + SM::kRowInvOff);
+  float *ks = reinterpret_cast<float *>(smem + SM::kKsOff), *vs = reinterpret_cast<float *>(smem + SM::kVsOff);
+  int *tstart = reinterpret_cast<int *>(ring + (size_t)p.stages * (2 * SM::kRaw));
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
+  if (tid == 0) {
+    for (int i = 0; i < 2 * kTqStages; ++i) {
+      mbar_init(full + i, kTma ? 1 : 32);
+      mbar_init(empty + i, 4);
+    }
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(k_full + b, 4);
+      mbar_init(vs_full + b, 4);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(v_full + b, 4);
+      mbar_init(s_full + b, c == p.test_stall ? kNever : 1);
+      mbar_init(p_full + b, kSoft);
+      mbar_init(o_done + b, 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  const CtaRange cr = plan_cta<TK>(p, tstart);  // contains __syncthreads
+  if (c >= cr.G) return;
+  const int t1 = cr.t1, s0 = cr.s0;
+
+  bool ok = true;
+  auto wait_ok = [&](uint64_t *bar, uint32_t parity) { role_wait(bar, parity, ok, abort_flag, p.wait_ns, p.status); };
+  // TMEM is allocated: every role but the producers waits for its address here
+  auto tmem_base = [&]() {
+    tc_fence_before();
+    named_bar_sync(kBarEnd, kEndThreads);
+    tc_fence_after();
+    return *tmem_slot;
+  };
+
+  if (warp >= Cfg::kProducer) {
+    regs_dec<Cfg::kRegsRest>();
+    if (warp > Cfg::kMmaWarp) return;
+    if (warp != Cfg::kMmaWarp) {
+      const bool is_v = warp != Cfg::kProducer;
+      produce_raw<FMT, D, kTma>(p, is_v ? &tmv : &tmk, static_cast<const uint8_t *>(is_v ? p.v : p.k), tstart, cr,
+                                ring + (is_v ? SM::kRaw : 0), full + (is_v ? kTqStages : 0),
+                                empty + (is_v ? kTqStages : 0), abort_flag);
+      return;
+    }
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(SM::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    const uint32_t tmem = tmem_base();
+    // ================================ MMA issuer ================================
+    const uint32_t id_s = umma_idesc_half(128, NR, 0, 0), id_o = umma_idesc_half(128, NR, 1, 1);
+    const uint64_t dQ0 = umma_sdesc(smem_u32(sQ), 16, 1024);
+    const uint64_t dV0 = umma_sdesc(smem_u32(sV), TK * 128, 1024);
+    const uint64_t dP0 = umma_sdesc(smem_u32(sP), TK * 128, 1024);
+    auto issue_s = [&](int jt) {
+      wait_ok(k_full + (jt & 3), (uint32_t)(jt >> 2) & 1u);
+      __syncwarp();
+      tc_fence_after();
+      const int b = jt & 1;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t qoff = (uint64_t)(((kk >> 2) * (NR * 128) + (kk & 3) * 32) >> 4);
+        umma_ts_warp(tmem + (1 + b) * NC, tmem + SM::kKCol + b * (D / 2) + kk * 8, dQ0 + qoff, id_s, kk > 0 ? 1u : 0u);
+      }
+      umma_commit_warp(s_full + b);
+    };
+    int jt = 0;
+    for (int s = s0; s < p.S && tstart[s] < t1; ++s) {
+      int lt0, lt1;
+      seg_tiles<false>(tstart, s, cr, lt0, lt1);
+      named_bar_sync(kBarQ, kSoft + 32);  // Q of this segment is in shared memory
+      issue_s(jt);
+      if (lt0 + 1 < lt1) issue_s(jt + 1);
+      for (int lt = lt0; lt < lt1; ++lt, ++jt) {
+        const int b = jt & 1;
+        wait_ok(v_full + b, (uint32_t)(jt >> 1) & 1u);
+        wait_ok(p_full + b, (uint32_t)(jt >> 1) & 1u);
+        __syncwarp();
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < TK / 16; ++kk) {
+          const uint64_t off = (uint64_t)((kk * 2048) >> 4);
+          umma_ss_warp(tmem, dV0 + (uint64_t)((b * SM::kVBytes) >> 4) + off, dP0 + (uint64_t)((b * TK * 128) >> 4) + off,
+                       id_o, kk > 0 || lt != lt0 ? 1u : 0u);
+        }
+        umma_commit_warp(o_done + b);
+        if (lt + 2 < lt1) issue_s(jt + 2);
+        __syncwarp();
+      }
+    }
+    // drain: every MMA issued has finished before TMEM is released
+    umma_commit_warp(drain);
+    mbar_wait(drain, 0u, p.wait_ns);
+    __syncwarp();
+    tc_fence_before();
+    named_bar_sync(kBarEnd, kEndThreads);
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(SM::kTmemCols) : "memory");
+    return;
+  }
+
+  if (warp >= Cfg::kKWarp) {
+    // ============================ K and V to halves ============================
+    regs_dec<Cfg::kRegsKv>();
+    const uint32_t tmem = tmem_base();
+    const bool is_v = warp >= Cfg::kVWarp;
+    const int key = (warp & 3) * 32 + lane;
+    uint64_t *fl = full + (is_v ? kTqStages : 0), *em = empty + (is_v ? kTqStages : 0);
+    uint64_t *sc_full = is_v ? vs_full : k_full, *freed = is_v ? o_done : s_full;
+    float *sc = (is_v ? vs : ks) + key;
+    const int n = t1 - cr.t0;
+    int st = 0;
+    uint32_t ph = 0;
+    for (int jt = 0; jt < n; ++jt) {
+      const int b = jt & 1;
+      wait_ok(fl + st, ph);
+      const uint8_t *row = ring + (size_t)st * (2 * SM::kRaw) + (is_v ? SM::kRaw : 0) + key * RB;
+      uint4 code[kChunks];
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) code[i] = reinterpret_cast<const uint4 *>(row)[i];
+      const uint4 tail = *reinterpret_cast<const uint4 *>(row + QRow<FMT, D>::kCodeBytes);
+      if (is_v) sc[(jt & 3) * 128] = tail_scale<FMT, D>(tail);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(em + st);
+        if (is_v) mbar_arrive(sc_full + (jt & 3));
+      }
+      if (++st == p.stages) {
+        st = 0;
+        ph ^= 1u;
+      }
+      if (jt >= 2) wait_ok(freed + b, (uint32_t)((jt - 2) >> 1) & 1u);
+      __syncwarp();
+      if (is_v) {
+        uint8_t *vt = sV + b * SM::kVBytes;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          uint32_t h[kRegs];
+          codes_to_halves<FMT>(code[i], tail_groups<FMT, D>(tail, i), h);
+#pragma unroll
+          for (int u = 0; u < kRegs / 4; ++u)
+            *reinterpret_cast<uint4 *>(vt + swz<TK>(key, i * (kRegs / 4) + u)) =
+                make_uint4(h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_full + b);
+      } else {
+        tc_fence_after();
+        sc[(jt & 3) * 128] = tail_scale<FMT, D>(tail);
+        const uint32_t tK = tmem + ((uint32_t)((warp & 3) * 32) << 16) + SM::kKCol + b * (D / 2);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          uint32_t h[kRegs];
+          codes_to_halves<FMT>(code[i], tail_groups<FMT, D>(tail, i), h);
+          if constexpr (kRegs == 16)
+            tmem_st16(tK + i * kRegs, h);
+          else
+            tmem_st8(tK + i * kRegs, h);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full + (jt & 3));
+      }
+    }
+    tc_fence_before();
+    named_bar_sync(kBarEnd, kEndThreads);
+    return;
+  }
+
+  // ================================== softmax ==================================
+  regs_inc<Cfg::kRegsSoft>();
+  const uint32_t tmem = tmem_base();
+  const int wg = WG == 1 ? 0 : warp >> 2;    // warpgroup: rows [r_wg, r_wg + NW) of the block
+  const int r_wg = wg * NW;
+  const int wq = WG == 1 ? warp : warp & 3;  // warp of the warpgroup
+  const int ktid = WG == 1 ? tid : tid & 127;// key of the tile, and output column of the epilogue
+  const int kBarRed = kBarRed0 + wg;
+  const uint32_t tO = tmem + ((uint32_t)(wq * 32) << 16);
+  const int group = p.Hq / p.Hkv;
+  int jt = 0;
+  // split segments this CTA holds a part of (at most its first and its last)
+  int n_split = 0, ms[2] = {0, 0}, mslot[2] = {0, 0}, mnp[2] = {0, 0}, mpart[2] = {0, 0};
+  for (int s = s0; s < p.S && tstart[s] < t1; ++s) {
+    const Seg g = seg_info(p, s, false);
+    int lt0, lt1;
+    seg_tiles<false>(tstart, s, cr, lt0, lt1);
+    const int first_cta = owner_cta(tstart[s], cr.total, cr.G);
+    const int n_parts = owner_cta(tstart[s + 1] - 1, cr.total, cr.G) - first_cta + 1;
+    if (lt0 == 0 && tid == 0) p.meta[s] = make_int2(s + first_cta, n_parts);
+    const int base = g.rb * NR, R = min(NR, p.R - base);  // the packed rows [base, base + R) of the kv-head
+    // bit r: this segment's row r is one of draft token t
+    auto token_rows = [&](int t) -> uint64_t {
+      const int lo = max(t * group - base, 0), hi = min((t + 1) * group - base, 64);
+      return hi <= lo ? 0ull : (hi - lo >= 64 ? ~0ull : (1ull << (hi - lo)) - 1) << lo;
+    };
+
+    // ---- Q of this segment: halves, scaled by a power of two, [D/64][NR rows][128 B], 128B swizzle ----
+    float q_unit;  // what a product of the scaled Q stands for, in base-2 score units
+    {
+      const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(p.q);
+      constexpr int kCh = D / 8, kQIt = (NR * kCh + kSoft - 1) / kSoft;
+      static_assert(NR * kCh % kSoft == 0, "every thread loads as many chunks");
+      uint4 v[kQIt];
+      uint32_t top = 0;  // largest finite |bf16|
+#pragma unroll
+      for (int u = 0; u < kQIt; ++u) {
+        const int e = tid + u * kSoft, row = e / kCh;
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (row < R) {
+          const int t = (base + row) / group, hq = g.hkv * group + (base + row) % group;
+          v[u] = __ldg(reinterpret_cast<const uint4 *>(qb + (((size_t)g.b * p.T + t) * p.Hq + hq) * D) + (e % kCh));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kQIt; ++u) {
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t lo = w[i] & 0x7fffu, hi = w[i] >> 16 & 0x7fffu;
+          top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+        }
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) reinterpret_cast<uint32_t *>(vred)[warp] = top;
+      named_bar_sync(kBarSoft, kSoft);
+#pragma unroll
+      for (int i = 0; i < 4 * WG; ++i) top = max(top, reinterpret_cast<uint32_t *>(vred)[i]);
+      const int k = top == 0 ? 0 : min(120, 141 - (int)(top >> 7));  // 14 - (exponent - 127)
+      const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+      q_unit = p.scale * kLog2e * __uint_as_float((uint32_t)(127 - k) << 23);
+#pragma unroll
+      for (int u = 0; u < kQIt; ++u) {
+        const int e = tid + u * kSoft, row = e / kCh, ch = e % kCh;
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          h[i] = half2_bits(__floats2half2_rn(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up));
+        *reinterpret_cast<uint4 *>(sQ + (ch >> 3) * (NR * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
+            make_uint4(h[0], h[1], h[2], h[3]);
+      }
+      fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    named_bar_sync(kBarQ, kSoft + 32);
+
+    // ---- draft visibility, when this part holds draft keys ----
+    const bool has_draft = lt1 * TK > g.n_prefix;
+    if (has_draft) {
+      if (warp == 0) {
+        const DraftPre dpre = draft_prefetch(p, g.b);
+        uint64_t lo, hi;
+        draft_rows(p, dpre, lo, hi);
+        if (lane < p.T) rowmask[lane] = lo;
+        if (lane + 32 < p.T) rowmask[lane + 32] = hi;
+      }
+      named_bar_sync(kBarSoft, kSoft);
+      if (tid < p.T) {
+        uint64_t km = 0;
+        for (int t = 0; t < p.T; ++t)
+          if ((rowmask[t] >> tid) & 1ull) km |= token_rows(t);
+        keymask[tid] = km;
+      }
+      named_bar_sync(kBarSoft, kSoft);
+    }
+
+    float mu[NW], lsum[NW];  // reference per row, log2 units; sums of P over this thread's keys
+#pragma unroll
+    for (int r = 0; r < NW; ++r) {
+      mu[r] = -INFINITY;
+      lsum[r] = 0.f;
+    }
+    float vref = 0.f;  // largest value scale seen
+
+    for (int lt = lt0; lt < lt1; ++lt, ++jt) {
+      const int b = jt & 1;
+      const uint32_t tS = tO + (1 + b) * NC + r_wg;
+      const int key = lt * TK + ktid;
+      const bool masked = lt * TK + TK > g.n_prefix;
+      uint64_t km_all = ~0ull;  // rows that see this key
+      if (masked) km_all = key >= g.nkeys ? 0ull : key >= g.n_prefix ? keymask[key - g.n_prefix] : ~0ull;
+      if (masked && R < 64) km_all &= (1ull << R) - 1ull;
+      const uint32_t km = (uint32_t)(km_all >> r_wg);  // (NW <= 32)
+      wait_ok(vs_full + (jt & 3), (uint32_t)(jt >> 2) & 1u);
+      const float vsc = vs[(jt & 3) * 128 + ktid];
+      const float vmine = km_all != 0ull && vsc == vsc ? vsc : 0.f;
+      wait_ok(k_full + (jt & 3), (uint32_t)(jt >> 2) & 1u);
+      const float cs = ks[(jt & 3) * 128 + ktid] * q_unit;
+      wait_ok(s_full + b, (uint32_t)(jt >> 1) & 1u);
+      // PV of tile jt - 2: its P buffer is free, and the barrier stays within a phase of its waiters
+      if (jt >= 2) wait_ok(o_done + b, (uint32_t)((jt - 2) >> 1) & 1u);
+      __syncwarp();
+      tc_fence_after();
+      float x[NW];
+      // scores of this key above the references (2^-6 of a weight apart), -inf where unseen
+      auto load_scores = [&]() {
+        tmem_ld_f<NW>(tS, x);
+        if (lt == lt0 && vref == 0.f) {
+          // first tile of the part: the scores of key 0 are the references
+          if (ktid == 0) {
+#pragma unroll
+            for (int r = 0; r < NW; ++r)
+              reinterpret_cast<float *>(red + r_wg)[r] = (km >> r) & 1u ? x[r] * cs : -INFINITY;
+          }
+          const float wm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmine)));
+          if (lane == 0) vred[warp] = wm;
+          named_bar_sync(kBarRed, 128);
+#pragma unroll
+          for (int r = 0; r < NW; r += 4) {
+            const float4 m4 = red[r_wg + (r >> 2)];
+            mu[r] = m4.x;
+            mu[r + 1] = m4.y;
+            mu[r + 2] = m4.z;
+            mu[r + 3] = m4.w;
+          }
+          vref = fmaxf(fmaxf(fmaxf(vred[4 * wg], vred[4 * wg + 1]), fmaxf(vred[4 * wg + 2], vred[4 * wg + 3])), 0x1p-126f);
+        }
+        if (masked) {
+#pragma unroll
+          for (int r = 0; r < NW; ++r)
+            x[r] = (km >> r) & 1u ? fmaf(x[r], cs, kTqBias - (mu[r] == -INFINITY ? 0.f : mu[r])) : -INFINITY;
+        } else {
+#pragma unroll
+          for (int r = 0; r < NW; r += 2) {
+            const float2 y = fma2(make_float2(x[r], x[r + 1]), make_float2(cs, cs),
+                                  make_float2(kTqBias - mu[r], kTqBias - mu[r + 1]));
+            x[r] = y.x;
+            x[r + 1] = y.y;
+          }
+        }
+      };
+      load_scores();
+      float dmax = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < NW; ++r) dmax = fmaxf(dmax, x[r]);
+      if (masked) {  // (a row's first key moves its reference, however small the score)
+#pragma unroll
+        for (int r = 0; r < NW; ++r)
+          if (mu[r] == -INFINITY && ((km >> r) & 1u)) dmax = INFINITY;
+      }
+      if (bar_red_or(kBarRed, 128, dmax > kTqBias + kTqMove || vmine > vref)) {
+        // move the references to the row maxima seen so far, and the value scale
+        WarpScatterMax<NW, 16>::run(x, lane);
+        if constexpr (NW == 32) {
+          reinterpret_cast<float *>(red + r_wg)[lane * 4 + wq] = x[0];
+        } else {
+          if ((lane & (32 / NW - 1)) == 0) reinterpret_cast<float *>(red + r_wg)[(lane / (32 / NW)) * 4 + wq] = x[0];
+        }
+        const float wm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmine)));
+        if (lane == 0) vred[warp] = wm;
+        named_bar_sync(kBarRed, 128);
+        const float vnew = fmaxf(vref, fmaxf(fmaxf(vred[4 * wg], vred[4 * wg + 1]), fmaxf(vred[4 * wg + 2], vred[4 * wg + 3])));
+        const float vdown = vref / vnew;
+        vref = vnew;
+#pragma unroll
+        for (int r = 0; r < NW; ++r) {
+          const float4 m4 = red[r_wg + r];
+          const float up = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)) - kTqBias;  // above the reference (or zero)
+          const bool none = mu[r] == -INFINITY;
+          const float mnew = none ? up : mu[r] + fmaxf(up, 0.f);
+          const float alpha = none ? 0.f : ex2_approx(mu[r] - mnew);
+          mu[r] = mnew;
+          lsum[r] *= alpha;
+          x[r] = alpha * vdown;
+        }
+        if (lt != lt0) {
+          wait_ok(o_done + (b ^ 1), (uint32_t)((jt - 1) >> 1) & 1u);  // O holds every PV up to tile jt - 1
+          __syncwarp();
+          tc_fence_after();
+          tmem_scale_cols<NW>(tO + r_wg, x);
+          tmem_st_wait();
+        }
+        load_scores();
+      }
+      // P^T row of this key: chunk cc holds rows 8cc .. 8cc + 7
+      uint8_t *pk = sP + b * (TK * 128) + ktid * 128;
+      const float ratio = vsc / vref;  // a power of two, at most 1
+      if (masked) {
+#pragma unroll
+        for (int cw = 0; cw < NW / 8; ++cw) {
+          uint32_t h[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int r = 8 * cw + 2 * q;
+            const float a = ex2_approx(x[r]), e = ex2_approx(x[r + 1]);  // (0 where unseen)
+            lsum[r] += a;
+            lsum[r + 1] += e;
+            // (the scale of a key that a row does not see may be anything)
+            h[q] = half2_bits(__floats2half2_rn((km >> r) & 1u ? a * ratio : 0.f, (km >> (r + 1)) & 1u ? e * ratio : 0.f));
+          }
+          *reinterpret_cast<uint4 *>(pk + (((r_wg / 8 + cw) ^ (ktid & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        if (km_all == 0ull) {
+          // a key that no row sees: zero V, so that 0 * V stays 0 whatever it held
+          wait_ok(v_full + b, (uint32_t)(jt >> 1) & 1u);
+#pragma unroll
+          for (int c0 = 0; c0 < D / 8 / WG; ++c0)
+            *reinterpret_cast<uint4 *>(sV + b * SM::kVBytes + swz<TK>(ktid, wg * (D / 8 / WG) + c0)) = make_uint4(0, 0, 0, 0);
+        }
+      } else {
+        const __half2 ratio2 = __float2half2_rn(ratio);
+#pragma unroll
+        for (int cw = 0; cw < NW / 8; ++cw) {
+          uint32_t h[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int r = 8 * cw + 2 * q;
+            const float a = ex2_approx(x[r]), e = ex2_approx(x[r + 1]);
+            const float2 s2 = add2(make_float2(lsum[r], lsum[r + 1]), make_float2(a, e));
+            lsum[r] = s2.x;
+            lsum[r + 1] = s2.y;
+            h[q] = half2_bits(__hmul2(__floats2half2_rn(a, e), ratio2));
+          }
+          *reinterpret_cast<uint4 *>(pk + (((r_wg / 8 + cw) ^ (ktid & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(p_full + b);
+    }
+
+    // ---- epilogue: column d = ktid of O / l for every row of this segment part ----
+    if (jt >= 2) wait_ok(o_done + (jt & 1), (uint32_t)((jt - 2) >> 1) & 1u);
+    wait_ok(o_done + ((jt - 1) & 1), (uint32_t)((jt - 1) >> 1) & 1u);
+    __syncwarp();
+    tc_fence_after();
+    const size_t slot = (size_t)(s + c);
+    float my_l = 0.f, my_mu = 0.f;
+    WarpScatterSum<NW, 16>::run(lsum, lane);
+    if ((lane & (32 / NW - 1)) == 0) reinterpret_cast<float *>(red + r_wg)[(lane / (32 / NW)) * 4 + wq] = lsum[0];
+    named_bar_sync(kBarSoft, kSoft);
+    if (ktid < NW) {
+      const float4 l4 = red[r_wg + ktid];
+      my_l = (l4.x + l4.y) + (l4.z + l4.w);
+    }
+#pragma unroll
+    for (int j = 0; j < NW; ++j) my_mu = ktid == j ? mu[j] : my_mu;
+    if (ktid < NW) {
+      const int r = r_wg + ktid;
+      const bool seen = !(my_l == 0.f);  // (NaN: a row that holds one)
+      row_inv[r] = r < R && seen ? __fdividef(vref, my_l) : 0.f;
+      if (r < R && ok) {
+        const int t = (base + r) / group, hq = g.hkv * group + (base + r) % group;
+        const float lse_nat = seen ? (my_mu - kTqBias + __log2f(my_l)) * kLn2 : -INFINITY;
+        if (n_parts == 1)
+          p.lse[((size_t)g.b * p.Hq + hq) * p.T + t] = lse_nat;
+        else
+          p.lse_part[slot * p.rows_pad + r] = lse_nat;
+      }
+    }
+    named_bar_sync(kBarSoft, kSoft);
+    constexpr int HR = 16;  // columns per TMEM load
+    if (n_parts > 1) {
+      // fp32 part: thread d stores column d of every row (a warp writes 128 contiguous bytes of a row)
+      float *orow = p.o_part + (slot * p.rows_pad + r_wg) * D + ktid;
+#pragma unroll
+      for (int h = 0; h < NW / HR; ++h) {
+        float ov[HR];
+        tmem_ld_f<HR>(tO + r_wg + h * HR, ov);
+        if (ok && (D == 128 || ktid < D)) {
+#pragma unroll
+          for (int j = 0; j < HR; ++j) orow[(h * HR + j) * D] = ov[j] * row_inv[r_wg + h * HR + j];
+        }
+      }
+      // publish the part (always, so the counters return to zero): the block barrier
+      // orders every thread's stores before thread 0's release increment
+      tc_fence_before();
+      named_bar_sync(kBarSoft, kSoft);
+      if (tid == 0 && c != p.test_drop_part)
+        red_release_inc_gpu(reinterpret_cast<unsigned *>(&p.merge_cnt[s].x), 2u * n_parts - 1u);
+      if (n_split < 2) {
+        ms[n_split] = s;
+        mslot[n_split] = s + first_cta;
+        mnp[n_split] = n_parts;
+        mpart[n_split] = c - first_cta;
+        ++n_split;
+      }
+    } else {
+      // final bf16 rows, staged in the Q buffer: the group rows of one draft token are contiguous in out
+      __nv_bfloat16 *stage_b = reinterpret_cast<__nv_bfloat16 *>(sQ);
+#pragma unroll
+      for (int h = 0; h < NW / HR; ++h) {
+        float ov[HR];
+        tmem_ld_f<HR>(tO + r_wg + h * HR, ov);
+        if (D == 128 || ktid < D) {
+#pragma unroll
+          for (int j = 0; j < HR; ++j)
+            stage_b[(r_wg + h * HR + j) * D + ktid] = __float2bfloat16_rn(ov[j] * row_inv[r_wg + h * HR + j]);
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      named_bar_sync(kBarSoft, kSoft);
+      if (ok && tid < p.T) {
+        const int t = tid, r0 = max(t * group - base, 0), n = min((t + 1) * group - base, R) - r0;
+        if (n > 0) {
+          __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
+                               (((size_t)g.b * p.T + t) * p.Hq + g.hkv * group + (base + r0 - t * group)) * D;
+          const __nv_bfloat16 *src = stage_b + (size_t)r0 * D;
+          if (p.out_align16) {
+            bulk_store_s2g(dst, src, (uint32_t)(n * D * 2));
+            bulk_commit();
+            bulk_wait_read_all();
+          } else {
+            for (int e = 0; e < n * D; ++e) dst[e] = src[e];
+          }
+        }
+      }
+      named_bar_sync(kBarSoft, kSoft);
+    }
+  }
+  bulk_wait_all();
+
+  // ---- merge of the split segments: each of a segment's CTAs merges a share of its rows ----
+  volatile int *merge_ok = abort_flag + 1;
+  for (int k = 0; k < n_split; ++k) {
+    const int s = ms[k], np = mnp[k];
+    if (tid == 0) *merge_ok = wait_parts_arrived(p, s, np) ? 1 : 0;
+    named_bar_sync(kBarSoft, kSoft);  // thread 0's acquire, then the barrier, orders the reads below
+    if (*merge_ok) {
+      const int seg = s / p.NRB, base = s % p.NRB * NR, R = min(NR, p.R - base);
+      const int r0 = mpart[k] * R / np, r1 = (mpart[k] + 1) * R / np;
+      if (np <= 4)
+        merge_rows_warp<8, 4, D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k], np, r0, r1, warp, 4 * WG, lane);
+      else
+        merge_rows_warp<D == 128 ? 32 : 16, 24, D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k], np, r0, r1, warp, 4 * WG,
+                                                   lane);
+    }
+    named_bar_sync(kBarSoft, kSoft);
+    // leave: np arrivals and np departures wrap the counter back to zero
+    if (tid == 0) red_relaxed_inc_gpu(reinterpret_cast<unsigned *>(&p.merge_cnt[s].x), 2u * np - 1u);
+  }
+  tc_fence_before();
+  named_bar_sync(kBarEnd, kEndThreads);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+// Stages of the ring that fit beside the rest (0: not even two).
+template <int FMT, int D, int NR>
+static int tq_stages(const AttnParams &p) {
+  using SM = TqSmem<FMT, D, NR>;
+  const long long left = (long long)kSmemLimit - 1024 - SM::kRingOff - (long long)(p.S + 1) * 4;
+  const long long n = left / (2 * SM::kRaw);
+  return n < 2 ? 0 : (int)(n > kTqStages ? kTqStages : n);
+}
+
+template <int FMT, int D, int NR, bool kTma>
+static cudaError_t launch_tq_t(AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
+                               cudaStream_t stream) {
+  using SM = TqSmem<FMT, D, NR>;
+  p.stages = tq_stages<FMT, D, NR>(p);
+  if (p.stages == 0) return cudaErrorInvalidValue;
+  auto kern = verify_attn_quant_kernel<FMT, D, NR, kTma>;
+  cudaError_t e = allow_smem(kern);
+  if (e != cudaSuccess) return e;
+  // cooperative: every CTA is resident, so the wait for a segment's parts ends
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(TqCfg<NR>::kThreads);
+  cfg.dynamicSmemBytes = 1024 + (size_t)SM::kRingOff + (size_t)p.stages * (2 * SM::kRaw) + (size_t)(p.S + 1) * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p, tmk, tmv);
+}
+
+template <int FMT, int D>
+static cudaError_t launch_tq(AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
+                             cudaStream_t stream) {
+  if (p.tma_box > 0)
+    return p.rows_pad == 16   ? launch_tq_t<FMT, D, 16, true>(p, tmk, tmv, grid, stream)
+           : p.rows_pad == 32 ? launch_tq_t<FMT, D, 32, true>(p, tmk, tmv, grid, stream)
+                              : launch_tq_t<FMT, D, 64, true>(p, tmk, tmv, grid, stream);
+  return p.rows_pad == 16   ? launch_tq_t<FMT, D, 16, false>(p, tmk, tmv, grid, stream)
+         : p.rows_pad == 32 ? launch_tq_t<FMT, D, 32, false>(p, tmk, tmv, grid, stream)
+                            : launch_tq_t<FMT, D, 64, false>(p, tmk, tmv, grid, stream);
+}
+
+}  // namespace va
