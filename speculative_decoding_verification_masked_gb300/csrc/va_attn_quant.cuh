@@ -22,20 +22,20 @@
 // a score exceeds it by more than 2^8, and with it the largest value scale.
 //
 // Roles, one CTA per SM, persistent over the stream-K cut of all tiles, cooperative:
-//   softmax    NR/32 warpgroups (one for 16 rows); a thread owns a key and up to 32 rows
+//   softmax    NR/16 warpgroups; a thread owns a key and 16 rows
 //   K          a warpgroup: a thread takes its key's row from the ring, makes halves
 //              and stores them to TMEM (two buffers)
 //   V          a warpgroup: the same into a swizzled tile in shared memory (two buffers)
 //   producers  two warps, K and V each: TMA boxes of whole rows (dense; pages of 8 rows
 //              and more), or 16-byte cp.async gathers
-//   issuer     a warp: MMAs, TMEM
+//   issuers    a warp for S (and TMEM), one for PV
 // K needs no shared memory this way: the tile's 32 KB of halves would be written once
 // and read once, at 128 bytes a cycle as long as HBM takes for a whole 4-bit tile.
 //
 // Barriers of tile j (buffer j % 2, scales j % 4):
 //   full_k/v[stage]   the ring's rows have landed;  empty_k/v[stage] they are in registers
-//   k_full[j % 4]     K in TMEM and its scales in shared memory
-//   vs_full[j % 4]    V's scales;  v_full[j % 2] V's tile
+//   k_full[j % 4]     K in TMEM, the scales of K and V in shared memory
+//   v_full[j % 2]     V's tile
 //   s_full[j % 2]     S of the tile (and its K buffer is free)
 //   p_full[j % 2]     P written, S read;  o_done[j % 2] PV done (P and V buffers free)
 // A scale buffer is written again for tile j + 4, behind the wait for PV of tile j + 1 (V)
@@ -64,15 +64,16 @@ constexpr float kTqMove = 8.f;  // a score this far above the reference moves it
 
 template <int NR>
 struct TqCfg {
-  static constexpr int kGroups = NR > 32 ? NR / 32 : 1;  // softmax warpgroups
+  static constexpr int kGroups = NR / 16;  // softmax warpgroups, 16 rows each
   static constexpr int kSoft = 128 * kGroups;
-  // (the last warpgroup: two producers, the issuer, and a warp without work)
-  static constexpr int kKWarp = 4 * kGroups, kVWarp = kKWarp + 4, kProducer = kVWarp + 4, kMmaWarp = kProducer + 2;
+  // (the last warpgroup: two producers and two issuers, of S and of PV)
+  static constexpr int kKWarp = 4 * kGroups, kVWarp = kKWarp + 4, kProducer = kVWarp + 4, kMmaWarp = kProducer + 2, kPvWarp = kMmaWarp + 1;
   static constexpr int kThreads = (kProducer + 4) * 32;
   // Registers a thread: the launch's, and what the warpgroups divide them into.
-  static constexpr int kRegsLaunch = kGroups == 1 ? 128 : 96;
-  static constexpr int kRegsSoft = kGroups == 1 ? 208 : 136, kRegsKv = kGroups == 1 ? 104 : 72,
-                       kRegsRest = kGroups == 1 ? 96 : 64;
+  static constexpr int kRegsLaunch = kGroups == 1 ? 128 : kGroups == 2 ? 96 : 72;
+  static constexpr int kRegsSoft = kGroups == 1 ? 160 : kGroups == 2 ? 112 : 80,
+                       kRegsKv = kGroups == 1 ? 128 : kGroups == 2 ? 88 : 64,
+                       kRegsRest = kGroups == 1 ? 96 : kGroups == 2 ? 80 : 56;
   static_assert(kGroups * kRegsSoft + 2 * kRegsKv + kRegsRest <= (kGroups + 3) * kRegsLaunch, "within the launch's registers");
   static_assert(kThreads * kRegsLaunch <= 65536, "a block's registers");
 };
@@ -97,7 +98,7 @@ struct TqSmem {
   static constexpr int kQOff = kPOff + 2 * kTqKeys * 128;
   static constexpr int kQBytes = (D / 64) * NR * 128;
   static constexpr int kBarOff = kQOff + kQBytes;
-  static constexpr int kNumBars = 4 * kTqStages + 4 + 4 + 2 + 2 + 2 + 2 + 1;
+  static constexpr int kNumBars = 4 * kTqStages + 4 + 2 + 2 + 2 + 2 + 2;
   static constexpr int kMiscOff = (kBarOff + kNumBars * 8 + 15) & ~15;  // tmem base, abort flag, merge flag
   static constexpr int kRowMaskOff = kMiscOff + 16;      // u64 [64]: draft visibility rows
   static constexpr int kKeyMaskOff = kRowMaskOff + 512;  // u64 [64]: per draft key, rows that see it
@@ -142,8 +143,9 @@ __device__ __forceinline__ void codes_to_halves(const uint4 &v, uint32_t two_gro
     const __half2 g = e4m3x2_to_half2(two_groups & 0xffffu);
     const __half2 g0 = __low2half2(g), g1 = __high2half2(g);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      h[i] = half2_bits(__hmul2(e2m1x2_to_half2(w[i / 4] >> (8 * (i & 3)) & 0xffu), i < 8 ? g0 : g1));
+    for (int i = 0; i < 4; ++i) e2m1x8_to_half2(w[i], h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) h[i] = half2_bits(__hmul2(*reinterpret_cast<__half2 *>(h + i), i < 8 ? g0 : g1));
   }
 }
 
@@ -272,14 +274,14 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
   constexpr int NW = NR / WG;  // rows of a softmax thread
   constexpr int kChunks = QRow<FMT, D>::kCodeBytes / 16, kRegs = CodeChunk<FMT>::kRegs;
   constexpr int kBarQ = 1, kBarSoft = 3, kBarEnd = 4, kBarRed0 = 5;  // kBarRed0 + softmax warpgroup
-  constexpr int kEndThreads = kSoft + 256 + 32;                      // all but the producers
+  constexpr int kEndThreads = kSoft + 256 + 64;                      // all but the producers
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t *sV = smem, *sP = smem + SM::kPOff, *sQ = smem + SM::kQOff, *ring = smem + SM::kRingOff;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SM::kBarOff);
   uint64_t *full = bars, *empty = bars + 2 * kTqStages;  // [K, V][stage]
-  uint64_t *k_full = bars + 4 * kTqStages, *vs_full = k_full + 4, *v_full = vs_full + 4, *s_full = v_full + 2,
-           *p_full = s_full + 2, *o_done = p_full + 2, *drain = o_done + 2;
+  uint64_t *k_full = bars + 4 * kTqStages, *v_full = k_full + 4, *s_full = v_full + 2, *p_full = s_full + 2,
+           *o_done = p_full + 2, *drains = o_done + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::kMiscOff);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::kMiscOff + 4);
   uint64_t *rowmask = reinterpret_cast<uint64_t *>(smem + SM::kRowMaskOff);
@@ -296,17 +298,15 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       mbar_init(full + i, kTma ? 1 : 32);
       mbar_init(empty + i, 4);
     }
-    for (int b = 0; b < 4; ++b) {
-      mbar_init(k_full + b, 4);
-      mbar_init(vs_full + b, 4);
-    }
+    for (int b = 0; b < 4; ++b) mbar_init(k_full + b, 8);
     for (int b = 0; b < 2; ++b) {
       mbar_init(v_full + b, 4);
       mbar_init(s_full + b, c == p.test_stall ? kNever : 1);
       mbar_init(p_full + b, kSoft);
       mbar_init(o_done + b, 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(drains + 0, 1);
+    mbar_init(drains + 1, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -326,66 +326,86 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
 
   if (warp >= Cfg::kProducer) {
     regs_dec<Cfg::kRegsRest>();
-    if (warp > Cfg::kMmaWarp) return;
-    if (warp != Cfg::kMmaWarp) {
+    if (warp < Cfg::kMmaWarp) {
       const bool is_v = warp != Cfg::kProducer;
       produce_raw<FMT, D, kTma>(p, is_v ? &tmv : &tmk, static_cast<const uint8_t *>(is_v ? p.v : p.k), tstart, cr,
                                 ring + (is_v ? SM::kRaw : 0), full + (is_v ? kTqStages : 0),
                                 empty + (is_v ? kTqStages : 0), abort_flag);
       return;
     }
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(SM::kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    const uint32_t tmem = tmem_base();
+    if (warp == Cfg::kMmaWarp) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                   "r"(SM::kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
     // ================================ MMA issuer ================================
-    const uint32_t id_s = umma_idesc_half(128, NR, 0, 0), id_o = umma_idesc_half(128, NR, 1, 1);
-    const uint64_t dQ0 = umma_sdesc(smem_u32(sQ), 16, 1024);
-    const uint64_t dV0 = umma_sdesc(smem_u32(sV), TK * 128, 1024);
-    const uint64_t dP0 = umma_sdesc(smem_u32(sP), TK * 128, 1024);
-    auto issue_s = [&](int jt) {
-      wait_ok(k_full + (jt & 3), (uint32_t)(jt >> 2) & 1u);
-      __syncwarp();
-      tc_fence_after();
-      const int b = jt & 1;
+    // Whatever addresses are made of is the same in every lane, and said to be (a
+    // shuffle from lane 0): descriptors then live in uniform registers, where the
+    // MMA takes them from.  Unknown to be uniform, an MMA took 85 to 137 cycles to
+    // issue beside the other roles, 48 alone.
+    auto uni = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
+    const uint32_t tmem = uni(tmem_base());
+    const uint32_t base = uni(smem_u32(smem));
+    uint32_t jt = 0;
+    if (warp == Cfg::kMmaWarp) {
+      const uint32_t id_s = umma_idesc_half(128, NR, 0, 0);
+      const uint64_t dQ0 = umma_sdesc(base + SM::kQOff, 16, 1024);
+      for (int s = s0; s < p.S && (int)uni(tstart[s]) < t1; ++s) {
+        int lt0, lt1;
+        seg_tiles<false>(tstart, s, cr, lt0, lt1);
+        const int n = (int)uni(lt1 - lt0);
+        named_bar_sync(kBarQ, kSoft + 32);  // Q of this segment is in shared memory
+        for (int i = 0; i < n; ++i, ++jt) {
+          const uint32_t b = jt & 1u;
+          // (two tiles ahead of the softmax: S of tile j - 2 has been read)
+          if (i >= 2) wait_ok(p_full + b, ((jt - 2) >> 1) & 1u);
+          wait_ok(k_full + (jt & 3), (jt >> 2) & 1u);
+          __syncwarp();
+          tc_fence_after();
+          const uint32_t tS = tmem + (1 + b) * NC, tK = tmem + SM::kKCol + b * (D / 2);
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t qoff = (uint64_t)(((kk >> 2) * (NR * 128) + (kk & 3) * 32) >> 4);
-        umma_ts_warp(tmem + (1 + b) * NC, tmem + SM::kKCol + b * (D / 2) + kk * 8, dQ0 + qoff, id_s, kk > 0 ? 1u : 0u);
-      }
-      umma_commit_warp(s_full + b);
-    };
-    int jt = 0;
-    for (int s = s0; s < p.S && tstart[s] < t1; ++s) {
-      int lt0, lt1;
-      seg_tiles<false>(tstart, s, cr, lt0, lt1);
-      named_bar_sync(kBarQ, kSoft + 32);  // Q of this segment is in shared memory
-      issue_s(jt);
-      if (lt0 + 1 < lt1) issue_s(jt + 1);
-      for (int lt = lt0; lt < lt1; ++lt, ++jt) {
-        const int b = jt & 1;
-        wait_ok(v_full + b, (uint32_t)(jt >> 1) & 1u);
-        wait_ok(p_full + b, (uint32_t)(jt >> 1) & 1u);
-        __syncwarp();
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < TK / 16; ++kk) {
-          const uint64_t off = (uint64_t)((kk * 2048) >> 4);
-          umma_ss_warp(tmem, dV0 + (uint64_t)((b * SM::kVBytes) >> 4) + off, dP0 + (uint64_t)((b * TK * 128) >> 4) + off,
-                       id_o, kk > 0 || lt != lt0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t qoff = (uint64_t)(((kk >> 2) * (NR * 128) + (kk & 3) * 32) >> 4);
+            umma_ts_warp(tS, tK + kk * 8, dQ0 + qoff, id_s, kk > 0 ? 1u : 0u);
+          }
+          umma_commit_warp(s_full + b);
+          __syncwarp();
         }
-        umma_commit_warp(o_done + b);
-        if (lt + 2 < lt1) issue_s(jt + 2);
-        __syncwarp();
+      }
+    } else {
+      const uint32_t id_o = umma_idesc_half(128, NR, 1, 1);
+      const uint64_t dV0 = umma_sdesc(base, TK * 128, 1024);
+      const uint64_t dP0 = umma_sdesc(base + SM::kPOff, TK * 128, 1024);
+      for (int s = s0; s < p.S && (int)uni(tstart[s]) < t1; ++s) {
+        int lt0, lt1;
+        seg_tiles<false>(tstart, s, cr, lt0, lt1);
+        const int n = (int)uni(lt1 - lt0);
+        for (int i = 0; i < n; ++i, ++jt) {
+          const uint32_t b = jt & 1u;
+          wait_ok(v_full + b, (jt >> 1) & 1u);
+          wait_ok(p_full + b, (jt >> 1) & 1u);
+          __syncwarp();
+          tc_fence_after();
+          const uint64_t dV = dV0 + (uint64_t)(b * (SM::kVBytes >> 4)), dP = dP0 + (uint64_t)(b * (TK * 128 >> 4));
+#pragma unroll
+          for (int kk = 0; kk < TK / 16; ++kk) {
+            const uint64_t off = (uint64_t)((kk * 2048) >> 4);
+            umma_ss_warp(tmem, dV + off, dP + off, id_o, kk > 0 || i > 0 ? 1u : 0u);
+          }
+          umma_commit_warp(o_done + b);
+          __syncwarp();
+        }
       }
     }
     // drain: every MMA issued has finished before TMEM is released
+    uint64_t *drain = drains + (warp - Cfg::kMmaWarp);
     umma_commit_warp(drain);
     mbar_wait(drain, 0u, p.wait_ns);
     __syncwarp();
     tc_fence_before();
     named_bar_sync(kBarEnd, kEndThreads);
+    if (warp != Cfg::kMmaWarp) return;
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(SM::kTmemCols) : "memory");
     return;
@@ -398,7 +418,7 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     const bool is_v = warp >= Cfg::kVWarp;
     const int key = (warp & 3) * 32 + lane;
     uint64_t *fl = full + (is_v ? kTqStages : 0), *em = empty + (is_v ? kTqStages : 0);
-    uint64_t *sc_full = is_v ? vs_full : k_full, *freed = is_v ? o_done : s_full;
+    uint64_t *freed = is_v ? o_done : s_full;
     float *sc = (is_v ? vs : ks) + key;
     const int n = t1 - cr.t0;
     int st = 0;
@@ -407,53 +427,51 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       const int b = jt & 1;
       wait_ok(fl + st, ph);
       const uint8_t *row = ring + (size_t)st * (2 * SM::kRaw) + (is_v ? SM::kRaw : 0) + key * RB;
-      uint4 code[kChunks];
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) code[i] = reinterpret_cast<const uint4 *>(row)[i];
       const uint4 tail = *reinterpret_cast<const uint4 *>(row + QRow<FMT, D>::kCodeBytes);
-      if (is_v) sc[(jt & 3) * 128] = tail_scale<FMT, D>(tail);
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(em + st);
-        if (is_v) mbar_arrive(sc_full + (jt & 3));
-      }
-      if (++st == p.stages) {
-        st = 0;
-        ph ^= 1u;
+      if (is_v) {
+        sc[(jt & 3) * 128] = tail_scale<FMT, D>(tail);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full + (jt & 3));
       }
       if (jt >= 2) wait_ok(freed + b, (uint32_t)((jt - 2) >> 1) & 1u);
       __syncwarp();
-      if (is_v) {
-        uint8_t *vt = sV + b * SM::kVBytes;
+      tc_fence_after();
+      if (!is_v) sc[(jt & 3) * 128] = tail_scale<FMT, D>(tail);
+      uint8_t *vt = sV + b * SM::kVBytes;
+      const uint32_t tK = tmem + ((uint32_t)((warp & 3) * 32) << 16) + SM::kKCol + b * (D / 2);
+      // (one copy of the conversion for K and V: warps of six roles share the instruction
+      // caches, and with two they waited for instructions a quarter of the time)
+      uint4 code[kChunks];
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          uint32_t h[kRegs];
-          codes_to_halves<FMT>(code[i], tail_groups<FMT, D>(tail, i), h);
+      for (int i = 0; i < kChunks; ++i) code[i] = reinterpret_cast<const uint4 *>(row)[i];
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        uint32_t h[kRegs];
+        codes_to_halves<FMT>(code[i], tail_groups<FMT, D>(tail, i), h);
+        if (is_v) {
 #pragma unroll
           for (int u = 0; u < kRegs / 4; ++u)
             *reinterpret_cast<uint4 *>(vt + swz<TK>(key, i * (kRegs / 4) + u)) =
                 make_uint4(h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
+        } else if constexpr (kRegs == 16) {
+          tmem_st16(tK + i * kRegs, h);
+        } else {
+          tmem_st8(tK + i * kRegs, h);
         }
+      }
+      if (is_v)
         fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_full + b);
-      } else {
-        tc_fence_after();
-        sc[(jt & 3) * 128] = tail_scale<FMT, D>(tail);
-        const uint32_t tK = tmem + ((uint32_t)((warp & 3) * 32) << 16) + SM::kKCol + b * (D / 2);
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          uint32_t h[kRegs];
-          codes_to_halves<FMT>(code[i], tail_groups<FMT, D>(tail, i), h);
-          if constexpr (kRegs == 16)
-            tmem_st16(tK + i * kRegs, h);
-          else
-            tmem_st8(tK + i * kRegs, h);
-        }
+      else
         tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(k_full + (jt & 3));
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(em + st);
+        mbar_arrive(is_v ? v_full + b : k_full + (jt & 3));
+      }
+      if (++st == p.stages) {
+        st = 0;
+        ph ^= 1u;
       }
     }
     tc_fence_before();
@@ -558,10 +576,10 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       named_bar_sync(kBarSoft, kSoft);
     }
 
-    float mu[NW], lsum[NW];  // reference per row, log2 units; sums of P over this thread's keys
+    float nm[NW], lsum[NW];  // bias less the reference of a row, log2 units; sums of P over this thread's keys
 #pragma unroll
     for (int r = 0; r < NW; ++r) {
-      mu[r] = -INFINITY;
+      nm[r] = INFINITY;  // no key seen
       lsum[r] = 0.f;
     }
     float vref = 0.f;  // largest value scale seen
@@ -574,19 +592,15 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       uint64_t km_all = ~0ull;  // rows that see this key
       if (masked) km_all = key >= g.nkeys ? 0ull : key >= g.n_prefix ? keymask[key - g.n_prefix] : ~0ull;
       if (masked && R < 64) km_all &= (1ull << R) - 1ull;
-      const uint32_t km = (uint32_t)(km_all >> r_wg);  // (NW <= 32)
-      wait_ok(vs_full + (jt & 3), (uint32_t)(jt >> 2) & 1u);
-      const float vsc = vs[(jt & 3) * 128 + ktid];
-      const float vmine = km_all != 0ull && vsc == vsc ? vsc : 0.f;
-      wait_ok(k_full + (jt & 3), (uint32_t)(jt >> 2) & 1u);
-      const float cs = ks[(jt & 3) * 128 + ktid] * q_unit;
+      const uint32_t km = (uint32_t)(km_all >> r_wg);  // (this thread's rows in the low bits)
       wait_ok(s_full + b, (uint32_t)(jt >> 1) & 1u);
-      // PV of tile jt - 2: its P buffer is free, and the barrier stays within a phase of its waiters
-      if (jt >= 2) wait_ok(o_done + b, (uint32_t)((jt - 2) >> 1) & 1u);
+      wait_ok(k_full + (jt & 3), (uint32_t)(jt >> 2) & 1u);
       __syncwarp();
       tc_fence_after();
+      const float vsc = vs[(jt & 3) * 128 + ktid], cs = ks[(jt & 3) * 128 + ktid] * q_unit;
+      const float vmine = km_all != 0ull && vsc == vsc ? vsc : 0.f;
       float x[NW];
-      // scores of this key above the references (2^-6 of a weight apart), -inf where unseen
+      // scores of this key above the references (and 2^6 in weight), -inf where unseen
       auto load_scores = [&]() {
         tmem_ld_f<NW>(tS, x);
         if (lt == lt0 && vref == 0.f) {
@@ -594,7 +608,7 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
           if (ktid == 0) {
 #pragma unroll
             for (int r = 0; r < NW; ++r)
-              reinterpret_cast<float *>(red + r_wg)[r] = (km >> r) & 1u ? x[r] * cs : -INFINITY;
+              reinterpret_cast<float *>(red + r_wg)[r] = (km >> r) & 1u ? kTqBias - x[r] * cs : INFINITY;
           }
           const float wm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmine)));
           if (lane == 0) vred[warp] = wm;
@@ -602,22 +616,21 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
 #pragma unroll
           for (int r = 0; r < NW; r += 4) {
             const float4 m4 = red[r_wg + (r >> 2)];
-            mu[r] = m4.x;
-            mu[r + 1] = m4.y;
-            mu[r + 2] = m4.z;
-            mu[r + 3] = m4.w;
+            nm[r] = m4.x;
+            nm[r + 1] = m4.y;
+            nm[r + 2] = m4.z;
+            nm[r + 3] = m4.w;
           }
           vref = fmaxf(fmaxf(fmaxf(vred[4 * wg], vred[4 * wg + 1]), fmaxf(vred[4 * wg + 2], vred[4 * wg + 3])), 0x1p-126f);
         }
         if (masked) {
 #pragma unroll
           for (int r = 0; r < NW; ++r)
-            x[r] = (km >> r) & 1u ? fmaf(x[r], cs, kTqBias - (mu[r] == -INFINITY ? 0.f : mu[r])) : -INFINITY;
+            x[r] = (km >> r) & 1u ? fmaf(x[r], cs, nm[r] == INFINITY ? kTqBias : nm[r]) : -INFINITY;
         } else {
 #pragma unroll
           for (int r = 0; r < NW; r += 2) {
-            const float2 y = fma2(make_float2(x[r], x[r + 1]), make_float2(cs, cs),
-                                  make_float2(kTqBias - mu[r], kTqBias - mu[r + 1]));
+            const float2 y = fma2(make_float2(x[r], x[r + 1]), make_float2(cs, cs), make_float2(nm[r], nm[r + 1]));
             x[r] = y.x;
             x[r + 1] = y.y;
           }
@@ -626,20 +639,16 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       load_scores();
       float dmax = -INFINITY;
 #pragma unroll
-      for (int r = 0; r < NW; ++r) dmax = fmaxf(dmax, x[r]);
+      for (int r = 0; r < NW; r += 2) dmax = max3f(dmax, x[r], x[r + 1]);
       if (masked) {  // (a row's first key moves its reference, however small the score)
 #pragma unroll
         for (int r = 0; r < NW; ++r)
-          if (mu[r] == -INFINITY && ((km >> r) & 1u)) dmax = INFINITY;
+          if (nm[r] == INFINITY && ((km >> r) & 1u)) dmax = INFINITY;
       }
       if (bar_red_or(kBarRed, 128, dmax > kTqBias + kTqMove || vmine > vref)) {
         // move the references to the row maxima seen so far, and the value scale
         WarpScatterMax<NW, 16>::run(x, lane);
-        if constexpr (NW == 32) {
-          reinterpret_cast<float *>(red + r_wg)[lane * 4 + wq] = x[0];
-        } else {
-          if ((lane & (32 / NW - 1)) == 0) reinterpret_cast<float *>(red + r_wg)[(lane / (32 / NW)) * 4 + wq] = x[0];
-        }
+        if ((lane & (32 / NW - 1)) == 0) reinterpret_cast<float *>(red + r_wg)[(lane / (32 / NW)) * 4 + wq] = x[0];
         const float wm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmine)));
         if (lane == 0) vred[warp] = wm;
         named_bar_sync(kBarRed, 128);
@@ -650,10 +659,10 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
         for (int r = 0; r < NW; ++r) {
           const float4 m4 = red[r_wg + r];
           const float up = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)) - kTqBias;  // above the reference (or zero)
-          const bool none = mu[r] == -INFINITY;
-          const float mnew = none ? up : mu[r] + fmaxf(up, 0.f);
-          const float alpha = none ? 0.f : ex2_approx(mu[r] - mnew);
-          mu[r] = mnew;
+          const bool none = nm[r] == INFINITY;
+          const float nnew = none ? kTqBias - up : nm[r] - fmaxf(up, 0.f);
+          const float alpha = none ? 0.f : ex2_approx(nnew - nm[r]);
+          nm[r] = nnew;
           lsum[r] *= alpha;
           x[r] = alpha * vdown;
         }
@@ -666,6 +675,8 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
         }
         load_scores();
       }
+      // PV of tile jt - 2: its P buffer is free (and the barrier stays within a phase of its waiters)
+      if (jt >= 2) wait_ok(o_done + b, (uint32_t)((jt - 2) >> 1) & 1u);
       // P^T row of this key: chunk cc holds rows 8cc .. 8cc + 7
       uint8_t *pk = sP + b * (TK * 128) + ktid * 128;
       const float ratio = vsc / vref;  // a power of two, at most 1
@@ -719,7 +730,7 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     __syncwarp();
     tc_fence_after();
     const size_t slot = (size_t)(s + c);
-    float my_l = 0.f, my_mu = 0.f;
+    float my_l = 0.f, my_nm = 0.f;
     WarpScatterSum<NW, 16>::run(lsum, lane);
     if ((lane & (32 / NW - 1)) == 0) reinterpret_cast<float *>(red + r_wg)[(lane / (32 / NW)) * 4 + wq] = lsum[0];
     named_bar_sync(kBarSoft, kSoft);
@@ -728,14 +739,14 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       my_l = (l4.x + l4.y) + (l4.z + l4.w);
     }
 #pragma unroll
-    for (int j = 0; j < NW; ++j) my_mu = ktid == j ? mu[j] : my_mu;
+    for (int j = 0; j < NW; ++j) my_nm = ktid == j ? nm[j] : my_nm;
     if (ktid < NW) {
       const int r = r_wg + ktid;
       const bool seen = !(my_l == 0.f);  // (NaN: a row that holds one)
       row_inv[r] = r < R && seen ? __fdividef(vref, my_l) : 0.f;
       if (r < R && ok) {
         const int t = (base + r) / group, hq = g.hkv * group + (base + r) % group;
-        const float lse_nat = seen ? (my_mu - kTqBias + __log2f(my_l)) * kLn2 : -INFINITY;
+        const float lse_nat = seen ? (__log2f(my_l) - my_nm) * kLn2 : -INFINITY;
         if (n_parts == 1)
           p.lse[((size_t)g.b * p.Hq + hq) * p.T + t] = lse_nat;
         else
@@ -814,11 +825,12 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     if (*merge_ok) {
       const int seg = s / p.NRB, base = s % p.NRB * NR, R = min(NR, p.R - base);
       const int r0 = mpart[k] * R / np, r1 = (mpart[k] + 1) * R / np;
+      // (parts in flight as the registers allow)
       if (np <= 4)
-        merge_rows_warp<8, 4, D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k], np, r0, r1, warp, 4 * WG, lane);
+        merge_rows_warp<WG == 1 ? 8 : 16, 4, D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k], np, r0, r1, warp, 4 * WG, lane);
       else
-        merge_rows_warp<D == 128 ? 32 : 16, 24, D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k], np, r0, r1, warp, 4 * WG,
-                                                   lane);
+        merge_rows_warp<D == 128 ? 32 : 16, WG == 1 ? 20 : WG == 2 ? 12 : 6, D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k],
+                                                                              np, r0, r1, warp, 4 * WG, lane);
     }
     named_bar_sync(kBarSoft, kSoft);
     // leave: np arrivals and np departures wrap the counter back to zero

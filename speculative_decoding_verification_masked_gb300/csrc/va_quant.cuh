@@ -37,6 +37,14 @@ __device__ __forceinline__ __half2 e2m1x2_to_half2(uint32_t byte) {
 __device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t two) {
   return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3));
 }
+// The eight e2m1 codes of a word as halves (the conversion reads its byte of the word).
+__device__ __forceinline__ void e2m1x8_to_half2(uint32_t w, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+      : "r"(w));
+}
 __device__ __forceinline__ float e4m3_to_float(uint32_t byte) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
 }
