@@ -22,7 +22,9 @@
 // a score exceeds it by more than 2^8, and with it the largest value scale.
 //
 // Roles, one CTA per SM, persistent over the stream-K cut of all tiles, cooperative:
-//   softmax    NR/16 warpgroups; a thread owns a key and 16 rows
+//   softmax    a warpgroup for even and one for odd tiles (64 rows: two each), so that two
+//              tiles are under way; a thread owns a key and up to 32 rows.  Each parity keeps
+//              its own references, sums and O, joined at the end of a part
 //   K          a warpgroup: a thread takes its key's row from the ring, makes halves
 //              and stores them to TMEM (two buffers)
 //   V          a warpgroup: the same into a swizzled tile in shared memory (two buffers)
@@ -64,19 +66,76 @@ constexpr float kTqMove = 8.f;  // a score this far above the reference moves it
 
 template <int NR>
 struct TqCfg {
-  static constexpr int kGroups = NR / 16;  // softmax warpgroups, 16 rows each
+  static constexpr int kRowGroups = NR > 32 ? NR / 32 : 1;  // of NW rows, a warpgroup each for even and odd tiles
+  static constexpr int NW = NR / kRowGroups;                // rows of a softmax thread
+  static constexpr int kGroups = 2 * kRowGroups;            // softmax warpgroups
   static constexpr int kSoft = 128 * kGroups;
   // (the last warpgroup: two producers and two issuers, of S and of PV)
-  static constexpr int kKWarp = 4 * kGroups, kVWarp = kKWarp + 4, kProducer = kVWarp + 4, kMmaWarp = kProducer + 2, kPvWarp = kMmaWarp + 1;
+  static constexpr int kKWarp = 4 * kGroups, kVWarp = kKWarp + 4, kProducer = kVWarp + 4, kMmaWarp = kProducer + 2;
   static constexpr int kThreads = (kProducer + 4) * 32;
   // Registers a thread: the launch's, and what the warpgroups divide them into.
-  static constexpr int kRegsLaunch = kGroups == 1 ? 128 : kGroups == 2 ? 96 : 72;
-  static constexpr int kRegsSoft = kGroups == 1 ? 160 : kGroups == 2 ? 112 : 80,
-                       kRegsKv = kGroups == 1 ? 128 : kGroups == 2 ? 88 : 64,
-                       kRegsRest = kGroups == 1 ? 96 : kGroups == 2 ? 80 : 56;
+  static constexpr int kRegsLaunch = kGroups == 2 ? 96 : 72;
+  static constexpr int kRegsSoft = kGroups == 2 ? 128 : 88, kRegsKv = kGroups == 2 ? 80 : 48, kRegsRest = kGroups == 2 ? 64 : 56;
   static_assert(kGroups * kRegsSoft + 2 * kRegsKv + kRegsRest <= (kGroups + 3) * kRegsLaunch, "within the launch's registers");
   static_assert(kThreads * kRegsLaunch <= 65536, "a block's registers");
 };
+
+// Shared memory by its 32-bit address: the roles' loops are short, and 64-bit address
+// arithmetic was a third of their instructions.
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float4 lds128f(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float2 lds64f(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void sts32f(uint32_t a, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// role_wait in few instructions: most warps wait most of the time, a try comes back after
+// some hundred cycles whatever time it is given, and looking at the clock after each took
+// a third of all instructions.
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)  // ns
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool tq_wait_on(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint64_t limit_ns,
+                                        int *status) {
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_sleep(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      record_status(status, VA_ERR_TIMEOUT);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
 
 template <int N>
 __device__ __forceinline__ void regs_dec() {
@@ -102,19 +161,19 @@ struct TqSmem {
   static constexpr int kMiscOff = (kBarOff + kNumBars * 8 + 15) & ~15;  // tmem base, abort flag, merge flag
   static constexpr int kRowMaskOff = kMiscOff + 16;      // u64 [64]: draft visibility rows
   static constexpr int kKeyMaskOff = kRowMaskOff + 512;  // u64 [64]: per draft key, rows that see it
-  static constexpr int kRedOff = kKeyMaskOff + 512;      // float4 [NR]: per-warp row maxima
-  static constexpr int kVRedOff = kRedOff + NR * 16;     // float [16]: per-warp largest value scales, Q maxima
-  static constexpr int kRowInvOff = kVRedOff + 64;       // float [NR]
-  static constexpr int kKsOff = kRowInvOff + NR * 4;     // float [4][128]
-  static constexpr int kVsOff = kKsOff + 4 * 512;        // float [4][128]
-  static constexpr int kRingOff = (kVsOff + 4 * 512 + 127) & ~127;
+  static constexpr int kRedOff = kKeyMaskOff + 512;      // float4 [2 NR]: per-warp row maxima and sums of each tile parity
+  static constexpr int kVRedOff = kRedOff + 2 * NR * 16; // float [16]: per-warp largest value scales, Q maxima
+  static constexpr int kRefOff = kVRedOff + 64;          // float [2 NR]: bias less the reference of a row
+  static constexpr int kAlphaOff = kRefOff + 2 * NR * 4; // float [2 NR]: what a moved reference scales by; then 1 / l factors
+  static constexpr int kKsOff = kAlphaOff + 2 * NR * 4;  // float2 [4][128]: scales of the tile's K and V rows
+  static constexpr int kRingOff = (kKsOff + 4 * 1024 + 127) & ~127;
   static constexpr int kNC = NR < 32 ? 32 : NR;          // TMEM columns per region
-  // O at 0, S at NC and 2NC, K at 3NC and 3NC + D/2
-  static constexpr int kKCol = 3 * kNC;
+  // O of even and odd tiles at 0 and NC, S at 2NC and 3NC, K at 4NC and 4NC + D/2
+  static constexpr int kKCol = 4 * kNC;
   static constexpr int kTmemCols = kKCol + D <= 256 ? 256 : 512;
   static_assert(kKCol + D <= 512, "TMEM plan");
   static_assert(kQOff % 1024 == 0 && kPOff % 1024 == 0 && kQBytes % 1024 == 0, "swizzle atoms");
-  static_assert(kRowInvOff % 16 == 0 && kKsOff % 16 == 0, "vector loads");
+  static_assert(kRefOff % 16 == 0 && kAlphaOff % 16 == 0 && kKsOff % 16 == 0, "vector loads");
   // d 64: what the unused lanes of the second V buffer read is the P buffers
   static_assert(D == 128 || kPOff + 16384 <= kQOff, "unused lanes stay inside");
 };
@@ -149,13 +208,7 @@ __device__ __forceinline__ void codes_to_halves(const uint4 &v, uint32_t two_gro
   }
 }
 
-// Two group scales of chunk c out of a row's tail, and the row scale.
-template <int FMT, int D>
-__device__ __forceinline__ uint32_t tail_groups(const uint4 &tail, int c) {
-  if constexpr (FMT == VA_KV_E4M3) return 0u;
-  const uint32_t w = c < 2 ? tail.x : tail.y;
-  return w >> (16 * (c & 1));
-}
+// The row scale out of a row's tail.
 template <int FMT, int D>
 __device__ __forceinline__ float tail_scale(const uint4 &tail) {
   return __uint_as_float(FMT == VA_KV_E4M3 ? tail.x : D == 128 ? tail.z : tail.y);
@@ -207,7 +260,9 @@ __device__ __forceinline__ void produce_raw(const AttnParams &p, const CUtensorM
     for (int lt = lt0; lt < lt1; ++lt, ++it) {
       const int page_now = page_next;
       page_next = box_page(lt + 1);
-      warp_role_wait(empty + st, ph ^ 1u, ok, abort_flag, p.wait_ns, p.status);
+      if (__builtin_expect(ok && !mbar_sleep(smem_u32(empty + st), ph ^ 1u), 0))
+        ok = tq_wait_on(smem_u32(empty + st), ph ^ 1u, abort_flag, p.wait_ns, p.status);
+      ok = __all_sync(0xffffffffu, ok);  // (a gather passes addresses between the lanes)
       if (ok) {
         uint8_t *dst = ring + (size_t)st * (2 * TK * RB);
         const int k0 = lt * TK;
@@ -270,14 +325,15 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
                              const __grid_constant__ CUtensorMap tmv) {
   using SM = TqSmem<FMT, D, NR>;
   using Cfg = TqCfg<NR>;
-  constexpr int TK = kTqKeys, NC = SM::kNC, WG = Cfg::kGroups, kSoft = Cfg::kSoft, RB = SM::kRow;
-  constexpr int NW = NR / WG;  // rows of a softmax thread
+  constexpr int TK = kTqKeys, NC = SM::kNC, WG = Cfg::kGroups, RG = Cfg::kRowGroups, NW = Cfg::NW, kSoft = Cfg::kSoft,
+                RB = SM::kRow;
+  constexpr int kXRows = NR > 32 ? 16 : NW;  // scores a softmax thread holds at once (registers)
   constexpr int kChunks = QRow<FMT, D>::kCodeBytes / 16, kRegs = CodeChunk<FMT>::kRegs;
   constexpr int kBarQ = 1, kBarSoft = 3, kBarEnd = 4, kBarRed0 = 5;  // kBarRed0 + softmax warpgroup
   constexpr int kEndThreads = kSoft + 256 + 64;                      // all but the producers
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  uint8_t *sV = smem, *sP = smem + SM::kPOff, *sQ = smem + SM::kQOff, *ring = smem + SM::kRingOff;
+  uint8_t *sV = smem, *sQ = smem + SM::kQOff, *ring = smem + SM::kRingOff;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SM::kBarOff);
   uint64_t *full = bars, *empty = bars + 2 * kTqStages;  // [K, V][stage]
   uint64_t *k_full = bars + 4 * kTqStages, *v_full = k_full + 4, *s_full = v_full + 2, *p_full = s_full + 2,
@@ -288,11 +344,14 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
   uint64_t *keymask = reinterpret_cast<uint64_t *>(smem + SM::kKeyMaskOff);
   float4 *red = reinterpret_cast<float4 *>(smem + SM::kRedOff);
   float *vred = reinterpret_cast<float *>(smem + SM::kVRedOff);
-  float *row_inv = reinterpret_cast<float *>(smem + SM::kRowInvOff);
-  float *ks = reinterpret_cast<float *>(smem + SM::kKsOff), *vs = reinterpret_cast<float *>(smem + SM::kVsOff);
+  float *refs = reinterpret_cast<float *>(smem + SM::kRefOff), *alphas = reinterpret_cast<float *>(smem + SM::kAlphaOff);
   int *tstart = reinterpret_cast<int *>(ring + (size_t)p.stages * (2 * SM::kRaw));
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
+  // (addresses of the same barriers)
+  const uint32_t smem_a = smem_u32(smem), bar_a = smem_a + SM::kBarOff;
+  const uint32_t a_full = bar_a, a_empty = bar_a + 16 * kTqStages, a_k_full = a_empty + 16 * kTqStages, a_v_full = a_k_full + 32,
+                 a_s_full = a_v_full + 16, a_p_full = a_s_full + 16, a_o_done = a_p_full + 16;
   if (tid == 0) {
     for (int i = 0; i < 2 * kTqStages; ++i) {
       mbar_init(full + i, kTma ? 1 : 32);
@@ -302,7 +361,7 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(v_full + b, 4);
       mbar_init(s_full + b, c == p.test_stall ? kNever : 1);
-      mbar_init(p_full + b, kSoft);
+      mbar_init(p_full + b, 128 * RG);
       mbar_init(o_done + b, 1);
     }
     mbar_init(drains + 0, 1);
@@ -315,7 +374,9 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
   const int t1 = cr.t1, s0 = cr.s0;
 
   bool ok = true;
-  auto wait_ok = [&](uint64_t *bar, uint32_t parity) { role_wait(bar, parity, ok, abort_flag, p.wait_ns, p.status); };
+  auto wait_ok = [&](uint32_t bar, uint32_t parity) {
+    if (__builtin_expect(ok && !mbar_sleep(bar, parity), 0)) ok = tq_wait_on(bar, parity, abort_flag, p.wait_ns, p.status);
+  };
   // TMEM is allocated: every role but the producers waits for its address here
   auto tmem_base = [&]() {
     tc_fence_before();
@@ -359,11 +420,11 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
         for (int i = 0; i < n; ++i, ++jt) {
           const uint32_t b = jt & 1u;
           // (two tiles ahead of the softmax: S of tile j - 2 has been read)
-          if (i >= 2) wait_ok(p_full + b, ((jt - 2) >> 1) & 1u);
-          wait_ok(k_full + (jt & 3), (jt >> 2) & 1u);
+          if (i >= 2) wait_ok(a_p_full + 8 * b, ((jt - 2) >> 1) & 1u);
+          wait_ok(a_k_full + 8 * (jt & 3), (jt >> 2) & 1u);
           __syncwarp();
           tc_fence_after();
-          const uint32_t tS = tmem + (1 + b) * NC, tK = tmem + SM::kKCol + b * (D / 2);
+          const uint32_t tS = tmem + (2 + b) * NC, tK = tmem + SM::kKCol + b * (D / 2);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t qoff = (uint64_t)(((kk >> 2) * (NR * 128) + (kk & 3) * 32) >> 4);
@@ -383,15 +444,15 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
         const int n = (int)uni(lt1 - lt0);
         for (int i = 0; i < n; ++i, ++jt) {
           const uint32_t b = jt & 1u;
-          wait_ok(v_full + b, (jt >> 1) & 1u);
-          wait_ok(p_full + b, (jt >> 1) & 1u);
+          wait_ok(a_v_full + 8 * b, (jt >> 1) & 1u);
+          wait_ok(a_p_full + 8 * b, (jt >> 1) & 1u);
           __syncwarp();
           tc_fence_after();
           const uint64_t dV = dV0 + (uint64_t)(b * (SM::kVBytes >> 4)), dP = dP0 + (uint64_t)(b * (TK * 128 >> 4));
 #pragma unroll
           for (int kk = 0; kk < TK / 16; ++kk) {
             const uint64_t off = (uint64_t)((kk * 2048) >> 4);
-            umma_ss_warp(tmem, dV + off, dP + off, id_o, kk > 0 || i > 0 ? 1u : 0u);
+            umma_ss_warp(tmem + b * NC, dV + off, dP + off, id_o, kk > 0 || i > 1 ? 1u : 0u);
           }
           umma_commit_warp(o_done + b);
           __syncwarp();
@@ -417,46 +478,53 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     const uint32_t tmem = tmem_base();
     const bool is_v = warp >= Cfg::kVWarp;
     const int key = (warp & 3) * 32 + lane;
-    uint64_t *fl = full + (is_v ? kTqStages : 0), *em = empty + (is_v ? kTqStages : 0);
-    uint64_t *freed = is_v ? o_done : s_full;
-    float *sc = (is_v ? vs : ks) + key;
+    const uint32_t fl = a_full + (is_v ? 8 * kTqStages : 0), em = fl + 16 * kTqStages;
+    const uint32_t freed = is_v ? a_o_done : a_s_full;
+    const uint32_t sc = smem_a + SM::kKsOff + key * 8 + (is_v ? 4 : 0);
+    const uint32_t row0 = smem_a + SM::kRingOff + (is_v ? SM::kRaw : 0) + key * RB;
+    // 16-byte chunk c of the key's V row: (vrow ^ 16 c), 16 KB further for the second half
+    const uint32_t vrow = smem_a + key * 128 + ((key & 7) << 4);
+    const uint32_t tK0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + SM::kKCol;
     const int n = t1 - cr.t0;
     int st = 0;
-    uint32_t ph = 0;
+    uint32_t ph = 0, row = row0;
     for (int jt = 0; jt < n; ++jt) {
-      const int b = jt & 1;
-      wait_ok(fl + st, ph);
-      const uint8_t *row = ring + (size_t)st * (2 * SM::kRaw) + (is_v ? SM::kRaw : 0) + key * RB;
-      const uint4 tail = *reinterpret_cast<const uint4 *>(row + QRow<FMT, D>::kCodeBytes);
+      const uint32_t b = (uint32_t)jt & 1u;
+      wait_ok(fl + 8 * st, ph);
+      const uint4 tail = lds128(row + QRow<FMT, D>::kCodeBytes);
+      const uint32_t sc_now = sc + (jt & 3) * 1024, kb = a_k_full + 8 * (jt & 3);
       if (is_v) {
-        sc[(jt & 3) * 128] = tail_scale<FMT, D>(tail);
+        sts32f(sc_now, tail_scale<FMT, D>(tail));
         __syncwarp();
-        if (lane == 0) mbar_arrive(k_full + (jt & 3));
+        if (lane == 0) mbar_arrive_at(kb);
       }
-      if (jt >= 2) wait_ok(freed + b, (uint32_t)((jt - 2) >> 1) & 1u);
+      if (jt >= 2) wait_ok(freed + 8 * b, (uint32_t)((jt - 2) >> 1) & 1u);
       __syncwarp();
       tc_fence_after();
-      if (!is_v) sc[(jt & 3) * 128] = tail_scale<FMT, D>(tail);
-      uint8_t *vt = sV + b * SM::kVBytes;
-      const uint32_t tK = tmem + ((uint32_t)((warp & 3) * 32) << 16) + SM::kKCol + b * (D / 2);
-      // (one copy of the conversion for K and V: warps of six roles share the instruction
-      // caches, and with two they waited for instructions a quarter of the time)
-      uint4 code[kChunks];
+      if (!is_v) sts32f(sc_now, tail_scale<FMT, D>(tail));
+      // 64 elements a pass; one copy of the conversion for K and V, rolled: the warps of six
+      // roles share the instruction caches
+      constexpr int kPer = kChunks / (D / 64);
+#pragma unroll 1
+      for (uint32_t half = 0; half < D / 64; ++half) {
+        const uint32_t dst = vrow + b * SM::kVBytes + half * (TK * 128), tK = tK0 + b * (D / 2) + half * 32;
+        const uint32_t groups = half == 0 ? tail.x : tail.y;
+        uint4 code[kPer];
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) code[i] = reinterpret_cast<const uint4 *>(row)[i];
+        for (int i = 0; i < kPer; ++i) code[i] = lds128(row + half * (kPer * 16) + i * 16);
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        uint32_t h[kRegs];
-        codes_to_halves<FMT>(code[i], tail_groups<FMT, D>(tail, i), h);
-        if (is_v) {
+        for (int i = 0; i < kPer; ++i) {
+          uint32_t h[kRegs];
+          codes_to_halves<FMT>(code[i], groups >> (16 * (i & 1)), h);
+          if (is_v) {
 #pragma unroll
-          for (int u = 0; u < kRegs / 4; ++u)
-            *reinterpret_cast<uint4 *>(vt + swz<TK>(key, i * (kRegs / 4) + u)) =
-                make_uint4(h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
-        } else if constexpr (kRegs == 16) {
-          tmem_st16(tK + i * kRegs, h);
-        } else {
-          tmem_st8(tK + i * kRegs, h);
+            for (int u = 0; u < kRegs / 4; ++u)
+              sts128(dst ^ ((i * (kRegs / 4) + u) << 4), h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
+          } else if constexpr (kRegs == 16) {
+            tmem_st16(tK + i * kRegs, h);
+          } else {
+            tmem_st8(tK + i * kRegs, h);
+          }
         }
       }
       if (is_v)
@@ -466,12 +534,14 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(em + st);
-        mbar_arrive(is_v ? v_full + b : k_full + (jt & 3));
+        mbar_arrive_at(em + 8 * st);
+        mbar_arrive_at(is_v ? a_v_full + 8 * b : kb);
       }
+      row += 2 * SM::kRaw;
       if (++st == p.stages) {
         st = 0;
         ph ^= 1u;
+        row = row0;
       }
     }
     tc_fence_before();
@@ -482,12 +552,17 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
   // ================================== softmax ==================================
   regs_inc<Cfg::kRegsSoft>();
   const uint32_t tmem = tmem_base();
-  const int wg = WG == 1 ? 0 : warp >> 2;    // warpgroup: rows [r_wg, r_wg + NW) of the block
-  const int r_wg = wg * NW;
-  const int wq = WG == 1 ? warp : warp & 3;  // warp of the warpgroup
-  const int ktid = WG == 1 ? tid : tid & 127;// key of the tile, and output column of the epilogue
+  const int wg = warp >> 2, par = wg / RG;   // warpgroup; the tiles it takes: jt % 2 == par
+  const int r_wg = (wg % RG) * NW;           // its rows [r_wg, r_wg + NW) of the block
+  const int wq = warp & 3, ktid = tid & 127; // warp of the warpgroup; key of the tile, output column of the epilogue
   const int kBarRed = kBarRed0 + wg;
-  const uint32_t tO = tmem + ((uint32_t)(wq * 32) << 16);
+  const uint32_t tLane = tmem + ((uint32_t)(wq * 32) << 16);
+  const uint32_t tO = tLane + par * NC + r_wg, tS = tLane + (2 + par) * NC + r_wg;
+  float4 *my_red = red + par * NR + r_wg;    // [NW]
+  float *ref = refs + par * NR + r_wg, *alpha = alphas + par * NR + r_wg;
+  const uint32_t a_ref = smem_u32(ref), a_scale = smem_a + SM::kKsOff + ktid * 8;
+  // 16-byte chunk cw of the thread's P^T row (8 rows of Q): (a_p ^ 16 cw)
+  const uint32_t a_p = (smem_a + SM::kPOff + par * (TK * 128) + ktid * 128 + ((ktid & 7) << 4)) ^ (r_wg / 8 << 4);
   const int group = p.Hq / p.Hkv;
   int jt = 0;
   // split segments this CTA holds a part of (at most its first and its last)
@@ -499,6 +574,7 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     const int first_cta = owner_cta(tstart[s], cr.total, cr.G);
     const int n_parts = owner_cta(tstart[s + 1] - 1, cr.total, cr.G) - first_cta + 1;
     if (lt0 == 0 && tid == 0) p.meta[s] = make_int2(s + first_cta, n_parts);
+    const int jt0 = jt;
     const int base = g.rb * NR, R = min(NR, p.R - base);  // the packed rows [base, base + R) of the kv-head
     // bit r: this segment's row r is one of draft token t
     auto token_rows = [&](int t) -> uint64_t {
@@ -511,7 +587,6 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     {
       const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(p.q);
       constexpr int kCh = D / 8, kQIt = (NR * kCh + kSoft - 1) / kSoft;
-      static_assert(NR * kCh % kSoft == 0, "every thread loads as many chunks");
       uint4 v[kQIt];
       uint32_t top = 0;  // largest finite |bf16|
 #pragma unroll
@@ -543,6 +618,7 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
 #pragma unroll
       for (int u = 0; u < kQIt; ++u) {
         const int e = tid + u * kSoft, row = e / kCh, ch = e % kCh;
+        if (row >= NR) break;  // (16 rows of d 64 are fewer chunks than threads)
         const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
         uint32_t h[4];
 #pragma unroll
@@ -576,196 +652,230 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       named_bar_sync(kBarSoft, kSoft);
     }
 
-    float nm[NW], lsum[NW];  // bias less the reference of a row, log2 units; sums of P over this thread's keys
+    // Reference of row r: ref[r] = kTqBias less it (infinity: no key seen), log2 units; in
+    // shared memory, where a vector load gives four rows to every thread.
+    float lsum[NW];    // sums of P over this thread's keys
 #pragma unroll
-    for (int r = 0; r < NW; ++r) {
-      nm[r] = INFINITY;  // no key seen
-      lsum[r] = 0.f;
-    }
-    float vref = 0.f;  // largest value scale seen
+    for (int r = 0; r < NW; ++r) lsum[r] = 0.f;
+    float vref = 0.f, rvref = 0.f;  // largest value scale seen (0: no tile yet), and one over it
+    const int lt_first = lt0 + ((jt ^ par) & 1);
+    jt += (jt ^ par) & 1;
 
-    for (int lt = lt0; lt < lt1; ++lt, ++jt) {
-      const int b = jt & 1;
-      const uint32_t tS = tO + (1 + b) * NC + r_wg;
-      const int key = lt * TK + ktid;
+    for (int lt = lt_first; lt < lt1; lt += 2, jt += 2) {
       const bool masked = lt * TK + TK > g.n_prefix;
       uint64_t km_all = ~0ull;  // rows that see this key
-      if (masked) km_all = key >= g.nkeys ? 0ull : key >= g.n_prefix ? keymask[key - g.n_prefix] : ~0ull;
-      if (masked && R < 64) km_all &= (1ull << R) - 1ull;
+      if (__builtin_expect(masked, 0)) {
+        const int key = lt * TK + ktid;
+        km_all = key >= g.nkeys ? 0ull : key >= g.n_prefix ? keymask[key - g.n_prefix] : ~0ull;
+        if (R < 64) km_all &= (1ull << R) - 1ull;
+      }
       const uint32_t km = (uint32_t)(km_all >> r_wg);  // (this thread's rows in the low bits)
-      wait_ok(s_full + b, (uint32_t)(jt >> 1) & 1u);
-      wait_ok(k_full + (jt & 3), (uint32_t)(jt >> 2) & 1u);
+      wait_ok(a_k_full + 8 * (jt & 3), (uint32_t)(jt >> 2) & 1u);
+      const float2 sc = lds64f(a_scale + (jt & 3) * 1024);
+      const float vsc = sc.y, cs = sc.x * q_unit;
+      wait_ok(a_s_full + 8 * par, (uint32_t)(jt >> 1) & 1u);
       __syncwarp();
       tc_fence_after();
-      const float vsc = vs[(jt & 3) * 128 + ktid], cs = ks[(jt & 3) * 128 + ktid] * q_unit;
-      const float vmine = km_all != 0ull && vsc == vsc ? vsc : 0.f;
-      float x[NW];
-      // scores of this key above the references (and 2^6 in weight), -inf where unseen
-      auto load_scores = [&]() {
-        tmem_ld_f<NW>(tS, x);
-        if (lt == lt0 && vref == 0.f) {
-          // first tile of the part: the scores of key 0 are the references
-          if (ktid == 0) {
+      float x[kXRows];
+      // scores of this key above the references (and 2^6 in weight), -inf where unseen: rows
+      // [h, h + kXRows)
+      auto load_scores = [&](int h) {
+        tmem_ld_f<kXRows>(tS + h, x);
+        if (__builtin_expect(masked, 0)) {
 #pragma unroll
-            for (int r = 0; r < NW; ++r)
-              reinterpret_cast<float *>(red + r_wg)[r] = (km >> r) & 1u ? kTqBias - x[r] * cs : INFINITY;
+          for (int r = 0; r < kXRows; r += 4) {
+            const float4 n4 = lds128f(a_ref + 4 * (h + r));
+            const float nn[4] = {n4.x, n4.y, n4.z, n4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              x[r + i] = (km >> (h + r + i)) & 1u ? fmaf(x[r + i], cs, nn[i] == INFINITY ? kTqBias : nn[i]) : -INFINITY;
           }
-          const float wm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmine)));
-          if (lane == 0) vred[warp] = wm;
-          named_bar_sync(kBarRed, 128);
-#pragma unroll
-          for (int r = 0; r < NW; r += 4) {
-            const float4 m4 = red[r_wg + (r >> 2)];
-            nm[r] = m4.x;
-            nm[r + 1] = m4.y;
-            nm[r + 2] = m4.z;
-            nm[r + 3] = m4.w;
-          }
-          vref = fmaxf(fmaxf(fmaxf(vred[4 * wg], vred[4 * wg + 1]), fmaxf(vred[4 * wg + 2], vred[4 * wg + 3])), 0x1p-126f);
-        }
-        if (masked) {
-#pragma unroll
-          for (int r = 0; r < NW; ++r)
-            x[r] = (km >> r) & 1u ? fmaf(x[r], cs, nm[r] == INFINITY ? kTqBias : nm[r]) : -INFINITY;
         } else {
 #pragma unroll
-          for (int r = 0; r < NW; r += 2) {
-            const float2 y = fma2(make_float2(x[r], x[r + 1]), make_float2(cs, cs), make_float2(nm[r], nm[r + 1]));
+          for (int r = 0; r < kXRows; r += 4) {
+            const float4 n4 = lds128f(a_ref + 4 * (h + r));
+            const float2 y = fma2(make_float2(x[r], x[r + 1]), make_float2(cs, cs), make_float2(n4.x, n4.y));
+            const float2 z = fma2(make_float2(x[r + 2], x[r + 3]), make_float2(cs, cs), make_float2(n4.z, n4.w));
             x[r] = y.x;
             x[r + 1] = y.y;
+            x[r + 2] = z.x;
+            x[r + 3] = z.y;
           }
         }
       };
-      load_scores();
-      float dmax = -INFINITY;
+      // First tile of the part: its row maxima are the references (the scores of one key as
+      // a first guess were passed by 2^8 in some row of most parts, once or twice, and each
+      // move costs as much as several tiles).  Later they move when a score passes one.
+      const bool first = vref == 0.f;
+      bool move = first;
+      if (__builtin_expect(!first, 1)) {
+        float dmax = -INFINITY;
 #pragma unroll
-      for (int r = 0; r < NW; r += 2) dmax = max3f(dmax, x[r], x[r + 1]);
-      if (masked) {  // (a row's first key moves its reference, however small the score)
+        for (int h = 0; h < NW; h += kXRows) {
+          load_scores(h);
 #pragma unroll
-        for (int r = 0; r < NW; ++r)
-          if (nm[r] == INFINITY && ((km >> r) & 1u)) dmax = INFINITY;
-      }
-      if (bar_red_or(kBarRed, 128, dmax > kTqBias + kTqMove || vmine > vref)) {
-        // move the references to the row maxima seen so far, and the value scale
-        WarpScatterMax<NW, 16>::run(x, lane);
-        if ((lane & (32 / NW - 1)) == 0) reinterpret_cast<float *>(red + r_wg)[(lane / (32 / NW)) * 4 + wq] = x[0];
-        const float wm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmine)));
-        if (lane == 0) vred[warp] = wm;
-        named_bar_sync(kBarRed, 128);
-        const float vnew = fmaxf(vref, fmaxf(fmaxf(vred[4 * wg], vred[4 * wg + 1]), fmaxf(vred[4 * wg + 2], vred[4 * wg + 3])));
-        const float vdown = vref / vnew;
-        vref = vnew;
+          for (int r = 0; r < kXRows; r += 2) dmax = max3f(dmax, x[r], x[r + 1]);
+          if (__builtin_expect(masked, 0)) {  // (a row's first key moves its reference, however small the score)
 #pragma unroll
-        for (int r = 0; r < NW; ++r) {
-          const float4 m4 = red[r_wg + r];
-          const float up = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)) - kTqBias;  // above the reference (or zero)
-          const bool none = nm[r] == INFINITY;
-          const float nnew = none ? kTqBias - up : nm[r] - fmaxf(up, 0.f);
-          const float alpha = none ? 0.f : ex2_approx(nnew - nm[r]);
-          nm[r] = nnew;
-          lsum[r] *= alpha;
-          x[r] = alpha * vdown;
+            for (int r = 0; r < kXRows; ++r)
+              if (((km >> (h + r)) & 1u) && ref[h + r] == INFINITY) dmax = INFINITY;
+          }
         }
-        if (lt != lt0) {
-          wait_ok(o_done + (b ^ 1), (uint32_t)((jt - 1) >> 1) & 1u);  // O holds every PV up to tile jt - 1
+        move = bar_red_or(kBarRed, 128, dmax > kTqBias + kTqMove || (vsc > vref && km_all != 0ull));
+      }
+      if (__builtin_expect(move, 0)) {
+        // the references to the row maxima seen so far, and the value scale to the largest
+#pragma unroll
+        for (int h = 0; h < NW; h += kXRows) {
+          if (first) {
+            tmem_ld_f<kXRows>(tS + h, x);
+#pragma unroll
+            for (int r = 0; r < kXRows; ++r) x[r] = (km >> (h + r)) & 1u ? fmaf(x[r], cs, kTqBias) : -INFINITY;
+          } else {
+            load_scores(h);
+          }
+          WarpScatterMax<kXRows, 16>::run(x, lane);
+          if ((lane & (32 / kXRows - 1)) == 0)
+            reinterpret_cast<float *>(my_red + h)[(lane / (32 / kXRows)) * 4 + wq] = x[0];
+        }
+        {  // (NaN and the scales of keys that nobody sees stay out)
+          const uint32_t wm = __reduce_max_sync(0xffffffffu, km_all != 0ull && vsc == vsc ? __float_as_uint(vsc) : 0u);
+          if (lane == 0) vred[warp] = __uint_as_float(wm);
+        }
+        named_bar_sync(kBarRed, 128);
+        if (ktid < NW) {
+          const float4 m4 = my_red[ktid];
+          const float up = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)) - kTqBias;  // above the reference (or zero)
+          const float old = first ? INFINITY : ref[ktid];
+          const bool none = old == INFINITY;
+          const float now = none ? kTqBias - up : old - fmaxf(up, 0.f);
+          alpha[ktid] = none ? 0.f : ex2_approx(now - old);
+          ref[ktid] = now;
+        }
+        const float vtile = fmaxf(fmaxf(vred[4 * wg], vred[4 * wg + 1]), fmaxf(vred[4 * wg + 2], vred[4 * wg + 3]));
+        const float vnew = fmaxf(fmaxf(vref, vtile), 0x1p-126f);
+        const float vdown = vref * (1.f / vnew);
+        vref = vnew;
+        rvref = 1.f / vref;
+        named_bar_sync(kBarRed, 128);
+        if (!first) {
+#pragma unroll
+          for (int r = 0; r < NW; ++r) lsum[r] *= alpha[r];
+          wait_ok(a_o_done + 8 * par, (uint32_t)((jt - 2) >> 1) & 1u);  // O holds every PV of this parity
           __syncwarp();
           tc_fence_after();
-          tmem_scale_cols<NW>(tO + r_wg, x);
-          tmem_st_wait();
+#pragma unroll
+          for (int h = 0; h < NW; h += 16) {
+            float a[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) a[r] = alpha[h + r] * vdown;
+            tmem_scale_cols<16>(tO + h, a);
+            tmem_st_wait();
+          }
         }
-        load_scores();
+        if (kXRows == NW) load_scores(0);
       }
       // PV of tile jt - 2: its P buffer is free (and the barrier stays within a phase of its waiters)
-      if (jt >= 2) wait_ok(o_done + b, (uint32_t)((jt - 2) >> 1) & 1u);
+      if (jt >= 2) wait_ok(a_o_done + 8 * par, (uint32_t)((jt - 2) >> 1) & 1u);
       // P^T row of this key: chunk cc holds rows 8cc .. 8cc + 7
-      uint8_t *pk = sP + b * (TK * 128) + ktid * 128;
-      const float ratio = vsc / vref;  // a power of two, at most 1
-      if (masked) {
+      const float ratio = vsc * rvref;  // a power of two, at most 1 (of a key that somebody sees)
+      const __half2 ratio2 = __float2half2_rn(ratio);
 #pragma unroll
-        for (int cw = 0; cw < NW / 8; ++cw) {
+      for (int h0 = 0; h0 < NW; h0 += kXRows) {
+        if (kXRows != NW) load_scores(h0);
+#pragma unroll
+        for (int cw = 0; cw < kXRows / 8; ++cw) {
           uint32_t h[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int r = 8 * cw + 2 * q;
-            const float a = ex2_approx(x[r]), e = ex2_approx(x[r + 1]);  // (0 where unseen)
-            lsum[r] += a;
-            lsum[r + 1] += e;
-            // (the scale of a key that a row does not see may be anything)
-            h[q] = half2_bits(__floats2half2_rn((km >> r) & 1u ? a * ratio : 0.f, (km >> (r + 1)) & 1u ? e * ratio : 0.f));
-          }
-          *reinterpret_cast<uint4 *>(pk + (((r_wg / 8 + cw) ^ (ktid & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-        }
-        if (km_all == 0ull) {
-          // a key that no row sees: zero V, so that 0 * V stays 0 whatever it held
-          wait_ok(v_full + b, (uint32_t)(jt >> 1) & 1u);
-#pragma unroll
-          for (int c0 = 0; c0 < D / 8 / WG; ++c0)
-            *reinterpret_cast<uint4 *>(sV + b * SM::kVBytes + swz<TK>(ktid, wg * (D / 8 / WG) + c0)) = make_uint4(0, 0, 0, 0);
-        }
-      } else {
-        const __half2 ratio2 = __float2half2_rn(ratio);
-#pragma unroll
-        for (int cw = 0; cw < NW / 8; ++cw) {
-          uint32_t h[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int r = 8 * cw + 2 * q;
-            const float a = ex2_approx(x[r]), e = ex2_approx(x[r + 1]);
+            const int xr = 8 * cw + 2 * q, r = h0 + xr;
+            const float a = ex2_approx(x[xr]), e = ex2_approx(x[xr + 1]);  // (0 where unseen)
             const float2 s2 = add2(make_float2(lsum[r], lsum[r + 1]), make_float2(a, e));
             lsum[r] = s2.x;
             lsum[r + 1] = s2.y;
-            h[q] = half2_bits(__hmul2(__floats2half2_rn(a, e), ratio2));
+            __half2 pr = __hmul2(__floats2half2_rn(a, e), ratio2);
+            if (__builtin_expect(masked, 0)) {  // (the scale of a key that a row does not see may be anything)
+              if (!((km >> r) & 1u)) pr.x = __ushort_as_half(0);
+              if (!((km >> (r + 1)) & 1u)) pr.y = __ushort_as_half(0);
+            }
+            h[q] = half2_bits(pr);
           }
-          *reinterpret_cast<uint4 *>(pk + (((r_wg / 8 + cw) ^ (ktid & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          sts128(a_p ^ ((h0 / 8 + cw) << 4), h[0], h[1], h[2], h[3]);
         }
+      }
+      if (__builtin_expect(masked && km_all == 0ull, 0)) {
+        // a key that no row sees: zero V, so that 0 * V stays 0 whatever it held
+        wait_ok(a_v_full + 8 * par, (uint32_t)(jt >> 1) & 1u);
+#pragma unroll
+        for (int c0 = 0; c0 < D / 8 / RG; ++c0)
+          *reinterpret_cast<uint4 *>(sV + par * SM::kVBytes + swz<TK>(ktid, (wg % RG) * (D / 8 / RG) + c0)) =
+              make_uint4(0, 0, 0, 0);
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(p_full + b);
+      mbar_arrive_at(a_p_full + 8 * par);
     }
-
-    // ---- epilogue: column d = ktid of O / l for every row of this segment part ----
-    if (jt >= 2) wait_ok(o_done + (jt & 1), (uint32_t)((jt - 2) >> 1) & 1u);
-    wait_ok(o_done + ((jt - 1) & 1), (uint32_t)((jt - 1) >> 1) & 1u);
+    // ---- epilogue: the two parities' O and l of every row of this part joined ----
+    // (a warpgroup waits for the PVs of its own tiles, whose phases it has followed, and
+    // meets the others at the barrier below)
+    const bool mine = lt_first < lt1;  // this parity had a tile
+    if (mine) wait_ok(a_o_done + 8 * par, (uint32_t)((jt - 2) >> 1) & 1u);
     __syncwarp();
     tc_fence_after();
+    jt = jt0 + (lt1 - lt0);
     const size_t slot = (size_t)(s + c);
-    float my_l = 0.f, my_nm = 0.f;
-    WarpScatterSum<NW, 16>::run(lsum, lane);
-    if ((lane & (32 / NW - 1)) == 0) reinterpret_cast<float *>(red + r_wg)[(lane / (32 / NW)) * 4 + wq] = lsum[0];
-    named_bar_sync(kBarSoft, kSoft);
-    if (ktid < NW) {
-      const float4 l4 = red[r_wg + ktid];
-      my_l = (l4.x + l4.y) + (l4.z + l4.w);
-    }
 #pragma unroll
-    for (int j = 0; j < NW; ++j) my_nm = ktid == j ? nm[j] : my_nm;
-    if (ktid < NW) {
-      const int r = r_wg + ktid;
-      const bool seen = !(my_l == 0.f);  // (NaN: a row that holds one)
-      row_inv[r] = r < R && seen ? __fdividef(vref, my_l) : 0.f;
-      if (r < R && ok) {
-        const int t = (base + r) / group, hq = g.hkv * group + (base + r) % group;
-        const float lse_nat = seen ? (__log2f(my_l) - my_nm) * kLn2 : -INFINITY;
+    for (int h = 0; h < NW; h += 16) {
+      WarpScatterSum<16, 16>::run(lsum + h, lane);
+      if ((lane & 1) == 0) reinterpret_cast<float *>(my_red + h)[(lane / 2) * 4 + wq] = mine ? lsum[h] : 0.f;
+    }
+    if (!mine && ktid < NW) ref[ktid] = INFINITY;
+    // (after the barrier: the other parity's readers of vred may still be in their last tile)
+    tc_fence_before();
+    named_bar_sync(kBarSoft, kSoft);
+    tc_fence_after();
+    if (lane == 0 && wq == 0) vred[wg] = mine ? vref : 0.f;
+    named_bar_sync(kBarSoft, kSoft);
+    if (tid < NR) {
+      // row tid: O = (f0 O_even + f1 O_odd), in units of the row sum
+      const float4 e4 = red[tid], d4 = red[NR + tid];
+      const float l0 = (e4.x + e4.y) + (e4.z + e4.w), l1 = (d4.x + d4.y) + (d4.z + d4.w);
+      const float n0 = refs[tid], n1 = refs[NR + tid], nm = fminf(n0, n1);
+      const float a0 = n0 == INFINITY ? 0.f : ex2_approx(nm - n0), a1 = n1 == INFINITY ? 0.f : ex2_approx(nm - n1);
+      const float l = l0 * a0 + l1 * a1;
+      const bool seen = !(l == 0.f);  // (NaN: a row that holds one)
+      const float inv = tid < R && seen ? 1.f / l : 0.f;
+      const int rg = tid / NW;
+      alphas[tid] = inv * a0 * vred[rg];
+      alphas[NR + tid] = inv * a1 * vred[RG + rg];
+      if (tid < R && ok) {
+        const int t = (base + tid) / group, hq = g.hkv * group + (base + tid) % group;
+        const float lse_nat = seen ? (__log2f(l) - nm) * kLn2 : -INFINITY;
         if (n_parts == 1)
           p.lse[((size_t)g.b * p.Hq + hq) * p.T + t] = lse_nat;
         else
-          p.lse_part[slot * p.rows_pad + r] = lse_nat;
+          p.lse_part[slot * p.rows_pad + tid] = lse_nat;
       }
     }
     named_bar_sync(kBarSoft, kSoft);
-    constexpr int HR = 16;  // columns per TMEM load
+    constexpr int HR = NR / WG;            // rows that a warpgroup writes
+    const int e0 = wg * HR;
+    const bool has0 = lt0 + (jt0 & 1) < lt1, has1 = lt0 + ((jt0 & 1) ^ 1) < lt1;  // (TMEM of no tile holds anything)
+    float ov[HR];
+    {
+      float od[HR];
+      tmem_ld_f<HR>(tLane + e0, ov);
+      tmem_ld_f<HR>(tLane + NC + e0, od);
+#pragma unroll
+      for (int j = 0; j < HR; ++j)
+        ov[j] = (has0 ? ov[j] * alphas[e0 + j] : 0.f) + (has1 ? od[j] * alphas[NR + e0 + j] : 0.f);
+    }
     if (n_parts > 1) {
-      // fp32 part: thread d stores column d of every row (a warp writes 128 contiguous bytes of a row)
-      float *orow = p.o_part + (slot * p.rows_pad + r_wg) * D + ktid;
+      // fp32 part: thread d stores column d of the rows (a warp writes 128 contiguous bytes of a row)
+      float *orow = p.o_part + (slot * p.rows_pad + e0) * D + ktid;
+      if (ok && (D == 128 || ktid < D)) {
 #pragma unroll
-      for (int h = 0; h < NW / HR; ++h) {
-        float ov[HR];
-        tmem_ld_f<HR>(tO + r_wg + h * HR, ov);
-        if (ok && (D == 128 || ktid < D)) {
-#pragma unroll
-          for (int j = 0; j < HR; ++j) orow[(h * HR + j) * D] = ov[j] * row_inv[r_wg + h * HR + j];
-        }
+        for (int j = 0; j < HR; ++j) orow[j * D] = ov[j];
       }
       // publish the part (always, so the counters return to zero): the block barrier
       // orders every thread's stores before thread 0's release increment
@@ -783,15 +893,9 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     } else {
       // final bf16 rows, staged in the Q buffer: the group rows of one draft token are contiguous in out
       __nv_bfloat16 *stage_b = reinterpret_cast<__nv_bfloat16 *>(sQ);
+      if (D == 128 || ktid < D) {
 #pragma unroll
-      for (int h = 0; h < NW / HR; ++h) {
-        float ov[HR];
-        tmem_ld_f<HR>(tO + r_wg + h * HR, ov);
-        if (D == 128 || ktid < D) {
-#pragma unroll
-          for (int j = 0; j < HR; ++j)
-            stage_b[(r_wg + h * HR + j) * D + ktid] = __float2bfloat16_rn(ov[j] * row_inv[r_wg + h * HR + j]);
-        }
+        for (int j = 0; j < HR; ++j) stage_b[(e0 + j) * D + ktid] = __float2bfloat16_rn(ov[j]);
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -827,10 +931,10 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       const int r0 = mpart[k] * R / np, r1 = (mpart[k] + 1) * R / np;
       // (parts in flight as the registers allow)
       if (np <= 4)
-        merge_rows_warp<WG == 1 ? 8 : 16, 4, D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k], np, r0, r1, warp, 4 * WG, lane);
+        merge_rows_warp<16, 4, D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k], np, r0, r1, warp, 4 * WG, lane);
       else
-        merge_rows_warp<D == 128 ? 32 : 16, WG == 1 ? 20 : WG == 2 ? 12 : 6, D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k],
-                                                                              np, r0, r1, warp, 4 * WG, lane);
+        merge_rows_warp<D == 128 ? 32 : 16, WG == 2 ? 16 : 8, D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k], np, r0, r1,
+                                                               warp, 4 * WG, lane);
     }
     named_bar_sync(kBarSoft, kSoft);
     // leave: np arrivals and np departures wrap the counter back to zero
