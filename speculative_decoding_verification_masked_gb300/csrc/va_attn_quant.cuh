@@ -225,7 +225,6 @@ __device__ __forceinline__ void produce_raw(const AttnParams &p, const CUtensorM
   constexpr int TK = kTqKeys;
   const int lane = threadIdx.x & 31;
   const uint64_t policy = l2_evict_first_policy();
-  if (kTma && lane == 0) prefetch_tmap(tm);
   const bool paged = p.layout == VA_LAYOUT_PAGED;
   // the row of key k (gather)
   auto row_of = [&](const Seg &g, int k) -> const uint8_t * {
@@ -319,6 +318,75 @@ __device__ __forceinline__ void produce_raw(const AttnParams &p, const CUtensorM
   }
 }
 
+// merge_rows_warp in few instructions: a warp a row, a lane a part's weight and then D/32
+// columns, eight parts' loads in flight.  Straight code that runs once is fetched from
+// far away: the unrolled merge took 3 us of a split call, about what ten tiles take.
+template <int D>
+__device__ __forceinline__ void merge_rows_compact(const AttnParams &p, int b, int hkv, int row_base, int slot0, int np,
+                                                   int r0, int r1, int warp_id, int n_warps, int lane) {
+  constexpr int C = D / 32;
+  const int group = p.Hq / p.Hkv;
+#pragma unroll 1
+  for (int row = r0 + warp_id; row < r1; row += n_warps) {
+    const float *l = p.lse_part + (size_t)slot0 * p.rows_pad + row;
+    const float *o = p.o_part + ((size_t)slot0 * p.rows_pad + row) * D + lane * C;
+    float M = -INFINITY, L = 0.f, acc[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) acc[i] = 0.f;
+#pragma unroll 1
+    for (int q0 = 0; q0 < np; q0 += 32) {
+      const float ls = q0 + lane < np ? __ldcg(l + (size_t)(q0 + lane) * p.rows_pad) : -INFINITY;
+      float m = ls;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, x));
+      m = max_nan(m, M);
+      const float a = M == -INFINITY ? 0.f : __expf(M - m), w = ls == -INFINITY ? 0.f : __expf(ls - m);
+      float sum = w;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      if (m == -INFINITY) continue;  // no part so far saw a key
+      L = L * a + sum;
+#pragma unroll
+      for (int i = 0; i < C; ++i) acc[i] *= a;
+      const int n = min(32, np - q0);
+#pragma unroll 1
+      for (int j0 = 0; j0 < n; j0 += 8) {
+        float v[8][C];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float *src = o + (size_t)(q0 + min(j0 + j, n - 1)) * p.rows_pad * D;
+          if constexpr (C == 4) {
+            const float4 u = __ldcg(reinterpret_cast<const float4 *>(src));
+            v[j][0] = u.x;
+            v[j][1] = u.y;
+            v[j][2] = u.z;
+            v[j][3] = u.w;
+          } else {
+            const float2 u = __ldcg(reinterpret_cast<const float2 *>(src));
+            v[j][0] = u.x;
+            v[j][1] = u.y;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float wj = j0 + j < n ? __shfl_sync(0xffffffffu, w, j0 + j) : 0.f;
+#pragma unroll
+          for (int i = 0; i < C; ++i) acc[i] = fmaf(wj, v[j][i], acc[i]);
+        }
+      }
+      M = m;
+    }
+    const float inv = L != 0.f ? 1.f / L : 0.f;
+    const int t = (row_base + row) / group, hq = hkv * group + (row_base + row) % group;
+    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (((size_t)b * p.T + t) * p.Hq + hq) * D + lane * C;
+    if constexpr (C == 4)
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+    else
+      *reinterpret_cast<uint32_t *>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
+    if (lane == 0) p.lse[((size_t)b * p.Hq + hq) * p.T + t] = L != 0.f ? M + __logf(L) : -INFINITY;
+  }
+}
+
 template <int FMT, int D, int NR, bool kTma>
 __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     verify_attn_quant_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
@@ -352,7 +420,12 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
   const uint32_t smem_a = smem_u32(smem), bar_a = smem_a + SM::kBarOff;
   const uint32_t a_full = bar_a, a_empty = bar_a + 16 * kTqStages, a_k_full = a_empty + 16 * kTqStages, a_v_full = a_k_full + 32,
                  a_s_full = a_v_full + 16, a_p_full = a_s_full + 16, a_o_done = a_p_full + 16;
+  if (kTma && tid == 32) {
+    prefetch_tmap(&tmk);
+    prefetch_tmap(&tmv);
+  }
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < 2 * kTqStages; ++i) {
       mbar_init(full + i, kTma ? 1 : 32);
       mbar_init(empty + i, 4);
@@ -564,6 +637,8 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
   // 16-byte chunk cw of the thread's P^T row (8 rows of Q): (a_p ^ 16 cw)
   const uint32_t a_p = (smem_a + SM::kPOff + par * (TK * 128) + ktid * 128 + ((ktid & 7) << 4)) ^ (r_wg / 8 << 4);
   const int group = p.Hq / p.Hkv;
+  const float inv_group = 1.f / (float)group;
+  auto token_of = [&](int r) { return __float2int_rd(((float)r + 0.5f) * inv_group); };  // r / group (r <= 4096)
   int jt = 0;
   // split segments this CTA holds a part of (at most its first and its last)
   int n_split = 0, ms[2] = {0, 0}, mslot[2] = {0, 0}, mnp[2] = {0, 0}, mpart[2] = {0, 0};
@@ -594,7 +669,7 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
         const int e = tid + u * kSoft, row = e / kCh;
         v[u] = make_uint4(0, 0, 0, 0);
         if (row < R) {
-          const int t = (base + row) / group, hq = g.hkv * group + (base + row) % group;
+          const int t = token_of(base + row), hq = g.hkv * group + (base + row) - t * group;
           v[u] = __ldg(reinterpret_cast<const uint4 *>(qb + (((size_t)g.b * p.T + t) * p.Hq + hq) * D) + (e % kCh));
         }
       }
@@ -672,7 +747,8 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       const uint32_t km = (uint32_t)(km_all >> r_wg);  // (this thread's rows in the low bits)
       wait_ok(a_k_full + 8 * (jt & 3), (uint32_t)(jt >> 2) & 1u);
       const float2 sc = lds64f(a_scale + (jt & 3) * 1024);
-      const float vsc = sc.y, cs = sc.x * q_unit;
+      // (a value row that is NaN makes the scores of its key NaN)
+      const float vsc = sc.y, cs = fmaf(sc.x, q_unit, vsc - vsc);
       wait_ok(a_s_full + 8 * par, (uint32_t)(jt >> 1) & 1u);
       __syncwarp();
       tc_fence_after();
@@ -778,8 +854,9 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       // PV of tile jt - 2: its P buffer is free (and the barrier stays within a phase of its waiters)
       if (jt >= 2) wait_ok(a_o_done + 8 * par, (uint32_t)((jt - 2) >> 1) & 1u);
       // P^T row of this key: chunk cc holds rows 8cc .. 8cc + 7
-      const float ratio = vsc * rvref;  // a power of two, at most 1 (of a key that somebody sees)
-      const __half2 ratio2 = __float2half2_rn(ratio);
+      // a power of two, at most 1 where somebody sees the key (elsewhere it may be anything and
+      // P is 0: the product has to be)
+      const __half2 ratio2 = __float2half2_rn(__saturatef(vsc * rvref));
 #pragma unroll
       for (int h0 = 0; h0 < NW; h0 += kXRows) {
         if (kXRows != NW) load_scores(h0);
@@ -793,12 +870,7 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
             const float2 s2 = add2(make_float2(lsum[r], lsum[r + 1]), make_float2(a, e));
             lsum[r] = s2.x;
             lsum[r + 1] = s2.y;
-            __half2 pr = __hmul2(__floats2half2_rn(a, e), ratio2);
-            if (__builtin_expect(masked, 0)) {  // (the scale of a key that a row does not see may be anything)
-              if (!((km >> r) & 1u)) pr.x = __ushort_as_half(0);
-              if (!((km >> (r + 1)) & 1u)) pr.y = __ushort_as_half(0);
-            }
-            h[q] = half2_bits(pr);
+            h[q] = half2_bits(__hmul2(__floats2half2_rn(a, e), ratio2));
           }
           sts128(a_p ^ ((h0 / 8 + cw) << 4), h[0], h[1], h[2], h[3]);
         }
@@ -849,7 +921,7 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       alphas[tid] = inv * a0 * vred[rg];
       alphas[NR + tid] = inv * a1 * vred[RG + rg];
       if (tid < R && ok) {
-        const int t = (base + tid) / group, hq = g.hkv * group + (base + tid) % group;
+        const int t = token_of(base + tid), hq = g.hkv * group + (base + tid) - t * group;
         const float lse_nat = seen ? (__log2f(l) - nm) * kLn2 : -INFINITY;
         if (n_parts == 1)
           p.lse[((size_t)g.b * p.Hq + hq) * p.T + t] = lse_nat;
@@ -929,12 +1001,7 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     if (*merge_ok) {
       const int seg = s / p.NRB, base = s % p.NRB * NR, R = min(NR, p.R - base);
       const int r0 = mpart[k] * R / np, r1 = (mpart[k] + 1) * R / np;
-      // (parts in flight as the registers allow)
-      if (np <= 4)
-        merge_rows_warp<16, 4, D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k], np, r0, r1, warp, 4 * WG, lane);
-      else
-        merge_rows_warp<D == 128 ? 32 : 16, WG == 2 ? 16 : 8, D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k], np, r0, r1,
-                                                               warp, 4 * WG, lane);
+      merge_rows_compact<D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k], np, r0, r1, warp, 4 * WG, lane);
     }
     named_bar_sync(kBarSoft, kSoft);
     // leave: np arrivals and np departures wrap the counter back to zero
