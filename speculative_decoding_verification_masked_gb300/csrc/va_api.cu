@@ -132,7 +132,7 @@ bool encode_rows_map(CUtensorMap *m, const void *base, int row_bytes, int Hkv, l
   const cuuint32_t estr[3] = {1, 1, 1};
   auto encode = [&] {
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
   if (encode() == CUDA_SUCCESS) return true;
@@ -451,7 +451,7 @@ va_status run_attention_quant(const Common &c, va_kv_format format, int layout, 
   memset(&p, 0, sizeof p);
   fill_attn(p, c, layout, k, v, len_cap, num_pages, page_size, page_table, max_pages);
   p.R = (s.Hq / s.Hkv) * s.T;
-  p.rows_pad = va::quant_block_rows(p.R);
+  p.rows_pad = va::quant_block_rows(p.R, format, s.D);
   p.RG = 4;
   p.NRB = (p.R + p.rows_pad - 1) / p.rows_pad;
   p.cps = 1;

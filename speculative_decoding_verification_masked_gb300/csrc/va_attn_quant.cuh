@@ -66,9 +66,10 @@ constexpr float kTqMove = 8.f;  // a score this far above the reference moves it
 
 template <int NR>
 struct TqCfg {
-  static constexpr int kRowGroups = NR > 32 ? NR / 32 : 1;  // of NW rows, a warpgroup each for even and odd tiles
+  static constexpr int kRowGroups = NR > 32 ? NR / 32 : 1;  // of NW rows, each with
+  static constexpr int kParities = NR > 32 ? 1 : 2;         // one warpgroup, or one for even and one for odd tiles
   static constexpr int NW = NR / kRowGroups;                // rows of a softmax thread
-  static constexpr int kGroups = 2 * kRowGroups;            // softmax warpgroups
+  static constexpr int kGroups = kParities * kRowGroups;    // softmax warpgroups
   static constexpr int kSoft = 128 * kGroups;
   // (the last warpgroup: two producers and two issuers, of S and of PV)
   static constexpr int kKWarp = 4 * kGroups, kVWarp = kKWarp + 4, kProducer = kVWarp + 4, kMmaWarp = kProducer + 2;
@@ -153,23 +154,24 @@ struct TqSmem {
   static constexpr int kVBytes = (D / 64) * kTqKeys * 128; // V tile in halves
   // (d 64: the PV MMA keeps M = 128; its lanes 64 .. 127 multiply the 16 KB that follow
   // the tile, inside the plan, and nobody reads them)
-  static constexpr int kPOff = 2 * kVBytes;                // P^T: per key a 128-byte row
-  static constexpr int kQOff = kPOff + 2 * kTqKeys * 128;
+  static constexpr int kPOff = 2 * kVBytes;                // P^T: per key a 128-byte row, for 64 rows of Q each
+  static constexpr int kPBytes = (NR > 64 ? 2 : 1) * kTqKeys * 128;
+  static constexpr int kQOff = kPOff + 2 * kPBytes;
   static constexpr int kQBytes = (D / 64) * NR * 128;
   static constexpr int kBarOff = kQOff + kQBytes;
   static constexpr int kNumBars = 4 * kTqStages + 4 + 2 + 2 + 2 + 2 + 2;
   static constexpr int kMiscOff = (kBarOff + kNumBars * 8 + 15) & ~15;  // tmem base, abort flag, merge flag
   static constexpr int kRowMaskOff = kMiscOff + 16;      // u64 [64]: draft visibility rows
-  static constexpr int kKeyMaskOff = kRowMaskOff + 512;  // u64 [64]: per draft key, rows that see it
-  static constexpr int kRedOff = kKeyMaskOff + 512;      // float4 [2 NR]: per-warp row maxima and sums of each tile parity
+  static constexpr int kKeyMaskOff = kRowMaskOff + 512;  // u32 [4][64]: per 32 rows and draft key, the rows that see it
+  static constexpr int kRedOff = kKeyMaskOff + 1024;     // float4 [2 NR]: per-warp row maxima and sums of each tile parity
   static constexpr int kVRedOff = kRedOff + 2 * NR * 16; // float [16]: per-warp largest value scales, Q maxima
   static constexpr int kRefOff = kVRedOff + 64;          // float [2 NR]: bias less the reference of a row
   static constexpr int kAlphaOff = kRefOff + 2 * NR * 4; // float [2 NR]: what a moved reference scales by; then 1 / l factors
   static constexpr int kKsOff = kAlphaOff + 2 * NR * 4;  // float2 [4][128]: scales of the tile's K and V rows
   static constexpr int kRingOff = (kKsOff + 4 * 1024 + 127) & ~127;
   static constexpr int kNC = NR < 32 ? 32 : NR;          // TMEM columns per region
-  // O of even and odd tiles at 0 and NC, S at 2NC and 3NC, K at 4NC and 4NC + D/2
-  static constexpr int kKCol = 4 * kNC;
+  // O (of even and of odd tiles), two S, two K of D/2 columns
+  static constexpr int kSCol = TqCfg<NR>::kParities * kNC, kKCol = kSCol + 2 * kNC;
   static constexpr int kTmemCols = kKCol + D <= 256 ? 256 : 512;
   static_assert(kKCol + D <= 512, "TMEM plan");
   static_assert(kQOff % 1024 == 0 && kPOff % 1024 == 0 && kQBytes % 1024 == 0, "swizzle atoms");
@@ -393,9 +395,9 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
                              const __grid_constant__ CUtensorMap tmv) {
   using SM = TqSmem<FMT, D, NR>;
   using Cfg = TqCfg<NR>;
-  constexpr int TK = kTqKeys, NC = SM::kNC, WG = Cfg::kGroups, RG = Cfg::kRowGroups, NW = Cfg::NW, kSoft = Cfg::kSoft,
+  constexpr int TK = kTqKeys, NC = SM::kNC, WG = Cfg::kGroups, RG = Cfg::kRowGroups, PAR = Cfg::kParities, NW = Cfg::NW, kSoft = Cfg::kSoft,
                 RB = SM::kRow;
-  constexpr int kXRows = NR > 32 ? 16 : NW;  // scores a softmax thread holds at once (registers)
+  constexpr int kXRows = WG > 2 ? 16 : NW;  // scores a softmax thread holds at once (registers)
   constexpr int kChunks = QRow<FMT, D>::kCodeBytes / 16, kRegs = CodeChunk<FMT>::kRegs;
   constexpr int kBarQ = 1, kBarSoft = 3, kBarEnd = 4, kBarRed0 = 5;  // kBarRed0 + softmax warpgroup
   constexpr int kEndThreads = kSoft + 256 + 64;                      // all but the producers
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::kMiscOff);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::kMiscOff + 4);
   uint64_t *rowmask = reinterpret_cast<uint64_t *>(smem + SM::kRowMaskOff);
-  uint64_t *keymask = reinterpret_cast<uint64_t *>(smem + SM::kKeyMaskOff);
+  uint32_t *keymask = reinterpret_cast<uint32_t *>(smem + SM::kKeyMaskOff);
   float4 *red = reinterpret_cast<float4 *>(smem + SM::kRedOff);
   float *vred = reinterpret_cast<float *>(smem + SM::kVRedOff);
   float *refs = reinterpret_cast<float *>(smem + SM::kRefOff), *alphas = reinterpret_cast<float *>(smem + SM::kAlphaOff);
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
           wait_ok(a_k_full + 8 * (jt & 3), (jt >> 2) & 1u);
           __syncwarp();
           tc_fence_after();
-          const uint32_t tS = tmem + (2 + b) * NC, tK = tmem + SM::kKCol + b * (D / 2);
+          const uint32_t tS = tmem + SM::kSCol + b * NC, tK = tmem + SM::kKCol + b * (D / 2);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t qoff = (uint64_t)(((kk >> 2) * (NR * 128) + (kk & 3) * 32) >> 4);
@@ -521,11 +523,11 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
           wait_ok(a_p_full + 8 * b, (jt >> 1) & 1u);
           __syncwarp();
           tc_fence_after();
-          const uint64_t dV = dV0 + (uint64_t)(b * (SM::kVBytes >> 4)), dP = dP0 + (uint64_t)(b * (TK * 128 >> 4));
+          const uint64_t dV = dV0 + (uint64_t)(b * (SM::kVBytes >> 4)), dP = dP0 + (uint64_t)(b * (SM::kPBytes >> 4));
 #pragma unroll
           for (int kk = 0; kk < TK / 16; ++kk) {
             const uint64_t off = (uint64_t)((kk * 2048) >> 4);
-            umma_ss_warp(tmem + b * NC, dV + off, dP + off, id_o, kk > 0 || i > 1 ? 1u : 0u);
+            umma_ss_warp(tmem + (PAR == 2 ? b * NC : 0), dV + off, dP + off, id_o, kk > 0 || i >= PAR ? 1u : 0u);
           }
           umma_commit_warp(o_done + b);
           __syncwarp();
@@ -625,17 +627,17 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
   // ================================== softmax ==================================
   regs_inc<Cfg::kRegsSoft>();
   const uint32_t tmem = tmem_base();
-  const int wg = warp >> 2, par = wg / RG;   // warpgroup; the tiles it takes: jt % 2 == par
-  const int r_wg = (wg % RG) * NW;           // its rows [r_wg, r_wg + NW) of the block
-  const int wq = warp & 3, ktid = tid & 127; // warp of the warpgroup; key of the tile, output column of the epilogue
+  const int wg = warp >> 2, par = PAR == 2 ? wg : 0;  // warpgroup; with two parities the tiles it takes: jt % 2 == par
+  const int rg = PAR == 2 ? 0 : wg, r_wg = rg * NW;   // its rows [r_wg, r_wg + NW) of the block
+  const int wq = warp & 3, ktid = tid & 127;          // warp of the warpgroup; key of the tile, output column of the epilogue
   const int kBarRed = kBarRed0 + wg;
   const uint32_t tLane = tmem + ((uint32_t)(wq * 32) << 16);
-  const uint32_t tO = tLane + par * NC + r_wg, tS = tLane + (2 + par) * NC + r_wg;
-  float4 *my_red = red + par * NR + r_wg;    // [NW]
+  const uint32_t tO = tLane + par * NC + r_wg;
+  float4 *my_red = red + par * NR + r_wg;             // [NW]
   float *ref = refs + par * NR + r_wg, *alpha = alphas + par * NR + r_wg;
   const uint32_t a_ref = smem_u32(ref), a_scale = smem_a + SM::kKsOff + ktid * 8;
-  // 16-byte chunk cw of the thread's P^T row (8 rows of Q): (a_p ^ 16 cw)
-  const uint32_t a_p = (smem_a + SM::kPOff + par * (TK * 128) + ktid * 128 + ((ktid & 7) << 4)) ^ (r_wg / 8 << 4);
+  // 16-byte chunk cw of the thread's P^T row (8 rows of Q): (a_p0 ^ 16 cw)
+  const uint32_t a_p0 = (smem_a + SM::kPOff + (r_wg / 64) * (TK * 128) + ktid * 128 + ((ktid & 7) << 4)) ^ ((r_wg / 8 & 7) << 4);
   const int group = p.Hq / p.Hkv;
   const float inv_group = 1.f / (float)group;
   auto token_of = [&](int r) { return __float2int_rd(((float)r + 0.5f) * inv_group); };  // r / group (r <= 4096)
@@ -651,10 +653,10 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     if (lt0 == 0 && tid == 0) p.meta[s] = make_int2(s + first_cta, n_parts);
     const int jt0 = jt;
     const int base = g.rb * NR, R = min(NR, p.R - base);  // the packed rows [base, base + R) of the kv-head
-    // bit r: this segment's row r is one of draft token t
-    auto token_rows = [&](int t) -> uint64_t {
-      const int lo = max(t * group - base, 0), hi = min((t + 1) * group - base, 64);
-      return hi <= lo ? 0ull : (hi - lo >= 64 ? ~0ull : (1ull << (hi - lo)) - 1) << lo;
+    // bit r: row 32 w + r of this segment is one of draft token t
+    auto token_rows = [&](int t, int w) -> uint32_t {
+      const int lo = min(max(t * group - base - 32 * w, 0), 32), hi = min(max((t + 1) * group - base - 32 * w, 0), 32);
+      return (hi == 32 ? ~0u : (1u << hi) - 1u) & (lo == 32 ? 0u : ~0u << lo);
     };
 
     // ---- Q of this segment: halves, scaled by a power of two, [D/64][NR rows][128 B], 128B swizzle ----
@@ -718,11 +720,16 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
         if (lane + 32 < p.T) rowmask[lane + 32] = hi;
       }
       named_bar_sync(kBarSoft, kSoft);
-      if (tid < p.T) {
-        uint64_t km = 0;
-        for (int t = 0; t < p.T; ++t)
-          if ((rowmask[t] >> tid) & 1ull) km |= token_rows(t);
-        keymask[tid] = km;
+      for (int e = tid; e < 64 * (NR > 32 ? NR / 32 : 1); e += kSoft) {
+        const int key = e & 63, w = e >> 6;
+        uint32_t km = 0;
+        if (key < p.T) {
+#pragma unroll 1
+          for (int t = 0; t < p.T; ++t)
+            if ((rowmask[t] >> key) & 1ull) km |= token_rows(t, w);
+        }
+        const int left = R - 32 * w;  // rows past the block's see nothing
+        keymask[e] = left >= 32 ? km : left <= 0 ? 0u : km & ((1u << left) - 1u);
       }
       named_bar_sync(kBarSoft, kSoft);
     }
@@ -733,23 +740,33 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
 #pragma unroll
     for (int r = 0; r < NW; ++r) lsum[r] = 0.f;
     float vref = 0.f, rvref = 0.f;  // largest value scale seen (0: no tile yet), and one over it
-    const int lt_first = lt0 + ((jt ^ par) & 1);
-    jt += (jt ^ par) & 1;
+    const int skip = PAR == 2 ? (jt ^ par) & 1 : 0, lt_first = lt0 + skip;
+    jt += skip;
 
-    for (int lt = lt_first; lt < lt1; lt += 2, jt += 2) {
+    for (int lt = lt_first; lt < lt1; lt += PAR, jt += PAR) {
       const bool masked = lt * TK + TK > g.n_prefix;
-      uint64_t km_all = ~0ull;  // rows that see this key
+      const uint32_t b = PAR == 2 ? (uint32_t)par : (uint32_t)jt & 1u;  // buffer of the tile
+      const uint32_t tS = tLane + SM::kSCol + b * NC + r_wg;
+      uint32_t km = ~0u;   // the thread's rows that see this key
+      bool any = true;     // some row of the block does
       if (__builtin_expect(masked, 0)) {
-        const int key = lt * TK + ktid;
-        km_all = key >= g.nkeys ? 0ull : key >= g.n_prefix ? keymask[key - g.n_prefix] : ~0ull;
-        if (R < 64) km_all &= (1ull << R) - 1ull;
+        const int key = lt * TK + ktid, d = key - g.n_prefix;
+        if (key >= g.nkeys) {
+          km = 0u;
+          any = false;
+        } else if (d >= 0) {
+          km = keymask[64 * rg + d];
+          uint32_t all = 0;
+#pragma unroll
+          for (int w = 0; w < (NR > 32 ? NR / 32 : 1); ++w) all |= keymask[64 * w + d];
+          any = all != 0u;
+        }
       }
-      const uint32_t km = (uint32_t)(km_all >> r_wg);  // (this thread's rows in the low bits)
       wait_ok(a_k_full + 8 * (jt & 3), (uint32_t)(jt >> 2) & 1u);
       const float2 sc = lds64f(a_scale + (jt & 3) * 1024);
       // (a value row that is NaN makes the scores of its key NaN)
       const float vsc = sc.y, cs = fmaf(sc.x, q_unit, vsc - vsc);
-      wait_ok(a_s_full + 8 * par, (uint32_t)(jt >> 1) & 1u);
+      wait_ok(a_s_full + 8 * b, (uint32_t)(jt >> 1) & 1u);
       __syncwarp();
       tc_fence_after();
       float x[kXRows];
@@ -797,7 +814,7 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
               if (((km >> (h + r)) & 1u) && ref[h + r] == INFINITY) dmax = INFINITY;
           }
         }
-        move = bar_red_or(kBarRed, 128, dmax > kTqBias + kTqMove || (vsc > vref && km_all != 0ull));
+        move = bar_red_or(kBarRed, 128, dmax > kTqBias + kTqMove || (vsc > vref && any));
       }
       if (__builtin_expect(move, 0)) {
         // the references to the row maxima seen so far, and the value scale to the largest
@@ -815,7 +832,7 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
             reinterpret_cast<float *>(my_red + h)[(lane / (32 / kXRows)) * 4 + wq] = x[0];
         }
         {  // (NaN and the scales of keys that nobody sees stay out)
-          const uint32_t wm = __reduce_max_sync(0xffffffffu, km_all != 0ull && vsc == vsc ? __float_as_uint(vsc) : 0u);
+          const uint32_t wm = __reduce_max_sync(0xffffffffu, any && vsc == vsc ? __float_as_uint(vsc) : 0u);
           if (lane == 0) vred[warp] = __uint_as_float(wm);
         }
         named_bar_sync(kBarRed, 128);
@@ -837,7 +854,11 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
         if (!first) {
 #pragma unroll
           for (int r = 0; r < NW; ++r) lsum[r] *= alpha[r];
-          wait_ok(a_o_done + 8 * par, (uint32_t)((jt - 2) >> 1) & 1u);  // O holds every PV of this parity
+          // O holds every PV up to the previous tile (of this parity)
+          if (PAR == 2)
+            wait_ok(a_o_done + 8 * b, (uint32_t)((jt - 2) >> 1) & 1u);
+          else
+            wait_ok(a_o_done + 8 * (b ^ 1u), (uint32_t)((jt - 1) >> 1) & 1u);
           __syncwarp();
           tc_fence_after();
 #pragma unroll
@@ -852,7 +873,8 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
         if (kXRows == NW) load_scores(0);
       }
       // PV of tile jt - 2: its P buffer is free (and the barrier stays within a phase of its waiters)
-      if (jt >= 2) wait_ok(a_o_done + 8 * par, (uint32_t)((jt - 2) >> 1) & 1u);
+      if (jt >= 2) wait_ok(a_o_done + 8 * b, (uint32_t)((jt - 2) >> 1) & 1u);
+      const uint32_t a_p = a_p0 + b * SM::kPBytes;
       // P^T row of this key: chunk cc holds rows 8cc .. 8cc + 7
       // a power of two, at most 1 where somebody sees the key (elsewhere it may be anything and
       // P is 0: the product has to be)
@@ -875,23 +897,27 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
           sts128(a_p ^ ((h0 / 8 + cw) << 4), h[0], h[1], h[2], h[3]);
         }
       }
-      if (__builtin_expect(masked && km_all == 0ull, 0)) {
+      if (__builtin_expect(!any, 0)) {
         // a key that no row sees: zero V, so that 0 * V stays 0 whatever it held
-        wait_ok(a_v_full + 8 * par, (uint32_t)(jt >> 1) & 1u);
+        wait_ok(a_v_full + 8 * b, (uint32_t)(jt >> 1) & 1u);
 #pragma unroll
         for (int c0 = 0; c0 < D / 8 / RG; ++c0)
-          *reinterpret_cast<uint4 *>(sV + par * SM::kVBytes + swz<TK>(ktid, (wg % RG) * (D / 8 / RG) + c0)) =
-              make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(sV + b * SM::kVBytes + swz<TK>(ktid, rg * (D / 8 / RG) + c0)) = make_uint4(0, 0, 0, 0);
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive_at(a_p_full + 8 * par);
+      mbar_arrive_at(a_p_full + 8 * b);
     }
     // ---- epilogue: the two parities' O and l of every row of this part joined ----
     // (a warpgroup waits for the PVs of its own tiles, whose phases it has followed, and
     // meets the others at the barrier below)
     const bool mine = lt_first < lt1;  // this parity had a tile
-    if (mine) wait_ok(a_o_done + 8 * par, (uint32_t)((jt - 2) >> 1) & 1u);
+    if (PAR == 2) {
+      if (mine) wait_ok(a_o_done + 8 * par, (uint32_t)((jt - 2) >> 1) & 1u);
+    } else {  // (the barrier of the tile before the last has been followed up to two tiles ago)
+      if (jt >= 2) wait_ok(a_o_done + 8 * (jt & 1), (uint32_t)((jt - 2) >> 1) & 1u);
+      wait_ok(a_o_done + 8 * ((jt - 1) & 1), (uint32_t)((jt - 1) >> 1) & 1u);
+    }
     __syncwarp();
     tc_fence_after();
     jt = jt0 + (lt1 - lt0);
@@ -909,17 +935,21 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     if (lane == 0 && wq == 0) vred[wg] = mine ? vref : 0.f;
     named_bar_sync(kBarSoft, kSoft);
     if (tid < NR) {
-      // row tid: O = (f0 O_even + f1 O_odd), in units of the row sum
-      const float4 e4 = red[tid], d4 = red[NR + tid];
-      const float l0 = (e4.x + e4.y) + (e4.z + e4.w), l1 = (d4.x + d4.y) + (d4.z + d4.w);
-      const float n0 = refs[tid], n1 = refs[NR + tid], nm = fminf(n0, n1);
-      const float a0 = n0 == INFINITY ? 0.f : ex2_approx(nm - n0), a1 = n1 == INFINITY ? 0.f : ex2_approx(nm - n1);
-      const float l = l0 * a0 + l1 * a1;
+      // row tid: O = f0 O_even + f1 O_odd, in units of the row sum
+      const float4 e4 = red[tid];
+      float l = (e4.x + e4.y) + (e4.z + e4.w), nm = refs[tid], f0 = 1.f, f1 = 0.f;
+      if constexpr (PAR == 2) {
+        const float4 d4 = red[NR + tid];
+        const float l1 = (d4.x + d4.y) + (d4.z + d4.w), n0 = nm, n1 = refs[NR + tid];
+        nm = fminf(n0, n1);
+        f0 = n0 == INFINITY ? 0.f : ex2_approx(nm - n0);
+        f1 = n1 == INFINITY ? 0.f : ex2_approx(nm - n1);
+        l = l * f0 + l1 * f1;
+      }
       const bool seen = !(l == 0.f);  // (NaN: a row that holds one)
       const float inv = tid < R && seen ? 1.f / l : 0.f;
-      const int rg = tid / NW;
-      alphas[tid] = inv * a0 * vred[rg];
-      alphas[NR + tid] = inv * a1 * vred[RG + rg];
+      alphas[tid] = inv * f0 * vred[PAR == 2 ? 0 : tid / NW];
+      if constexpr (PAR == 2) alphas[NR + tid] = inv * f1 * vred[1];
       if (tid < R && ok) {
         const int t = token_of(base + tid), hq = g.hkv * group + (base + tid) - t * group;
         const float lse_nat = seen ? (__log2f(l) - nm) * kLn2 : -INFINITY;
@@ -932,15 +962,18 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     named_bar_sync(kBarSoft, kSoft);
     constexpr int HR = NR / WG;            // rows that a warpgroup writes
     const int e0 = wg * HR;
-    const bool has0 = lt0 + (jt0 & 1) < lt1, has1 = lt0 + ((jt0 & 1) ^ 1) < lt1;  // (TMEM of no tile holds anything)
     float ov[HR];
-    {
+    tmem_ld_f<HR>(tLane + e0, ov);
+    if constexpr (PAR == 2) {
+      const bool has0 = lt0 + (jt0 & 1) < lt1, has1 = lt0 + ((jt0 & 1) ^ 1) < lt1;  // (TMEM of no tile holds anything)
       float od[HR];
-      tmem_ld_f<HR>(tLane + e0, ov);
       tmem_ld_f<HR>(tLane + NC + e0, od);
 #pragma unroll
       for (int j = 0; j < HR; ++j)
         ov[j] = (has0 ? ov[j] * alphas[e0 + j] : 0.f) + (has1 ? od[j] * alphas[NR + e0 + j] : 0.f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < HR; ++j) ov[j] *= alphas[e0 + j];
     }
     if (n_parts > 1) {
       // fp32 part: thread d stores column d of the rows (a warp writes 128 contiguous bytes of a row)
@@ -1046,16 +1079,27 @@ static cudaError_t launch_tq_t(AttnParams &p, const CUtensorMap &tmk, const CUte
   return cudaLaunchKernelEx(&cfg, kern, p, tmk, tmv);
 }
 
+template <int FMT, int D, bool kTma>
+static cudaError_t launch_tq_blocks(AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
+                                    cudaStream_t stream) {
+  if constexpr (quant_block_rows(128, FMT, D) == 128)
+    return launch_tq_t<FMT, D, 128, kTma>(p, tmk, tmv, grid, stream);
+  else
+    return cudaErrorInvalidValue;
+}
+
 template <int FMT, int D>
 static cudaError_t launch_tq(AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
                              cudaStream_t stream) {
   if (p.tma_box > 0)
     return p.rows_pad == 16   ? launch_tq_t<FMT, D, 16, true>(p, tmk, tmv, grid, stream)
            : p.rows_pad == 32 ? launch_tq_t<FMT, D, 32, true>(p, tmk, tmv, grid, stream)
-                              : launch_tq_t<FMT, D, 64, true>(p, tmk, tmv, grid, stream);
+           : p.rows_pad == 64 ? launch_tq_t<FMT, D, 64, true>(p, tmk, tmv, grid, stream)
+                              : launch_tq_blocks<FMT, D, true>(p, tmk, tmv, grid, stream);
   return p.rows_pad == 16   ? launch_tq_t<FMT, D, 16, false>(p, tmk, tmv, grid, stream)
          : p.rows_pad == 32 ? launch_tq_t<FMT, D, 32, false>(p, tmk, tmv, grid, stream)
-                            : launch_tq_t<FMT, D, 64, false>(p, tmk, tmv, grid, stream);
+         : p.rows_pad == 64 ? launch_tq_t<FMT, D, 64, false>(p, tmk, tmv, grid, stream)
+                            : launch_tq_blocks<FMT, D, false>(p, tmk, tmv, grid, stream);
 }
 
 }  // namespace va
