@@ -320,66 +320,89 @@ __device__ __forceinline__ void produce_raw(const AttnParams &p, const CUtensorM
   }
 }
 
-// merge_rows_warp in few instructions: a warp a row, a lane a part's weight and then D/32
-// columns, eight parts' loads in flight.  Straight code that runs once is fetched from
-// far away: the unrolled merge took 3 us of a split call, about what ten tiles take.
+// Merge of rows [r0, r1) of a split segment (as merge_rows_warp) in few instructions, by
+// groups of `wpr` warps to a row, each with every wpr-th part: a lane holds the weight of a
+// part, then D/32 columns.  Straight code that runs once is fetched from far away: the
+// unrolled merge took 3 us of a split call, about what four tiles take.  `part` is shared
+// memory for n_warps x D floats; every softmax thread calls it (barrier `bar`).
 template <int D>
 __device__ __forceinline__ void merge_rows_compact(const AttnParams &p, int b, int hkv, int row_base, int slot0, int np,
-                                                   int r0, int r1, int warp_id, int n_warps, int lane) {
+                                                   int r0, int r1, int warp_id, int n_warps, int lane, float *part,
+                                                   int bar) {
   constexpr int C = D / 32;
-  const int group = p.Hq / p.Hkv;
+  const int group = p.Hq / p.Hkv, n = r1 - r0;
+  const int wpr = n > 0 ? max(1, n_warps / n) : 1;  // warps to a row
+  const int step = n_warps / wpr;                   // rows at once
+  const int sub = warp_id % wpr;
 #pragma unroll 1
-  for (int row = r0 + warp_id; row < r1; row += n_warps) {
-    const float *l = p.lse_part + (size_t)slot0 * p.rows_pad + row;
-    const float *o = p.o_part + ((size_t)slot0 * p.rows_pad + row) * D + lane * C;
-    float M = -INFINITY, L = 0.f, acc[C];
+  for (int i0 = 0; i0 < n; i0 += step) {
+    const int row = r0 + i0 + warp_id / wpr;
+    const bool act = warp_id / wpr < step && row < r1;
+    float L = 0.f, M = -INFINITY, acc[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) acc[i] = 0.f;
+    if (act) {
+      const float *l = p.lse_part + (size_t)slot0 * p.rows_pad + row;
+      const float *o = p.o_part + ((size_t)slot0 * p.rows_pad + row) * D + lane * C;
 #pragma unroll 1
-    for (int q0 = 0; q0 < np; q0 += 32) {
-      const float ls = q0 + lane < np ? __ldcg(l + (size_t)(q0 + lane) * p.rows_pad) : -INFINITY;
-      float m = ls;
+      for (int q0 = 0; q0 < np; q0 += 32) {
+        const float ls = q0 + lane < np ? __ldcg(l + (size_t)(q0 + lane) * p.rows_pad) : -INFINITY;
+        float m = ls;
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, x));
-      m = max_nan(m, M);
-      const float a = M == -INFINITY ? 0.f : __expf(M - m), w = ls == -INFINITY ? 0.f : __expf(ls - m);
-      float sum = w;
+        for (int x = 16; x > 0; x >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, x));
+        m = max_nan(m, M);
+        if (m == -INFINITY) continue;  // no part so far saw a key
+        const float a = M == -INFINITY ? 0.f : __expf(M - m), w = ls == -INFINITY ? 0.f : __expf(ls - m);
+        float sum = w;
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-      if (m == -INFINITY) continue;  // no part so far saw a key
-      L = L * a + sum;
+        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        L = L * a + sum;
 #pragma unroll
-      for (int i = 0; i < C; ++i) acc[i] *= a;
-      const int n = min(32, np - q0);
+        for (int i = 0; i < C; ++i) acc[i] *= a;
+        const int cnt = min(32, np - q0);
 #pragma unroll 1
-      for (int j0 = 0; j0 < n; j0 += 8) {
-        float v[8][C];
+        for (int j0 = sub; j0 < cnt; j0 += 8 * wpr) {
+          float v[8][C];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float *src = o + (size_t)(q0 + min(j0 + j, n - 1)) * p.rows_pad * D;
-          if constexpr (C == 4) {
-            const float4 u = __ldcg(reinterpret_cast<const float4 *>(src));
-            v[j][0] = u.x;
-            v[j][1] = u.y;
-            v[j][2] = u.z;
-            v[j][3] = u.w;
-          } else {
-            const float2 u = __ldcg(reinterpret_cast<const float2 *>(src));
-            v[j][0] = u.x;
-            v[j][1] = u.y;
+          for (int j = 0; j < 8; ++j) {
+            const float *src = o + (size_t)(q0 + min(j0 + j * wpr, cnt - 1)) * p.rows_pad * D;
+            if constexpr (C == 4) {
+              const float4 u = __ldcg(reinterpret_cast<const float4 *>(src));
+              v[j][0] = u.x;
+              v[j][1] = u.y;
+              v[j][2] = u.z;
+              v[j][3] = u.w;
+            } else {
+              const float2 u = __ldcg(reinterpret_cast<const float2 *>(src));
+              v[j][0] = u.x;
+              v[j][1] = u.y;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float wj = __shfl_sync(0xffffffffu, w, min(j0 + j * wpr, cnt - 1));
+#pragma unroll
+            for (int i = 0; i < C; ++i) acc[i] = fmaf(j0 + j * wpr < cnt ? wj : 0.f, v[j][i], acc[i]);
           }
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float wj = j0 + j < n ? __shfl_sync(0xffffffffu, w, j0 + j) : 0.f;
-#pragma unroll
-          for (int i = 0; i < C; ++i) acc[i] = fmaf(wj, v[j][i], acc[i]);
-        }
+        M = m;
       }
-      M = m;
     }
+    if (wpr > 1) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) part[warp_id * D + lane * C + i] = acc[i];
+      named_bar_sync(bar, n_warps * 32);
+      if (act && sub == 0) {
+#pragma unroll 1
+        for (int w = 1; w < wpr; ++w)
+#pragma unroll
+          for (int i = 0; i < C; ++i) acc[i] += part[(warp_id + w) * D + lane * C + i];
+      }
+      named_bar_sync(bar, n_warps * 32);
+    }
+    if (!act || sub != 0) continue;
     const float inv = L != 0.f ? 1.f / L : 0.f;
-    const int t = (row_base + row) / group, hq = hkv * group + (row_base + row) % group;
+    const int t = (row_base + row) / group, hq = hkv * group + (row_base + row) - t * group;
     __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (((size_t)b * p.T + t) * p.Hq + hq) * D + lane * C;
     if constexpr (C == 4)
       *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
@@ -387,6 +410,45 @@ __device__ __forceinline__ void merge_rows_compact(const AttnParams &p, int b, i
       *reinterpret_cast<uint32_t *>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
     if (lane == 0) p.lse[((size_t)b * p.Hq + hq) * p.T + t] = L != 0.f ? M + __logf(L) : -INFINITY;
   }
+}
+
+// Tile i0 of CTA c when `total` tiles are cut into G near-equal ranges, [c total / G], in 32
+// bits (G <= 2^10: 64-bit divisions are long calls), and the CTA that owns tile t.
+__device__ __forceinline__ int tq_first_tile(int c, int total, int G) { return c * (total / G) + c * (total % G) / G; }
+__device__ __forceinline__ int tq_owner(int t, int total, int G) {
+  int c = min(G - 1, (int)((float)t * (float)G / (float)total));
+  while (c > 0 && tq_first_tile(c, total, G) > t) --c;
+  while (c + 1 < G && tq_first_tile(c + 1, total, G) <= t) ++c;
+  return c;
+}
+
+// plan_cta without them.
+__device__ __forceinline__ CtaRange tq_plan(const AttnParams &p, int *tstart) {
+#pragma unroll 1
+  for (int s = threadIdx.x; s < p.S; s += blockDim.x) {
+    const Seg g = seg_info(p, s, true);
+    tstart[s] = (g.nkeys + kTqKeys - 1) / kTqKeys;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) warp_scan_inplace(tstart, p.S);
+  __syncthreads();
+  CtaRange r;
+  const int total = tstart[p.S], c = blockIdx.x;
+  r.total = total;
+  r.cost = 0;
+  r.G = min((int)gridDim.x, total);
+  r.t0 = r.t1 = r.s0 = 0;
+  if (c < r.G) {
+    r.t0 = tq_first_tile(c, total, r.G);
+    r.t1 = tq_first_tile(c + 1, total, r.G);
+    int lo = 0, hi = p.S - 1;  // first segment whose tile range reaches past t0
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (tstart[mid + 1] > r.t0) hi = mid; else lo = mid + 1;
+    }
+    r.s0 = lo;
+  }
+  return r;
 }
 
 template <int FMT, int D, int NR, bool kTma>
@@ -444,7 +506,7 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  const CtaRange cr = plan_cta<TK>(p, tstart);  // contains __syncthreads
+  const CtaRange cr = tq_plan(p, tstart);  // contains __syncthreads
   if (c >= cr.G) return;
   const int t1 = cr.t1, s0 = cr.s0;
 
@@ -648,9 +710,6 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     const Seg g = seg_info(p, s, false);
     int lt0, lt1;
     seg_tiles<false>(tstart, s, cr, lt0, lt1);
-    const int first_cta = owner_cta(tstart[s], cr.total, cr.G);
-    const int n_parts = owner_cta(tstart[s + 1] - 1, cr.total, cr.G) - first_cta + 1;
-    if (lt0 == 0 && tid == 0) p.meta[s] = make_int2(s + first_cta, n_parts);
     const int jt0 = jt;
     const int base = g.rb * NR, R = min(NR, p.R - base);  // the packed rows [base, base + R) of the kv-head
     // bit r: row 32 w + r of this segment is one of draft token t
@@ -908,6 +967,8 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       tc_fence_before();
       mbar_arrive_at(a_p_full + 8 * b);
     }
+    const int first_cta = tq_owner(tstart[s], (int)cr.total, cr.G);
+    const int n_parts = tq_owner(tstart[s + 1] - 1, (int)cr.total, cr.G) - first_cta + 1;
     // ---- epilogue: the two parities' O and l of every row of this part joined ----
     // (a warpgroup waits for the PVs of its own tiles, whose phases it has followed, and
     // meets the others at the barrier below)
@@ -1034,7 +1095,8 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     if (*merge_ok) {
       const int seg = s / p.NRB, base = s % p.NRB * NR, R = min(NR, p.R - base);
       const int r0 = mpart[k] * R / np, r1 = (mpart[k] + 1) * R / np;
-      merge_rows_compact<D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k], np, r0, r1, warp, 4 * WG, lane);
+      merge_rows_compact<D>(p, seg / p.Hkv, seg % p.Hkv, base, mslot[k], np, r0, r1, warp, 4 * WG, lane,
+                            reinterpret_cast<float *>(smem + SM::kPOff), kBarSoft);
     }
     named_bar_sync(kBarSoft, kSoft);
     // leave: np arrivals and np departures wrap the counter back to zero

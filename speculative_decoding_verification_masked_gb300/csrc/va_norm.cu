@@ -7,9 +7,9 @@
 // One block per token.  D/16 lanes (rounded up to a power of two, LPR) hold a row: a
 // lane has the 8 elements from 8c on of the first half and their partners of the
 // second, so the rotation stays in the lane and the sum of squares takes log2(LPR)
-// shuffles.  A lane's column c is the same in every row, so its cosines, sines and
-// weights are in registers for all heads.  Rows are loaded kRows at a time, before the token's
-// angles are known.
+// shuffles.  Rows are loaded kRows at a time, before the token's angles are known; what a
+// token's rows share (cosines and sines, from shared memory, and the weights, from the
+// first-level cache) is loaded again for each, which leaves registers for more blocks.
 //
 // Angles: base^(-2i/D) / 2 pi comes from the host as a 64-bit binary fraction; its
 // product with the position modulo 2^64 is the phase modulo one turn, exact to 2^-34
@@ -58,10 +58,10 @@ struct Eight<float> {
 };
 
 template <typename T, int LPR>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kNormThreads, sizeof(T) == 2 ? 9 : 7) norm_rope_kernel(const NormParams p) {
   constexpr int kPass = kNormThreads / LPR;      // rows of a pass
   constexpr int kRows = sizeof(T) == 2 ? 3 : 2;  // rows of a thread, loads first
-  __shared__ float2 cs[128];                     // cosine and sine of pair i
+  __shared__ __align__(16) float2 cs[128];       // cosine and sine of pair i
   const int tid = threadIdx.x, c = tid % LPR;
   const int half = p.D / 2, rows = p.Hq + p.Hkv;
   const bool act = 8 * c < half;
@@ -84,7 +84,6 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormParam
   };
   const int r_first = tid / LPR;
   load(r_first);
-  float cosv[8], sinv[8];
   if (p.positions != nullptr) {
     const int pos = __ldg(p.positions + blockIdx.x);
     for (int i = tid; i < half; i += kNormThreads) {
@@ -95,12 +94,6 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormParam
       cs[i] = make_float2(co, s);
     }
     __syncthreads();
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float2 v = p.positions != nullptr && act ? cs[8 * c + j] : make_float2(1.f, 0.f);
-    cosv[j] = v.x;
-    sinv[j] = v.y;
   }
   const float inv_d = 1.f / (float)p.D;
   for (int r0 = r_first; r0 - r_first < rows; r0 += kRows * kPass) {
@@ -137,15 +130,20 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormParam
           e[j] = e[j] * rs * fh[j];
         }
       }
-      float x[8], y[8];
+      if (p.positions != nullptr) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[j] = fmaf(a[j], cosv[j], -(e[j] * sinv[j]));
-        y[j] = fmaf(e[j], cosv[j], a[j] * sinv[j]);
+        for (int j = 0; j < 8; j += 2) {
+          const float4 v = *reinterpret_cast<const float4 *>(cs + 8 * c + j);  // (cos, sin) of pairs j and j + 1
+          const float a0 = a[j], a1 = a[j + 1];
+          a[j] = fmaf(a0, v.x, -(e[j] * v.y));
+          e[j] = fmaf(e[j], v.x, a0 * v.y);
+          a[j + 1] = fmaf(a1, v.z, -(e[j + 1] * v.w));
+          e[j + 1] = fmaf(e[j + 1], v.z, a1 * v.w);
+        }
       }
       T *dst = is_q ? qo + (size_t)r * p.D : ko + (size_t)(r - p.Hq) * p.D;
-      Eight<T>::store(dst, x);
-      Eight<T>::store(dst + half, y);
+      Eight<T>::store(dst, a);
+      Eight<T>::store(dst + half, e);
     }
   }
 }

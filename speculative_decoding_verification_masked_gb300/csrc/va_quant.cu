@@ -140,7 +140,7 @@ __device__ __forceinline__ float group_quotient(float y, float g, float inv) {
 }
 
 template <int FMT, int D, typename T>
-__global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kQuantThreads, 8) quantize_kernel(const QuantParams p) {
   using R = QRow<FMT, D>;
   constexpr int LPR = D / 16;                     // lanes of a row
   constexpr int kPass = kQuantThreads / LPR;      // rows of a pass
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantPara
 }
 
 template <int FMT, int D, typename T>
-__global__ void __launch_bounds__(kQuantThreads) dequantize_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kQuantThreads, 8) dequantize_kernel(const QuantParams p) {
   using R = QRow<FMT, D>;
   constexpr int LPR = D / 16;
   constexpr int kPass = kQuantThreads / LPR;
