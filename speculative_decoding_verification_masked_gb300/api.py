@@ -646,14 +646,18 @@ def verify_evict_kv_paged(k_pages, v_pages, page_table, seqlens, indices, n_indi
 # ----------------------------------------------------------------------------
 
 KV_FORMATS = {"e4m3": 0, "e2m1": 1}
+_ROW_BYTES = {}
 
 
 def kv_row_bytes(fmt, D) -> int:
     """Bytes of a quantised row (one token of one kv-head): caches of format `fmt`
     ("e4m3" or "e2m1") are uint8 [B][len][Hkv][kv_row_bytes], or pages of such rows."""
-    n = int(lib().verify_kv_row_bytes(_format(fmt), int(D)))
-    if n == 0:
-        raise ValueError(f"caches held in {fmt} take D = 64 or 128, not {D}")
+    n = _ROW_BYTES.get((fmt, D))
+    if n is None:
+        n = int(lib().verify_kv_row_bytes(_format(fmt), int(D)))
+        if n == 0:
+            raise ValueError(f"caches held in {fmt} take D = 64 or 128, not {D}")
+        _ROW_BYTES[fmt, D] = n
     return n
 
 
@@ -664,24 +668,24 @@ def _format(fmt) -> int:
         raise ValueError(f"unknown cache format {fmt!r}; use 'e4m3' or 'e2m1'") from None
 
 
-def _rows(t, name, shape, dtype, dev) -> VaRows:
-    """Rows of D elements of a [B][T][heads][D] tensor: heads side by side, any
-    batch and token stride (a part of a projection's output)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
+def _rows(t, name, shape, dtype, dev):
+    """Rows of D elements of a [B][T][heads][D] tensor, by reference: heads side by
+    side, any batch and token stride (a part of a projection's output)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+            sb, st, sh, sd = t.stride()
+            if (sd == 1 or shape[3] == 1) and (sh == shape[3] or shape[2] == 1):
+                return ctypes.byref(VaRows(t.data_ptr(), sb, st))
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+    except AttributeError:
+        raise TypeError(f"{name}: expected a torch.Tensor") from None
     if not t.is_cuda:
         raise ValueError("tensor arguments must live on the GPU")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, the others on cuda:{dev}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
-    B, T, H, D = shape
-    sb, st, sh, sd = t.stride()
-    if (D > 1 and sd != 1) or (H > 1 and sh != D):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return VaRows(t.data_ptr(), sb if B > 1 else 0, st if T > 1 else 0)
+    raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
 
 
 def verify_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, eps=1e-6, rope_base=10000.0, q_out=None,
@@ -699,11 +703,14 @@ def verify_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, eps=1e-
         new = _made(lambda: [torch.empty(s, dtype=dtype, device=q.device) if o is None else o
                              for s, o in ((sq, q_out), (sk, k_out))], dev, stream)
         q_out, k_out = new
-    _run_on(dev, stream, "verify_norm_rope", ctypes.byref(shape), ctypes.byref(_rows(q, "q", sq, dtype, dev)),
-            ctypes.byref(_rows(k, "k", sk, dtype, dev)), _arg(q_weight, "q_weight", (D,), dtype, dev),
+    _run_on(dev, stream, "verify_norm_rope", ctypes.byref(shape), _rows(q, "q", sq, dtype, dev),
+            _rows(k, "k", sk, dtype, dev), _arg(q_weight, "q_weight", (D,), dtype, dev),
             _arg(k_weight, "k_weight", (D,), dtype, dev), eps, _arg(positions, "positions", (B, T), _I32, dev),
-            ctypes.byref(_rows(q_out, "q_out", sq, dtype, dev)), ctypes.byref(_rows(k_out, "k_out", sk, dtype, dev)))
+            _rows(q_out, "q_out", sq, dtype, dev), _rows(k_out, "k_out", sk, dtype, dev))
     return q_out, k_out
+
+
+_QUANT_CALLS = {(w, y): f"verify_{w}_kv_{y}" for w in ("quantize", "dequantize") for y in ("dense", "paged")}
 
 
 def _quant_call(what, layout, k, v, k_cache, v_cache, table, start, fmt, n_tokens, workspace, stream):
@@ -712,13 +719,13 @@ def _quant_call(what, layout, k, v, k_cache, v_cache, table, start, fmt, n_token
     dev, dtype = k.get_device(), k.dtype
     shape = VaShape(B, T, Hkv, Hkv, D, _dtype_code(k), 1.0, 0.0)
     code, cache = _format(fmt), (n0, n1, Hkv, kv_row_bytes(fmt, D))
-    plain = ctypes.byref(_rows(k, "k", rows, dtype, dev)), ctypes.byref(_rows(v, "v", rows, dtype, dev))
+    plain = _rows(k, "k", rows, dtype, dev), _rows(v, "v", rows, dtype, dev)
     caches = (_arg(k_cache, "the key cache", cache, torch.uint8, dev),
               _req(v_cache, "the value cache", cache, torch.uint8, dev), *_cache_args(layout, n0, n1, B, table, dev))
     first = _req(start, "start" if what == "dequantize" else "seqlens", (B,), _I32, dev)
     count = _arg(n_tokens, "n_tokens", (B,), _I32, dev)
     args = (*plain, *caches, first, count) if what == "quantize" else (*caches, first, count, *plain)
-    _run_on(dev, stream, f"verify_{what}_kv_{layout}", ctypes.byref(shape), code, *args, _status_ptr(workspace, dev))
+    _run_on(dev, stream, _QUANT_CALLS[what, layout], ctypes.byref(shape), code, *args, _status_ptr(workspace, dev))
 
 
 def verify_quantize_kv_dense(k, v, k_cache, v_cache, seqlens, fmt, n_tokens=None, workspace: Workspace = None,

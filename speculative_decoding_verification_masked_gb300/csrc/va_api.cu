@@ -748,22 +748,22 @@ va_status rope_common(const va_shape *shape, void *q, void *k, const int32_t *se
 }
 
 // Rows of a [B][T][heads][D] tensor: every row 16-byte aligned; where they are
-// written, no two in one place.
+// written, no two in one place.  (The stride of a single sequence or token is not looked at.)
 va_status check_rows(const va_rows *r, const char *name, const va_shape &s, int heads, bool written, va::TokenRows &out) {
-  const int elem = s.dtype == VA_DTYPE_BF16 ? 2 : 4;
   if (r == nullptr || r->ptr == nullptr) return fail(VA_ERR_INVALID_ARG, "%s must not be NULL", name);
-  if (!aligned(r->ptr, 16) || r->batch_stride % (16 / elem) != 0 || r->token_stride % (16 / elem) != 0)
-    return fail(VA_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned", name);
-  const int64_t lim = (int64_t)1 << 40;
-  if (r->batch_stride < 0 || r->token_stride < 0 || r->batch_stride > lim || r->token_stride > lim)
+  const int64_t each = s.dtype == VA_DTYPE_BF16 ? 8 : 4, lim = (int64_t)1 << 40;
+  const int64_t bat = s.B > 1 ? r->batch_stride : 0, tok = s.T > 1 ? r->token_stride : 0;
+  if (bat < 0 || tok < 0 || bat > lim || tok > lim)
     return fail(VA_ERR_INVALID_ARG, "%s: strides must be in [0, 2^40]", name);
+  if (!aligned(r->ptr, 16) || bat % each != 0 || tok % each != 0)
+    return fail(VA_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned", name);
   if (written) {
-    const int64_t row = (int64_t)heads * s.D, tok = s.T > 1 ? r->token_stride : row, bat = s.B > 1 ? r->batch_stride : row;
-    const bool apart = tok >= row && bat >= row &&
+    const int64_t row = (int64_t)heads * s.D;
+    const bool apart = (s.T == 1 || tok >= row) && (s.B == 1 || bat >= row) &&
                        (s.T == 1 || s.B == 1 || bat / s.T >= tok || tok / s.B >= bat);
     if (!apart) return fail(VA_ERR_INVALID_ARG, "%s: the strides put rows in one place", name);
   }
-  out = {r->ptr, (long long)r->batch_stride, (long long)r->token_stride};
+  out = {r->ptr, (long long)bat, (long long)tok};
   return VA_OK;
 }
 

@@ -7,9 +7,10 @@
 // One block per token.  D/16 lanes (rounded up to a power of two, LPR) hold a row: a
 // lane has the 8 elements from 8c on of the first half and their partners of the
 // second, so the rotation stays in the lane and the sum of squares takes log2(LPR)
-// shuffles.  Rows are loaded kRows at a time, before the token's angles are known; what a
-// token's rows share (cosines and sines, from shared memory, and the weights, from the
-// first-level cache) is loaded again for each, which leaves registers for more blocks.
+// shuffles.  Weights and angles are folded into four factors a pair, once per token
+// and kind of head, in shared memory (an element's weight times the cosine or sine
+// that it meets), so a row costs packed products alone: a 16K-token prompt was bound by
+// its instructions, not by HBM.  Rows are loaded kRows at a time, before the factors are known.
 //
 // Angles: base^(-2i/D) / 2 pi comes from the host as a 64-bit binary fraction; its
 // product with the position modulo 2^64 is the phase modulo one turn, exact to 2^-34
@@ -57,11 +58,23 @@ struct Eight<float> {
   }
 };
 
+template <typename T>
+__device__ __forceinline__ float weight_at(const void *w, int i) {
+  if (w == nullptr) return 1.f;
+  if constexpr (sizeof(T) == 2)
+    return __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[i]);
+  else
+    return static_cast<const float *>(w)[i];
+}
+
 template <typename T, int LPR>
-__global__ void __launch_bounds__(kNormThreads, sizeof(T) == 2 ? 9 : 7) norm_rope_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kNormThreads, 8) norm_rope_kernel(const NormParams p) {
   constexpr int kPass = kNormThreads / LPR;      // rows of a pass
-  constexpr int kRows = sizeof(T) == 2 ? 3 : 2;  // rows of a thread, loads first
-  __shared__ __align__(16) float2 cs[128];       // cosine and sine of pair i
+  constexpr int kRows = sizeof(T) == 2 ? 3 : 1;  // rows of a thread, loads first
+  // [query, key heads][0: (first half by cosine, second half by sine, negated) of two pairs, 1: (second
+  // half by cosine, first half by sine)][pair of pairs of a lane][lane]: neighbouring lanes read
+  // neighbouring vectors
+  __shared__ float4 fac[2][2][4][16];
   const int tid = threadIdx.x, c = tid % LPR;
   const int half = p.D / 2, rows = p.Hq + p.Hkv;
   const bool act = 8 * c < half;
@@ -84,14 +97,26 @@ __global__ void __launch_bounds__(kNormThreads, sizeof(T) == 2 ? 9 : 7) norm_rop
   };
   const int r_first = tid / LPR;
   load(r_first);
-  if (p.positions != nullptr) {
-    const int pos = __ldg(p.positions + blockIdx.x);
+  {
+    const int pos = p.positions != nullptr ? __ldg(p.positions + blockIdx.x) : 0;
     for (int i = tid; i < half; i += kNormThreads) {
-      // half turns in [-1, 1)
-      const int turn = (int)(((uint64_t)(int64_t)pos * p.turns[i]) >> 32);
-      float s, co;
-      sincospif((float)turn * 0x1p-31f, &s, &co);
-      cs[i] = make_float2(co, s);
+      float s = 0.f, co = 1.f;
+      if (p.positions != nullptr) {
+        // half turns in [-1, 1)
+        const int turn = (int)(((uint64_t)(int64_t)pos * p.turns[i]) >> 32);
+        sincospif((float)turn * 0x1p-31f, &s, &co);
+      }
+#pragma unroll
+      for (int kind = 0; kind < 2; ++kind) {
+        const void *w = kind == 0 ? p.q_weight : p.k_weight;
+        const float wl = weight_at<T>(w, i), wh = weight_at<T>(w, i + half);
+        float *f = reinterpret_cast<float *>(&fac[kind][0][i % 8 / 2][i / 8]) + (i & 1);
+        float *g = reinterpret_cast<float *>(&fac[kind][1][i % 8 / 2][i / 8]) + (i & 1);
+        f[0] = wl * co;
+        f[2] = -(wh * s);
+        g[0] = wh * co;
+        g[2] = wl * s;
+      }
     }
     __syncthreads();
   }
@@ -102,48 +127,42 @@ __global__ void __launch_bounds__(kNormThreads, sizeof(T) == 2 ? 9 : 7) norm_rop
     for (int u = 0; u < kRows; ++u) {
       const int r = r0 + u * kPass;
       const bool in = r < rows && act, is_q = r < p.Hq;
-      const T *w = static_cast<const T *>(is_q ? p.q_weight : p.k_weight);
-      float a[8], e[8];
+      float2 a[4], e[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) a[j] = e[j] = 0.f;
+      for (int j = 0; j < 4; ++j) a[j] = e[j] = make_float2(0.f, 0.f);
       if (in) {
-        lo[u].get(a);
-        hi[u].get(e);
+        lo[u].get(reinterpret_cast<float(&)[8]>(a));
+        hi[u].get(reinterpret_cast<float(&)[8]>(e));
       }
-      float ss = 0.f;
+      float2 ss2 = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(a[j], a[j], fmaf(e[j], e[j], ss));
+      for (int j = 0; j < 4; ++j) ss2 = fma2(a[j], a[j], fma2(e[j], e[j], ss2));
+      float ss = ss2.x + ss2.y;
 #pragma unroll
       for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       if (!in) continue;
-      if (w != nullptr) {
-        Eight<T> wl, wh;
-        float fl[8], fh[8];
-        wl.load(w + 8 * c);
-        wh.load(w + 8 * c + half);
-        wl.get(fl);
-        wh.get(fh);
-        const float rs = 1.f / sqrtf(fmaf(ss, inv_d, p.eps));
+      if ((is_q ? p.q_weight : p.k_weight) != nullptr) {
+        // one Newton step: the approximate root alone is off by two units
+        const float v = fmaf(ss, inv_d, p.eps), y = rsqrtf(v);
+        const float rs = fmaf(fmaf(-(v * y), y, 1.f), 0.5f * y, y);
+        const float2 rs2 = v > 0x1p-100f && v < 0x1p100f ? make_float2(rs, rs) : make_float2(1.f / sqrtf(v), 1.f / sqrtf(v));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          a[j] = a[j] * rs * fl[j];
-          e[j] = e[j] * rs * fh[j];
+        for (int j = 0; j < 4; ++j) {
+          a[j] = mul2(a[j], rs2);
+          e[j] = mul2(e[j], rs2);
         }
       }
-      if (p.positions != nullptr) {
+      const int kind = is_q ? 0 : 1;
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float4 v = *reinterpret_cast<const float4 *>(cs + 8 * c + j);  // (cos, sin) of pairs j and j + 1
-          const float a0 = a[j], a1 = a[j + 1];
-          a[j] = fmaf(a0, v.x, -(e[j] * v.y));
-          e[j] = fmaf(e[j], v.x, a0 * v.y);
-          a[j + 1] = fmaf(a1, v.z, -(e[j + 1] * v.w));
-          e[j + 1] = fmaf(e[j + 1], v.z, a1 * v.w);
-        }
+      for (int j = 0; j < 4; ++j) {
+        const float4 u0 = fac[kind][0][j][c], u1 = fac[kind][1][j][c];
+        const float2 x = fma2(a[j], make_float2(u0.x, u0.y), mul2(e[j], make_float2(u0.z, u0.w)));
+        e[j] = fma2(e[j], make_float2(u1.x, u1.y), mul2(a[j], make_float2(u1.z, u1.w)));
+        a[j] = x;
       }
       T *dst = is_q ? qo + (size_t)r * p.D : ko + (size_t)(r - p.Hq) * p.D;
-      Eight<T>::store(dst, a);
-      Eight<T>::store(dst + half, e);
+      Eight<T>::store(dst, reinterpret_cast<const float(&)[8]>(a));
+      Eight<T>::store(dst + half, reinterpret_cast<const float(&)[8]>(e));
     }
   }
 }
