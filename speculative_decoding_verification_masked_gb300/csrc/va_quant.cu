@@ -42,6 +42,25 @@ __device__ __forceinline__ void quant_range(const QuantParams &p, int b, int &st
   }
 }
 
+// Token and head of row r0 + u * kPass of a sequence (heads fastest), walked from row to
+// row: a division each was a quarter of the quantising kernel's instructions.
+template <int kPass>
+struct RowWalk {
+  int t, h;
+  __device__ __forceinline__ RowWalk(int r, int heads) {
+    t = r / heads;
+    h = r - t * heads;
+  }
+  __device__ __forceinline__ void next(const QuantParams &p) {
+    t += p.pass_tokens;
+    h += p.pass_heads;
+    if (h >= p.Hkv) {
+      h -= p.Hkv;
+      ++t;
+    }
+  }
+};
+
 // 16 consecutive elements as they are in memory, and as fp32.
 template <typename T>
 struct Sixteen;
@@ -125,13 +144,14 @@ __device__ __forceinline__ float sixth_to_odd(float y) {
 //    the border itself in the first case and on the right side in the second.
 //  fp32 input: the quotient is rounded once from its residual, then moved off a
 //    border that it has only been rounded to.
+// (q0: y * inv)
 template <typename T>
-__device__ __forceinline__ float group_quotient(float y, float g, float inv) {
+__device__ __forceinline__ float group_quotient(float y, float g, float inv, float q0) {
   if constexpr (sizeof(T) == 2) {
-    return __uint_as_float((__float_as_uint(y * inv) + 0x800u) & 0xfffff000u);
+    return __uint_as_float((__float_as_uint(q0) + 0x800u) & 0xfffff000u);
   } else {
-    const float a = fabsf(y), q0 = a * inv;
-    const float q = fmaf(fmaf(-q0, g, a), inv, q0);
+    const float a = fabsf(y), qa = fabsf(q0);
+    const float q = fmaf(fmaf(-qa, g, a), inv, qa);
     const float r = fmaf(-q, g, a);
     const uint32_t b = __float_as_uint(q);
     // (a zero stays one, with its sign)
@@ -156,14 +176,19 @@ __global__ void __launch_bounds__(kQuantThreads, 8) quantize_kernel(const QuantP
   const int r0 = blockIdx.x * kPass * kRows + threadIdx.x / LPR;
   if (blockIdx.x * kPass * kRows >= rows) return;
   Sixteen<T> in[kRows];
+  RowWalk<kPass> at(r0, p.Hkv);
+  const RowWalk<kPass> first = at;
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
-    const int r = min(r0 + u * kPass, rows - 1);  // (lanes past the end repeat the last row)
-    in[u].load(x + (size_t)(r / p.Hkv) * src.token + (size_t)(r % p.Hkv) * D);
+    const bool live = r0 + u * kPass < rows;  // (lanes past the end take the first row again)
+    in[u].load(x + (size_t)(live ? at.t : 0) * src.token + (size_t)(live ? at.h : 0) * D);
+    at.next(p);
   }
+  at = first;
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
-    const int r = r0 + u * kPass;
+    const int r = r0 + u * kPass, row_t = at.t, row_h = at.h;
+    at.next(p);
     float f[16];
     in[u].get(f);
     float amax = 0.f;
@@ -182,8 +207,8 @@ __global__ void __launch_bounds__(kQuantThreads, 8) quantize_kernel(const QuantP
       if constexpr (FMT == VA_KV_E4M3) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint32_t two =
-              __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * up, f[2 * i + 1] * up), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t two = __nv_cvt_float2_to_fp8x2(mul2(make_float2(f[2 * i], f[2 * i + 1]), make_float2(up, up)),
+                                                        __NV_SATFINITE, __NV_E4M3);
           code[i / 2] |= two << (16 * (i & 1));
         }
       } else {
@@ -191,8 +216,11 @@ __global__ void __launch_bounds__(kQuantThreads, 8) quantize_kernel(const QuantP
         const float g = e4m3_to_float(group), inv = g > 0.f ? __frcp_rn(g) : 0.f;  // (g = 0: codes +-0)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float a = group_quotient<T>(f[2 * i] * up, g, inv), c = group_quotient<T>(f[2 * i + 1] * up, g, inv);
-          const uint32_t two = __nv_cvt_float2_to_fp4x2(make_float2(a, c), __NV_E2M1, cudaRoundNearest);
+          const float2 y = mul2(make_float2(f[2 * i], f[2 * i + 1]), make_float2(up, up));
+          const float2 q0 = mul2(y, make_float2(inv, inv));
+          const uint32_t two = __nv_cvt_float2_to_fp4x2(
+              make_float2(group_quotient<T>(y.x, g, inv, q0.x), group_quotient<T>(y.y, g, inv, q0.y)), __NV_E2M1,
+              cudaRoundNearest);
           code[i / 4] |= two << (8 * (i & 3));
         }
       }
@@ -212,7 +240,7 @@ __global__ void __launch_bounds__(kQuantThreads, 8) quantize_kernel(const QuantP
       tail[0] = w;
     }
     if (r >= rows) continue;
-    uint8_t *dst = quant_row(p, cache, R::kBytes, b, start + r / p.Hkv, r % p.Hkv);
+    uint8_t *dst = quant_row(p, cache, R::kBytes, b, start + row_t, row_h);
     if (dst == nullptr) continue;
     if constexpr (FMT == VA_KV_E4M3)
       reinterpret_cast<uint4 *>(dst)[li] = make_uint4(code[0], code[1], code[2], code[3]);
@@ -237,14 +265,18 @@ __global__ void __launch_bounds__(kQuantThreads, 8) dequantize_kernel(const Quan
   const int rows = n * p.Hkv;
   T *y = static_cast<T *>(const_cast<void *>(out.p)) + (size_t)b * out.batch + li * 16;
   const int r0 = blockIdx.x * kPass * kRows + threadIdx.x / LPR;
+  if (blockIdx.x * kPass * kRows >= rows) return;
   uint4 code[kRows], tail[kRows];
   bool live[kRows];
+  RowWalk<kPass> at(r0, p.Hkv);
+  const RowWalk<kPass> first = at;
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
-    const int r = r0 + u * kPass;
+    const int r = r0 + u * kPass, row_t = at.t, row_h = at.h;
+    at.next(p);
     live[u] = false;
     if (r >= rows) continue;
-    const uint8_t *src = quant_row(p, cache, R::kBytes, b, start + r / p.Hkv, r % p.Hkv);
+    const uint8_t *src = quant_row(p, cache, R::kBytes, b, start + row_t, row_h);
     if (src == nullptr) continue;
     live[u] = true;
     if constexpr (FMT == VA_KV_E4M3) {
@@ -255,10 +287,12 @@ __global__ void __launch_bounds__(kQuantThreads, 8) dequantize_kernel(const Quan
     }
     tail[u] = __ldg(reinterpret_cast<const uint4 *>(src + R::kCodeBytes));
   }
+  at = first;
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
+    const int row_t = at.t, row_h = at.h;
+    at.next(p);
     if (!live[u]) continue;
-    const int r = r0 + u * kPass;
     float f[16];
     const uint32_t w[4] = {code[u].x, code[u].y, code[u].z, code[u].w};
     float s;
@@ -283,14 +317,16 @@ __global__ void __launch_bounds__(kQuantThreads, 8) dequantize_kernel(const Quan
     }
     Sixteen<T> o;
     o.set(f);
-    o.store(y + (size_t)(r / p.Hkv) * out.token + (size_t)(r % p.Hkv) * D);
+    o.store(y + (size_t)row_t * out.token + (size_t)row_h * D);
   }
 }
 
 namespace {
 template <int FMT, int D, typename T>
-cudaError_t launch_t(const QuantParams &p, bool write, cudaStream_t stream) {
-  const int per_block = kQuantThreads / (D / 16) * (write && sizeof(T) == 4 ? 2 : 4);
+cudaError_t launch_t(QuantParams p, bool write, cudaStream_t stream) {
+  const int pass = kQuantThreads / (D / 16), per_block = pass * (write && sizeof(T) == 4 ? 2 : 4);
+  p.pass_tokens = pass / p.Hkv;
+  p.pass_heads = pass % p.Hkv;
   const long long rows = (long long)p.T * p.Hkv;
   const dim3 grid((unsigned)((rows + per_block - 1) / per_block), (unsigned)p.B, 2);
   if (write)

@@ -41,6 +41,7 @@ struct QuantParams {
   const int32_t *start;           // [B] first slot
   const int32_t *n_tokens;        // [B] or nullptr: T
   int *status;                    // may be nullptr
+  int pass_tokens, pass_heads;    // rows of a block's pass, as whole tokens and heads (set by the launcher)
 };
 
 cudaError_t launch_quantize_kv(const QuantParams &p, cudaStream_t stream);
