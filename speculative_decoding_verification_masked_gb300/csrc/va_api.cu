@@ -484,6 +484,10 @@ va_status run_attention_quant(const Common &c, va_kv_format format, int layout, 
   const long long tiles_cap = (long long)p.S * (((long long)len_cap + 127) / 128);
   if (tiles_cap >= (1ll << 31)) return fail(VA_ERR_UNSUPPORTED, "problem too large (%lld key tiles)", tiles_cap);
   const int grid = (int)(tiles_cap < sms ? tiles_cap : sms);
+  // the heads and row blocks of a sequence in step, where that leaves at most a sixteenth of
+  // the CTAs without work
+  const int lanes = s.Hkv * p.NRB, in_step = grid / lanes * lanes;
+  p.lanes = in_step > 0 && (grid - in_step) * 16 <= grid ? lanes : 1;
   auto launch = format == VA_KV_E4M3
                     ? (s.D == 128 ? va::launch_attention_e4m3_d128 : va::launch_attention_e4m3_d64)
                     : (s.D == 128 ? va::launch_attention_e2m1_d128 : va::launch_attention_e2m1_d64);

@@ -78,7 +78,8 @@ struct AttnParams {
   int test_drop_part;  // test hook: this CTA's parts of split segments never arrive (-1: off)
   int test_stall;      // test hook: this CTA's softmax is never told that scores are ready (-1: off)
   ModParams mod;
-  int stages;          // caches held in 8 or 4 bits: stages of the ring of raw rows
+  // caches held in 8 or 4 bits: stages of the ring of raw rows; segments whose CTAs go in step
+  int stages, lanes;
 };
 
 size_t attn_smem_required(const AttnParams &p);
