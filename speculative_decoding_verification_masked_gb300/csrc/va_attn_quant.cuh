@@ -67,7 +67,7 @@ constexpr float kTqMove = 8.f;  // a score this far above the reference moves it
 template <int NR>
 struct TqCfg {
   static constexpr int kRowGroups = NR > 32 ? NR / 32 : 1;  // of NW rows, each with
-  static constexpr int kParities = NR > 32 ? 1 : 2;         // one warpgroup, or one for even and one for odd tiles
+  static constexpr int kParities = NR > 64 ? 1 : 2;         // one warpgroup, or one for even and one for odd tiles
   static constexpr int NW = NR / kRowGroups;                // rows of a softmax thread
   static constexpr int kGroups = kParities * kRowGroups;    // softmax warpgroups
   static constexpr int kSoft = 128 * kGroups;
@@ -318,6 +318,16 @@ __device__ __forceinline__ void produce_raw(const AttnParams &p, const CUtensorM
       return __ldg(p.page_table + (size_t)g.b * p.max_pages + (k >> p.page_shift));
     };
     int page_next = box_page(lt0);
+    // (gather) the rows of the next tile, looked up before this tile's copies are issued
+    const uint8_t *rows[TK / 32];
+    auto look_up = [&](int lt) {
+#pragma unroll
+      for (int j = 0; j < TK / 32; ++j) {
+        const int k = lt * TK + 32 * j + lane;
+        rows[j] = lt < lt1 && k < g.nkeys ? row_of(g, k) : cache;
+      }
+    };
+    if constexpr (!kTma) look_up(lt0);
     for (int lt = lt0; lt < lt1; ++lt, ++it) {
       const int page_now = page_next;
       page_next = box_page(lt + 1);
@@ -350,10 +360,13 @@ __device__ __forceinline__ void produce_raw(const AttnParams &p, const CUtensorM
           }
         } else {
           constexpr int CPR = RB / 16;  // 16-byte chunks of a row
+          const uint8_t *now[TK / 32];
+#pragma unroll
+          for (int j = 0; j < TK / 32; ++j) now[j] = rows[j];
+          look_up(lt + 1);
 #pragma unroll
           for (int j = 0; j < TK / 32; ++j) {
-            const int k = k0 + 32 * j + lane;
-            const uint8_t *mine = k < g.nkeys ? row_of(g, k) : cache;
+            const uint8_t *mine = now[j];
 #pragma unroll
             for (int i = 0; i < CPR; ++i) {
               const int e = 32 * i + lane, r = e / CPR, c = e % CPR;
@@ -710,8 +723,8 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
   // ================================== softmax ==================================
   regs_inc<Cfg::kRegsSoft>();
   const uint32_t tmem = tmem_base();
-  const int wg = warp >> 2, par = PAR == 2 ? wg : 0;  // warpgroup; with two parities the tiles it takes: jt % 2 == par
-  const int rg = PAR == 2 ? 0 : wg, r_wg = rg * NW;   // its rows [r_wg, r_wg + NW) of the block
+  const int wg = warp >> 2, par = PAR == 2 ? wg / RG : 0;  // warpgroup; with two parities the tiles it takes: jt % 2 == par
+  const int rg = wg % RG, r_wg = rg * NW;                  // its rows [r_wg, r_wg + NW) of the block
   const int wq = warp & 3, ktid = tid & 127;          // warp of the warpgroup; key of the tile, output column of the epilogue
   const int kBarRed = kBarRed0 + wg;
   const uint32_t tLane = tmem + ((uint32_t)(wq * 32) << 16);
@@ -1033,8 +1046,8 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       }
       const bool seen = !(l == 0.f);  // (NaN: a row that holds one)
       const float inv = tid < R && seen ? 1.f / l : 0.f;
-      alphas[tid] = inv * f0 * vred[PAR == 2 ? 0 : tid / NW];
-      if constexpr (PAR == 2) alphas[NR + tid] = inv * f1 * vred[1];
+      alphas[tid] = inv * f0 * vred[tid / NW];
+      if constexpr (PAR == 2) alphas[NR + tid] = inv * f1 * vred[RG + tid / NW];
       if (tid < R && ok) {
         const int t = token_of(base + tid), hq = g.hkv * group + (base + tid) - t * group;
         const float lse_nat = seen ? (__log2f(l) - nm) * kLn2 : -INFINITY;
