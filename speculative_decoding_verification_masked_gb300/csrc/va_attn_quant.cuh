@@ -420,22 +420,9 @@ __device__ __forceinline__ void merge_rows_compact(const AttnParams &p, int b, i
 #pragma unroll 1
       for (int q0 = 0; q0 < np; q0 += 32) {
         const float ls = q0 + lane < np ? __ldcg(l + (size_t)(q0 + lane) * p.rows_pad) : -INFINITY;
-        float m = ls;
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, x));
-        m = max_nan(m, M);
-        if (m == -INFINITY) continue;  // no part so far saw a key
-        const float a = M == -INFINITY ? 0.f : __expf(M - m), w = ls == -INFINITY ? 0.f : __expf(ls - m);
-        float sum = w;
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        L = L * a + sum;
-#pragma unroll
-        for (int i = 0; i < C; ++i) acc[i] *= a;
         const int cnt = min(32, np - q0);
-#pragma unroll 1
-        for (int j0 = sub; j0 < cnt; j0 += 8 * wpr) {
-          float v[8][C];
+        float v[8][C];
+        auto load = [&](int j0) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float *src = o + (size_t)(q0 + min(j0 + j * wpr, cnt - 1)) * p.rows_pad * D;
@@ -451,6 +438,23 @@ __device__ __forceinline__ void merge_rows_compact(const AttnParams &p, int b, i
               v[j][1] = u.y;
             }
           }
+        };
+        load(sub);  // (before the weights are known)
+        float m = ls;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, x));
+        m = max_nan(m, M);
+        if (m == -INFINITY) continue;  // no part so far saw a key
+        const float a = M == -INFINITY ? 0.f : __expf(M - m), w = ls == -INFINITY ? 0.f : __expf(ls - m);
+        float sum = w;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        L = L * a + sum;
+#pragma unroll
+        for (int i = 0; i < C; ++i) acc[i] *= a;
+#pragma unroll 1
+        for (int j0 = sub; j0 < cnt; j0 += 8 * wpr) {
+          if (j0 != sub) load(j0);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float wj = __shfl_sync(0xffffffffu, w, min(j0 + j * wpr, cnt - 1));
@@ -522,22 +526,17 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     prefetch_tmap(&tmk);
     prefetch_tmap(&tmv);
   }
-  if (tid == 0) {
-#pragma unroll 1
-    for (int i = 0; i < 2 * kTqStages; ++i) {
-      mbar_init(full + i, kTma ? 1 : 32);
-      mbar_init(empty + i, 4);
-    }
-    for (int b = 0; b < 4; ++b) mbar_init(k_full + b, 8);
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(v_full + b, 4);
-      mbar_init(s_full + b, c == p.test_stall ? kNever : 1);
-      mbar_init(p_full + b, 128 * RG);
-      mbar_init(o_done + b, 1);
-    }
-    mbar_init(drains + 0, 1);
-    mbar_init(drains + 1, 1);
-    *abort_flag = 0;
+  if (tid < SM::kNumBars) {  // a barrier a thread, in the order of their addresses
+    uint64_t *bar = bars + tid;
+    const int n = bar < empty  ? (kTma ? 1 : 32)
+                  : bar < k_full ? 4
+                  : bar < v_full ? 8
+                  : bar < s_full ? 4
+                  : bar < p_full ? (c == p.test_stall ? kNever : 1)
+                  : bar < o_done ? 128 * RG
+                                 : 1;
+    mbar_init(bar, n);
+    if (tid == 0) *abort_flag = 0;
     fence_mbar_init();
   }
   const TqRange cr = tq_plan(p, tstart);  // contains __syncthreads
