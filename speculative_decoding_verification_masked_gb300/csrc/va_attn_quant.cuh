@@ -18,13 +18,14 @@
 // scale to the largest one seen is exact but below 2^-14, where it is off by 2^-25.
 // Scores, row sums, O and the merge are fp32.
 //
-// The softmax reference of a row moves as in the bf16 kernel of this orientation, when
-// a score exceeds it by more than 2^8, and with it the largest value scale.
+// The softmax reference of a row is its maximum over the first tile and moves when a score
+// exceeds it by more than 2^8 in weight, and with it the largest value scale.
 //
 // Roles, one CTA per SM, persistent over the stream-K cut of all tiles, cooperative:
-//   softmax    a warpgroup for even and one for odd tiles (64 rows: two each), so that two
-//              tiles are under way; a thread owns a key and up to 32 rows.  Each parity keeps
-//              its own references, sums and O, joined at the end of a part
+//   softmax    up to 64 rows a warpgroup (64: two) for even and one for odd tiles, so that two
+//              tiles are under way, each parity with its own references, sums and O, joined
+//              at the end of a part; 128 rows four warpgroups for every tile (TMEM holds one
+//              O).  A thread owns a key and up to 32 rows
 //   K          a warpgroup: a thread takes its key's row from the ring, makes halves
 //              and stores them to TMEM (two buffers)
 //   V          a warpgroup: the same into a swizzled tile in shared memory (two buffers)
@@ -43,6 +44,22 @@
 // A scale buffer is written again for tile j + 4, behind the wait for PV of tile j + 1 (V)
 // or S of tile j + 2 (K), both of which come after the softmax of tile j.
 // Every wait is bounded; a role that gives up goes on without waiting.
+//
+// What bounds it (one GB300; a tile is 20.5 KB of 4-bit rows, 0.44 us of an SM's share of
+// the measured copy rate):
+//   up to 32 rows  the conversion's instructions and its latency, 0.75 to 0.85 us a tile: about
+//                  4000 warp instructions, 1500 of them two conversions' worth of codes; four
+//                  schedulers at two thirds.  64 single-token sequences of 1K to 16K keys in
+//                  64-row pages: 210 us, 3.2 TB/s
+//   64, 128 rows   the softmax's instructions (8 a score and thread): 64 nodes over 128K keys
+//                  225 us
+//   short calls    12 us of launch, plan, first tile, unit ends and merge, most of it code
+//                  fetched for the first time (8 tokens over 32K keys: 25 us, ten of them tiles)
+// Steps that led here, 131072 keys, 8 kv-heads, 4 bits, one token / 8 / 64 tokens in us:
+// one softmax warpgroup of 32 rows, everything unrolled 75 / 83 / 352; two issuers and
+// descriptors in uniform registers 53 / 62 / 283; parities, 32-bit shared addresses, waits
+// that sleep, maxima of the first tile 53 / 60 / 308; P scaled without selects 52 / 58 / 261;
+// blocks of 128 rows - / - / 217.
 #pragma once
 
 #include <cuda.h>
@@ -230,8 +247,8 @@ __device__ __forceinline__ int tq_owner(int t, int total, int G) {
 // side in memory, a row of 48 to 144 bytes each: CTAs go through the sequences in step,
 // CTA c with lane c % lanes and part c / lanes of the lane's tiles, so that what one of
 // them reads of a DRAM page or a cache line the others need at that moment.  With each
-// lane's tiles after the other (lanes = 1: segments are units), 64 sequences of single
-// tokens read 1.4 times their bytes from HBM and took @@ us against @@.
+// lane's tiles after the other (lanes = 1: segments are units), 64 single-token
+// sequences over 8192 keys read 1.4 times their bytes from HBM and took 262 us instead of 190.
 struct TqRange {
   int units, lanes, lane;  // unit u of this lane is segment u * lanes + lane
   int total, G, part;      // tiles of the lane, parts they are cut into, this CTA's
