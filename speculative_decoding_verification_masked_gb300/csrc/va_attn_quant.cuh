@@ -26,9 +26,9 @@
 //              tiles are under way, each parity with its own references, sums and O, joined
 //              at the end of a part; 128 rows four warpgroups for every tile (TMEM holds one
 //              O).  A thread owns a key and up to 32 rows
-//   K          a warpgroup: a thread takes its key's row from the ring, makes halves
-//              and stores them to TMEM (two buffers)
-//   V          a warpgroup: the same into a swizzled tile in shared memory (two buffers)
+//   K          a warpgroup (up to 16 rows: two, for even and odd tiles): a thread takes its
+//              key's row from the ring, makes halves and stores them to TMEM (two buffers)
+//   V          as many: the same into a swizzled tile in shared memory (two buffers)
 //   producers  two warps, K and V each: TMA boxes of whole rows (dense; pages of 8 rows
 //              and more), or 16-byte cp.async gathers
 //   issuers    a warp for S (and TMEM), one for PV
@@ -41,8 +41,8 @@
 //   v_full[j % 2]     V's tile
 //   s_full[j % 2]     S of the tile (and its K buffer is free)
 //   p_full[j % 2]     P written, S read;  o_done[j % 2] PV done (P and V buffers free)
-// A scale buffer is written again for tile j + 4, behind the wait for PV of tile j + 1 (V)
-// or S of tile j + 2 (K), both of which come after the softmax of tile j.
+// A scale buffer is written again for tile j + 4, behind the wait for PV of tile j + 1 (V;
+// two warpgroups: of tile j) or S of tile j + 2 (K), which come after the softmax of tile j.
 // Every wait is bounded; a role that gives up goes on without waiting.
 //
 // What bounds it (one GB300; a tile is 20.5 KB of 4-bit rows, 0.44 us of an SM's share of
@@ -59,7 +59,8 @@
 // one softmax warpgroup of 32 rows, everything unrolled 75 / 83 / 352; two issuers and
 // descriptors in uniform registers 53 / 62 / 283; parities, 32-bit shared addresses, waits
 // that sleep, maxima of the first tile 53 / 60 / 308; P scaled without selects 52 / 58 / 261;
-// blocks of 128 rows - / - / 217.
+// blocks of 128 rows - / - / 217; two pairs of converting warpgroups up to 16 rows 46 / - / -
+// (up to 32 rows their registers would leave the softmax too few).
 #pragma once
 
 #include <cuda.h>
@@ -88,13 +89,19 @@ struct TqCfg {
   static constexpr int NW = NR / kRowGroups;                // rows of a softmax thread
   static constexpr int kGroups = kParities * kRowGroups;    // softmax warpgroups
   static constexpr int kSoft = 128 * kGroups;
+  // warpgroups that convert K, and V: up to 16 rows one for even and one for odd tiles
+  static constexpr int kPairs = NR == 16 ? 2 : 1;
   // (the last warpgroup: two producers and two issuers, of S and of PV)
-  static constexpr int kKWarp = 4 * kGroups, kVWarp = kKWarp + 4, kProducer = kVWarp + 4, kMmaWarp = kProducer + 2;
+  static constexpr int kKWarp = 4 * kGroups, kVWarp = kKWarp + 4 * kPairs, kProducer = kVWarp + 4 * kPairs,
+                       kMmaWarp = kProducer + 2;
   static constexpr int kThreads = (kProducer + 4) * 32;
   // Registers a thread: the launch's, and what the warpgroups divide them into.
-  static constexpr int kRegsLaunch = kGroups == 2 ? 96 : 72;
-  static constexpr int kRegsSoft = kGroups == 2 ? 128 : 88, kRegsKv = kGroups == 2 ? 80 : 48, kRegsRest = kGroups == 2 ? 64 : 56;
-  static_assert(kGroups * kRegsSoft + 2 * kRegsKv + kRegsRest <= (kGroups + 3) * kRegsLaunch, "within the launch's registers");
+  static constexpr int kWarpgroups = kGroups + 2 * kPairs + 1;
+  static constexpr int kRegsLaunch = kWarpgroups == 5 ? 96 : 72;
+  static constexpr int kRegsSoft = NR == 16 ? 96 : NR == 32 ? 128 : 88, kRegsKv = NR == 16 ? 64 : NR == 32 ? 80 : 48,
+                       kRegsRest = NR == 32 ? 64 : 56;
+  static_assert(kGroups * kRegsSoft + 2 * kPairs * kRegsKv + kRegsRest <= kWarpgroups * kRegsLaunch,
+                "within the launch's registers");
   static_assert(kThreads * kRegsLaunch <= 65536, "a block's registers");
 };
 
@@ -514,10 +521,10 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
   using Cfg = TqCfg<NR>;
   constexpr int TK = kTqKeys, NC = SM::kNC, WG = Cfg::kGroups, RG = Cfg::kRowGroups, PAR = Cfg::kParities, NW = Cfg::NW, kSoft = Cfg::kSoft,
                 RB = SM::kRow;
-  constexpr int kXRows = WG > 2 ? 16 : NW;  // scores a softmax thread holds at once (registers)
+  constexpr int kXRows = NR > 32 ? 16 : NW;  // scores a softmax thread holds at once (registers)
   constexpr int kChunks = QRow<FMT, D>::kCodeBytes / 16, kRegs = CodeChunk<FMT>::kRegs;
   constexpr int kBarQ = 1, kBarSoft = 3, kBarEnd = 4, kBarRed0 = 5;  // kBarRed0 + softmax warpgroup
-  constexpr int kEndThreads = kSoft + 256 + 64;                      // all but the producers
+  constexpr int kEndThreads = kSoft + 256 * Cfg::kPairs + 64;        // all but the producers
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t *sV = smem, *sQ = smem + SM::kQOff, *ring = smem + SM::kRingOff;
@@ -673,10 +680,11 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     const uint32_t vrow = smem_a + key * 128 + ((key & 7) << 4);
     const uint32_t tK0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + SM::kKCol;
     const int n = t1 - cr.t0;
-    int st = 0;
-    uint32_t ph = 0, row = row0;
-    for (int jt = 0; jt < n; ++jt) {
-      const uint32_t b = (uint32_t)jt & 1u;
+    const int jt0 = Cfg::kPairs == 2 ? (warp - Cfg::kKWarp) >> 2 & 1 : 0;  // its first tile
+    int st = jt0;
+    uint32_t ph = 0;
+    for (int jt = jt0; jt < n; jt += Cfg::kPairs) {
+      const uint32_t b = (uint32_t)jt & 1u, row = row0 + st * (2 * SM::kRaw);
       wait_ok(fl + 8 * st, ph);
       const uint4 tail = lds128(row + QRow<FMT, D>::kCodeBytes);
       const uint32_t sc_now = sc + (jt & 3) * 1024, kb = a_k_full + 8 * (jt & 3);
@@ -724,11 +732,10 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
         mbar_arrive_at(em + 8 * st);
         mbar_arrive_at(is_v ? a_v_full + 8 * b : kb);
       }
-      row += 2 * SM::kRaw;
-      if (++st == p.stages) {
-        st = 0;
+      st += Cfg::kPairs;
+      if (st >= p.stages) {
+        st -= p.stages;
         ph ^= 1u;
-        row = row0;
       }
     }
     tc_fence_before();
