@@ -681,10 +681,17 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     const uint32_t tK0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + SM::kKCol;
     const int n = t1 - cr.t0;
     const int jt0 = Cfg::kPairs == 2 ? (warp - Cfg::kKWarp) >> 2 & 1 : 0;  // its first tile
+    // A wait for a phase also ends while the phase two before it is open.  With three stages
+    // a stage goes back and forth between the two warpgroups, and the rows of tile j can have
+    // landed, and been converted, before those of tile j - 1: what comes next in its stage
+    // waits until tile j - 1 has left it.  (Two, and any even number: the same warpgroup had
+    // the stage.  Five and more: the MMA of tile j - 4, waited for, is behind tile j - 5.)
+    const bool behind = Cfg::kPairs == 2 && p.stages == 3;
     int st = jt0;
     uint32_t ph = 0;
     for (int jt = jt0; jt < n; jt += Cfg::kPairs) {
       const uint32_t b = (uint32_t)jt & 1u, row = row0 + st * (2 * SM::kRaw);
+      if (behind) wait_ok(em + 8 * st, ph ^ 1u);
       wait_ok(fl + 8 * st, ph);
       const uint4 tail = lds128(row + QRow<FMT, D>::kCodeBytes);
       const uint32_t sc_now = sc + (jt & 3) * 1024, kb = a_k_full + 8 * (jt & 3);

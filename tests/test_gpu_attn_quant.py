@@ -267,6 +267,48 @@ def test_one_workspace_for_many_shapes_and_the_same_bits_again():
         va.verify_attn_check_status(ws)
 
 
+@pytest.mark.parametrize("fmt,D", FORMATS)
+@pytest.mark.parametrize("T,page", [(1, 0), (4, 64), (4, 4), (8, 0), (16, 64), (32, 0)])
+def test_every_block_size_over_many_tiles_from_memory(fmt, D, T, page):
+    """Caches past the L2, dozens of tiles to a CTA: stages go round many times, and rows
+    land out of order.  The same bits every time."""
+    g = torch.Generator("cuda").manual_seed(T)
+    Hq, Hkv, L, ps = 32, 8, 131072, page or 131072 + 128
+    nb, n = va.kv_row_bytes(fmt, D), (L + 128) // ps
+    x = [torch.randn(n, ps, Hkv, D, generator=g, device="cuda").bfloat16() for _ in range(2)]
+    cache = [torch.zeros(n, ps, Hkv, nb, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    zero = torch.zeros(n, dtype=torch.int32, device="cuda")
+    va.verify_quantize_kv_dense(*x, *cache, zero, fmt)
+    rows = [torch.empty_like(y) for y in x]
+    va.verify_dequantize_kv_dense(*cache, zero, fmt, k_out=rows[0], v_out=rows[1])
+    table = torch.randperm(n, generator=g, device="cuda", dtype=torch.int32)
+    q = torch.randn(1, T, Hq, D, generator=g, device="cuda").bfloat16()
+    lens = torch.full((1,), L, dtype=torch.int32, device="cuda")
+    ws = va.Workspace(64 << 20)
+
+    def call():
+        if page:
+            return va.verify_attn_paged_quant(q, *cache, table[None], lens, fmt, workspace=ws)
+        return va.verify_attn_dense_quant(q, *cache, lens, fmt, workspace=ws)
+
+    out, lse = call()
+    for _ in range(8):
+        o, l = call()
+        assert torch.equal(o, out) and torch.equal(l, lse)
+    va.verify_attn_check_status(ws)
+    k, v = (y[table.long()].reshape(-1, Hkv, D) if page else y[0] for y in rows)
+    seen = torch.arange(L + T, device="cuda")[None] <= L + torch.arange(T, device="cuda")[:, None]
+    for h in range(Hkv):
+        kh, vh = k[: L + T, h].double(), v[: L + T, h].double()
+        z = torch.einsum("tgd,kd->gtk", q[0, :, 4 * h:4 * h + 4].double(), kh) / D ** 0.5
+        z = z.masked_fill(~seen, -torch.inf)
+        w = torch.softmax(z, -1)
+        want, mag = ((w @ y).transpose(0, 1) for y in (vh, vh.abs()))
+        over = (out[0, :, 4 * h:4 * h + 4].double() - want).abs() - (2.0 ** -8 * want.abs() + 2.0 ** -10 * mag)
+        assert float(over.max()) <= 0
+        assert float((lse[0, 4 * h:4 * h + 4].double() - torch.logsumexp(z, -1)).abs().max()) <= LSE
+
+
 def test_bad_lengths_and_pages_are_recorded():
     c = Case(1, "e2m1", 128, [100, 60], 4, 4, 2, 16)
     ws = va.Workspace(16 << 20)
