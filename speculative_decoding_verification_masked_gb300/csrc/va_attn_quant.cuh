@@ -26,7 +26,7 @@
 //              tiles are under way, each parity with its own references, sums and O, joined
 //              at the end of a part; 128 rows four warpgroups for every tile (TMEM holds one
 //              O).  A thread owns a key and up to 32 rows
-//   K          a warpgroup (up to 16 rows: two, for even and odd tiles): a thread takes its
+//   K          a warpgroup (up to 32 rows: two, for even and odd tiles): a thread takes its
 //              key's row from the ring, makes halves and stores them to TMEM (two buffers)
 //   V          as many: the same into a swizzled tile in shared memory (two buffers)
 //   producers  two warps, K and V each: TMA boxes of whole rows (dense; pages of 8 rows
@@ -59,8 +59,7 @@
 // one softmax warpgroup of 32 rows, everything unrolled 75 / 83 / 352; two issuers and
 // descriptors in uniform registers 53 / 62 / 283; parities, 32-bit shared addresses, waits
 // that sleep, maxima of the first tile 53 / 60 / 308; P scaled without selects 52 / 58 / 261;
-// blocks of 128 rows - / - / 217; two pairs of converting warpgroups up to 16 rows 46 / - / -
-// (up to 32 rows their registers would leave the softmax too few).
+// blocks of 128 rows - / - / 217; two pairs of converting warpgroups up to 32 rows 46 / 54 / -.
 #pragma once
 
 #include <cuda.h>
@@ -89,17 +88,16 @@ struct TqCfg {
   static constexpr int NW = NR / kRowGroups;                // rows of a softmax thread
   static constexpr int kGroups = kParities * kRowGroups;    // softmax warpgroups
   static constexpr int kSoft = 128 * kGroups;
-  // warpgroups that convert K, and V: up to 16 rows one for even and one for odd tiles
-  static constexpr int kPairs = NR == 16 ? 2 : 1;
+  // warpgroups that convert K, and V: up to 32 rows one for even and one for odd tiles
+  static constexpr int kPairs = NR <= 32 ? 2 : 1;
   // (the last warpgroup: two producers and two issuers, of S and of PV)
   static constexpr int kKWarp = 4 * kGroups, kVWarp = kKWarp + 4 * kPairs, kProducer = kVWarp + 4 * kPairs,
                        kMmaWarp = kProducer + 2;
   static constexpr int kThreads = (kProducer + 4) * 32;
   // Registers a thread: the launch's, and what the warpgroups divide them into.
   static constexpr int kWarpgroups = kGroups + 2 * kPairs + 1;
-  static constexpr int kRegsLaunch = kWarpgroups == 5 ? 96 : 72;
-  static constexpr int kRegsSoft = NR == 16 ? 96 : NR == 32 ? 128 : 88, kRegsKv = NR == 16 ? 64 : NR == 32 ? 80 : 48,
-                       kRegsRest = NR == 32 ? 64 : 56;
+  static constexpr int kRegsLaunch = 72;
+  static constexpr int kRegsSoft = NR == 16 ? 96 : NR == 32 ? 128 : 88, kRegsKv = NR == 16 ? 64 : 48, kRegsRest = 56;
   static_assert(kGroups * kRegsSoft + 2 * kPairs * kRegsKv + kRegsRest <= kWarpgroups * kRegsLaunch,
                 "within the launch's registers");
   static_assert(kThreads * kRegsLaunch <= 65536, "a block's registers");
