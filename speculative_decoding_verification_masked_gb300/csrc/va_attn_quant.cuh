@@ -191,6 +191,9 @@ struct TqSmem {
   static constexpr int kAlphaOff = kRefOff + 2 * NR * 4; // float [2 NR]: what a moved reference scales by; then 1 / l factors
   static constexpr int kKsOff = kAlphaOff + 2 * NR * 4;  // float2 [4][128]: scales of the tile's K and V rows
   static constexpr int kRingOff = (kKsOff + 4 * 1024 + 127) & ~127;
+  // fewest stages, beside the largest plan
+  static constexpr int kStages = (kSmemLimit - 1024 - kRingOff - (kMaxSegments + 1) * 4) / (2 * kRaw);
+  static_assert(kStages >= 2, "a ring");
   static constexpr int kNC = NR < 32 ? 32 : NR;          // TMEM columns per region
   // O (of even and of odd tiles), two S, two K of D/2 columns
   static constexpr int kSCol = TqCfg<NR>::kParities * kNC, kKCol = kSCol + 2 * kNC;
@@ -684,12 +687,12 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     // landed, and been converted, before those of tile j - 1: what comes next in its stage
     // waits until tile j - 1 has left it.  (Two, and any even number: the same warpgroup had
     // the stage.  Five and more: the MMA of tile j - 4, waited for, is behind tile j - 5.)
-    const bool behind = Cfg::kPairs == 2 && p.stages == 3;
+    constexpr bool kBehind = Cfg::kPairs == 2 && SM::kStages <= 3;
     int st = jt0;
-    uint32_t ph = 0;
+    uint32_t ph = 0, row = row0 + jt0 * (2 * SM::kRaw);
     for (int jt = jt0; jt < n; jt += Cfg::kPairs) {
-      const uint32_t b = (uint32_t)jt & 1u, row = row0 + st * (2 * SM::kRaw);
-      if (behind) wait_ok(em + 8 * st, ph ^ 1u);
+      const uint32_t b = (uint32_t)jt & 1u;
+      if constexpr (kBehind) wait_ok(em + 8 * st, ph ^ 1u);
       wait_ok(fl + 8 * st, ph);
       const uint4 tail = lds128(row + QRow<FMT, D>::kCodeBytes);
       const uint32_t sc_now = sc + (jt & 3) * 1024, kb = a_k_full + 8 * (jt & 3);
@@ -737,9 +740,11 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
         mbar_arrive_at(em + 8 * st);
         mbar_arrive_at(is_v ? a_v_full + 8 * b : kb);
       }
+      row += Cfg::kPairs * (2 * SM::kRaw);
       st += Cfg::kPairs;
       if (st >= p.stages) {
         st -= p.stages;
+        row = row0 + st * (2 * SM::kRaw);
         ph ^= 1u;
       }
     }
@@ -1174,13 +1179,12 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// Stages of the ring that fit beside the rest (0: not even two).
+// Stages of the ring that fit beside the rest.
 template <int FMT, int D, int NR>
 static int tq_stages(const AttnParams &p) {
   using SM = TqSmem<FMT, D, NR>;
-  const long long left = (long long)kSmemLimit - 1024 - SM::kRingOff - (long long)(p.S + 1) * 4;
-  const long long n = left / (2 * SM::kRaw);
-  return n < 2 ? 0 : (int)(n > kTqStages ? kTqStages : n);
+  const int n = (kSmemLimit - 1024 - SM::kRingOff - (p.S + 1) * 4) / (2 * SM::kRaw);  // S <= kMaxSegments
+  return n > kTqStages ? kTqStages : n;
 }
 
 template <int FMT, int D, int NR, bool kTma>
@@ -1188,7 +1192,6 @@ static cudaError_t launch_tq_t(AttnParams &p, const CUtensorMap &tmk, const CUte
                                cudaStream_t stream) {
   using SM = TqSmem<FMT, D, NR>;
   p.stages = tq_stages<FMT, D, NR>(p);
-  if (p.stages == 0) return cudaErrorInvalidValue;
   auto kern = verify_attn_quant_kernel<FMT, D, NR, kTma>;
   cudaError_t e = allow_smem(kern);
   if (e != cudaSuccess) return e;

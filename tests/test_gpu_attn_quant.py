@@ -309,6 +309,36 @@ def test_every_block_size_over_many_tiles_from_memory(fmt, D, T, page):
         assert float((lse[0, 4 * h:4 * h + 4].double() - torch.logsumexp(z, -1)).abs().max()) <= LSE
 
 
+@pytest.mark.parametrize("fmt,D", FORMATS)
+@pytest.mark.parametrize("B,T", [(256, 1), (256, 16), (255, 32), (257, 4)])
+def test_as_many_segments_as_a_call_takes(fmt, D, B, T):
+    """2048 segments, whose plan takes 8 KB from the ring of stages; more are refused."""
+    g = torch.Generator("cuda").manual_seed(B)
+    Hq, Hkv, N = 16, 8, 300
+    x = [torch.randn(B, N, Hkv, D, generator=g, device="cuda").bfloat16() for _ in range(2)]
+    cache = [torch.zeros(B, N, Hkv, va.kv_row_bytes(fmt, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    va.verify_quantize_kv_dense(*x, *cache, zero, fmt)
+    k, v = va.verify_dequantize_kv_dense(*cache, zero, fmt, N)
+    q = torch.randn(B, T, Hq, D, generator=g, device="cuda").bfloat16()
+    lens = torch.randint(0, N - T + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    if B * Hkv > 2048:
+        with pytest.raises(va.VerifyAttnError):
+            va.verify_attn_dense_quant(q, *cache, lens, fmt)
+        return
+    out, lse = va.verify_attn_dense_quant(q, *cache, lens, fmt)
+    for b in range(0, B, 13):
+        n = int(lens[b]) + T
+        kb, vb = (y[b, :n].double().repeat_interleave(Hq // Hkv, 1) for y in (k, v))
+        z = torch.einsum("thd,khd->htk", q[b].double(), kb) / D ** 0.5
+        seen = torch.arange(n, device="cuda")[None] <= n - T + torch.arange(T, device="cuda")[:, None]
+        z = z.masked_fill(~seen, -torch.inf)
+        w = torch.softmax(z, -1)
+        want, mag = (torch.einsum("htk,khd->thd", w, y) for y in (vb, vb.abs()))
+        assert float(((out[b].double() - want).abs() - (2.0 ** -8 * want.abs() + 2.0 ** -10 * mag)).max()) <= 0
+        assert float((lse[b].double() - torch.logsumexp(z, -1)).abs().max()) <= LSE
+
+
 def test_bad_lengths_and_pages_are_recorded():
     c = Case(1, "e2m1", 128, [100, 60], 4, 4, 2, 16)
     ws = va.Workspace(16 << 20)
