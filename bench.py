@@ -657,16 +657,17 @@ def rope_oracle_sample(B=4):
 # built from hash to those captured.
 _HEADERS = ['va_common.cuh', 'va_pipeline.cuh', 'va_mod.cuh', 'va_tcgen05.cuh', 'va_kernels.h', 'va_rope_fused.cuh',
             'va_merge.cuh']
-KERNEL_SOURCES = {"tc": ["va_attn_tc.cu"] + _HEADERS, "tck": ["va_attn_tck.cu", "va_attn_tck.cuh"] + _HEADERS}
+KERNEL_SOURCES = {"tc": ["va_attn_tc.cu"] + _HEADERS,
+                  "tck": ["va_attn_tck.cu", "va_attn_tck.cuh", "va_rowreduce.cuh"] + _HEADERS}
 PROFILED_TRAFFIC = {
-    "tree": {"sources": "tc", "sha256": "cd212dcfc4330700094765a269c57c1e244352e368298fa5932e651fe940f722",
-             "kernel": "verify_attn_tc_kernel<2, TMA>", "bytes": 541424896},
-    "chain": {"sources": "tck", "sha256": "ca669ac3fa53988905cf1703fe684493208bb616ebeb0dd52b8adcff48c5af4e",
-              "kernel": "verify_attn_tck_kernel<128, 32, TMA>", "bytes": 137643008},
-    "sparse": {"sources": "tck", "sha256": "ca669ac3fa53988905cf1703fe684493208bb616ebeb0dd52b8adcff48c5af4e",
-               "kernel": "verify_attn_tck_kernel<128, 32, gather>", "bytes": 140987904},
-    "paged": {"sources": "tck", "sha256": "ca669ac3fa53988905cf1703fe684493208bb616ebeb0dd52b8adcff48c5af4e",
-              "kernel": "verify_attn_tck_kernel<128, 64, TMA>", "bytes": 1471213568},
+    "tree": {"sources": "tc", "sha256": "0f769aae2351e72d85c28a5fef1e1168852a22cc83640d8515dde4bd6fd0ca3e",
+             "kernel": "verify_attn_tc_kernel<2, TMA>", "bytes": 541523200},
+    "chain": {"sources": "tck", "sha256": "ad549822f3dfefac898eaa9e4a82fd7487274ac13fa795aee2da95bf89ced1f4",
+              "kernel": "verify_attn_tck_kernel<128, 32, TMA>", "bytes": 137681664},
+    "sparse": {"sources": "tck", "sha256": "ad549822f3dfefac898eaa9e4a82fd7487274ac13fa795aee2da95bf89ced1f4",
+               "kernel": "verify_attn_tck_kernel<128, 32, gather>", "bytes": 141012992},
+    "paged": {"sources": "tck", "sha256": "ad549822f3dfefac898eaa9e4a82fd7487274ac13fa795aee2da95bf89ced1f4",
+              "kernel": "verify_attn_tck_kernel<128, 64, TMA>", "bytes": 1470019072},
 }
 
 
