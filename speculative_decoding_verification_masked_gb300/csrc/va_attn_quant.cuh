@@ -737,7 +737,9 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive_at(em + 8 * st);
+        // (having given up on a wait, it frees no stage: the copies into it may be under way,
+        // and its barrier takes no second announcement before they land)
+        if (ok) mbar_arrive_at(em + 8 * st);
         mbar_arrive_at(is_v ? a_v_full + 8 * b : kb);
       }
       row += Cfg::kPairs * (2 * SM::kRaw);

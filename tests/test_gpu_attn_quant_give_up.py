@@ -60,3 +60,12 @@ def test_a_part_that_never_arrives(form):
     c = Case(3, fmt, D, [9000], T, Hq, Hkv, page, "tree")
     L = va.api.lib()
     _gives_up(c, lambda: L.verify_attn_test_inject(WAIT_NS, 0), lambda: L.verify_attn_test_inject(0, -1))
+
+
+@pytest.mark.parametrize("form", ["16 rows", "32 rows, pages of 16", "32 rows, pages of 2", "64 rows", "128 rows"])
+def test_a_block_with_many_tiles_left_when_it_gives_up(form):
+    """Ten tiles to a block, more than its ring holds: it loads none over copies under way."""
+    fmt, D, T, Hq, Hkv, page = FORMS[form]
+    c = Case(3, fmt, D, [4000 + 37 * i for i in range(24)], T, Hq, Hkv, page, "chain")
+    L = va.api.lib()
+    _gives_up(c, lambda: L.verify_attn_test_stall(WAIT_NS, 5), lambda: L.verify_attn_test_stall(0, -1))
