@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kNormThreads, 8) norm_rope_kernel(const NormPa
     __syncthreads();
   }
   const float inv_d = 1.f / (float)p.D;
+  const bool turned = p.positions != nullptr;
   for (int r0 = r_first; r0 - r_first < rows; r0 += kRows * kPass) {
     if (r0 != r_first) load(r0);
 #pragma unroll
@@ -157,9 +158,13 @@ __global__ void __launch_bounds__(kNormThreads, 8) norm_rope_kernel(const NormPa
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float4 u0 = fac[kind][0][j][c], u1 = fac[kind][1][j][c];
-        const float2 x = fma2(a[j], make_float2(u0.x, u0.y), mul2(e[j], make_float2(u0.z, u0.w)));
-        e[j] = fma2(e[j], make_float2(u1.x, u1.y), mul2(a[j], make_float2(u1.z, u1.w)));
+        float2 x = mul2(a[j], make_float2(u0.x, u0.y)), y = mul2(e[j], make_float2(u1.x, u1.y));
+        if (turned) {  // (without, an infinity stays out of its partner)
+          x = fma2(e[j], make_float2(u0.z, u0.w), x);
+          y = fma2(a[j], make_float2(u1.z, u1.w), y);
+        }
         a[j] = x;
+        e[j] = y;
       }
       T *dst = is_q ? qo + (size_t)r * p.D : ko + (size_t)(r - p.Hq) * p.D;
       Eight<T>::store(dst, reinterpret_cast<const float(&)[8]>(a));

@@ -129,6 +129,22 @@ def test_zero_rows_and_rows_that_are_not_finite():
     assert torch.isfinite(y[rest]).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_without_positions_an_infinity_stays_in_its_place(dtype):
+    """No rotation: what is not finite meets its row's sum of squares, not its partner.  Rows
+    without a weight are copied as they are."""
+    x = torch.randn(2, 3, 6, 128, device="cuda").to(TYPES[dtype])
+    x[0, 1, 2, 7], x[1, 2, 3, 70], x[0, 0, 5, 3], x[1, 1, 4, 90] = (float(s) for s in ("inf", "nan", "-inf", "nan"))
+    x[1, 0, 0, :64], x[1, 0, 1, 64:] = -0.0, -0.0
+    w = torch.ones(128, device="cuda", dtype=x.dtype)
+    q, k = va.verify_norm_rope(x[:, :, :4], x[:, :, 4:], None, w)
+    assert torch.equal(q.nan_to_num(7.0), x[:, :, :4].nan_to_num(7.0)) and torch.equal(q.isnan(), x[:, :, :4].isnan())
+    assert torch.equal(torch.signbit(q) & ~q.isnan(), torch.signbit(x[:, :, :4]) & ~q.isnan())
+    nan = k[0, 0, 1].isnan()
+    assert nan[3] and int(nan.sum()) == 1 and (k[0, 0, 1][~nan] == 0).all()  # (an infinite root)
+    assert k[1, 1, 0].isnan().all()
+
+
 def test_graph_and_refusals():
     x = torch.randn(2, 5, 10, 128, device="cuda").bfloat16()
     q, k = x[:, :, :8], x[:, :, 8:]
