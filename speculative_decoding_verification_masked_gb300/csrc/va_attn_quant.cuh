@@ -47,10 +47,9 @@
 //
 // What bounds it (one GB300; a tile is 20.5 KB of 4-bit rows, 0.44 us of an SM's share of
 // the measured copy rate):
-//   up to 32 rows  the conversion's instructions and its latency, 0.75 to 0.85 us a tile: about
-//                  4000 warp instructions, 1500 of them two conversions' worth of codes; four
-//                  schedulers at two thirds.  64 single-token sequences of 1K to 16K keys in
-//                  64-row pages: 210 us, 3.2 TB/s
+//   up to 32 rows  instructions, 0.65 to 0.8 us a tile: about 4000 of a warp, 1500 of them two
+//                  conversions' worth of codes; four schedulers at 70 to 80%.  64 single-token
+//                  sequences of 1K to 16K keys in 64-row pages: 205 us, 3.3 TB/s
 //   64, 128 rows   the softmax's instructions (8 a score and thread): 64 nodes over 128K keys
 //                  225 us
 //   short calls    12 us of launch, plan, first tile, unit ends and merge, most of it code
@@ -745,8 +744,8 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       row += Cfg::kPairs * (2 * SM::kRaw);
       st += Cfg::kPairs;
       if (st >= p.stages) {
-        st -= p.stages;
-        row = row0 + st * (2 * SM::kRaw);
+        st = Cfg::kPairs == 1 ? 0 : st - p.stages;
+        row = Cfg::kPairs == 1 ? row0 : row0 + st * (2 * SM::kRaw);
         ph ^= 1u;
       }
     }
