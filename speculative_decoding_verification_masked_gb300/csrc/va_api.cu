@@ -132,7 +132,7 @@ bool encode_rows_map(CUtensorMap *m, const void *base, int row_bytes, int Hkv, l
   const cuuint32_t estr[3] = {1, 1, 1};
   auto encode = [&] {
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
   if (encode() == CUDA_SUCCESS) return true;
