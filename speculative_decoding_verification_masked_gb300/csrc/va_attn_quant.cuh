@@ -334,14 +334,17 @@ __device__ __forceinline__ void produce_raw(const AttnParams &p, const CUtensorM
     const Seg g = seg_info(p, s, false);
     int lt0, lt1;
     cr.tiles(tstart, u, lt0, lt1);
-    // the page entry of this lane's box, fetched one tile ahead
+    // Page entries of 32 boxes at a time, a lane each (2 to 32 tiles'), and those of the next
+    // 32 on their way: an entry a tile ahead made a tile take the latency of its load
+    // (64 single-token sequences in 64-row pages: 188 us).
     const int BR = p.tma_box;
-    auto box_page = [&](int lt) {
+    const int boxes = kTma ? TK / BR : 1, ahead = 32 / boxes;  // of a tile; tiles
+    auto box_pages = [&](int lt) {
       const int k = lt * TK + lane * BR;
-      if (!kTma || !paged || lt >= lt1 || lane >= TK / BR || k >= g.nkeys) return 0;
+      if (!kTma || !paged || k >= g.nkeys) return 0;
       return __ldg(p.page_table + (size_t)g.b * p.max_pages + (k >> p.page_shift));
     };
-    int page_next = box_page(lt0);
+    int lt_pages = lt0, pages = box_pages(lt0), pages_next = box_pages(lt0 + ahead);
     // (gather) the rows of the next tile, looked up before this tile's copies are issued
     const uint8_t *rows[TK / 32];
     auto look_up = [&](int lt) {
@@ -353,8 +356,11 @@ __device__ __forceinline__ void produce_raw(const AttnParams &p, const CUtensorM
     };
     if constexpr (!kTma) look_up(lt0);
     for (int lt = lt0; lt < lt1; ++lt, ++it) {
-      const int page_now = page_next;
-      page_next = box_page(lt + 1);
+      if (kTma && lt == lt_pages + ahead) {
+        lt_pages = lt;
+        pages = pages_next;
+        pages_next = box_pages(lt + ahead);
+      }
       if (__builtin_expect(ok && !mbar_sleep(smem_u32(empty + st), ph ^ 1u), 0))
         ok = tq_wait_on(smem_u32(empty + st), ph ^ 1u, abort_flag, p.wait_ns, p.status);
       ok = __all_sync(0xffffffffu, ok);  // (a gather passes addresses between the lanes)
@@ -365,7 +371,8 @@ __device__ __forceinline__ void produce_raw(const AttnParams &p, const CUtensorM
           // dense: one box; rows past the segment's end arrive too (other tokens, or
           // zeros past the cache) and are masked.  Paged: a box a page; boxes that
           // start past the end are not loaded.
-          const int nb = paged ? min(TK / BR, (g.nkeys - k0 + BR - 1) / BR) : 1;
+          const int nb = paged ? min(boxes, (g.nkeys - k0 + BR - 1) / BR) : 1;
+          const int page_now = __shfl_sync(0xffffffffu, pages, ((lt - lt_pages) * boxes + lane) & 31);
           if (lane == 0) mbar_arrive_expect_tx(full + st, (uint32_t)(nb * BR * RB));
           __syncwarp();
           if (lane < nb) {
