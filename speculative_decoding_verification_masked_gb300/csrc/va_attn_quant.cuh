@@ -311,21 +311,6 @@ __device__ __forceinline__ void produce_raw(const AttnParams &p, const CUtensorM
   const int lane = threadIdx.x & 31;
   const uint64_t policy = l2_evict_first_policy();
   const bool paged = p.layout == VA_LAYOUT_PAGED;
-  // the row of key k (gather)
-  auto row_of = [&](const Seg &g, int k) -> const uint8_t * {
-    size_t row;
-    if (paged) {
-      int page = __ldg(p.page_table + (size_t)g.b * p.max_pages + (k >> p.page_shift));
-      if (page < 0 || page >= p.num_pages) {
-        record_status(p.status, VA_ERR_DEVICE_BOUNDS);
-        page = 0;
-      }
-      row = ((size_t)page << p.page_shift) + (k & ((1 << p.page_shift) - 1));
-    } else {
-      row = (size_t)g.b * p.len_cap + k;
-    }
-    return cache + (row * p.Hkv + g.hkv) * RB;
-  };
   bool ok = true;
   int st = 0, it = 0;
   uint32_t ph = 0;
@@ -345,13 +330,15 @@ __device__ __forceinline__ void produce_raw(const AttnParams &p, const CUtensorM
       return __ldg(p.page_table + (size_t)g.b * p.max_pages + (k >> p.page_shift));
     };
     int lt_pages = lt0, pages = box_pages(lt0), pages_next = box_pages(lt0 + ahead);
-    // (gather) the rows of the next tile, looked up before this tile's copies are issued
-    const uint8_t *rows[TK / 32];
+    // (gather) the page entries of a tile's rows, four a lane, on their way while the tile
+    // before is copied: turned into addresses at once, a tile took their latency too (64
+    // single-token sequences in 4-row pages: 503 us)
+    int entries[TK / 32];
     auto look_up = [&](int lt) {
 #pragma unroll
       for (int j = 0; j < TK / 32; ++j) {
         const int k = lt * TK + 32 * j + lane;
-        rows[j] = lt < lt1 && k < g.nkeys ? row_of(g, k) : cache;
+        entries[j] = lt < lt1 && k < g.nkeys ? __ldg(p.page_table + (size_t)g.b * p.max_pages + (k >> p.page_shift)) : 0;
       }
     };
     if constexpr (!kTma) look_up(lt0);
@@ -393,7 +380,16 @@ __device__ __forceinline__ void produce_raw(const AttnParams &p, const CUtensorM
           constexpr int CPR = RB / 16;  // 16-byte chunks of a row
           const uint8_t *now[TK / 32];
 #pragma unroll
-          for (int j = 0; j < TK / 32; ++j) now[j] = rows[j];
+          for (int j = 0; j < TK / 32; ++j) {
+            const int k = k0 + 32 * j + lane;
+            int page = entries[j];
+            if (page < 0 || page >= p.num_pages) {
+              record_status(p.status, VA_ERR_DEVICE_BOUNDS);
+              page = 0;
+            }
+            const size_t row = ((size_t)page << p.page_shift) + (k & ((1 << p.page_shift) - 1));
+            now[j] = cache + (row * p.Hkv + g.hkv) * RB;
+          }
           look_up(lt + 1);
 #pragma unroll
           for (int j = 0; j < TK / 32; ++j) {
