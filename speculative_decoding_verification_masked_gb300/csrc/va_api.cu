@@ -475,7 +475,8 @@ va_status run_attention_quant(const Common &c, va_kv_format format, int layout, 
     p.tma_box = 128;
   } else if (page_size >= 8) {
     // one box a page (at most 128 rows), on a 128-byte boundary of the ring.  Smaller
-    // pages, or a pool the map cannot describe, are gathered.
+    // pages, or a pool the map cannot describe, are gathered.  (Boxes of 8 rows or gathered:
+    // 64 single-token 4-bit sequences 246 or 234 us, of 16 tokens in 8 bits 233 or 277.)
     const int box = page_size < 128 ? page_size : 128;
     if (rows < (1ll << 31) && encode_rows_map(&tmk, k, row, s.Hkv, rows, box) &&
         encode_rows_map(&tmv, v, row, s.Hkv, rows, box))

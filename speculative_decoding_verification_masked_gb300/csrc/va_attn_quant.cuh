@@ -49,7 +49,7 @@
 // the measured copy rate):
 //   up to 32 rows  instructions, 0.65 to 0.8 us a tile: about 4000 of a warp, 1500 of them two
 //                  conversions' worth of codes; four schedulers at 70 to 80%.  64 single-token
-//                  sequences of 1K to 16K keys in 64-row pages: 205 us, 3.3 TB/s
+//                  sequences of 1K to 16K keys in 64-row pages: 190 us, 3.6 TB/s
 //   64, 128 rows   the softmax's instructions (8 a score and thread): 64 nodes over 128K keys
 //                  225 us
 //   short calls    12 us of launch, plan, first tile, unit ends and merge, most of it code
@@ -255,7 +255,7 @@ __device__ __forceinline__ int tq_owner(int t, int total, int G) {
 // CTA c with lane c % lanes and part c / lanes of the lane's tiles, so that what one of
 // them reads of a DRAM page or a cache line the others need at that moment.  With each
 // lane's tiles after the other (lanes = 1: segments are units), 64 single-token
-// sequences over 8192 keys read 1.4 times their bytes from HBM and took 262 us instead of 190.
+// sequences over 8192 keys read 1.4 times their bytes from HBM: 262 us, in step 190 (now 167).
 struct TqRange {
   int units, lanes, lane;  // unit u of this lane is segment u * lanes + lane
   int total, G, part;      // tiles of the lane, parts they are cut into, this CTA's
@@ -321,7 +321,7 @@ __device__ __forceinline__ void produce_raw(const AttnParams &p, const CUtensorM
     cr.tiles(tstart, u, lt0, lt1);
     // Page entries of 32 boxes at a time, a lane each (2 to 32 tiles'), and those of the next
     // 32 on their way: an entry a tile ahead made a tile take the latency of its load
-    // (64 single-token sequences in 64-row pages: 188 us).
+    // (64 single-token sequences over 8192 keys in 64-row pages: 188 us, now 167).
     const int BR = p.tma_box;
     const int boxes = kTma ? TK / BR : 1, ahead = 32 / boxes;  // of a tile; tiles
     auto box_pages = [&](int lt) {
@@ -332,7 +332,7 @@ __device__ __forceinline__ void produce_raw(const AttnParams &p, const CUtensorM
     int lt_pages = lt0, pages = box_pages(lt0), pages_next = box_pages(lt0 + ahead);
     // (gather) the page entries of a tile's rows, four a lane, on their way while the tile
     // before is copied: turned into addresses at once, a tile took their latency too (64
-    // single-token sequences in 4-row pages: 503 us)
+    // single-token sequences over 8192 keys in 4-row pages: 503 us, now 234)
     int entries[TK / 32];
     auto look_up = [&](int lt) {
 #pragma unroll
