@@ -14,8 +14,8 @@
 // 2^14 .. 2^15, and rounded to half: an element keeps all its bits down to 2^-32 of the
 // largest and is off by 2^-40 of it at most.  P is rounded to half: relative 2^-12,
 // an eighth of the half step that the bf16 output is rounded by.  Weights are
-// 2^6 at the row's reference and at most 2^14; P times the ratio of the key's value
-// scale to the largest one seen is exact but below 2^-14, where it is off by 2^-25.
+// 2^6 at the row's reference and at most 2^14; times the ratio of the key's value scale to
+// the largest one seen they are rounded once, below 2^-14 by 2^-25 at most.
 // Scores, row sums, O and the merge are fp32.
 //
 // The softmax reference of a row is its maximum over the first tile and moves when a score
@@ -1007,9 +1007,10 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       if (jt >= 2) wait_ok(a_o_done + 8 * b, (uint32_t)((jt - 2) >> 1) & 1u);
       const uint32_t a_p = a_p0 + b * SM::kPBytes;
       // P^T row of this key: chunk cc holds rows 8cc .. 8cc + 7
-      // a power of two, at most 1 where somebody sees the key (elsewhere it may be anything and
-      // P is 0: the product has to be)
-      const __half2 ratio2 = __float2half2_rn(__saturatef(vsc * rvref));
+      // A power of two, at most 1 where somebody sees the key (elsewhere it may be anything and
+      // P is 0: the product has to be).  It multiplies in fp32: as a half it is 0 below 2^-24,
+      // where its product with a weight is not.
+      const float ratio = __saturatef(vsc * rvref);
 #pragma unroll
       for (int h0 = 0; h0 < NW; h0 += kXRows) {
         if (kXRows != NW) load_scores(h0);
@@ -1023,7 +1024,8 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
             const float2 s2 = add2(make_float2(lsum[r], lsum[r + 1]), make_float2(a, e));
             lsum[r] = s2.x;
             lsum[r + 1] = s2.y;
-            h[q] = half2_bits(__hmul2(__floats2half2_rn(a, e), ratio2));
+            const float2 w2 = mul2(make_float2(a, e), make_float2(ratio, ratio));
+            h[q] = half2_bits(__floats2half2_rn(w2.x, w2.y));
           }
           sts128(a_p ^ ((h0 / 8 + cw) << 4), h[0], h[1], h[2], h[3]);
         }
