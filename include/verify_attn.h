@@ -609,9 +609,10 @@ va_status verify_dequantize_kv_paged(const va_shape *shape, va_kv_format format,
  * out.  The draft rows are in the cache already (verify_quantize_kv_*).  Scores,
  * sums and the merge are fp32; a weight is rounded to half precision (relative
  * 2^-12) before it multiplies its value row, times the row's scale against the
- * largest value scale seen (off by 2^-31 at most, where the row is much smaller),
- * and a query against the largest element of its block of rows (off by 2^-40 of
- * that at most).  B * Hkv * ceil(Hq/Hkv*T / 64) <= 2048.
+ * largest value scale of the keys that the query sees (off by 2^-31 of that at most,
+ * where the row is much smaller; keys that only others of its block of rows see
+ * count from 2^140 times that scale on), and a query against the largest element of
+ * its block of rows (off by 2^-40 of that at most).  B * Hkv * ceil(Hq/Hkv*T / 64) <= 2048.
  * A row that sees no key gets out = 0 and lse = -inf, one that holds a NaN, or sees
  * a key whose row scale is NaN, NaN for both.  What a key that no row sees holds
  * does not matter.

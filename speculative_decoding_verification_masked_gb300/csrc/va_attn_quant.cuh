@@ -15,11 +15,15 @@
 // largest and is off by 2^-40 of it at most.  P is rounded to half: relative 2^-12,
 // an eighth of the half step that the bf16 output is rounded by.  Weights are
 // 2^6 at the row's reference and at most 2^14; times the ratio of the key's value scale to
-// the largest one seen they are rounded once, below 2^-14 by 2^-25 at most.
+// the largest one that the row sees they are rounded once, below 2^-14 by 2^-25 at most.
 // Scores, row sums, O and the merge are fp32.
 //
 // The softmax reference of a row is its maximum over the first tile and moves when a score
-// exceeds it by more than 2^8 in weight, and with it the largest value scale.
+// exceeds it by more than 2^8 in weight, and with it the largest value scale.  The rows of a
+// block see the same keys, and so the same value scales, up to the draft keys.  A tile of those
+// with a larger scale shifts each row's reference by the largest scale that the row sees (with
+// one scale for the block, a draft row of 2^30 on one branch of a tree took all weights of the
+// others): P = weight 2^shift * scale / unit, and the row sums are in units of 2^shift as well.
 //
 // Roles, one CTA per SM, persistent over the stream-K cut of all tiles, cooperative:
 //   softmax    up to 64 rows a warpgroup (64: two) for even and one for odd tiles, so that two
@@ -79,6 +83,11 @@ constexpr int kTqKeys = 128;    // keys per tile
 constexpr int kTqStages = 8;    // most stages of the ring
 constexpr float kTqBias = 6.f;  // log2 of the weight at the reference
 constexpr float kTqMove = 8.f;  // a score this far above the reference moves it
+// References shifted by value scales: the unit is 2^-60 of the largest scale that a row of
+// the block sees, a shift -60 to 60, so that weights and sums stay within fp32.  Rows whose
+// scale is down to 2^-120 of the largest one (2^-140 with the room that halves have below 2^6)
+// lose nothing.
+constexpr float kTqShift = 60.f;
 
 template <int NR>
 struct TqCfg {
@@ -112,6 +121,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 __device__ __forceinline__ float4 lds128f(uint32_t a) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
 __device__ __forceinline__ float2 lds64f(uint32_t a) {
@@ -185,10 +199,11 @@ struct TqSmem {
   static constexpr int kRowMaskOff = kMiscOff + 16;      // u64 [64]: draft visibility rows
   static constexpr int kKeyMaskOff = kRowMaskOff + 512;  // u32 [4][64]: per 32 rows and draft key, the rows that see it
   static constexpr int kRedOff = kKeyMaskOff + 1024;     // float4 [2 NR]: per-warp row maxima and sums of each tile parity
-  static constexpr int kVRedOff = kRedOff + 2 * NR * 16; // float [16]: per-warp largest value scales, Q maxima
-  static constexpr int kRefOff = kVRedOff + 64;          // float [2 NR]: bias less the reference of a row
+  static constexpr int kVRedOff = kRedOff + 2 * NR * 16; // float [2][16]: per-warp largest value scales (also Q maxima), those of the prefix
+  static constexpr int kRefOff = kVRedOff + 128;         // float [2 NR]: bias less the reference of a row
   static constexpr int kAlphaOff = kRefOff + 2 * NR * 4; // float [2 NR]: what a moved reference scales by; then 1 / l factors
-  static constexpr int kKsOff = kAlphaOff + 2 * NR * 4;  // float2 [4][128]: scales of the tile's K and V rows
+  static constexpr int kVRowOff = kAlphaOff + 2 * NR * 4; // float [NR] (one parity): largest value scale that a row has seen
+  static constexpr int kKsOff = kVRowOff + (TqCfg<NR>::kParities == 1 ? NR * 4 : 0);  // float2 [4][128]: scales of the tile's K and V rows
   static constexpr int kRingOff = (kKsOff + 4 * 1024 + 127) & ~127;
   // fewest stages, beside the largest plan
   static constexpr int kStages = (kSmemLimit - 1024 - kRingOff - (kMaxSegments + 1) * 4) / (2 * kRaw);
@@ -233,6 +248,9 @@ __device__ __forceinline__ void codes_to_halves(const uint4 &v, uint32_t two_gro
     for (int i = 0; i < 16; ++i) h[i] = half2_bits(__hmul2(*reinterpret_cast<__half2 *>(h + i), i < 8 ? g0 : g1));
   }
 }
+
+// log2 of a power of two.
+__device__ __forceinline__ float exponent_of(float pow2) { return (float)((__float_as_int(pow2) >> 23) - 127); }
 
 // The row scale out of a row's tail.
 template <int FMT, int D>
@@ -870,7 +888,11 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     float lsum[NW];    // sums of P over this thread's keys
 #pragma unroll
     for (int r = 0; r < NW; ++r) lsum[r] = 0.f;
-    float vref = 0.f, rvref = 0.f;  // largest value scale seen (0: no tile yet), and one over it
+    // unit of the value scales: the largest one seen (0: no tile yet), or below it once rows have
+    // shifts of their own (apart); and one over it
+    float vref = 0.f, rvref = 0.f;
+    [[maybe_unused]] bool apart = false;
+    [[maybe_unused]] float *vrow = reinterpret_cast<float *>(smem + SM::kVRowOff) + r_wg;
     const int skip = PAR == 2 ? (jt ^ par) & 1 : 0, lt_first = lt0 + skip;
     jt += skip;
 
@@ -945,7 +967,8 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
               if (((km >> (h + r)) & 1u) && ref[h + r] == INFINITY) dmax = INFINITY;
           }
         }
-        move = bar_red_or(kBarRed, 128, dmax > kTqBias + kTqMove || (vsc > vref && any));
+        // (two parities: a draft of 64 tokens has one tile in each)
+        move = bar_red_or(kBarRed, 128, dmax > kTqBias + kTqMove || ((vsc > vref || (PAR == 1 && apart)) && any));
       }
       if (__builtin_expect(move, 0)) {
         // the references to the row maxima seen so far, and the value scale to the largest
@@ -965,22 +988,70 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
         {  // (NaN and the scales of keys that nobody sees stay out)
           const uint32_t wm = __reduce_max_sync(0xffffffffu, any && vsc == vsc ? __float_as_uint(vsc) : 0u);
           if (lane == 0) vred[warp] = __uint_as_float(wm);
+          if (NR <= 32 && masked) {  // of the prefix, which every row sees
+            const bool prefix = lt * TK + ktid < g.n_prefix;
+            const uint32_t wp = __reduce_max_sync(0xffffffffu, prefix && vsc == vsc ? __float_as_uint(vsc) : 0u);
+            if (lane == 0) vred[16 + warp] = __uint_as_float(wp);
+          }
         }
         named_bar_sync(kBarRed, 128);
+        const float vtile = fmaxf(fmaxf(vred[4 * wg], vred[4 * wg + 1]), fmaxf(vred[4 * wg + 2], vred[4 * wg + 3]));
+        const bool shift = masked && (first || (PAR == 1 && apart) || vtile > vref);
+        float vnew = fmaxf(fmaxf(vref, vtile), 0x1p-126f);
+        if (shift) vnew = fmaxf(fmaxf(PAR == 1 && apart ? vref : vref * 0x1p-60f, vtile * 0x1p-60f), 0x1p-126f);
+        float up = 0.f, vmax = 0x1p-126f;  // of row ktid: its largest score above the reference (or zero), its largest value scale
         if (ktid < NW) {
           const float4 m4 = my_red[ktid];
-          const float up = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)) - kTqBias;  // above the reference (or zero)
+          up = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)) - kTqBias;
+        }
+        if (__builtin_expect(shift, 0)) {
+          // Largest value scale of the tile's keys that a row sees (NaN stays out).  Up to 32 rows
+          // the row's own thread goes through the draft keys, above a reduction over the keys as
+          // for the scores.  (What this block does to the registers of the loop around it: one
+          // token over 131072 4-bit keys 46.2 us, with the reduction 47.5, 64 sequences of one
+          // token over 8192 keys 168 and 173; 16 tokens over 8-bit keys 79.6 and 76.6, 64 over
+          // 4-bit keys 222 and 216.)
+          if constexpr (NR <= 32) {
+            const float4 pre = *reinterpret_cast<const float4 *>(vred + 16 + 4 * wg);
+            const int d0 = g.n_prefix - lt * TK;  // the tile's first draft key
+            uint32_t a_sc = a_scale + (jt & 3) * 1024 - ktid * 8 + max(d0, 0) * 8 + 4;
+            uint32_t a_km = smem_a + SM::kKeyMaskOff + 256 * rg + max(-d0, 0) * 4;
+            vmax = fmaxf(fmaxf(pre.x, pre.y), fmaxf(pre.z, pre.w));
+            if (ktid < NW) {
+#pragma unroll 1
+              for (int i = min(d0 + p.T, TK) - max(d0, 0); i > 0; --i, a_sc += 8, a_km += 4)
+                if ((lds32(a_km) >> ktid) & 1u) vmax = fmaxf(vmax, __uint_as_float(lds32(a_sc)));
+            }
+          } else {
+            named_bar_sync(kBarRed, 128);  // (the maxima of the scores have been read)
+#pragma unroll
+            for (int h = 0; h < NW; h += kXRows) {
+#pragma unroll
+              for (int r = 0; r < kXRows; ++r) x[r] = ((km >> (h + r)) & 1u) && vsc == vsc ? vsc : 0.f;
+              WarpScatterMax<kXRows, 16>::run(x, lane);
+              if ((lane & (32 / kXRows - 1)) == 0)
+                reinterpret_cast<float *>(my_red + h)[(lane / (32 / kXRows)) * 4 + wq] = x[0];
+            }
+            named_bar_sync(kBarRed, 128);
+            const float4 m4 = my_red[ktid & (NW - 1)];
+            vmax = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+          }
+          vmax = fmaxf(fmaxf(vmax, 0x1p-126f), PAR == 1 && apart ? vrow[ktid & (NW - 1)] : vref);
+        }
+        if (ktid < NW) {
           const float old = first ? INFINITY : ref[ktid];
           const bool none = old == INFINITY;
-          const float now = none ? kTqBias - up : old - fmaxf(up, 0.f);
+          const float was = PAR == 1 && apart ? fminf(exponent_of(vref) - exponent_of(vrow[ktid]), kTqShift) : 0.f;
+          const float is = shift ? fminf(exponent_of(vnew) - exponent_of(vmax), kTqShift) : 0.f;
+          const float now = (none ? kTqBias - up : old - was - fmaxf(up - was, 0.f)) + is;
           alpha[ktid] = none ? 0.f : ex2_approx(now - old);
           ref[ktid] = now;
+          if (PAR == 1 && shift) vrow[ktid] = vmax;
         }
-        const float vtile = fmaxf(fmaxf(vred[4 * wg], vred[4 * wg + 1]), fmaxf(vred[4 * wg + 2], vred[4 * wg + 3]));
-        const float vnew = fmaxf(fmaxf(vref, vtile), 0x1p-126f);
         const float vdown = vref * (1.f / vnew);
         vref = vnew;
         rvref = 1.f / vref;
+        if (PAR == 1) apart = shift;
         named_bar_sync(kBarRed, 128);
         if (!first) {
 #pragma unroll
@@ -1007,10 +1078,10 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       if (jt >= 2) wait_ok(a_o_done + 8 * b, (uint32_t)((jt - 2) >> 1) & 1u);
       const uint32_t a_p = a_p0 + b * SM::kPBytes;
       // P^T row of this key: chunk cc holds rows 8cc .. 8cc + 7
-      // A power of two, at most 1 where somebody sees the key (elsewhere it may be anything and
-      // P is 0: the product has to be).  It multiplies in fp32: as a half it is 0 below 2^-24,
-      // where its product with a weight is not.
-      const float ratio = __saturatef(vsc * rvref);
+      // A power of two, at most 2^60 where somebody sees the key (elsewhere it may be anything
+      // and P is 0: the product has to be).  It multiplies in fp32: as a half it is 0 below
+      // 2^-24, where its product with a weight is not.
+      const float ratio = fminf(fabsf(vsc * rvref), 0x1p60f);
 #pragma unroll
       for (int h0 = 0; h0 < NW; h0 += kXRows) {
         if (kXRows != NW) load_scores(h0);

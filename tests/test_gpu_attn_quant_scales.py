@@ -93,3 +93,23 @@ def test_a_large_value_row_of_next_to_no_weight(fmt, D, T, Hq, Hkv, up):
     q = (1 + 0.3 * rng.standard_normal((2, T, Hq, D))).astype(np.float32)
     c = Case(up, fmt, D, [40, 333], T, Hq, Hkv, 0, "chain", keys, vals, q)
     check(c, *c.run())
+
+
+@pytest.mark.parametrize("fmt,D", FORMATS)
+@pytest.mark.parametrize("T,Hq,Hkv", BLOCKS)
+@pytest.mark.parametrize("mode", ["tree", "mask"])
+@pytest.mark.parametrize("up", [15, 30, 100])
+def test_large_value_rows_on_other_branches(fmt, D, T, Hq, Hkv, mode, up):
+    """Draft rows that some rows of a block see and others do not, with values 2^15 to 2^100
+    times the others': a row is as exact as the keys that it sees let it be.  Prefixes that put
+    the draft into the first tile, into two tiles, and into parts of a split segment."""
+    def vals(rng, n):
+        x = rng.standard_normal((n, Hkv, D))
+        f = np.zeros(T)
+        for t, more in ((2, up), (T // 2, up / 2), (T - 1, up)):
+            f[t] += more
+        x[n - T:] *= (2.0 ** np.minimum(f, 100))[:, None, None]  # (2^150 is past the row scale's fp32)
+        return x
+
+    c = Case(up + T, fmt, D, [0, 100, 300, 4500], T, Hq, Hkv, 16 if T == 29 else 0, mode, None, vals)
+    check(c, *c.run())
