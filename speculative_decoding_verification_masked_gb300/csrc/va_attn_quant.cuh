@@ -83,11 +83,12 @@ constexpr int kTqKeys = 128;    // keys per tile
 constexpr int kTqStages = 8;    // most stages of the ring
 constexpr float kTqBias = 6.f;  // log2 of the weight at the reference
 constexpr float kTqMove = 8.f;  // a score this far above the reference moves it
-// References shifted by value scales: the unit is 2^-60 of the largest scale that a row of
-// the block sees, a shift -60 to 60, so that weights and sums stay within fp32.  Rows whose
-// scale is down to 2^-120 of the largest one (2^-140 with the room that halves have below 2^6)
-// lose nothing.
-constexpr float kTqShift = 60.f;
+// References shifted by value scales: the unit is the largest scale that a row of the block
+// sees, or 2^40, and a shift at most 2^80, so that weights and sums stay within fp32 (2^30 keys of
+// weight 2^14).  A row whose own scale is above 2^-80 of the unit, 2^-100 with the room that
+// halves have below 2^6, loses nothing.  (With the unit at 2^-60 of the largest, shifts of 60
+// everywhere, the lse of every short sequence was off by up to 7e-6.)
+constexpr float kTqShift = 80.f, kTqUnit = 0x1p40f;
 
 template <int NR>
 struct TqCfg {
@@ -888,8 +889,8 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
     float lsum[NW];    // sums of P over this thread's keys
 #pragma unroll
     for (int r = 0; r < NW; ++r) lsum[r] = 0.f;
-    // unit of the value scales: the largest one seen (0: no tile yet), or below it once rows have
-    // shifts of their own (apart); and one over it
+    // unit of the value scales: the largest one seen (0: no tile yet), at most kTqUnit once rows
+    // have shifts of their own (apart); and one over it
     float vref = 0.f, rvref = 0.f;
     [[maybe_unused]] bool apart = false;
     [[maybe_unused]] float *vrow = reinterpret_cast<float *>(smem + SM::kVRowOff) + r_wg;
@@ -998,7 +999,7 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
         const float vtile = fmaxf(fmaxf(vred[4 * wg], vred[4 * wg + 1]), fmaxf(vred[4 * wg + 2], vred[4 * wg + 3]));
         const bool shift = masked && (first || (PAR == 1 && apart) || vtile > vref);
         float vnew = fmaxf(fmaxf(vref, vtile), 0x1p-126f);
-        if (shift) vnew = fmaxf(fmaxf(PAR == 1 && apart ? vref : vref * 0x1p-60f, vtile * 0x1p-60f), 0x1p-126f);
+        if (shift) vnew = fminf(vnew, kTqUnit);
         float up = 0.f, vmax = 0x1p-126f;  // of row ktid: its largest score above the reference (or zero), its largest value scale
         if (ktid < NW) {
           const float4 m4 = my_red[ktid];
@@ -1078,10 +1079,10 @@ __global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
       if (jt >= 2) wait_ok(a_o_done + 8 * b, (uint32_t)((jt - 2) >> 1) & 1u);
       const uint32_t a_p = a_p0 + b * SM::kPBytes;
       // P^T row of this key: chunk cc holds rows 8cc .. 8cc + 7
-      // A power of two, at most 2^60 where somebody sees the key (elsewhere it may be anything
+      // A power of two, at most 2^80 where somebody sees the key (elsewhere it may be anything
       // and P is 0: the product has to be).  It multiplies in fp32: as a half it is 0 below
       // 2^-24, where its product with a weight is not.
-      const float ratio = fminf(fabsf(vsc * rvref), 0x1p60f);
+      const float ratio = fminf(fabsf(vsc * rvref), 0x1p80f);
 #pragma unroll
       for (int h0 = 0; h0 < NW; h0 += kXRows) {
         if (kXRows != NW) load_scores(h0);

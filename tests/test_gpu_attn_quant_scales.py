@@ -113,3 +113,12 @@ def test_large_value_rows_on_other_branches(fmt, D, T, Hq, Hkv, mode, up):
 
     c = Case(up + T, fmt, D, [0, 100, 300, 4500], T, Hq, Hkv, 16 if T == 29 else 0, mode, None, vals)
     check(c, *c.run())
+
+
+@pytest.mark.parametrize("fmt,D", FORMATS)
+@pytest.mark.parametrize("T,Hq,Hkv", BLOCKS)
+def test_short_sequences_keep_their_lse(fmt, D, T, Hq, Hkv):
+    """Small scores over a few keys, where the bar of an lse is 2^-20 and little more."""
+    q = (2.0 ** -7 * np.random.default_rng(T).standard_normal((5, T, Hq, D))).astype(np.float32)
+    c = Case(T, fmt, D, [0, 1, 9, 70, 200], T, Hq, Hkv, 0, "tree", None, None, q)
+    check(c, *c.run())
