@@ -608,11 +608,11 @@ va_status verify_dequantize_kv_paged(const va_shape *shape, va_kv_format format,
  * lengths, workspace (verify_attn_workspace_size), outputs and errors; bf16 q and
  * out.  The draft rows are in the cache already (verify_quantize_kv_*).  Scores,
  * sums and the merge are fp32; a weight is rounded to half precision (relative
- * 2^-12) before it multiplies its value row, times the row's scale against the
+ * 2^-11) before it multiplies its value row, times the row's scale against the
  * largest value scale of the keys that the query sees (off by 2^-31 of that at most,
  * where the row is much smaller; keys that it does not see have no part in it while that
  * scale is above 2^-60, or 2^-100 of theirs), and a query against the largest element
- * of its block of rows (off by 2^-40 of that at most).  B * Hkv * ceil(Hq/Hkv*T / 64) <= 2048.
+ * of its block of rows (off by 2^-39 of that at most).  B * Hkv * ceil(Hq/Hkv*T / 64) <= 2048.
  * A row that sees no key gets out = 0 and lse = -inf, one that holds a NaN, or sees
  * a key whose row scale is NaN, NaN for both.  What a key that no row sees holds
  * does not matter.

@@ -11,9 +11,9 @@
 // one thread), and a key's P for the value row.  Nothing of a row is read twice.
 //
 // Roundings.  Q is scaled by one power of two for the block, its largest element to
-// 2^14 .. 2^15, and rounded to half: an element keeps all its bits down to 2^-32 of the
-// largest and is off by 2^-40 of it at most.  P is rounded to half: relative 2^-12,
-// an eighth of the half step that the bf16 output is rounded by.  Weights are
+// 2^14 .. 2^15, and rounded to half: an element keeps all its 8 bits down to 2^-31 of the
+// largest and is off by 2^-39 of it at most (2^-25 of 2^14).  P is rounded to half: relative
+// 2^-11, an eighth of the 2^-8 that the bf16 output is rounded by.  Weights are
 // 2^6 at the row's reference and at most 2^14; times the ratio of the key's value scale to
 // the largest one that the row sees they are rounded once, below 2^-14 by 2^-25 at most.
 // Scores, row sums, O and the merge are fp32.

@@ -115,6 +115,46 @@ def test_large_value_rows_on_other_branches(fmt, D, T, Hq, Hkv, mode, up):
     check(c, *c.run())
 
 
+def quiet_keys(D, loud):
+    """Keys that are zero in their first `loud` elements."""
+    def keys(rng, n, Hkv=2):
+        x = rng.standard_normal((n, Hkv, D))
+        x[..., :loud] = 0
+        return x
+
+    return keys
+
+
+@pytest.mark.parametrize("fmt,D", FORMATS)
+@pytest.mark.parametrize("T,Hq,Hkv", BLOCKS)
+@pytest.mark.parametrize("top", [10, 20, 30])
+def test_queries_of_very_different_size_in_a_block(fmt, D, T, Hq, Hkv, top):
+    """Rows whose largest elements are 1 to 2^top times those that meet a key: one power of two
+    for a block of rows leaves the small ones what the documented 2^-39 of its largest does."""
+    rng = np.random.default_rng(top + T)
+    q = rng.standard_normal((3, T, Hq, D)).astype(np.float32)
+    q[..., :16] *= 2.0 ** rng.choice([0, top // 2, top - 1, top], size=(3, T, Hq, 1))
+    q[:, :, ::2, 16:] *= 2.0 ** -5
+    c = Case(top * T, fmt, D, [0, 77, 2500], T, Hq, Hkv, 0, "tree", lambda rng, n: quiet_keys(D, 16)(rng, n, Hkv), None, q)
+    check(c, *c.run())
+
+
+@pytest.mark.parametrize("fmt,D", FORMATS)
+def test_the_worst_rounding_of_a_query(fmt, D):
+    """An element of 1.5 2^-38 beside one of 1: half a unit of the scaled query, 2^-39 of the
+    largest, in a score that is nothing else."""
+    q = np.zeros((1, 1, 1, D), np.float32)
+    q[..., 0], q[..., 1] = 1, 1.5 * 2.0 ** -38
+
+    def keys(rng, n):
+        x = np.zeros((n, 1, D))
+        x[..., 1] = 1
+        return x
+
+    c = Case(1, fmt, D, [0], 1, 1, 1, 0, "chain", keys, None, q)
+    check(c, *c.run(scale=2.0 ** 38), scale=2.0 ** 38)
+
+
 @pytest.mark.parametrize("fmt,D", FORMATS)
 @pytest.mark.parametrize("T,Hq,Hkv", BLOCKS)
 def test_short_sequences_keep_their_lse(fmt, D, T, Hq, Hkv):
