@@ -156,6 +156,28 @@ def test_the_worst_rounding_of_a_query(fmt, D):
 
 
 @pytest.mark.parametrize("fmt,D", FORMATS)
+@pytest.mark.parametrize("L,T,Hq,Hkv", [(300, 4, 4, 2), (20, 40, 4, 2), (20000, 4, 4, 2), (20000, 16, 8, 2), (20000, 64, 4, 1)])
+@pytest.mark.parametrize("name", ["k", "v"])
+@pytest.mark.parametrize("where", ["prefix", "draft"])
+def test_a_key_stored_as_nan_reaches_out_and_lse(fmt, D, L, T, Hq, Hkv, name, where):
+    """A key or value row whose scale is NaN makes out and lse NaN in every row that sees it,
+    through the parities' join and the merge of a split segment, and in no other."""
+    c = Case(L + T, fmt, D, [L, 33], T, Hq, Hkv, 0, "chain")
+    plain, plain_lse = (x.clone() for x in c.run())
+    at = Q.row_bytes(fmt, D) - 16 + (0 if fmt == "e4m3" else D // 16)
+    slot = L // 2 if where == "prefix" else L + 2
+    row = c.cache[name][0, slot, Hkv - 1]
+    row[:] = 0
+    row[at:at + 4] = torch.tensor([0, 0, 192, 127], dtype=torch.uint8)
+    out, lse = c.run()
+    want = torch.zeros(2, T, Hq, dtype=torch.bool, device="cuda")
+    want[0, 0 if where == "prefix" else 2:, Hq - Hq // Hkv:] = True
+    assert torch.equal(torch.isnan(out).all(-1), want) and torch.equal(torch.isnan(out).any(-1), want)
+    assert torch.equal(torch.isnan(lse), want.transpose(1, 2))
+    assert torch.equal(out[~want], plain[~want]) and torch.equal(lse.transpose(1, 2)[~want], plain_lse.transpose(1, 2)[~want])
+
+
+@pytest.mark.parametrize("fmt,D", FORMATS)
 @pytest.mark.parametrize("T,Hq,Hkv", BLOCKS)
 def test_short_sequences_keep_their_lse(fmt, D, T, Hq, Hkv):
     """Small scores over a few keys, where the bar of an lse is 2^-20 and little more."""
