@@ -13,9 +13,10 @@
 // its instructions, not by HBM, and went from 94 to 63 us (5.4 TB/s, 79% of the measured copy
 // rate; weights and angles of a pair apart, in registers, before).  Rows are loaded kRows at a time, before the factors are known.
 //
-// Angles: base^(-2i/D) / 2 pi comes from the host as a 64-bit binary fraction; its
-// product with the position modulo 2^64 is the phase modulo one turn, exact to 2^-34
-// of a turn for any 32-bit position, without a 64-bit float on the device.
+// Angles: base^(-2i/D) / 2 pi comes from the host as a binary fraction, good to 2^-55 (a
+// double; base >= 1), in 64 bits; its product with the position modulo 2^64 is the phase
+// modulo one turn, off by |position| 2^-55 for any 32-bit position, without a 64-bit float on
+// the device.  The phase is cut to 32 bits (2^-32 of a turn) and rounded to fp32 (2^-26).
 #include "va_common.cuh"
 #include "va_quant.h"
 

@@ -1,0 +1,37 @@
+"""The angles of the norm with rotation: unit vectors come back as cosine and sine.
+
+Bar, from the arithmetic: an angle is off by at most 2^-26 + 2^-32 + |position| 2^-55 of a
+turn, 2 pi as much in either result, its cosine and sine by 2^-23 (two units below 1);
+the factors 1 and 0 that they meet round nothing.  The fp64 angle of the reference is
+reduced by whole turns first (|position| 2^-53 of it at most, and the same for its frequency).
+"""
+import numpy as np
+import pytest
+import torch
+
+import speculative_decoding_verification_masked_gb300 as va
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # collected on CPU-only machines, skipped there
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+
+@pytest.mark.parametrize("D", [16, 128, 256])
+@pytest.mark.parametrize("base", [10000.0, 500000.0])
+@pytest.mark.parametrize("lo,hi", [(0, 1 << 10), (0, 1 << 20), (-(1 << 24), 1 << 24), (-(1 << 31), 1 << 31)])
+def test_angles(D, base, lo, hi):
+    rng = np.random.default_rng(D)
+    T = 5000
+    p = rng.integers(lo, hi, size=(1, T)).astype(np.int32)
+    p[0, :4] = [lo, hi - 1, 1, 0]
+    x = torch.zeros(1, T, 2, D, device="cuda")
+    x[..., : D // 2] = 1  # (1, 0) in every pair: (cos, sin)
+    q, k = va.verify_norm_rope(x[:, :, :1], x[:, :, 1:], positions=torch.from_numpy(p).cuda(), rope_base=base)
+    assert torch.equal(q, k)
+    got = q[0, :, 0].double().cpu().numpy()
+    turns = np.longdouble(base) ** (-2 * np.arange(D // 2, dtype=np.longdouble) / D) / (2 * np.longdouble(np.pi))
+    ang = 2 * np.pi * np.fmod(p[0, :, None].astype(np.float64) * turns.astype(np.float64), 1.0)
+    bar = 2 * np.pi * (2.0 ** -26 + 2.0 ** -32 + np.abs(p[0, :, None].astype(np.float64)) * (2.0 ** -55 + 2.0 ** -53 + 2.0 ** -53)) + 2.0 ** -23
+    assert (np.abs(got[:, : D // 2] - np.cos(ang)) <= bar).all()
+    assert (np.abs(got[:, D // 2:] - np.sin(ang)) <= bar).all()
