@@ -517,13 +517,13 @@ va_status verify_evict_kv_paged(const va_shape *shape, void *k_pages, void *v_pa
  *   y = x / sqrt(mean(x^2) + eps) * weight       (the head's weight given)
  *   y rotated as verify_rope_draft_* rotates     (positions given)
  * with q_weight for the query heads and k_weight for the key heads, each [D] of
- * the element type; NULL leaves those rows unnormed.  positions [B][T] int32,
+ * the element type, 16-byte aligned; NULL leaves those rows unnormed.  positions [B][T] int32,
  * any value; NULL rotates nothing.  Angles are good to 2^-26 + 2^-32 + |position| 2^-55
  * of a turn (rope_base >= 1): rounded to fp32, cut to 32 bits, and the 53 bits of a
  * frequency.
  *   shape: B, T, Hq, Hkv, D, dtype bf16 or fp32 and rope_base (read with
  *     positions); any T with B * T < 2^31; D a multiple of 16, at most 256; Hq
- *     and Hkv need not divide.  scale is not used.
+ *     and Hkv need not divide, Hq + Hkv <= 65536.  scale is not used.
  *   q, k and the outputs are rows of D elements, 16-byte aligned; head h of
  *     token t of sequence b starts (b * batch stride + t * token stride + h * D)
  *     elements from the pointer, strides in elements and such that every row is
