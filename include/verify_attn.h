@@ -528,6 +528,9 @@ va_status verify_evict_kv_paged(const va_shape *shape, void *k_pages, void *v_pa
  *     token t of sequence b starts (b * batch stride + t * token stride + h * D)
  *     elements from the pointer, strides in elements and such that every row is
  *     16-byte aligned (q and k may lie side by side in one projection's output).
+ *     Strides are in [0, 2^40]; those of an output put no two rows in one place:
+ *     the tokens of a sequence lie apart and before the next sequence's, or the
+ *     sequences of a token before the next token's.
  *     An output may be its own input, with the same strides; any other overlap
  *     of outputs and inputs is undefined.
  */

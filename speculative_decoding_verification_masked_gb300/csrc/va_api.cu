@@ -764,8 +764,9 @@ va_status check_rows(const va_rows *r, const char *name, const va_shape &s, int 
     return fail(VA_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned", name);
   if (written) {
     const int64_t row = (int64_t)heads * s.D;
+    // one sequence behind the other's last token, or one token behind the other's last sequence
     const bool apart = (s.T == 1 || tok >= row) && (s.B == 1 || bat >= row) &&
-                       (s.T == 1 || s.B == 1 || bat / s.T >= tok || tok / s.B >= bat);
+                       (s.T == 1 || s.B == 1 || (bat - row) / (s.T - 1) >= tok || (tok - row) / (s.B - 1) >= bat);
     if (!apart) return fail(VA_ERR_INVALID_ARG, "%s: the strides put rows in one place", name);
   }
   out = {r->ptr, (long long)bat, (long long)tok};

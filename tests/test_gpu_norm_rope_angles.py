@@ -35,3 +35,24 @@ def test_angles(D, base, lo, hi):
     bar = 2 * np.pi * (2.0 ** -26 + 2.0 ** -32 + np.abs(p[0, :, None].astype(np.float64)) * (2.0 ** -55 + 2.0 ** -53 + 2.0 ** -53)) + 2.0 ** -23
     assert (np.abs(got[:, : D // 2] - np.cos(ang)) <= bar).all()
     assert (np.abs(got[:, D // 2:] - np.sin(ang)) <= bar).all()
+
+
+@pytest.mark.parametrize("token_major", [False, True])
+def test_outputs_without_room_behind_the_last_row(token_major):
+    """Output rows with gaps between them and none behind the last: what lies in the gaps stays."""
+    B, T, H, D, gap = 3, 5, 4, 64, 32
+    row = H * D
+    near, far = row + gap, ((B if token_major else T) - 1) * (row + gap) + row
+    strides = (near, far, D, 1) if token_major else (far, near, D, 1)
+    x = torch.randn(B, T, 2 * H, D, device="cuda").bfloat16()
+    w = torch.ones(D, device="cuda").bfloat16()
+    pos = torch.arange(B * T, dtype=torch.int32, device="cuda").view(B, T)
+    want = va.verify_norm_rope(x[:, :, :H], x[:, :, H:], w, w, pos)
+    size = 1 + (B - 1) * strides[0] + (T - 1) * strides[1] + row - 1
+    flat = torch.full((2, size + 16), 7.0, device="cuda").bfloat16()
+    out = [f[:size].as_strided((B, T, H, D), strides) for f in flat]
+    va.verify_norm_rope(x[:, :, :H], x[:, :, H:], w, w, pos, q_out=out[0], k_out=out[1])
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    for f, o in zip(flat, out):
+        o.fill_(7.0)
+        assert (f == 7.0).all()
