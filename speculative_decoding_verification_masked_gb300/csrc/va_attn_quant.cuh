@@ -90,7 +90,7 @@ constexpr float kTqMove = 8.f;  // a score this far above the reference moves it
 // everywhere, the lse of every short sequence was off by up to 7e-6.)
 constexpr float kTqShift = 80.f, kTqUnit = 0x1p40f;
 
-template <int NR>
+template <int NR, bool kTma = true>
 struct TqCfg {
   static constexpr int kRowGroups = NR > 32 ? NR / 32 : 1;  // of NW rows, each with
   static constexpr int kParities = NR > 64 ? 1 : 2;         // one warpgroup, or one for even and one for odd tiles
@@ -106,7 +106,11 @@ struct TqCfg {
   // Registers a thread: the launch's, and what the warpgroups divide them into.
   static constexpr int kWarpgroups = kGroups + 2 * kPairs + 1;
   static constexpr int kRegsLaunch = 72;
-  static constexpr int kRegsSoft = NR == 16 ? 96 : NR == 32 ? 128 : 88, kRegsKv = NR == 16 ? 64 : 48, kRegsRest = 56;
+  // (128 rows with 88, 48 and 56: 64 tokens over 131072 4-bit keys 218 us; with 96, 40 and 40
+  // 208, but gathers, whose addresses live in the rest, 269 instead of 251 over 2 x 65536 keys)
+  static constexpr bool kWide = NR == 128 && kTma;
+  static constexpr int kRegsSoft = NR == 16 ? 96 : NR == 32 ? 128 : kWide ? 96 : 88,
+                       kRegsKv = NR == 16 ? 64 : kWide ? 40 : 48, kRegsRest = kWide ? 40 : 56;
   static_assert(kGroups * kRegsSoft + 2 * kPairs * kRegsKv + kRegsRest <= kWarpgroups * kRegsLaunch,
                 "within the launch's registers");
   static_assert(kThreads * kRegsLaunch <= 65536, "a block's registers");
@@ -536,11 +540,11 @@ __device__ __forceinline__ void merge_rows_compact(const AttnParams &p, int b, i
 }
 
 template <int FMT, int D, int NR, bool kTma>
-__global__ void __launch_bounds__(TqCfg<NR>::kThreads, 1)
+__global__ void __launch_bounds__(TqCfg<NR, kTma>::kThreads, 1)
     verify_attn_quant_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
                              const __grid_constant__ CUtensorMap tmv) {
   using SM = TqSmem<FMT, D, NR>;
-  using Cfg = TqCfg<NR>;
+  using Cfg = TqCfg<NR, kTma>;
   constexpr int TK = kTqKeys, NC = SM::kNC, WG = Cfg::kGroups, RG = Cfg::kRowGroups, PAR = Cfg::kParities, NW = Cfg::NW, kSoft = Cfg::kSoft,
                 RB = SM::kRow;
   constexpr int kXRows = NR > 32 ? 16 : NW;  // scores a softmax thread holds at once (registers)
