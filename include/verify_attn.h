@@ -616,7 +616,8 @@ va_status verify_dequantize_kv_paged(const va_shape *shape, va_kv_format format,
  * largest value scale of the keys that the query sees (off by 2^-31 of that at most,
  * where the row is much smaller; keys that it does not see have no part in it while that
  * scale is above 2^-60, or 2^-100 of theirs), and a query against the largest element
- * of its block of rows (off by 2^-39 of that at most).  B * Hkv * ceil(Hq/Hkv*T / 64) <= 2048.
+ * of its block of rows (off by 2^-39 of that at most).  B * Hkv * ceil(Hq/Hkv*T / 64) <= 2048
+ * (/ 128 for 4-bit rows of D 128 where Hq/Hkv*T > 64).
  * A row that sees no key gets out = 0 and lse = -inf, one that holds a NaN, or sees
  * a key whose row scale is NaN, NaN for both.  What a key that no row sees holds
  * does not matter.

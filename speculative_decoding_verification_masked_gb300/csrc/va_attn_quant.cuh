@@ -49,15 +49,19 @@
 // two warpgroups: of tile j) or S of tile j + 2 (K), which come after the softmax of tile j.
 // Every wait is bounded; a role that gives up goes on without waiting.
 //
-// What bounds it (one GB300; a tile is 20.5 KB of 4-bit rows, 0.44 us of an SM's share of
-// the measured copy rate):
-//   up to 32 rows  instructions, 0.65 to 0.8 us a tile: about 4000 of a warp, 1500 of them two
-//                  conversions' worth of codes; four schedulers at 70 to 80%.  64 single-token
-//                  sequences of 1K to 16K keys in 64-row pages: 190 us, 3.6 TB/s
-//   64, 128 rows   the softmax's instructions (8 a score and thread): 64 nodes over 128K keys
-//                  225 us
-//   short calls    12 us of launch, plan, first tile, unit ends and merge, most of it code
-//                  fetched for the first time (8 tokens over 32K keys: 25 us, ten of them tiles)
+// What bounds it (one GB300; a tile is 20.5 KB of 4-bit rows, 0.44 us of an SM's share of the
+// measured copy rate): neither bytes nor tensor cores, but the warp instructions of a tile and
+// the waits between its roles.  131072 keys, 8 kv-heads; instructions a tile and the part of the
+// schedulers' slots that issue (profiled; long scoreboard is the largest stall of all):
+//   16 rows    3780, 58%: one token 47 us (over a 16-bit cache 83)
+//   32 rows    4150, 49%: 8 tokens 55 us (84)
+//   64 rows    5590, 48%: 16 tokens 77 us over 8-bit rows, 82 over 4-bit ones (89)
+//   128 rows   8690, 62%: 64 tokens 208 us (108: there a thread has a row, one sum and one
+//              reference, and nothing is converted; over 8 bits four blocks of 64 rows, 268)
+//   short calls  12 us of launch, plan, first tile, unit ends and merge, most of it code
+//              fetched for the first time (8 tokens over 32K keys: 24.6 us, ten of them tiles)
+// Above 16 rows the softmax spills (48 to 112 bytes of stores in the code), 10 to 24 of a tile's
+// instructions, 88 with 128 rows.
 // Steps that led here, 131072 keys, 8 kv-heads, 4 bits, one token / 8 / 64 tokens in us:
 // one softmax warpgroup of 32 rows, everything unrolled 75 / 83 / 352; two issuers and
 // descriptors in uniform registers 53 / 62 / 283; parities, 32-bit shared addresses, waits
@@ -278,7 +282,7 @@ __device__ __forceinline__ int tq_owner(int t, int total, int G) {
 // CTA c with lane c % lanes and part c / lanes of the lane's tiles, so that what one of
 // them reads of a DRAM page or a cache line the others need at that moment.  With each
 // lane's tiles after the other (lanes = 1: segments are units), 64 single-token
-// sequences over 8192 keys read 1.4 times their bytes from HBM: 262 us, in step 190 (now 167).
+// sequences over 8192 keys read 1.4 times their bytes from HBM: 262 us, in step 190 (now 168).
 struct TqRange {
   int units, lanes, lane;  // unit u of this lane is segment u * lanes + lane
   int total, G, part;      // tiles of the lane, parts they are cut into, this CTA's

@@ -5,9 +5,11 @@
 // elements (one group of the 4-bit format) each; a row's largest magnitude comes
 // from log2(D/16) shuffles, and the first lane writes the row's 16-byte tail.
 // A row of 128 bf16 values moves 256 + 144 (80) bytes, and a thread has kRows rows' loads
-// in flight.  Reading back is bound by HBM: 64K tokens of 8 heads from 4 bits in 67.6 us, 5.15
-// TB/s.  Writing 4 bits is bound by its instructions (about nine an element, the quotient's
-// exact rounding three of them): 11K tokens in 17.8 us, 3.3 TB/s.
+// in flight.  64K tokens of 8 heads, in us (floor at the measured copy rate): read from 4 bits
+// 66 (51), from 8 bits 66 (60), bound by HBM; written in 8 bits 61 (60), in 4 bits 73 (51), which
+// issues 82% of all slots (about nine instructions an element, the quotient's exact rounding
+// three of them).  A chunk of 11K tokens is one wave of short blocks: 17.8 us to 4 bits from cold
+// caches (8.6), with the loads' latency as the largest stall and 68% of the slots issued.
 #include "va_common.cuh"
 #include "va_quant.cuh"
 #include "va_quant.h"
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(kQuantThreads, 8) quantize_kernel(const QuantP
     // a row that holds an infinity or a NaN reads back as NaN
     const bool bad = !(row <= 3.402823466e38f);
     const int e = row_exponent<FMT>(row);
-    const float up = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e (e <= 119, so normal; e >= -126)
+    const float up = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e (normal: e is -126 to 120)
     const uint32_t scale = bad ? 0x7fc00000u : (uint32_t)(e + 127) << 23;
     uint32_t group = 0, code[4] = {0u, 0u, 0u, 0u};
     if (!bad) {
