@@ -323,12 +323,20 @@ def _bf16_rows(cache):
     return cache
 
 
+def _bf16_pair(k, v):
+    """_bf16_rows of a K and a V cache, which are held alike."""
+    if isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor) and torch.uint8 in (k.dtype, v.dtype) and \
+            (k.dtype != v.dtype or k.shape != v.shape):
+        raise ValueError(f"caches of {k.dtype} {list(k.shape)} and {v.dtype} {list(v.shape)} are not of the same rows")
+    return _bf16_rows(k), _bf16_rows(v)
+
+
 def verify_commit_kv_dense(k_cache, v_cache, seqlens, path, n_accept, seqlens_out=None,
                            workspace: Workspace = None, stream=None):
     """Move the accepted draft rows of k_cache / v_cache [B][len][Hkv][D] in
     place to the slots after each prefix; returns seqlens + n_accept.  (Here and
     in the eviction a cache may hold quantised rows, uint8 [..][kv_row_bytes].)"""
-    k_cache, v_cache = _bf16_rows(k_cache), _bf16_rows(v_cache)
+    k_cache, v_cache = _bf16_pair(k_cache, v_cache)
     B, cap, Hkv, D = k_cache.shape
     T = path.shape[1]
     if seqlens_out is None:
@@ -343,7 +351,7 @@ def verify_commit_kv_dense(k_cache, v_cache, seqlens, path, n_accept, seqlens_ou
 def verify_commit_kv_paged(k_pages, v_pages, page_table, seqlens, path, n_accept, seqlens_out=None,
                            workspace: Workspace = None, stream=None):
     """The same commit through a page table; pages [P][page][Hkv][D]."""
-    k_pages, v_pages = _bf16_rows(k_pages), _bf16_rows(v_pages)
+    k_pages, v_pages = _bf16_pair(k_pages, v_pages)
     P, ps, Hkv, D = k_pages.shape
     B, max_pages = page_table.shape
     T = path.shape[1]
@@ -603,7 +611,7 @@ class EvictScratch(Workspace):
 
 
 def _evict_call(layout, k, v, table, seqlens, indices, n_indices, weight, seqlens_out, scratch, workspace, stream):
-    k, v = _bf16_rows(k), _bf16_rows(v)
+    k, v = _bf16_pair(k, v)
     n0, n1, Hkv, D = cache = _sizes(k, "the key cache", 4)
     B, _, m = _sizes(indices, "indices", 3)
     stride = _sizes(weight, "weight", 3)[2] if weight is not None else 0
