@@ -515,6 +515,7 @@ va_status verify_evict_kv_paged(const va_shape *shape, void *k_pages, void *v_pa
  * over a projection's output, out of place or in place.  For every row x (one
  * head of one token), in fp32 and rounded once:
  *   y = x / sqrt(mean(x^2) + eps) * weight       (the head's weight given)
+ *                            (zeros where the sum of squares passes 2^128)
  *   y rotated as verify_rope_draft_* rotates     (positions given)
  * with q_weight for the query heads and k_weight for the key heads, each [D] of
  * the element type, 16-byte aligned; NULL leaves those rows unnormed.  positions [B][T] int32,
@@ -556,7 +557,8 @@ va_status verify_norm_rope(const va_shape *shape, const va_rows *q, const va_row
  * With amax the row's largest magnitude, s = 2^e for the least e >= -126 with
  * amax <= 448 * 2^e (e4m3) or amax <= 6 * 448 * 2^e (e2m1); g is the largest
  * magnitude of the group / (6 s), and a code x / s or x / (g s), each rounded to
- * the nearest representable value, ties to even, saturating (g = 0: code 0).
+ * the nearest representable value, ties to even, saturating (g = 0: zeros, with the
+ * element's sign).
  * These roundings are exact: the bytes are the same for every call.  A row that
  * holds an infinity or a NaN has s = NaN and reads back as NaN.
  *   Caches take the place of K and V caches of rows of D elements:

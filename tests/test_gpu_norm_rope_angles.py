@@ -56,3 +56,20 @@ def test_outputs_without_room_behind_the_last_row(token_major):
     for f, o in zip(flat, out):
         o.fill_(7.0)
         assert (f == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_at_the_ends_of_the_range(dtype):
+    """Squares past 2^128 give zeros, and squares below fp32's range count as none beside eps;
+    the rows around them are what they were."""
+    x = torch.randn(1, 4, 3, 64, device="cuda").to(dtype)
+    w = torch.ones(64, device="cuda", dtype=dtype)
+    plain = va.verify_norm_rope(x[:, :, :2], x[:, :, 2:], w, w)[0]
+    x[0, 1, 0], x[0, 2, 1] = 2.0 ** 64, 2.0 ** -80
+    out = va.verify_norm_rope(x[:, :, :2], x[:, :, 2:], w, w, eps=1e-6)[0]
+    assert (out[0, 1, 0] == 0).all()
+    want = torch.full((64,), 2.0 ** -80 * 1000, dtype=torch.float64)  # 1 / sqrt(1e-6)
+    assert ((out[0, 2, 1].double().cpu() - want).abs() <= (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -20) * want).all()
+    same = torch.ones(4, 2, dtype=torch.bool)
+    same[1, 0] = same[2, 1] = False
+    assert torch.equal(out[0][same], plain[0][same])
