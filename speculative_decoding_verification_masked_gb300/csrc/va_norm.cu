@@ -12,6 +12,8 @@
 // that it meets), so a row costs packed products alone: a 16K-token prompt was bound by
 // its instructions, not by HBM, and went from 94 to 63 us (5.4 TB/s, 79% of the measured copy
 // rate; weights and angles of a pair apart, in registers, before).  Rows are loaded kRows at a time, before the factors are known.
+// (Eight blocks an SM leave 64 registers a thread: 8 bytes of spills, 0.3% of the instructions.)
+// fp32 rows are bound by HBM: 16384 tokens in 99.7 us, 99% of the copy rate.
 //
 // Angles: base^(-2i/D) / 2 pi comes from the host as a binary fraction, good to 2^-55 (a
 // double; base >= 1), in 64 bits; its product with the position modulo 2^64 is the phase
